@@ -1,13 +1,16 @@
 """MI355X (gfx950) chunk-wise fast-weight update of In-Place Test-Time Training.
 
 The computation lives in libttt.so (hand-written HIP kernels behind a C ABI,
-declared in include/ttt.h); this package only binds it.
+declared in include/ttt.h); this package only binds it. Beside the layer stand
+the operators around it: the norms between layers with their gate and residual
+scales, and their gradients.
 """
 from .binding import (  # noqa: F401
     EXPORTS,
     LIB_PATH,
     PHASES,
     Handle,
+    NormGrads,
     TTTError,
     lib,
     ttt_destroy,
@@ -17,6 +20,10 @@ from .binding import (  # noqa: F401
     ttt_init,
     ttt_last_error,
     ttt_phase_times,
+    ttt_norm_post,
+    ttt_norm_post_grad,
+    ttt_norm_pre,
+    ttt_norm_pre_grad,
     ttt_plan,
     ttt_reset,
     ttt_set_clip,

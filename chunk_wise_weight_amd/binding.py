@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, List, Optional, Tuple
+from typing import Dict, List, NamedTuple, Optional, Tuple
 
 import torch  # loads the HIP runtime the library binds to (same libamdhip64 soname)
 
@@ -21,7 +21,8 @@ ERRORS = {-1: "TTT_E_NULL", -2: "TTT_E_SHAPE", -3: "TTT_E_DTYPE", -4: "TTT_E_NOM
           -6: "TTT_E_NODEV", -7: "TTT_E_ARG"}
 EXPORTS = ("ttt_init", "ttt_forward_chunked", "ttt_forward_docs", "ttt_reset", "ttt_destroy", "ttt_last_error",
            "ttt_set_group_chunks", "ttt_set_clip", "ttt_set_target_conv", "ttt_plan", "ttt_set_profiling", "ttt_phase_times",
-           "ttt_workspace_bytes", "ttt_set_output_f32", "ttt_state_delta", "ttt_forward_chunked_noalloc")
+           "ttt_workspace_bytes", "ttt_set_output_f32", "ttt_state_delta", "ttt_forward_chunked_noalloc",
+           "ttt_norm_pre", "ttt_norm_post", "ttt_norm_ws_bytes", "ttt_norm_pre_grad", "ttt_norm_post_grad")
 
 _lib = None
 
@@ -74,6 +75,15 @@ def lib() -> ctypes.CDLL:
     L.ttt_state_delta.restype = i32
     L.ttt_forward_chunked_noalloc.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
     L.ttt_forward_chunked_noalloc.restype = i32
+    i64, sz = ctypes.c_int64, ctypes.c_size_t
+    L.ttt_norm_pre.argtypes = [vp, i32, vp, i32, f32, i64, i32, vp, i32, vp]
+    L.ttt_norm_post.argtypes = [vp, i32, vp, i32, vp, vp, i32, vp, i32, f32, f32, f32, i64, i32, vp, vp, i32, vp]
+    L.ttt_norm_ws_bytes.argtypes = [i64, i32, ctypes.POINTER(sz)]
+    L.ttt_norm_pre_grad.argtypes = [vp, i32, vp, i32, vp, i32, vp, f32, i64, i32, vp, vp, vp, sz, vp]
+    L.ttt_norm_post_grad.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, vp, i32, vp, i32, f32, f32, f32, i64, i32, vp,
+                                     vp, vp, vp, vp, vp, sz, vp]
+    for fn in (L.ttt_norm_pre, L.ttt_norm_post, L.ttt_norm_ws_bytes, L.ttt_norm_pre_grad, L.ttt_norm_post_grad):
+        fn.restype = i32
     _lib = L
     return L
 
@@ -297,3 +307,233 @@ def ttt_workspace_bytes(h: Handle) -> int:
     n = ctypes.c_size_t()
     _check(lib().ttt_workspace_bytes(h.ptr, ctypes.byref(n)), "ttt_workspace_bytes")
     return n.value
+
+
+# ---- the operators around the layer ----
+#
+# They take no handle. Tensors must be contiguous and on the current device; an
+# output that is not given is allocated. With `stream` the work, and the
+# outputs made here, belong to that stream, as under torch.cuda.stream(stream);
+# what the tensors hold must be ready on it. They record no autograd graph:
+# each gradient is a call of its own.
+
+_DT = {torch.float32: TTT_F32, torch.bfloat16: TTT_BF16}
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
+
+
+class _Call:
+    """The stream and device of one call, and the tensors it was given."""
+
+    def __init__(self, first: torch.Tensor, stream):
+        self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+        self.stream = stream
+        if stream is not None and stream.device.index != self.device:
+            raise ValueError("stream must be on the current device")
+        self.where = first.device
+
+    def arg(self, t: Optional[torch.Tensor], name: str, dtype=None, shape=None) -> Optional[int]:
+        """A tensor's address (None for None), after its checks."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+        if dtype is None:
+            if t.dtype not in _DT:
+                raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+        elif t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} must be on the current device")
+        if self.stream is not None:
+            t.record_stream(self.stream)
+        return t.data_ptr()
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.where)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.where)
+
+    def scratch(self, nbytes: int) -> torch.Tensor:
+        return self.empty((nbytes,), torch.uint8)
+
+    def on(self) -> int:
+        return (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
+
+
+def _tensor(t, name: str) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    return t
+
+
+def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    if _tensor(t, name).dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    d = t.shape[-1]
+    return (t.numel() // d if d else 0), d
+
+
+def _params_dtype(*params) -> torch.dtype:
+    """The one dtype of a call's parameters (those that are None say nothing)."""
+    dt = None
+    for name, p in params:
+        if p is None:
+            continue
+        if dt is not None and _tensor(p, name).dtype != dt:
+            raise ValueError("the gains and a gate per channel must have one dtype")
+        dt = _tensor(p, name).dtype
+    if dt is not None and dt not in _DT:
+        raise ValueError(f"the gains and a gate per channel must be float32 or bfloat16, got {dt}")
+    return dt or torch.float32
+
+
+def _gate_kind(gate, y: torch.Tensor, d: int) -> int:
+    if gate is None:
+        return GATE_NONE
+    if y.dim() < 2:
+        raise ValueError("with a gate, h and y need a row dimension")
+    if _tensor(gate, "gate").shape == (d,):
+        return GATE_CHANNEL
+    if gate.shape == y.shape:
+        return GATE_TOKEN
+    raise ValueError(f"gate must have shape ({d},) or that of y, got {tuple(gate.shape)}")
+
+
+def _norm_ws(rows: int, d: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().ttt_norm_ws_bytes(rows, d, ctypes.byref(n)), "ttt_norm_ws_bytes")
+    return n.value
+
+
+def ttt_norm_pre(h: torch.Tensor, w: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 x: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """The norm before a block: x = w * h * rms(h) over the last dimension (w None: no gain).
+
+    h [...][d] float32 or bfloat16; x has h's shape and `dtype` (default: h's; a float32 h may give a bfloat16 x).
+    """
+    rows, d = _rows(h, "h")
+    c = _Call(h, stream)
+    ph, pw = c.arg(h, "h"), c.arg(w, "w", None, (d,))
+    wdt = _params_dtype(("w", w))
+    if x is None:
+        x = c.empty(h.shape, dtype or h.dtype)
+    px = c.arg(x, "x", dtype, h.shape)
+    _check(lib().ttt_norm_pre(ph, _DT[h.dtype], pw, _DT[wdt], eps, rows, d, px, _DT[x.dtype], c.on()), "ttt_norm_pre")
+    return x
+
+
+def ttt_norm_post(h: torch.Tensor, y: torch.Tensor, w: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
+                  w_next: Optional[torch.Tensor] = None, next_norm: bool = False, o: Optional[torch.Tensor] = None,
+                  x: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                  stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """After a block: o = alpha * h + beta * gate * w * y * rms(y), and with next_norm (or w_next or x given) also the
+    next block's input x = w_next * o * rms(o). Returns (o, x or None).
+
+    h [...][d] the residual stream, y (the same shape) what the block gave; gate [d], y's shape (in y's dtype) or None;
+    x in `dtype` (default: y's). o may be h: the stream is then updated in place.
+    """
+    rows, d = _rows(h, "h")
+    c = _Call(h, stream)
+    ph, py = c.arg(h, "h"), c.arg(y, "y", None, h.shape)
+    kind = _gate_kind(gate, y, d)
+    pw, pn = c.arg(w, "w", None, (d,)), c.arg(w_next, "w_next", None, (d,))
+    pg = c.arg(gate, "gate", y.dtype if kind == GATE_TOKEN else None)
+    wdt = _params_dtype(("w", w), ("w_next", w_next), ("gate", gate if kind == GATE_CHANNEL else None))
+    if o is None:
+        o = c.empty(h.shape, h.dtype)
+    po = c.arg(o, "o", h.dtype, h.shape)
+    if x is None and (next_norm or w_next is not None):
+        x = c.empty(h.shape, dtype or y.dtype)
+    px = c.arg(x, "x", dtype, h.shape)
+    _check(lib().ttt_norm_post(ph, _DT[h.dtype], py, _DT[y.dtype], pw, pg, kind, pn, _DT[wdt], alpha, beta, eps, rows,
+                               d, po, px, _DT[y.dtype if x is None else x.dtype], c.on()), "ttt_norm_post")
+    return o, x
+
+
+def ttt_norm_pre_grad(dx: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      dh_in: Optional[torch.Tensor] = None, dh: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gradients of ttt_norm_pre: (dh, dw) from dx; dh_in, the gradient h has from elsewhere, is added to dh (which may
+    be the same tensor). dw [d] is float32, None without a gain."""
+    rows, d = _rows(h, "h")
+    c = _Call(h, stream)
+    ph, pdx = c.arg(h, "h"), c.arg(dx, "dx", None, h.shape)
+    pw, pin = c.arg(w, "w", None, (d,)), c.arg(dh_in, "dh_in", h.dtype, h.shape)
+    wdt = _params_dtype(("w", w))
+    if dh is None:
+        dh = c.empty(h.shape, h.dtype)
+    pdh = c.arg(dh, "dh", h.dtype, h.shape)
+    dw = ws = None
+    nws = 0
+    if w is not None:
+        dw = c.empty((d,), torch.float32)
+        nws = _norm_ws(rows, d)
+        ws = c.scratch(nws)
+    _check(lib().ttt_norm_pre_grad(pdx, _DT[dx.dtype], ph, _DT[h.dtype], pw, _DT[wdt], pin, eps, rows, d, pdh,
+                                   dw.data_ptr() if dw is not None else None, ws.data_ptr() if ws is not None else None,
+                                   nws, c.on()), "ttt_norm_pre_grad")
+    return dh, dw
+
+
+class NormGrads(NamedTuple):
+    """What ttt_norm_post_grad gives; None where there is no such input."""
+
+    dh: torch.Tensor
+    dy: torch.Tensor
+    dw: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dw_next: Optional[torch.Tensor]
+
+
+def ttt_norm_post_grad(dh_in: Optional[torch.Tensor], dx: Optional[torch.Tensor], o: Optional[torch.Tensor],
+                       y: torch.Tensor, w: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                       alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
+                       w_next: Optional[torch.Tensor] = None, dh: Optional[torch.Tensor] = None,
+                       dy: Optional[torch.Tensor] = None, stream=None) -> NormGrads:
+    """Gradients of ttt_norm_post from dh_in (the gradient o has from elsewhere, or None) and dx (the gradient of x, or
+    None; one of the two is needed), with o as ttt_norm_post gave it (needed with dx) and y. dh has the residual
+    stream's dtype and may be dh_in; dy may be y. dw, dw_next and a [d] gate's gradient are float32."""
+    rows, d = _rows(y, "y")
+    c = _Call(y, stream)
+    if dh_in is None and dx is None:
+        raise ValueError("dh_in or dx must be given")
+    if dx is not None and o is None:
+        raise ValueError("o must be given with dx")
+    hdt = _tensor(dh_in, "dh_in").dtype if dh_in is not None else _tensor(o, "o").dtype
+    py, pin = c.arg(y, "y"), c.arg(dh_in, "dh_in", None, y.shape)
+    pdx, po = c.arg(dx, "dx", None, y.shape), c.arg(o if dx is not None else None, "o", hdt, y.shape)
+    if hdt not in _DT:
+        raise ValueError(f"o must be float32 or bfloat16, got {hdt}")
+    kind = _gate_kind(gate, y, d)
+    pw, pn = c.arg(w, "w", None, (d,)), c.arg(w_next, "w_next", None, (d,))
+    pg = c.arg(gate, "gate", y.dtype if kind == GATE_TOKEN else None)
+    wdt = _params_dtype(("w", w), ("w_next", w_next), ("gate", gate if kind == GATE_CHANNEL else None))
+    if dh is None:
+        dh = c.empty(y.shape, hdt)
+    if dy is None:
+        dy = c.empty(y.shape, y.dtype)
+    pdh, pdy = c.arg(dh, "dh", hdt, y.shape), c.arg(dy, "dy", y.dtype, y.shape)
+    dw = c.empty((d,), torch.float32) if w is not None else None
+    dn = c.empty((d,), torch.float32) if w_next is not None and dx is not None else None
+    dg = None
+    if kind == GATE_CHANNEL:
+        dg = c.empty((d,), torch.float32)
+    elif kind == GATE_TOKEN:
+        dg = c.empty(y.shape, y.dtype)
+    ws, nws = None, 0
+    if dw is not None or dn is not None or kind == GATE_CHANNEL:
+        nws = _norm_ws(rows, d)
+        ws = c.scratch(nws)
+    out = [None if t is None else t.data_ptr() for t in (dw, dg, dn, ws)]
+    _check(lib().ttt_norm_post_grad(pin, pdx, _DT[y.dtype if dx is None else dx.dtype], po, _DT[hdt], py, _DT[y.dtype],
+                                    pw, pg, kind, pn, _DT[wdt], alpha, beta, eps, rows, d, pdh, pdy, out[0], out[1],
+                                    out[2], out[3], nws, c.on()), "ttt_norm_post_grad")
+    return NormGrads(dh, dy, dw, dg, dn)

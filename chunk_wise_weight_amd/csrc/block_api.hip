@@ -1,0 +1,267 @@
+// C ABI of the operators around the layer: argument checks and launches. No
+// call allocates, keeps state or waits.
+#include <cmath>
+#include <initializer_list>
+
+#include "../../include/ttt.h"
+#include "errors.h"
+#include "norm.h"
+
+namespace {
+
+constexpr int kMaxWidth = 65536;
+constexpr long long kMaxRows = 0x7fffffffLL;
+
+bool known(ttt_dtype t) { return t == TTT_F32 || t == TTT_BF16; }
+size_t size_of(ttt_dtype t) { return t == TTT_BF16 ? 2 : 4; }
+
+// An array of a call: its bytes, and the size of one element.
+struct Span {
+  const char *name;
+  const void *p;
+  size_t bytes, elem;
+};
+
+bool overlap(const Span &a, const Span &b) {
+  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+  const char *x = (const char *)a.p, *y = (const char *)b.p;
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
+// Outputs against inputs and one another. in_place: pairs (output, input) that
+// may be the same array.
+struct Pair {
+  const void *out, *in;
+};
+int check_spans(const char *where, std::initializer_list<Span> in, std::initializer_list<Span> out,
+                std::initializer_list<Pair> in_place) {
+  for (const Span &s : in)
+    if ((uintptr_t)s.p % s.elem) return ttt_fail(TTT_E_ARG, "%s: %s is not aligned to its elements", where, s.name);
+  for (const Span *o = out.begin(); o != out.end(); ++o) {
+    if ((uintptr_t)o->p % o->elem) return ttt_fail(TTT_E_ARG, "%s: %s is not aligned to its elements", where, o->name);
+    for (const Span &s : in) {
+      if (!overlap(*o, s)) continue;
+      bool ok = false;
+      for (const Pair &p : in_place) ok = ok || (p.out == o->p && p.in == s.p && o->p == s.p && o->bytes == s.bytes);
+      if (!ok) return ttt_fail(TTT_E_ARG, "%s: %s overlaps %s", where, o->name, s.name);
+    }
+    for (const Span *q = out.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return ttt_fail(TTT_E_ARG, "%s: %s overlaps %s", where, o->name, q->name);
+  }
+  return TTT_OK;
+}
+
+int check_norm(const char *where, ttt_dtype h, ttt_dtype y, ttt_dtype x, ttt_dtype w, bool post, bool next, float alpha,
+               float beta, float eps, int64_t rows, int d) {
+  if (!known(h) || !known(w) || (post && !known(y)) || (next && !known(x)))
+    return ttt_fail(TTT_E_DTYPE, "%s: unknown dtype", where);
+  if (post && y == TTT_F32 && h == TTT_BF16)
+    return ttt_fail(TTT_E_DTYPE, "%s: an fp32 y needs an fp32 residual stream", where);
+  if (next && x == TTT_F32 && (h == TTT_BF16 || (post && y == TTT_BF16)))
+    return ttt_fail(TTT_E_DTYPE, "%s: an fp32 x needs fp32 inputs", where);
+  if (d < 8 || d > kMaxWidth) return ttt_fail(TTT_E_SHAPE, "%s: d must be in [8, %d], got %d", where, kMaxWidth, d);
+  if (rows < 0 || rows > kMaxRows)
+    return ttt_fail(TTT_E_SHAPE, "%s: rows must be in [0, 2^31), got %lld", where, (long long)rows);
+  if (!(eps >= 1e-30f) || !std::isfinite(eps)) return ttt_fail(TTT_E_ARG, "%s: eps must be finite, at least 1e-30", where);
+  if (!std::isfinite(alpha) || !std::isfinite(beta)) return ttt_fail(TTT_E_ARG, "%s: alpha, beta must be finite", where);
+  return TTT_OK;
+}
+
+int check_gate(const char *where, const void *gate, int kind, int64_t rows) {
+  if (kind != TTT_GATE_NONE && kind != TTT_GATE_CHANNEL && kind != TTT_GATE_TOKEN)
+    return ttt_fail(TTT_E_ARG, "%s: unknown gate kind %d", where, kind);
+  if (kind != TTT_GATE_NONE && !gate && (kind == TTT_GATE_CHANNEL || rows > 0))
+    return ttt_fail(TTT_E_NULL, "%s: gate is NULL", where);
+  return TTT_OK;
+}
+
+size_t gate_bytes(int kind, int64_t rows, int d, size_t token, size_t channel) {
+  return kind == TTT_GATE_TOKEN ? (size_t)rows * d * token : kind == TTT_GATE_CHANNEL ? (size_t)d * channel : 0;
+}
+
+NormTypes types(ttt_dtype h, ttt_dtype y, ttt_dtype x) { return NormTypes{h == TTT_F32, y == TTT_F32, x == TTT_F32}; }
+
+int check_ws(const char *where, const void *ws, size_t have, size_t need) {
+  if (!ws) return ttt_fail(TTT_E_NULL, "%s: the workspace is NULL", where);
+  if ((uintptr_t)ws % 16) return ttt_fail(TTT_E_ARG, "%s: the workspace must be 16-byte aligned", where);
+  if (have < need) return ttt_fail(TTT_E_SHAPE, "%s: needs %zu bytes of workspace, got %zu", where, need, have);
+  return TTT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ttt_norm_pre(const void *h, ttt_dtype h_dt, const void *w, ttt_dtype w_dt, float eps, int64_t rows, int d, void *x,
+                 ttt_dtype x_dt, void *hip_stream) {
+  static const char *kWhere = "ttt_norm_pre";
+  int rc = check_norm(kWhere, h_dt, h_dt, x_dt, w_dt, false, true, 1.f, 1.f, eps, rows, d);
+  if (rc) return rc;
+  if (rows > 0 && (!h || !x)) return ttt_fail(TTT_E_NULL, "%s: h or x is NULL", kWhere);
+  const size_t n = (size_t)rows * d;
+  rc = check_spans(kWhere, {{"h", h, n * size_of(h_dt), size_of(h_dt)}, {"w", w, d * size_of(w_dt), size_of(w_dt)}},
+                   {{"x", x, n * size_of(x_dt), size_of(x_dt)}}, {});
+  if (rc) return rc;
+  rc = ttt_check_device();
+  if (rc || rows == 0) return rc;
+  NormArgs a{};
+  a.rows = rows;
+  a.d = d;
+  a.eps = eps;
+  a.alpha = a.beta = 1.f;
+  a.h = h;
+  a.w_next = w;
+  a.p_f32 = w_dt == TTT_F32;
+  a.x = x;
+  return ttt_launched(launch_norm_fwd(a, types(h_dt, h_dt, x_dt), (hipStream_t)hip_stream), kWhere);
+}
+
+int ttt_norm_post(const void *h, ttt_dtype h_dt, const void *y, ttt_dtype y_dt, const void *w, const void *gate,
+                  int gate_kind, const void *w_next, ttt_dtype w_dt, float alpha, float beta, float eps, int64_t rows,
+                  int d, void *o, void *x, ttt_dtype x_dt, void *hip_stream) {
+  static const char *kWhere = "ttt_norm_post";
+  int rc = check_norm(kWhere, h_dt, y_dt, x_dt, w_dt, true, x != nullptr, alpha, beta, eps, rows, d);
+  if (!rc) rc = check_gate(kWhere, gate, gate_kind, rows);
+  if (rc) return rc;
+  if (rows > 0 && (!h || !y || !o)) return ttt_fail(TTT_E_NULL, "%s: h, y or o is NULL", kWhere);
+  const size_t n = (size_t)rows * d, ws = size_of(w_dt);
+  const size_t ge = gate_kind == TTT_GATE_TOKEN ? size_of(y_dt) : ws;
+  if (gate_kind == TTT_GATE_NONE) gate = nullptr;
+  rc = check_spans(kWhere,
+                   {{"h", h, n * size_of(h_dt), size_of(h_dt)},
+                    {"y", y, n * size_of(y_dt), size_of(y_dt)},
+                    {"w", w, d * ws, ws},
+                    {"gate", gate, gate_bytes(gate_kind, rows, d, size_of(y_dt), ws), ge},
+                    {"w_next", w_next, d * ws, ws}},
+                   {{"o", o, n * size_of(h_dt), size_of(h_dt)}, {"x", x, n * size_of(x_dt), x ? size_of(x_dt) : 1}},
+                   {{o, h}});
+  if (rc) return rc;
+  rc = ttt_check_device();
+  if (rc || rows == 0) return rc;
+  NormArgs a{};
+  a.rows = rows;
+  a.d = d;
+  a.eps = eps;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.h = h;
+  a.y = y;
+  a.w = w;
+  a.gate = gate;
+  a.token_gate = gate_kind == TTT_GATE_TOKEN;
+  a.w_next = w_next;
+  a.p_f32 = w_dt == TTT_F32;
+  a.o = o;
+  a.x = x;
+  return ttt_launched(launch_norm_fwd(a, types(h_dt, y_dt, x_dt), (hipStream_t)hip_stream), kWhere);
+}
+
+int ttt_norm_ws_bytes(int64_t rows, int d, size_t *bytes) {
+  if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_norm_ws_bytes: bytes is NULL");
+  const int rc = check_norm("ttt_norm_ws_bytes", TTT_F32, TTT_F32, TTT_F32, TTT_F32, true, true, 1.f, 1.f, 1.f, rows, d);
+  if (rc) return rc;
+  *bytes = norm_ws_bytes(rows, d);
+  return TTT_OK;
+}
+
+int ttt_norm_pre_grad(const void *dx, ttt_dtype x_dt, const void *h, ttt_dtype h_dt, const void *w, ttt_dtype w_dt,
+                      const void *dh_in, float eps, int64_t rows, int d, void *dh, float *dw, void *ws, size_t ws_bytes,
+                      void *hip_stream) {
+  static const char *kWhere = "ttt_norm_pre_grad";
+  int rc = check_norm(kWhere, h_dt, h_dt, x_dt, w_dt, false, true, 1.f, 1.f, eps, rows, d);
+  if (rc) return rc;
+  if (rows > 0 && (!dx || !h || !dh)) return ttt_fail(TTT_E_NULL, "%s: dx, h or dh is NULL", kWhere);
+  if (dw && (rc = check_ws(kWhere, ws, ws_bytes, norm_ws_bytes(rows, d)))) return rc;
+  const size_t n = (size_t)rows * d, hs = size_of(h_dt);
+  rc = check_spans(kWhere,
+                   {{"dx", dx, n * size_of(x_dt), size_of(x_dt)},
+                    {"h", h, n * hs, hs},
+                    {"w", w, d * size_of(w_dt), size_of(w_dt)},
+                    {"dh_in", dh_in, n * hs, hs}},
+                   {{"dh", dh, n * hs, hs},
+                    {"dw", dw, (size_t)d * 4, 4},
+                    {"ws", dw ? ws : nullptr, norm_ws_bytes(rows, d), 4}},
+                   {{dh, dh_in}});
+  if (rc) return rc;
+  rc = ttt_check_device();
+  if (rc) return rc;
+  NormArgs a{};
+  a.rows = rows;
+  a.d = d;
+  a.eps = eps;
+  a.alpha = a.beta = 1.f;
+  a.h = h;
+  a.w_next = w;
+  a.p_f32 = w_dt == TTT_F32;
+  a.dx = dx;
+  a.dh_in = dh_in;
+  a.dh = dh;
+  a.dw_next = dw;
+  a.part = dw ? (float *)ws : nullptr;
+  return ttt_launched(launch_norm_bwd(a, types(h_dt, h_dt, x_dt), false, true, (hipStream_t)hip_stream), kWhere);
+}
+
+int ttt_norm_post_grad(const void *dh_in, const void *dx, ttt_dtype x_dt, const void *o, ttt_dtype h_dt, const void *y,
+                       ttt_dtype y_dt, const void *w, const void *gate, int gate_kind, const void *w_next,
+                       ttt_dtype w_dt, float alpha, float beta, float eps, int64_t rows, int d, void *dh, void *dy,
+                       float *dw, void *dgate, float *dw_next, void *ws, size_t ws_bytes, void *hip_stream) {
+  static const char *kWhere = "ttt_norm_post_grad";
+  const bool next = dx != nullptr;
+  int rc = check_norm(kWhere, h_dt, y_dt, x_dt, w_dt, true, next, alpha, beta, eps, rows, d);
+  if (!rc) rc = check_gate(kWhere, gate, gate_kind, rows);
+  if (rc) return rc;
+  const bool token = gate_kind == TTT_GATE_TOKEN;
+  if (rows > 0 && (!dh_in && !dx)) return ttt_fail(TTT_E_NULL, "%s: dh_in and dx are both NULL", kWhere);
+  if (rows > 0 && ((next && !o) || !y || !dh || !dy)) return ttt_fail(TTT_E_NULL, "%s: o, y, dh or dy is NULL", kWhere);
+  if (rows > 0 && token && !dgate) return ttt_fail(TTT_E_NULL, "%s: dgate is NULL", kWhere);
+  if (gate_kind == TTT_GATE_NONE) gate = dgate = nullptr;
+  float *dgate_c = token ? nullptr : (float *)dgate;
+  // without dx no gradient reaches w_next; in a call without rows dx says nothing, and dw_next is zero
+  if (!next && rows > 0) dw_next = nullptr;
+  const bool part = dw || dgate_c || dw_next;
+  if (part && (rc = check_ws(kWhere, ws, ws_bytes, norm_ws_bytes(rows, d)))) return rc;
+  const size_t n = (size_t)rows * d, hs = size_of(h_dt), ys = size_of(y_dt), ps = size_of(w_dt);
+  rc = check_spans(kWhere,
+                   {{"dh_in", dh_in, n * hs, hs},
+                    {"dx", dx, n * size_of(x_dt), next ? size_of(x_dt) : 1},
+                    {"o", next ? o : nullptr, n * hs, hs},
+                    {"y", y, n * ys, ys},
+                    {"w", w, d * ps, ps},
+                    {"gate", gate, gate_bytes(gate_kind, rows, d, ys, ps), token ? ys : ps},
+                    {"w_next", w_next, d * ps, ps}},
+                   {{"dh", dh, n * hs, hs},
+                    {"dy", dy, n * ys, ys},
+                    {"dw", dw, (size_t)d * 4, 4},
+                    {"dgate", dgate, gate_bytes(gate_kind, rows, d, ys, 4), token ? ys : 4},
+                    {"dw_next", dw_next, (size_t)d * 4, 4},
+                    {"ws", part ? ws : nullptr, norm_ws_bytes(rows, d), 4}},
+                   {{dh, dh_in}, {dy, y}});
+  if (rc) return rc;
+  rc = ttt_check_device();
+  if (rc) return rc;
+  NormArgs a{};
+  a.rows = rows;
+  a.d = d;
+  a.eps = eps;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.h = o;
+  a.y = y;
+  a.w = w;
+  a.gate = gate;
+  a.token_gate = token;
+  a.w_next = w_next;
+  a.p_f32 = w_dt == TTT_F32;
+  a.dx = dx;
+  a.dh_in = dh_in;
+  a.dh = dh;
+  a.dy = dy;
+  a.dgate_t = token ? dgate : nullptr;
+  a.dw = dw;
+  a.dgate_c = dgate_c;
+  a.dw_next = dw_next;
+  a.part = part ? (float *)ws : nullptr;
+  return ttt_launched(launch_norm_bwd(a, types(h_dt, y_dt, x_dt), true, next, (hipStream_t)hip_stream), kWhere);
+}
+
+}  // extern "C"

@@ -1,0 +1,574 @@
+// RMS norms before and after a block, fused with the block's gate and the
+// residual scales, and their gradients.
+//
+//   after a block   q = (mean y^2 + eps)^-1/2,  o = alpha h + beta a w y q
+//   before a block  r = (mean o^2 + eps)^-1/2,  x = w' o r   (of the unrounded o)
+//
+// (a: a gate per channel, per token, or none). Every row is read once and
+// written once: a row's elements stay in the registers of the threads that
+// own its columns between the row sum and the use of its result. All sums are
+// fp32. The gradients of the parameters are sums over the rows: a thread adds
+// its columns over the rows its workgroup takes, in registers, and a second
+// kernel adds the workgroups' partial sums in a fixed order.
+#include "norm.h"
+#include "vec8.h"
+
+namespace {
+
+constexpr int kCUs = 256;
+// threads a launch keeps on each CU
+constexpr int kFwdPerCu = 2048, kBwdPerCu = 2048;
+constexpr int kMaxNarrow = 8192;  // widest row whose elements stay in registers: 1024 threads of 8
+
+// How rows lie on threads: `tr` threads own a row, 8 elements each (a power
+// of two below a wave for narrow rows, else whole waves), `rpb` rows per
+// workgroup.
+struct Map {
+  int tr, rpb, threads;
+};
+
+Map row_map(int d) {
+  const int v = (d + 7) / 8;
+  Map m;
+  if (v > kMaxNarrow / 8) {
+    m.tr = 1024;
+  } else if (v > 32) {
+    m.tr = (v + 63) / 64 * 64;
+  } else {
+    m.tr = 8;
+    while (m.tr < v) m.tr *= 2;
+  }
+  m.rpb = m.tr <= 64 ? 256 / m.tr : 1;
+  m.threads = m.tr * m.rpb;
+  return m;
+}
+
+// workgroups of a launch that keeps `per_cu` threads on each CU
+unsigned grid_rows(long long rows, const Map &m, int per_cu) {
+  const long long want = (rows + m.rpb - 1) / m.rpb;
+  long long most = (long long)kCUs * (per_cu / m.threads > 0 ? per_cu / m.threads : 1);
+  return (unsigned)(want < most ? want : most);
+}
+
+// Sums of NS values over the tr threads of a row, the result in every one of
+// them. Waves of one row add through `red`; its two halves take turns, so one
+// barrier per sum is enough: a half is written again only after the barrier
+// of the sum between, which every reader of the half has then passed.
+template <int NS>
+__device__ __forceinline__ void row_sum(float (&s)[NS], int tr, float (*red)[16][NS], int &turn) {
+  const int width = tr < 64 ? tr : 64;
+  for (int o = width / 2; o > 0; o >>= 1) {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) s[k] += __shfl_xor(s[k], o);
+  }
+  if (tr <= 64) return;
+  const int wave = threadIdx.x >> 6, nw = tr >> 6;
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) red[turn][wave][k] = s[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < NS; ++k) s[k] = 0.f;
+#pragma unroll 2  // unrolled further, the loads of all waves' sums would hold a hundred registers
+  for (int w = 0; w < nw; ++w) {
+#pragma unroll
+    for (int k = 0; k < NS; ++k) s[k] += red[turn][w][k];
+  }
+  turn ^= 1;
+}
+
+// r of a row from its sum of squares
+__device__ __forceinline__ float row_rms(float sumsq, int d, float eps) { return rsqrtf(sumsq / (float)d + eps); }
+
+template <typename T>
+__device__ __forceinline__ const T *row_of(const void *p, long long row, int d) {
+  return reinterpret_cast<const T *>(p) + row * d;
+}
+template <typename T>
+__device__ __forceinline__ T *row_of(void *p, long long row, int d) {
+  return reinterpret_cast<T *>(p) + row * d;
+}
+
+// The eight columns of a thread: from 8 * c on, or, where the row ends sooner
+// (R: its width is no multiple of 8), its last eight. Such a thread computes
+// and writes its neighbour's columns a second time, to the same values, and
+// leaves them out of its row sums; every element of a row is read before any
+// is written (the row sums lie between), so outputs may lie on inputs all the
+// same. Threads past the row's end have none.
+template <bool R>
+struct Cols {
+  int at, first;  // first column, and which of the eight is the first of its own
+  bool mine;
+  __device__ __forceinline__ Cols(int c, int d) {
+    mine = c * 8 < d;
+    at = R && c * 8 + 8 > d ? d - 8 : c * 8;
+    first = c * 8 - at;
+  }
+  __device__ __forceinline__ float own(int j, float v) const { return !R || j >= first ? v : 0.f; }
+};
+
+// ---- forward ----
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R>
+__global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs A, int tr, int rpb) {
+  __shared__ float red[2][16][1];
+  int turn = 0;
+  const int d = A.d, sub = threadIdx.x / tr;
+  const Cols<R> cols(threadIdx.x % tr, d);
+  const int c = cols.at;
+  const bool mine = cols.mine;
+  float w[8], wn[8], ga[8];
+  if (POST) {
+    load_param(A.w, A.p_f32, c, mine, w);
+    load_param(A.token_gate ? nullptr : A.gate, A.p_f32, c, mine, ga);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] *= A.beta * ga[j];
+  }
+  if (NEXT) load_param(A.w_next, A.p_f32, c, mine, wn);
+  for (long long row0 = (long long)blockIdx.x * rpb; row0 < A.rows; row0 += (long long)gridDim.x * rpb) {
+    const long long row = row0 + sub;
+    const bool on = mine && row < A.rows;
+    float o[8];
+    load_w(row_of<H>(A.h, row, d) + c, on, o);
+    if (POST) {
+      float y[8];
+      load_w(row_of<Y>(A.y, row, d) + c, on, y);
+      float t[8];
+      if (A.token_gate)
+        load_w(row_of<Y>(A.gate, row, d) + c, on, t);
+      else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = 1.f;
+      }
+      float s[1] = {0.f};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[0] += cols.own(j, y[j] * y[j]);
+      row_sum<1>(s, tr, red, turn);
+      const float q = row_rms(s[0], d, A.eps);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = A.alpha * o[j] + w[j] * t[j] * (y[j] * q);
+      store_w(row_of<H>(A.o, row, d) + c, on, o);
+    }
+    if (NEXT) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[0] += cols.own(j, o[j] * o[j]);
+      row_sum<1>(s, tr, red, turn);
+      const float r = row_rms(s[0], d, A.eps);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = wn[j] * (o[j] * r);
+      store_w(row_of<X>(A.x, row, d) + c, on, o);
+    }
+  }
+}
+
+// Rows too wide for registers: the row is read again for each step (from the
+// caches), one workgroup per row. Each element is written by the thread that
+// last reads it, so an output may lie on its input here too.
+template <typename H, typename Y, typename X, bool POST, bool NEXT, int W>
+__global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormArgs A) {
+  __shared__ float red[2][16][1];
+  int turn = 0;
+  const int d = A.d, v = d / W;
+  for (long long row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    const H *h = row_of<H>(A.h, row, d);
+    const Y *y = row_of<Y>(A.y, row, d);
+    const Y *ta = row_of<Y>(A.gate, row, d);
+    float q = 0.f, r = 0.f;
+    auto after = [&](int c, float (&o)[W]) {  // o of W columns
+      load_w(h + c * W, true, o);
+      if (POST) {
+        float yy[W], w[W], a[W];
+        load_w(y + c * W, true, yy);
+        load_param(A.w, A.p_f32, c * W, true, w);
+        if (A.token_gate)
+          load_w(ta + c * W, true, a);
+        else
+          load_param(A.gate, A.p_f32, c * W, true, a);
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[j] = A.alpha * o[j] + A.beta * a[j] * w[j] * (yy[j] * q);
+      }
+    };
+    if (POST) {
+      float s[1] = {0.f};
+      for (int c = threadIdx.x; c < v; c += 1024) {
+        float yy[W];
+        load_w(y + c * W, true, yy);
+#pragma unroll
+        for (int j = 0; j < W; ++j) s[0] += yy[j] * yy[j];
+      }
+      row_sum<1>(s, 1024, red, turn);
+      q = row_rms(s[0], d, A.eps);
+    }
+    if (NEXT) {
+      float s[1] = {0.f};
+      for (int c = threadIdx.x; c < v; c += 1024) {
+        float o[W];
+        after(c, o);
+#pragma unroll
+        for (int j = 0; j < W; ++j) s[0] += o[j] * o[j];
+      }
+      row_sum<1>(s, 1024, red, turn);
+      r = row_rms(s[0], d, A.eps);
+    }
+    for (int c = threadIdx.x; c < v; c += 1024) {
+      float o[W];
+      after(c, o);
+      if (POST) store_w(row_of<H>(A.o, row, d) + c * W, true, o);
+      if (NEXT) {
+        float wn[W];
+        load_param(A.w_next, A.p_f32, c * W, true, wn);
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[j] = wn[j] * (o[j] * r);
+        store_w(row_of<X>(A.x, row, d) + c * W, true, o);
+      }
+    }
+  }
+}
+
+// ---- gradients ----
+//
+//   do = dh_in + r (g - (o r) m),  g = dx w',  m = mean(g o r)
+//   p  = beta a w do,  dy = q (p - (y q) mean(p y q)),  dh = alpha do
+//   over the rows: dw' = sum dx o r;  S = sum do a_t y q (a_t: the gate per
+//   token, or 1), from which dw = beta a_c S and, per channel, da = beta w S;
+//   per token da = beta do w y q.
+//
+// mean(p y q) needs do, which needs r and m. Put in, sum(p y) is a sum of
+// three products that do not: with k = beta a w,
+//   sum(k do y) = sum(k dh_in y) + r sum(k g y) - r^2 m sum(k o y),
+// so one pass over the registers and one exchange between the waves gives all
+// the row's sums.
+
+// What a gradient call keeps of one row after its sums.
+struct RowStat {
+  float r, r2m, q, q2s;
+};
+
+template <bool POST, bool NEXT>
+__device__ __forceinline__ RowStat row_stat(const float (&s)[6], int d, float eps) {
+  RowStat t{0.f, 0.f, 0.f, 0.f};
+  const float inv = 1.f / (float)d;
+  float py = s[3];
+  if (NEXT) {
+    t.r = row_rms(s[0], d, eps);
+    t.r2m = t.r * t.r * (s[1] * t.r * inv);
+    py += t.r * s[4] - t.r2m * s[5];
+  }
+  if (POST) {
+    t.q = row_rms(s[2], d, eps);
+    t.q2s = t.q * t.q * (py * t.q * inv);
+  }
+  return t;
+}
+
+// the terms of one element of the row's sums
+template <bool POST, bool NEXT>
+__device__ __forceinline__ void add_terms(float (&s)[6], float o, float g, float di, float y, float k) {
+  if (NEXT) {
+    s[0] += o * o;
+    s[1] += g * o;
+  }
+  if (POST) {
+    const float ky = k * y;
+    s[2] += y * y;
+    s[3] += ky * di;
+    if (NEXT) {
+      s[4] += ky * g;
+      s[5] += ky * o;
+    }
+  }
+}
+
+// partial sums of workgroup b: [b][2][d]: the gradient of w', then S
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R>
+__global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs A, int tr, int rpb) {
+  __shared__ float red[2][16][6];
+  __shared__ float acc[2][256 * 8];  // workgroups of several rows (256 threads) add their rows' columns here
+  int turn = 0;
+  const int d = A.d, sub = threadIdx.x / tr;
+  const Cols<R> cols(threadIdx.x % tr, d);
+  const int c = cols.at;
+  const bool mine = cols.mine;
+  float w[8], wn[8], k[8], dwn[8], ds[8];
+  if (POST) {
+    load_param(A.w, A.p_f32, c, mine, w);
+    load_param(A.token_gate ? nullptr : A.gate, A.p_f32, c, mine, k);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[j] *= A.beta;
+      k[j] *= w[j];
+    }
+  }
+  if (NEXT) load_param(A.w_next, A.p_f32, c, mine, wn);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) dwn[j] = ds[j] = 0.f;
+
+  for (long long row0 = (long long)blockIdx.x * rpb; row0 < A.rows; row0 += (long long)gridDim.x * rpb) {
+    const long long row = row0 + sub;
+    const bool on = mine && row < A.rows;
+    float o[8], g[8], di[8], y[8], a[8];
+    if (NEXT) {
+      load_w(row_of<H>(A.h, row, d) + c, on, o);
+      load_w(row_of<X>(A.dx, row, d) + c, on, g);
+    }
+    load_w(row_of<H>(A.dh_in, row, d) + c, on && A.dh_in, di);
+    if (POST) {
+      load_w(row_of<Y>(A.y, row, d) + c, on, y);
+      if (A.token_gate)
+        load_w(row_of<Y>(A.gate, row, d) + c, on, a);
+      else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = 1.f;
+      }
+    }
+    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      add_terms<POST, NEXT>(s, NEXT ? cols.own(j, o[j]) : 0.f, NEXT ? g[j] * wn[j] : 0.f, di[j],
+                            POST ? cols.own(j, y[j]) : 0.f, POST ? k[j] * a[j] : 0.f);
+    row_sum<6>(s, tr, red, turn);
+    const RowStat t = row_stat<POST, NEXT>(s, d, A.eps);
+    float dh[8], dy[8], da[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float v = di[j];
+      if (NEXT) {
+        v += t.r * (g[j] * wn[j]) - t.r2m * o[j];
+        dwn[j] += g[j] * (o[j] * t.r);
+      }
+      dh[j] = A.alpha * v;
+      if (POST) {
+        const float yn = y[j] * t.q;
+        ds[j] += v * a[j] * yn;
+        da[j] = v * w[j] * yn;
+        dy[j] = t.q * (k[j] * a[j] * v) - t.q2s * y[j];
+      }
+    }
+    store_w(row_of<H>(A.dh, row, d) + c, on, dh);
+    if (POST) {
+      store_w(row_of<Y>(A.dy, row, d) + c, on, dy);
+      if (A.token_gate) store_w(row_of<Y>(A.dgate_t, row, d) + c, on, da);
+    }
+  }
+  if (!A.part) return;
+  float *part = A.part + (long long)blockIdx.x * 2 * d;
+  if (rpb == 1) {
+    if (NEXT) store_w(part + c, mine, dwn);
+    if (POST) store_w(part + d + c, mine, ds);
+    return;
+  }
+  if (mine) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      acc[0][sub * tr * 8 + c + j] = dwn[j];
+      acc[1][sub * tr * 8 + c + j] = ds[j];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < d; i += blockDim.x) {
+    float s0 = 0.f, s1 = 0.f;
+    for (int u = 0; u < rpb; ++u) {
+      s0 += acc[0][u * tr * 8 + i];
+      s1 += acc[1][u * tr * 8 + i];
+    }
+    if (NEXT) part[i] = s0;
+    if (POST) part[d + i] = s1;
+  }
+}
+
+// Rows too wide for registers: sums in one pass over the row, results in a
+// second, and the columns' partial sums in the workgroup's slice of the
+// workspace (each element only ever touched by the same thread).
+template <typename H, typename Y, typename X, bool POST, bool NEXT, int W>
+__global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormArgs A) {
+  __shared__ float red[2][16][6];
+  int turn = 0;
+  const int d = A.d, v = d / W;
+  float *part = A.part ? A.part + (long long)blockIdx.x * 2 * d : nullptr;
+  bool first = true;
+  for (long long row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    float o[W], g[W], di[W], y[W], a[W], w[W], k[W], dxv[W];
+    auto read = [&](int c) {
+      if (NEXT) {
+        load_w(row_of<H>(A.h, row, d) + c * W, true, o);
+        load_w(row_of<X>(A.dx, row, d) + c * W, true, dxv);
+        load_param(A.w_next, A.p_f32, c * W, true, g);
+#pragma unroll
+        for (int j = 0; j < W; ++j) g[j] *= dxv[j];
+      }
+      load_w(row_of<H>(A.dh_in, row, d) + c * W, A.dh_in != nullptr, di);
+      if (POST) {
+        load_w(row_of<Y>(A.y, row, d) + c * W, true, y);
+        load_param(A.w, A.p_f32, c * W, true, w);
+        if (A.token_gate) {
+          load_w(row_of<Y>(A.gate, row, d) + c * W, true, a);
+#pragma unroll
+          for (int j = 0; j < W; ++j) k[j] = 1.f;
+        } else {
+          load_param(A.gate, A.p_f32, c * W, true, k);
+#pragma unroll
+          for (int j = 0; j < W; ++j) a[j] = 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          w[j] *= A.beta;
+          k[j] *= w[j] * a[j];
+        }
+      }
+    };
+    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int c = threadIdx.x; c < v; c += 1024) {
+      read(c);
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        add_terms<POST, NEXT>(s, NEXT ? o[j] : 0.f, NEXT ? g[j] : 0.f, di[j], POST ? y[j] : 0.f, POST ? k[j] : 0.f);
+    }
+    row_sum<6>(s, 1024, red, turn);
+    const RowStat t = row_stat<POST, NEXT>(s, d, A.eps);
+    for (int c = threadIdx.x; c < v; c += 1024) {
+      read(c);
+      float dh[W], dy[W], da[W], dwn[W], ds[W];
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        float u = di[j];
+        if (NEXT) {
+          u += t.r * g[j] - t.r2m * o[j];
+          dwn[j] = dxv[j] * (o[j] * t.r);
+        }
+        dh[j] = A.alpha * u;
+        if (POST) {
+          const float yn = y[j] * t.q;
+          ds[j] = u * a[j] * yn;
+          da[j] = u * w[j] * yn;
+          dy[j] = t.q * (k[j] * u) - t.q2s * y[j];
+        }
+      }
+      store_w(row_of<H>(A.dh, row, d) + c * W, true, dh);
+      if (POST) {
+        store_w(row_of<Y>(A.dy, row, d) + c * W, true, dy);
+        if (A.token_gate) store_w(row_of<Y>(A.dgate_t, row, d) + c * W, true, da);
+      }
+      if (part) {
+        float old[W];
+        if (NEXT) {
+          load_w(part + c * W, !first, old);
+#pragma unroll
+          for (int j = 0; j < W; ++j) old[j] += dwn[j];
+          store_w(part + c * W, true, old);
+        }
+        if (POST) {
+          load_w(part + d + c * W, !first, old);
+#pragma unroll
+          for (int j = 0; j < W; ++j) old[j] += ds[j];
+          store_w(part + d + c * W, true, old);
+        }
+      }
+    }
+    first = false;
+  }
+}
+
+// The parameters' gradients from the workgroups' partial sums (nparts of
+// them; none for a call without rows). 64 columns per workgroup, 16 threads
+// across them with 4 columns each and 16 slices of the partial sums.
+__global__ __launch_bounds__(256) void k_norm_params(NormArgs A, int nparts) {
+  __shared__ float sum[16][64];
+  const int d = A.d, which = blockIdx.y;
+  if (which == 0 ? !A.dw_next : (!A.dw && !A.dgate_c)) return;
+  const int lane = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int c = blockIdx.x * 64 + lane * 4;
+  const float *p = A.part + (long long)which * d;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int b = slice; b < nparts; b += 16) {
+    const float *q = p + (long long)b * 2 * d + c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] += c + j < d ? q[j] : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sum[slice][lane * 4 + j] = s[j];
+  __syncthreads();
+  const int i = blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x >= 64 || i >= d) return;
+  float t = 0.f;
+  for (int k = 0; k < 16; ++k) t += sum[k][threadIdx.x];
+  if (which == 0) {
+    A.dw_next[i] = t;
+    return;
+  }
+  auto param = [&](const void *q) {
+    return !q ? 1.f : A.p_f32 ? reinterpret_cast<const float *>(q)[i] : bf16_to_f32(reinterpret_cast<const bf16_t *>(q)[i]);
+  };
+  if (A.dw) A.dw[i] = A.beta * (A.token_gate ? 1.f : param(A.gate)) * t;
+  if (A.dgate_c) A.dgate_c[i] = A.beta * param(A.w) * t;
+}
+
+// ---- which instance ----
+template <typename H, typename Y, typename X, bool POST, bool NEXT>
+hipError_t fwd(const NormArgs &a, hipStream_t s) {
+  const Map m = row_map(a.d);
+  const dim3 grid(grid_rows(a.rows, m, kFwdPerCu)), block(m.threads);
+  if (a.d > kMaxNarrow && a.d % 8)
+    hipLaunchKernelGGL((k_norm_fwd_wide<H, Y, X, POST, NEXT, 1>), grid, block, 0, s, a);
+  else if (a.d > kMaxNarrow)
+    hipLaunchKernelGGL((k_norm_fwd_wide<H, Y, X, POST, NEXT, 8>), grid, block, 0, s, a);
+  else if (a.d % 8)
+    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, true>), grid, block, 0, s, a, m.tr, m.rpb);
+  else
+    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, false>), grid, block, 0, s, a, m.tr, m.rpb);
+  return hipGetLastError();
+}
+
+template <typename H, typename Y, typename X, bool POST, bool NEXT>
+hipError_t bwd(const NormArgs &a, hipStream_t s) {
+  const Map m = row_map(a.d);
+  const unsigned grid = grid_rows(a.rows, m, kBwdPerCu);
+  if (grid > 0) {
+    if (a.d > kMaxNarrow && a.d % 8)
+      hipLaunchKernelGGL((k_norm_bwd_wide<H, Y, X, POST, NEXT, 1>), dim3(grid), dim3(1024), 0, s, a);
+    else if (a.d > kMaxNarrow)
+      hipLaunchKernelGGL((k_norm_bwd_wide<H, Y, X, POST, NEXT, 8>), dim3(grid), dim3(1024), 0, s, a);
+    else if (a.d % 8)
+      hipLaunchKernelGGL((k_norm_bwd<H, Y, X, POST, NEXT, true>), dim3(grid), dim3(m.threads), 0, s, a, m.tr, m.rpb);
+    else
+      hipLaunchKernelGGL((k_norm_bwd<H, Y, X, POST, NEXT, false>), dim3(grid), dim3(m.threads), 0, s, a, m.tr, m.rpb);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.part) hipLaunchKernelGGL(k_norm_params, dim3((a.d + 63) / 64, 2), dim3(256), 0, s, a, (int)grid);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t norm_ws_bytes(long long rows, int d) {
+  const unsigned grid = grid_rows(rows, row_map(d), kBwdPerCu);
+  return (size_t)(grid > 0 ? grid : 1) * 2 * d * sizeof(float);
+}
+
+#define NORM_CASES(CALL)                                                                                  \
+  if (post && next) {                                                                                     \
+    if (t.h && t.y && t.x) return CALL<float, float, float, true, true>(a, s);                            \
+    if (t.h && t.y) return CALL<float, float, bf16_t, true, true>(a, s);                                  \
+    if (t.h && !t.y && !t.x) return CALL<float, bf16_t, bf16_t, true, true>(a, s);                        \
+    if (!t.h && !t.y && !t.x) return CALL<bf16_t, bf16_t, bf16_t, true, true>(a, s);                      \
+  } else if (post) {                                                                                      \
+    if (t.h && t.y) return CALL<float, float, float, true, false>(a, s);                                  \
+    if (t.h) return CALL<float, bf16_t, bf16_t, true, false>(a, s);                                       \
+    if (!t.y) return CALL<bf16_t, bf16_t, bf16_t, true, false>(a, s);                                     \
+  } else {                                                                                                \
+    if (t.h && t.x) return CALL<float, float, float, false, true>(a, s);                                  \
+    if (t.h) return CALL<float, float, bf16_t, false, true>(a, s);                                        \
+    if (!t.x) return CALL<bf16_t, bf16_t, bf16_t, false, true>(a, s);                                     \
+  }                                                                                                       \
+  return hipErrorInvalidValue
+
+hipError_t launch_norm_fwd(const NormArgs &a, NormTypes t, hipStream_t s) {
+  if (a.rows <= 0) return hipSuccess;
+  const bool post = a.y != nullptr, next = a.x != nullptr;
+  NORM_CASES(fwd);
+}
+
+hipError_t launch_norm_bwd(const NormArgs &a, NormTypes t, bool post, bool next, hipStream_t s) {
+  NORM_CASES(bwd);
+}

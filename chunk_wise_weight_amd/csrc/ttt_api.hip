@@ -21,13 +21,17 @@
 // the sequential apply-then-update loop up to rounding.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cmath>
+#include <cstdarg>
+#include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <string>
 #include <vector>
 
 #include "../../include/ttt.h"
+#include "errors.h"
 #include "launch.h"
 
 namespace {
@@ -198,6 +202,43 @@ int check_device(int *dev_out) {
   *dev_out = dev;
   return TTT_OK;
 }
+
+}  // namespace
+
+int ttt_fail(int code, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  std::vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  try {
+    g_err = buf;
+  } catch (...) {
+    g_err.clear();
+  }
+  return code;
+}
+
+int ttt_check_device() {
+  // asking for a device's properties costs tens of microseconds, so a device found good is not asked again
+  static std::atomic<bool> good[kMaxDevices];
+  int dev = -1;
+  if (hipGetDevice(&dev) == hipSuccess && dev >= 0 && dev < kMaxDevices && good[dev].load(std::memory_order_relaxed))
+    return TTT_OK;
+  try {
+    const int rc = check_device(&dev);
+    if (rc == TTT_OK && dev < kMaxDevices) good[dev].store(true, std::memory_order_relaxed);
+    return rc;
+  } catch (...) {
+    return ttt_fail(TTT_E_NOMEM, "out of host memory");
+  }
+}
+
+int ttt_launched(hipError_t e, const char *what) {
+  return e == hipSuccess ? TTT_OK : ttt_fail(TTT_E_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+namespace {
 
 void free_handle(ttt_handle *h) {
   if (!h) return;

@@ -296,6 +296,82 @@ int ttt_phase_times(ttt_handle *h, float *ms, int n);
 /* ttt_workspace_bytes — device bytes the handle currently owns (weights, states, scratch). */
 int ttt_workspace_bytes(ttt_handle *h, size_t *bytes);
 
+/*
+ * What stands around the layers of a stack. These entry points take no
+ * handle: each works on the arrays it is given, on the current device, and
+ * keeps nothing between calls. They allocate nothing (where scratch is needed
+ * the caller brings it, `ws`, 16-byte aligned, of at least the bytes the
+ * matching _ws_bytes query names; its contents need not be kept, and calls
+ * that may overlap in time need a workspace each), so they can be captured
+ * into a HIP graph. Arrays need only the alignment of their elements. Unless
+ * said otherwise an output may not overlap an input or another output
+ * (TTT_E_ARG); where "in place" is allowed it means the very same array.
+ */
+
+/*
+ * The norms around a block (rows of d elements, 8 <= d <= 65536):
+ *
+ *   rms(v)         = (mean(v^2) + eps)^-1/2 over the row
+ *   ttt_norm_pre   : x = w * h * rms(h)                 the norm before a block
+ *   ttt_norm_post  : o = alpha * h + beta * gate * w * y * rms(y)
+ *                    the norm after a block, its gate and the residual scales;
+ *                    with x not NULL also the next block's norm,
+ *                    x = w_next * o * rms(o), of o before it is rounded
+ *
+ * With w = NULL the rows are normalised without a gain (the layer's
+ * RMS-normalised input rows). Sums are fp32, and each result is rounded once:
+ * |elements| past 1e18, whose squares leave fp32, are not supported.
+ *
+ *   rows    : 0 .. 2^31-1.
+ *   h, o    : [rows][d] residual stream, h_dt. o may be h (in place).
+ *   y       : [rows][d] what the block gave, y_dt.
+ *   x       : [rows][d] the block's input, x_dt.
+ *   types   : (h, x) fp32/fp32, fp32/bf16 or bf16/bf16; (h, y) the same three,
+ *             or fp32/fp32 with a bf16 x.
+ *   w, w_next : [d] gains, w_dt, or NULL (ones).
+ *   gate    : TTT_GATE_NONE (gate ignored), TTT_GATE_CHANNEL ([d], w_dt) or
+ *             TTT_GATE_TOKEN ([rows][d], y_dt).
+ *   alpha, beta : finite; eps: finite, at least 1e-30.
+ */
+enum { TTT_GATE_NONE = 0, TTT_GATE_CHANNEL = 1, TTT_GATE_TOKEN = 2 };
+int ttt_norm_pre(const void *h, ttt_dtype h_dt, const void *w, ttt_dtype w_dt, float eps, int64_t rows, int d, void *x,
+                 ttt_dtype x_dt, void *hip_stream);
+int ttt_norm_post(const void *h, ttt_dtype h_dt, const void *y, ttt_dtype y_dt, const void *w, const void *gate,
+                  int gate_kind, const void *w_next, ttt_dtype w_dt, float alpha, float beta, float eps, int64_t rows,
+                  int d, void *o, void *x, ttt_dtype x_dt, void *hip_stream);
+
+/*
+ * Their gradients.
+ *
+ *   ttt_norm_pre_grad  : from dx (the gradient of x) and dh_in (the gradient
+ *                        of h from elsewhere, e.g. the residual path; NULL:
+ *                        none) the gradient dh of h, dh_in included, and dw
+ *                        ([d] fp32; NULL: not wanted).
+ *   ttt_norm_post_grad : from dx (NULL: no norm followed, or no gradient came
+ *                        through it) and dh_in (the gradient of o from
+ *                        elsewhere; NULL: none; one of the two is needed), with
+ *                        o as ttt_norm_post wrote it (read only with dx) and y:
+ *                        dh [rows][d] (gradient of h), dy [rows][d], dw and
+ *                        dw_next ([d] fp32), and dgate: [d] fp32 for a gate
+ *                        per channel, [rows][d] of y's type for one per
+ *                        token. dw, dw_next and dgate per channel may be NULL;
+ *                        dgate per token may not. dw_next is not written
+ *                        without dx.
+ *
+ * dh has h_dt and may be dh_in (in place); dy has y_dt and may be y. The sums
+ * over the rows are fp32, in an order fixed by (rows, d): the same call gives
+ * the same bits. With rows = 0 the parameters' gradients are written as zero.
+ * ws is needed when a parameter's gradient is wanted.
+ */
+int ttt_norm_ws_bytes(int64_t rows, int d, size_t *bytes);
+int ttt_norm_pre_grad(const void *dx, ttt_dtype x_dt, const void *h, ttt_dtype h_dt, const void *w, ttt_dtype w_dt,
+                      const void *dh_in, float eps, int64_t rows, int d, void *dh, float *dw, void *ws, size_t ws_bytes,
+                      void *hip_stream);
+int ttt_norm_post_grad(const void *dh_in, const void *dx, ttt_dtype x_dt, const void *o, ttt_dtype h_dt, const void *y,
+                       ttt_dtype y_dt, const void *w, const void *gate, int gate_kind, const void *w_next,
+                       ttt_dtype w_dt, float alpha, float beta, float eps, int64_t rows, int d, void *dh, void *dy,
+                       float *dw, void *dgate, float *dw_next, void *ws, size_t ws_bytes, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
