@@ -2,8 +2,8 @@
 
 The computation lives in libttt.so (hand-written HIP kernels behind a C ABI,
 declared in include/ttt.h); this package only binds it. Beside the layer stand
-the operators around it: the norms between layers with their gate and residual
-scales, and their gradients.
+the operators around it: token embedding, the norms between layers with their
+gate and residual scales, and the gradients of both.
 """
 from .binding import (  # noqa: F401
     EXPORTS,
@@ -14,6 +14,8 @@ from .binding import (  # noqa: F401
     TTTError,
     lib,
     ttt_destroy,
+    ttt_embed,
+    ttt_embed_grad,
     ttt_forward_chunked,
     ttt_forward_chunked_noalloc,
     ttt_forward_docs,

@@ -22,7 +22,8 @@ ERRORS = {-1: "TTT_E_NULL", -2: "TTT_E_SHAPE", -3: "TTT_E_DTYPE", -4: "TTT_E_NOM
 EXPORTS = ("ttt_init", "ttt_forward_chunked", "ttt_forward_docs", "ttt_reset", "ttt_destroy", "ttt_last_error",
            "ttt_set_group_chunks", "ttt_set_clip", "ttt_set_target_conv", "ttt_plan", "ttt_set_profiling", "ttt_phase_times",
            "ttt_workspace_bytes", "ttt_set_output_f32", "ttt_state_delta", "ttt_forward_chunked_noalloc",
-           "ttt_norm_pre", "ttt_norm_post", "ttt_norm_ws_bytes", "ttt_norm_pre_grad", "ttt_norm_post_grad")
+           "ttt_norm_pre", "ttt_norm_post", "ttt_norm_ws_bytes", "ttt_norm_pre_grad", "ttt_norm_post_grad",
+           "ttt_embed", "ttt_embed_grad_ws_bytes", "ttt_embed_grad")
 
 _lib = None
 
@@ -82,7 +83,11 @@ def lib() -> ctypes.CDLL:
     L.ttt_norm_pre_grad.argtypes = [vp, i32, vp, i32, vp, i32, vp, f32, i64, i32, vp, vp, vp, sz, vp]
     L.ttt_norm_post_grad.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, vp, i32, vp, i32, f32, f32, f32, i64, i32, vp,
                                      vp, vp, vp, vp, vp, sz, vp]
-    for fn in (L.ttt_norm_pre, L.ttt_norm_post, L.ttt_norm_ws_bytes, L.ttt_norm_pre_grad, L.ttt_norm_post_grad):
+    L.ttt_embed.argtypes = [vp, i32, i32, i32, vp, i64, i32, i32, f32, vp, i32, vp]
+    L.ttt_embed_grad_ws_bytes.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+    L.ttt_embed_grad.argtypes = [vp, i32, vp, i64, i32, i32, f32, i32, i32, vp, i32, i32, vp, sz, vp]
+    for fn in (L.ttt_norm_pre, L.ttt_norm_post, L.ttt_norm_ws_bytes, L.ttt_norm_pre_grad, L.ttt_norm_post_grad,
+               L.ttt_embed, L.ttt_embed_grad_ws_bytes, L.ttt_embed_grad):
         fn.restype = i32
     _lib = L
     return L
@@ -537,3 +542,69 @@ def ttt_norm_post_grad(dh_in: Optional[torch.Tensor], dx: Optional[torch.Tensor]
                                     pw, pg, kind, pn, _DT[wdt], alpha, beta, eps, rows, d, pdh, pdy, out[0], out[1],
                                     out[2], out[3], nws, c.on()), "ttt_norm_post_grad")
     return NormGrads(dh, dy, dw, dg, dn)
+
+
+def _ids_arg(c: _Call, ids: torch.Tensor) -> Tuple[int, int, int, int]:
+    """(address, row stride, rows, tokens per row) of a call's ids: int32, contiguous, or 2-D with rows apart (a
+    [:, :T] view of the layer's [B][T+1] ids)."""
+    if _tensor(ids, "ids").dtype != torch.int32:
+        raise ValueError(f"ids must be {torch.int32}, got {ids.dtype}")
+    if not ids.is_cuda:
+        raise ValueError("ids must be a device tensor")
+    if ids.get_device() != c.device:
+        raise ValueError("ids must be on the current device")
+    if c.stream is not None:
+        ids.record_stream(c.stream)
+    if ids.dim() == 2 and not ids.is_contiguous():
+        B, T = ids.shape
+        if ids.stride(1) != 1 or ids.stride(0) < T:
+            raise ValueError("ids must be contiguous or a 2-D view of contiguous rows")
+        return ids.data_ptr(), ids.stride(0), B, T
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous or a 2-D view of contiguous rows")
+    n = ids.numel()
+    return ids.data_ptr(), n, 1, n
+
+
+def ttt_embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, x: Optional[torch.Tensor] = None,
+              dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """Token embedding: x[t] = scale * E[ids[t]], a zero row for an id outside [0, vocab).
+
+    E [vocab][d]; ids int32 of any shape, or a 2-D view of contiguous rows; x is ids.shape + (d,) in `dtype` (default:
+    the table's)."""
+    if _tensor(E, "E").dim() != 2:
+        raise ValueError("E must be [vocab][d]")
+    c = _Call(E, stream)
+    vocab, d = E.shape
+    pE = c.arg(E, "E")
+    pi, ld, B, T = _ids_arg(c, ids)
+    shape = ids.shape + (d,)
+    if x is None:
+        x = c.empty(shape, dtype or E.dtype)
+    px = c.arg(x, "x", dtype, shape)
+    _check(lib().ttt_embed(pE, _DT[E.dtype], vocab, d, pi, ld, B, T, scale, px, _DT[x.dtype], c.on()), "ttt_embed")
+    return x
+
+
+def ttt_embed_grad(dx: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float = 1.0,
+                   dE: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32, accumulate: bool = False,
+                   stream=None) -> torch.Tensor:
+    """Gradient of ttt_embed's table: dE[v] = scale * sum of dx[t] over ids[t] = v, [vocab][d] in `dtype` (or that of
+    a given dE). With accumulate the sums are added to dE, which must then be given."""
+    c = _Call(_tensor(dx, "dx"), stream)
+    pi, ld, B, T = _ids_arg(c, ids)
+    if dx.dim() != ids.dim() + 1 or dx.shape[:-1] != ids.shape:
+        raise ValueError(f"dx must be ids' shape and d, got {tuple(dx.shape)} for ids {tuple(ids.shape)}")
+    d = dx.shape[-1]
+    pdx = c.arg(dx, "dx")
+    if dE is None:
+        if accumulate:
+            raise ValueError("dE must be given to accumulate into")
+        dE = c.empty((vocab, d), dtype)
+    pE = c.arg(dE, "dE", None, (vocab, d))
+    n = ctypes.c_size_t()
+    _check(lib().ttt_embed_grad_ws_bytes(B, T, vocab, d, ctypes.byref(n)), "ttt_embed_grad_ws_bytes")
+    ws = c.scratch(n.value)
+    _check(lib().ttt_embed_grad(pdx, _DT[dx.dtype], pi, ld, B, T, scale, vocab, d, pE, _DT[dE.dtype],
+                                1 if accumulate else 0, ws.data_ptr(), n.value, c.on()), "ttt_embed_grad")
+    return dE

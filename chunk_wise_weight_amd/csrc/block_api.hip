@@ -4,6 +4,7 @@
 #include <initializer_list>
 
 #include "../../include/ttt.h"
+#include "embed.h"
 #include "errors.h"
 #include "norm.h"
 
@@ -11,6 +12,8 @@ namespace {
 
 constexpr int kMaxWidth = 65536;
 constexpr long long kMaxRows = 0x7fffffffLL;
+constexpr long long kMaxTokens = 1LL << 27;
+constexpr int kMaxVocab = 1 << 30;
 
 bool known(ttt_dtype t) { return t == TTT_F32 || t == TTT_BF16; }
 size_t size_of(ttt_dtype t) { return t == TTT_BF16 ? 2 : 4; }
@@ -86,6 +89,21 @@ int check_ws(const char *where, const void *ws, size_t have, size_t need) {
   if ((uintptr_t)ws % 16) return ttt_fail(TTT_E_ARG, "%s: the workspace must be 16-byte aligned", where);
   if (have < need) return ttt_fail(TTT_E_SHAPE, "%s: needs %zu bytes of workspace, got %zu", where, need, have);
   return TTT_OK;
+}
+
+int check_tokens(const char *where, int B, int T, int64_t ids_ld, int vocab, int d, float scale) {
+  if (d < 8 || d > kMaxWidth) return ttt_fail(TTT_E_SHAPE, "%s: d must be in [8, %d], got %d", where, kMaxWidth, d);
+  if (vocab < 1 || vocab > kMaxVocab)
+    return ttt_fail(TTT_E_SHAPE, "%s: vocab must be in [1, 2^30], got %d", where, vocab);
+  if (B < 0 || T < 0 || (long long)B * T > kMaxTokens)
+    return ttt_fail(TTT_E_SHAPE, "%s: B and T must not be negative and B * T at most 2^27", where);
+  if (ids_ld < T || ids_ld > (1LL << 40)) return ttt_fail(TTT_E_SHAPE, "%s: ids_ld must be at least T", where);
+  if (!std::isfinite(scale)) return ttt_fail(TTT_E_ARG, "%s: scale must be finite", where);
+  return TTT_OK;
+}
+
+size_t ids_bytes(int B, int T, int64_t ids_ld) {
+  return (long long)B * T ? ((size_t)(B - 1) * ids_ld + T) * sizeof(int32_t) : 0;
 }
 
 }  // namespace
@@ -262,6 +280,69 @@ int ttt_norm_post_grad(const void *dh_in, const void *dx, ttt_dtype x_dt, const 
   a.dw_next = dw_next;
   a.part = part ? (float *)ws : nullptr;
   return ttt_launched(launch_norm_bwd(a, types(h_dt, y_dt, x_dt), true, next, (hipStream_t)hip_stream), kWhere);
+}
+
+int ttt_embed(const void *E, ttt_dtype E_dt, int vocab, int d, const int32_t *ids, int64_t ids_ld, int B, int T,
+              float scale, void *x, ttt_dtype x_dt, void *hip_stream) {
+  static const char *kWhere = "ttt_embed";
+  if (!known(E_dt) || !known(x_dt)) return ttt_fail(TTT_E_DTYPE, "%s: unknown dtype", kWhere);
+  int rc = check_tokens(kWhere, B, T, ids_ld, vocab, d, scale);
+  if (rc) return rc;
+  const long long n = (long long)B * T;
+  if (n > 0 && (!E || !ids || !x)) return ttt_fail(TTT_E_NULL, "%s: E, ids or x is NULL", kWhere);
+  rc = check_spans(kWhere,
+                   {{"E", E, (size_t)vocab * d * size_of(E_dt), size_of(E_dt)}, {"ids", ids, ids_bytes(B, T, ids_ld), 4}},
+                   {{"x", x, (size_t)n * d * size_of(x_dt), size_of(x_dt)}}, {});
+  if (rc) return rc;
+  rc = ttt_check_device();
+  if (rc) return rc;
+  EmbedArgs a{};
+  a.ids = TokenIds{ids, ids_ld, T, (int)n};
+  a.E = E;
+  a.x = x;
+  a.vocab = vocab;
+  a.d = d;
+  a.scale = scale;
+  return ttt_launched(launch_embed(a, E_dt == TTT_F32, x_dt == TTT_F32, (hipStream_t)hip_stream), kWhere);
+}
+
+int ttt_embed_grad_ws_bytes(int B, int T, int vocab, int d, size_t *bytes) {
+  if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_embed_grad_ws_bytes: bytes is NULL");
+  const int rc = check_tokens("ttt_embed_grad_ws_bytes", B, T, T, vocab, d, 1.f);
+  if (rc) return rc;
+  *bytes = embed_grad_ws_bytes((long long)B * T, vocab, d);
+  return TTT_OK;
+}
+
+int ttt_embed_grad(const void *dx, ttt_dtype dx_dt, const int32_t *ids, int64_t ids_ld, int B, int T, float scale,
+                   int vocab, int d, void *dE, ttt_dtype dE_dt, int accumulate, void *ws, size_t ws_bytes,
+                   void *hip_stream) {
+  static const char *kWhere = "ttt_embed_grad";
+  if (!known(dx_dt) || !known(dE_dt)) return ttt_fail(TTT_E_DTYPE, "%s: unknown dtype", kWhere);
+  int rc = check_tokens(kWhere, B, T, ids_ld, vocab, d, scale);
+  if (rc) return rc;
+  const long long n = (long long)B * T;
+  if (n > 0 && (!dx || !ids)) return ttt_fail(TTT_E_NULL, "%s: dx or ids is NULL", kWhere);
+  if (!dE) return ttt_fail(TTT_E_NULL, "%s: dE is NULL", kWhere);
+  const size_t need = embed_grad_ws_bytes(n, vocab, d);
+  rc = check_ws(kWhere, ws, ws_bytes, need);
+  if (rc) return rc;
+  rc = check_spans(kWhere,
+                   {{"dx", dx, (size_t)n * d * size_of(dx_dt), size_of(dx_dt)}, {"ids", ids, ids_bytes(B, T, ids_ld), 4}},
+                   {{"dE", dE, (size_t)vocab * d * size_of(dE_dt), size_of(dE_dt)}, {"ws", ws, need, 4}}, {});
+  if (rc) return rc;
+  rc = ttt_check_device();
+  if (rc) return rc;
+  EmbedGradArgs a{};
+  a.ids = TokenIds{ids, ids_ld, T, (int)n};
+  a.dx = dx;
+  a.dE = dE;
+  a.vocab = vocab;
+  a.d = d;
+  a.accumulate = accumulate != 0;
+  a.scale = scale;
+  a.ws = ws;
+  return ttt_launched(launch_embed_grad(a, dx_dt == TTT_F32, dE_dt == TTT_F32, (hipStream_t)hip_stream), kWhere);
 }
 
 }  // extern "C"

@@ -372,6 +372,38 @@ int ttt_norm_post_grad(const void *dh_in, const void *dx, ttt_dtype x_dt, const 
                        ttt_dtype w_dt, float alpha, float beta, float eps, int64_t rows, int d, void *dh, void *dy,
                        float *dw, void *dgate, float *dw_next, void *ws, size_t ws_bytes, void *hip_stream);
 
+/*
+ * Token embedding and its gradient:
+ *
+ *   ttt_embed      : x[t] = scale * E[ids[t]], rounded once
+ *   ttt_embed_grad : dE[v] = scale * sum of dx[t] over the tokens t with
+ *                    ids[t] = v, summed in fp32, rounded once. With
+ *                    accumulate = 0 all of dE is written (zero rows for ids
+ *                    that do not occur); otherwise the sums are added to the
+ *                    rows that occur and the others are left alone.
+ *
+ * An id outside [0, vocab) gives a zero row and takes no gradient (its row of
+ * dx is not read), like the zero target rows of the layer.
+ *
+ *   E, dE : [vocab][d], fp32 or bf16; vocab 1 .. 2^30, d 8 .. 65536.
+ *   ids   : [B][T] int32, rows ids_ld >= T elements apart (so the [B][T+1] ids
+ *           of ttt_forward_chunked serve with ids_ld = T + 1). B, T >= 0,
+ *           B * T at most 2^27.
+ *   x, dx : [B][T][d], fp32 or bf16, each independent of the table's type.
+ *   scale : finite.
+ *
+ * The gradient sorts the tokens by id and sums each row's in the order of
+ * their positions, a long row's in pieces of 64: the same call gives the same
+ * bits. ws: see ttt_embed_grad_ws_bytes (about 16 bytes per token, 8 per table
+ * row and d / 8 bytes per token for the pieces).
+ */
+int ttt_embed(const void *E, ttt_dtype E_dt, int vocab, int d, const int32_t *ids, int64_t ids_ld, int B, int T,
+              float scale, void *x, ttt_dtype x_dt, void *hip_stream);
+int ttt_embed_grad_ws_bytes(int B, int T, int vocab, int d, size_t *bytes);
+int ttt_embed_grad(const void *dx, ttt_dtype dx_dt, const int32_t *ids, int64_t ids_ld, int B, int T, float scale,
+                   int vocab, int d, void *dE, ttt_dtype dE_dt, int accumulate, void *ws, size_t ws_bytes,
+                   void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
