@@ -3,7 +3,8 @@
 The computation lives in libttt.so (hand-written HIP kernels behind a C ABI,
 declared in include/ttt.h); this package only binds it. Beside the layer stand
 the operators around it: token embedding, the norms between layers with their
-gate and residual scales, and the gradients of both.
+gate and residual scales, the gradients of both, and the norm of many gradients
+with clipping.
 """
 from .binding import (  # noqa: F401
     EXPORTS,
@@ -13,6 +14,7 @@ from .binding import (  # noqa: F401
     NormGrads,
     TTTError,
     lib,
+    ttt_clip_grads,
     ttt_destroy,
     ttt_embed,
     ttt_embed_grad,
@@ -20,6 +22,7 @@ from .binding import (  # noqa: F401
     ttt_forward_chunked_noalloc,
     ttt_forward_docs,
     ttt_init,
+    ttt_grad_norm,
     ttt_last_error,
     ttt_phase_times,
     ttt_norm_post,

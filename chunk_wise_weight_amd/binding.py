@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Dict, List, NamedTuple, Optional, Tuple
 
 import torch  # loads the HIP runtime the library binds to (same libamdhip64 soname)
@@ -23,7 +24,7 @@ EXPORTS = ("ttt_init", "ttt_forward_chunked", "ttt_forward_docs", "ttt_reset", "
            "ttt_set_group_chunks", "ttt_set_clip", "ttt_set_target_conv", "ttt_plan", "ttt_set_profiling", "ttt_phase_times",
            "ttt_workspace_bytes", "ttt_set_output_f32", "ttt_state_delta", "ttt_forward_chunked_noalloc",
            "ttt_norm_pre", "ttt_norm_post", "ttt_norm_ws_bytes", "ttt_norm_pre_grad", "ttt_norm_post_grad",
-           "ttt_embed", "ttt_embed_grad_ws_bytes", "ttt_embed_grad")
+           "ttt_embed", "ttt_embed_grad_ws_bytes", "ttt_embed_grad", "ttt_grad_ws_bytes", "ttt_grad_norm", "ttt_clip_grads")
 
 _lib = None
 
@@ -86,7 +87,10 @@ def lib() -> ctypes.CDLL:
     L.ttt_embed.argtypes = [vp, i32, i32, i32, vp, i64, i32, i32, f32, vp, i32, vp]
     L.ttt_embed_grad_ws_bytes.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
     L.ttt_embed_grad.argtypes = [vp, i32, vp, i64, i32, i32, f32, i32, i32, vp, i32, i32, vp, sz, vp]
-    for fn in (L.ttt_norm_pre, L.ttt_norm_post, L.ttt_norm_ws_bytes, L.ttt_norm_pre_grad, L.ttt_norm_post_grad,
+    L.ttt_grad_ws_bytes.argtypes = [i32, ctypes.POINTER(sz)]
+    L.ttt_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, sz, vp]
+    L.ttt_clip_grads.argtypes = [vp, vp, vp, i32, f32, vp, vp, vp, sz, vp]
+    for fn in (L.ttt_grad_ws_bytes, L.ttt_grad_norm, L.ttt_clip_grads, L.ttt_norm_pre, L.ttt_norm_post, L.ttt_norm_ws_bytes, L.ttt_norm_pre_grad, L.ttt_norm_post_grad,
                L.ttt_embed, L.ttt_embed_grad_ws_bytes, L.ttt_embed_grad):
         fn.restype = i32
     _lib = L
@@ -329,12 +333,12 @@ GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 class _Call:
     """The stream and device of one call, and the tensors it was given."""
 
-    def __init__(self, first: torch.Tensor, stream):
+    def __init__(self, where: torch.device, stream):
         self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
         self.stream = stream
         if stream is not None and stream.device.index != self.device:
             raise ValueError("stream must be on the current device")
-        self.where = first.device
+        self.where = where
 
     def arg(self, t: Optional[torch.Tensor], name: str, dtype=None, shape=None) -> Optional[int]:
         """A tensor's address (None for None), after its checks."""
@@ -424,7 +428,7 @@ def ttt_norm_pre(h: torch.Tensor, w: Optional[torch.Tensor] = None, eps: float =
     h [...][d] float32 or bfloat16; x has h's shape and `dtype` (default: h's; a float32 h may give a bfloat16 x).
     """
     rows, d = _rows(h, "h")
-    c = _Call(h, stream)
+    c = _Call(h.device, stream)
     ph, pw = c.arg(h, "h"), c.arg(w, "w", None, (d,))
     wdt = _params_dtype(("w", w))
     if x is None:
@@ -446,7 +450,7 @@ def ttt_norm_post(h: torch.Tensor, y: torch.Tensor, w: Optional[torch.Tensor] = 
     x in `dtype` (default: y's). o may be h: the stream is then updated in place.
     """
     rows, d = _rows(h, "h")
-    c = _Call(h, stream)
+    c = _Call(h.device, stream)
     ph, py = c.arg(h, "h"), c.arg(y, "y", None, h.shape)
     kind = _gate_kind(gate, y, d)
     pw, pn = c.arg(w, "w", None, (d,)), c.arg(w_next, "w_next", None, (d,))
@@ -469,7 +473,7 @@ def ttt_norm_pre_grad(dx: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tenso
     """Gradients of ttt_norm_pre: (dh, dw) from dx; dh_in, the gradient h has from elsewhere, is added to dh (which may
     be the same tensor). dw [d] is float32, None without a gain."""
     rows, d = _rows(h, "h")
-    c = _Call(h, stream)
+    c = _Call(h.device, stream)
     ph, pdx = c.arg(h, "h"), c.arg(dx, "dx", None, h.shape)
     pw, pin = c.arg(w, "w", None, (d,)), c.arg(dh_in, "dh_in", h.dtype, h.shape)
     wdt = _params_dtype(("w", w))
@@ -507,7 +511,7 @@ def ttt_norm_post_grad(dh_in: Optional[torch.Tensor], dx: Optional[torch.Tensor]
     None; one of the two is needed), with o as ttt_norm_post gave it (needed with dx) and y. dh has the residual
     stream's dtype and may be dh_in; dy may be y. dw, dw_next and a [d] gate's gradient are float32."""
     rows, d = _rows(y, "y")
-    c = _Call(y, stream)
+    c = _Call(y.device, stream)
     if dh_in is None and dx is None:
         raise ValueError("dh_in or dx must be given")
     if dx is not None and o is None:
@@ -574,7 +578,7 @@ def ttt_embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, x: Optiona
     the table's)."""
     if _tensor(E, "E").dim() != 2:
         raise ValueError("E must be [vocab][d]")
-    c = _Call(E, stream)
+    c = _Call(E.device, stream)
     vocab, d = E.shape
     pE = c.arg(E, "E")
     pi, ld, B, T = _ids_arg(c, ids)
@@ -591,7 +595,7 @@ def ttt_embed_grad(dx: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float
                    stream=None) -> torch.Tensor:
     """Gradient of ttt_embed's table: dE[v] = scale * sum of dx[t] over ids[t] = v, [vocab][d] in `dtype` (or that of
     a given dE). With accumulate the sums are added to dE, which must then be given."""
-    c = _Call(_tensor(dx, "dx"), stream)
+    c = _Call(_tensor(dx, "dx").device, stream)
     pi, ld, B, T = _ids_arg(c, ids)
     if dx.dim() != ids.dim() + 1 or dx.shape[:-1] != ids.shape:
         raise ValueError(f"dx must be ids' shape and d, got {tuple(dx.shape)} for ids {tuple(ids.shape)}")
@@ -608,3 +612,75 @@ def ttt_embed_grad(dx: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float
     _check(lib().ttt_embed_grad(pdx, _DT[dx.dtype], pi, ld, B, T, scale, vocab, d, pE, _DT[dE.dtype],
                                 1 if accumulate else 0, ws.data_ptr(), n.value, c.on()), "ttt_embed_grad")
     return dE
+
+
+class _Many:
+    """Lists of tensors as the library takes them: host arrays of addresses, element counts and types."""
+
+    def __init__(self, c: _Call, grads):
+        for t in grads:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"grads must be tensors, got {type(t).__name__}")
+        self.dtypes = [t.dtype for t in grads]
+        if not _DT.keys() >= set(self.dtypes):
+            raise ValueError("grads must be float32 or bfloat16")
+        self.n = len(grads)
+        self.sizes = [t.numel() for t in grads]
+        self.ptrs = self._addresses(c, grads, "grads")
+        self._keep = (array("Q", self.ptrs), array("q", self.sizes), array("i", [_DT[d] for d in self.dtypes]))
+        self.args = tuple(a.buffer_info()[0] for a in self._keep) + (self.n,)
+
+    @staticmethod
+    def _addresses(c: _Call, ts, name: str) -> List[int]:
+        if not all([t.is_contiguous() for t in ts]):
+            raise ValueError(f"{name} must be contiguous")
+        if not all([t.is_cuda for t in ts]):
+            raise ValueError(f"{name} must be device tensors")
+        if not {t.get_device() for t in ts} <= {c.device}:
+            raise ValueError(f"{name} must be on the current device")
+        if c.stream is not None:
+            for t in ts:
+                t.record_stream(c.stream)
+        return [t.data_ptr() for t in ts]
+
+    def outputs(self, c: _Call, out) -> array:
+        if len(out) != self.n:
+            raise ValueError(f"out must have one tensor per gradient, got {len(out)} for {self.n}")
+        for t in out:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"out must be tensors, got {type(t).__name__}")
+        if [t.dtype for t in out] != self.dtypes or [t.numel() for t in out] != self.sizes:
+            raise ValueError("out must have the gradients' dtypes and sizes")
+        return array("Q", self._addresses(c, out, "out"))
+
+
+def _grads_call(grads, norm, stream):
+    grads = list(grads)
+    where = grads[0].device if grads and isinstance(grads[0], torch.Tensor) else torch.device("cuda")
+    c = _Call(where, stream)
+    m = _Many(c, grads)
+    if norm is None:
+        norm = c.empty((1,), torch.float32)
+    pn = c.arg(norm, "norm", torch.float32, (1,))
+    n = ctypes.c_size_t()
+    _check(lib().ttt_grad_ws_bytes(m.n, ctypes.byref(n)), "ttt_grad_ws_bytes")
+    return c, m, norm, pn, c.scratch(n.value), n.value
+
+
+def ttt_grad_norm(grads, norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The 2-norm of all the tensors together, as a float32 device tensor of one element. grads: a list of contiguous
+    float32 or bfloat16 tensors."""
+    c, m, norm, pn, ws, nws = _grads_call(grads, norm, stream)
+    _check(lib().ttt_grad_norm(*m.args, pn, ws.data_ptr(), nws, c.on()), "ttt_grad_norm")
+    return norm
+
+
+def ttt_clip_grads(grads, tau: float, out=None, norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Scales the gradients by min(1, tau / N), N the 2-norm of them all, in place or into `out` (a list of tensors like
+    them). Returns N as it was before, a float32 device tensor of one element. Where N is not finite the gradients
+    stay as they are."""
+    c, m, norm, pn, ws, nws = _grads_call(grads, norm, stream)
+    po = None if out is None else m.outputs(c, out)
+    _check(lib().ttt_clip_grads(*m.args, tau, None if po is None else po.buffer_info()[0], pn, ws.data_ptr(), nws,
+                                c.on()), "ttt_clip_grads")
+    return norm

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libttt.so")
 PROBE_SRC = os.path.join(PKG, "probes", "mfma_clock.hip")
 PROBE = os.path.join(PKG, "probes", "mfma_clock")
 SOURCES = ["ttt_api.hip", "kernels_bf16.hip", "kernels_f32.hip", "kernels_clip.hip", "kernels_target.hip", "kernels_misc.hip",
-           "block_api.hip", "kernels_norm.hip", "kernels_embed.hip"]
+           "block_api.hip", "kernels_norm.hip", "kernels_embed.hip", "kernels_grads.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

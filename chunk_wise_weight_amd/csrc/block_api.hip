@@ -1,11 +1,14 @@
 // C ABI of the operators around the layer: argument checks and launches. No
 // call allocates, keeps state or waits.
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <vector>
 
 #include "../../include/ttt.h"
 #include "embed.h"
 #include "errors.h"
+#include "grads.h"
 #include "norm.h"
 
 namespace {
@@ -104,6 +107,125 @@ int check_tokens(const char *where, int B, int T, int64_t ids_ld, int vocab, int
 
 size_t ids_bytes(int B, int T, int64_t ids_ld) {
   return (long long)B * T ? ((size_t)(B - 1) * ids_ld + T) * sizeof(int32_t) : 0;
+}
+
+// ---- many tensors ----
+
+constexpr int kMaxTensors = 1 << 20;
+constexpr long long kMaxNumel = 1LL << 40;  // of all tensors: their chunks of 32768 count in 32 bits
+
+size_t grad_ws(int n) { return ((size_t)kGradGroups + n / kGradTable + 1) * sizeof(double); }
+
+int check_grads(const char *where, const void *const *grads, const int64_t *numel, const int32_t *dt, int n,
+                const float *norm, const void *ws, size_t ws_bytes) {
+  if (n < 0 || n > kMaxTensors) return ttt_fail(TTT_E_SHAPE, "%s: n must be in [0, 2^20], got %d", where, n);
+  if (n > 0 && (!grads || !numel || !dt)) return ttt_fail(TTT_E_NULL, "%s: grads, numel or dt is NULL", where);
+  if (!norm) return ttt_fail(TTT_E_NULL, "%s: norm is NULL", where);
+  if ((uintptr_t)norm % 4) return ttt_fail(TTT_E_ARG, "%s: norm is not aligned to its elements", where);
+  const int rc = check_ws(where, ws, ws_bytes, grad_ws(n));
+  if (rc) return rc;
+  long long total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (!known((ttt_dtype)dt[i])) return ttt_fail(TTT_E_DTYPE, "%s: tensor %d has an unknown dtype", where, i);
+    if (numel[i] < 0 || numel[i] > kMaxNumel || (total += numel[i]) > kMaxNumel)
+      return ttt_fail(TTT_E_SHAPE, "%s: tensor %d has %lld elements; together at most 2^40 are taken", where, i,
+                      (long long)numel[i]);
+    if (numel[i] > 0 && !grads[i]) return ttt_fail(TTT_E_NULL, "%s: tensor %d is NULL", where, i);
+    if ((uintptr_t)grads[i] % size_of((ttt_dtype)dt[i]))
+      return ttt_fail(TTT_E_ARG, "%s: tensor %d is not aligned to its elements", where, i);
+  }
+  return TTT_OK;
+}
+
+// Where outputs and workspace lie: each overlaps nothing but, in place, its own gradient.
+struct Extent {
+  uintptr_t lo, hi;
+  bool out;
+};
+int check_extents(const char *where, std::vector<Extent> &e) {
+  std::sort(e.begin(), e.end(), [](const Extent &a, const Extent &b) { return a.lo < b.lo; });
+  uintptr_t any = 0, outs = 0;  // ends of what came before
+  for (const Extent &x : e) {
+    if (x.lo < outs || (x.out && x.lo < any)) return ttt_fail(TTT_E_ARG, "%s: an output overlaps another array", where);
+    any = std::max(any, x.hi);
+    if (x.out) outs = std::max(outs, x.hi);
+  }
+  return TTT_OK;
+}
+
+// The tables of a call, empty tensors left out and tensors that follow one
+// another in memory (views of one buffer) taken as one. Chunks are as small as
+// gives every workgroup of the norm one, between 2048 and 32768 elements.
+std::vector<GradTable> grad_tables(const void *const *grads, const int64_t *numel, const int32_t *dt, int n,
+                                   void *const *out) {
+  struct One {
+    const char *g;
+    char *o;
+    long long n;
+    int f32;
+  };
+  std::vector<One> all;
+  all.reserve(n);
+  long long total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] == 0) continue;
+    const int f32 = dt[i] == TTT_F32;
+    const One x{(const char *)grads[i], out ? (char *)out[i] : (char *)grads[i], (long long)numel[i], f32};
+    total += x.n;
+    if (!all.empty()) {
+      One &p = all.back();
+      const long long bytes = p.n * (p.f32 ? 4 : 2);
+      if (p.f32 == x.f32 && p.g + bytes == x.g && p.o + bytes == x.o) {
+        p.n += x.n;
+        continue;
+      }
+    }
+    all.push_back(x);
+  }
+  long long chunk = (total / kGradGroups + 2047) / 2048 * 2048;
+  chunk = std::min(std::max(chunk, 2048LL), 32768LL);
+  std::vector<GradTable> tables;
+  for (size_t i = 0; i < all.size(); ++i) {
+    if (tables.empty() || tables.back().n == kGradTable) {
+      tables.emplace_back();
+      tables.back().n = 0;
+      tables.back().first[0] = 0;
+      tables.back().chunk = (uint32_t)chunk;
+    }
+    GradTable &t = tables.back();
+    const long long chunks = (all[i].n + chunk - 1) / chunk;
+    t.g[t.n] = all[i].g;
+    t.out[t.n] = all[i].o;
+    t.tail[t.n] = (uint32_t)(all[i].n - (chunks - 1) * chunk);
+    t.f32[t.n] = (uint8_t)all[i].f32;
+    t.first[t.n + 1] = t.first[t.n] + (uint32_t)chunks;
+    ++t.n;
+  }
+  return tables;
+}
+
+// Norm of the tables and, with `clip`, the scaling by it.
+int run_grads(const char *where, const std::vector<GradTable> &tables, bool clip, float tau, float *norm, double *part,
+              hipStream_t s) {
+  long long chunks = 0;
+  for (const GradTable &t : tables) chunks += t.first[t.n];
+  // workgroups of a table: its share of kGradGroups
+  auto groups = [&](const GradTable &t) {
+    const long long c = t.first[t.n], most = std::max(1LL, kGradGroups * c / std::max(1LL, chunks));
+    return (int)std::min(c, most);
+  };
+  int n = 0;
+  for (const GradTable &t : tables) {
+    const int rc = ttt_launched(launch_grad_squares(t, part + n, groups(t), s), where);
+    if (rc) return rc;
+    n += groups(t);
+  }
+  if (!clip || tables.empty()) return ttt_launched(launch_grad_norm(part, n, norm, s), where);
+  for (const GradTable &t : tables) {
+    const int rc = ttt_launched(launch_grad_scale(t, part, n, tau, &t == &tables[0] ? norm : nullptr, groups(t), s), where);
+    if (rc) return rc;
+  }
+  return TTT_OK;
 }
 
 }  // namespace
@@ -343,6 +465,64 @@ int ttt_embed_grad(const void *dx, ttt_dtype dx_dt, const int32_t *ids, int64_t 
   a.scale = scale;
   a.ws = ws;
   return ttt_launched(launch_embed_grad(a, dx_dt == TTT_F32, dE_dt == TTT_F32, (hipStream_t)hip_stream), kWhere);
+}
+
+int ttt_grad_ws_bytes(int n, size_t *bytes) {
+  if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_grad_ws_bytes: bytes is NULL");
+  if (n < 0 || n > kMaxTensors) return ttt_fail(TTT_E_SHAPE, "ttt_grad_ws_bytes: n must be in [0, 2^20], got %d", n);
+  *bytes = grad_ws(n);
+  return TTT_OK;
+}
+
+int ttt_grad_norm(const void *const *grads, const int64_t *numel, const int32_t *dt, int n, float *norm, void *ws,
+                  size_t ws_bytes, void *hip_stream) {
+  static const char *kWhere = "ttt_grad_norm";
+  try {
+    int rc = check_grads(kWhere, grads, numel, dt, n, norm, ws, ws_bytes);
+    if (rc) return rc;
+    std::vector<Extent> e;
+    for (int i = 0; i < n; ++i)
+      if (numel[i])
+        e.push_back({(uintptr_t)grads[i], (uintptr_t)grads[i] + numel[i] * size_of((ttt_dtype)dt[i]), false});
+    e.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, true});
+    e.push_back({(uintptr_t)ws, (uintptr_t)ws + grad_ws(n), true});
+    rc = check_extents(kWhere, e);
+    if (!rc) rc = ttt_check_device();
+    if (rc) return rc;
+    return run_grads(kWhere, grad_tables(grads, numel, dt, n, nullptr), false, 0.f, norm, (double *)ws,
+                     (hipStream_t)hip_stream);
+  } catch (...) {
+    return ttt_fail(TTT_E_NOMEM, "%s: out of host memory", kWhere);
+  }
+}
+
+int ttt_clip_grads(const void *const *grads, const int64_t *numel, const int32_t *dt, int n, float tau,
+                   void *const *out, float *norm, void *ws, size_t ws_bytes, void *hip_stream) {
+  static const char *kWhere = "ttt_clip_grads";
+  try {
+    int rc = check_grads(kWhere, grads, numel, dt, n, norm, ws, ws_bytes);
+    if (rc) return rc;
+    if (!(tau > 0.f)) return ttt_fail(TTT_E_ARG, "%s: tau must be greater than 0", kWhere);
+    std::vector<Extent> e;
+    for (int i = 0; i < n; ++i) {
+      if (!numel[i]) continue;
+      const size_t elem = size_of((ttt_dtype)dt[i]), bytes = numel[i] * elem;
+      const void *o = out ? out[i] : grads[i];
+      if (!o) return ttt_fail(TTT_E_NULL, "%s: output %d is NULL", kWhere, i);
+      if ((uintptr_t)o % elem) return ttt_fail(TTT_E_ARG, "%s: output %d is not aligned to its elements", kWhere, i);
+      e.push_back({(uintptr_t)o, (uintptr_t)o + bytes, true});
+      if (o != grads[i]) e.push_back({(uintptr_t)grads[i], (uintptr_t)grads[i] + bytes, false});
+    }
+    e.push_back({(uintptr_t)norm, (uintptr_t)norm + 4, true});
+    e.push_back({(uintptr_t)ws, (uintptr_t)ws + grad_ws(n), true});
+    rc = check_extents(kWhere, e);
+    if (!rc) rc = ttt_check_device();
+    if (rc) return rc;
+    return run_grads(kWhere, grad_tables(grads, numel, dt, n, out), true, tau, norm, (double *)ws,
+                     (hipStream_t)hip_stream);
+  } catch (...) {
+    return ttt_fail(TTT_E_NOMEM, "%s: out of host memory", kWhere);
+  }
 }
 
 }  // extern "C"

@@ -404,6 +404,37 @@ int ttt_embed_grad(const void *dx, ttt_dtype dx_dt, const int32_t *ids, int64_t 
                    int vocab, int d, void *dE, ttt_dtype dE_dt, int accumulate, void *ws, size_t ws_bytes,
                    void *hip_stream);
 
+/*
+ * The global gradient norm over many tensors, and clipping by it:
+ *
+ *   ttt_grad_norm  : *norm = N = (sum over all tensors of g^2)^1/2
+ *   ttt_clip_grads : the same, and out[i] = g[i] * min(1, tau / N)
+ *
+ * (The layer's own updates are clipped by ttt_set_clip.) Squares are summed in
+ * fp64, in an order fixed by the sizes: the same call gives the same bits. A
+ * norm that is not finite (a gradient holds an infinity or NaN) clips nothing:
+ * the gradients come out as they are, and *norm says so. The host learns of
+ * nothing and waits for nothing.
+ *
+ *   grads : host array of n device pointers; numel, dt: host arrays of their
+ *           element counts (together at most 2^40) and types (ttt_dtype). The
+ *           arrays may be freed on return. n 0 .. 2^20; n = 0 gives norm 0.
+ *   out   : host array of n device pointers, each of its gradient's type and
+ *           size, and each either the gradient itself (in place) or a copy
+ *           that overlaps nothing; NULL: all in place. In place nothing is
+ *           written unless the norm passes tau. A tensor may then not be
+ *           listed twice (TTT_E_ARG); for the norm alone it may, and counts
+ *           twice.
+ *   tau   : greater than 0; +inf clips nothing.
+ *   norm  : device, one float (inf where N is past fp32).
+ *   ws    : device, ttt_grad_ws_bytes(n) bytes.
+ */
+int ttt_grad_ws_bytes(int n, size_t *bytes);
+int ttt_grad_norm(const void *const *grads, const int64_t *numel, const int32_t *dt, int n, float *norm, void *ws,
+                  size_t ws_bytes, void *hip_stream);
+int ttt_clip_grads(const void *const *grads, const int64_t *numel, const int32_t *dt, int n, float tau,
+                   void *const *out, float *norm, void *ws, size_t ws_bytes, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
