@@ -16,7 +16,9 @@
 
 namespace {
 
-constexpr int kCUs = 256;
+// x larger than this is written past the caches: the last level of them holds 256 MiB, and at half a GiB little of it
+// would be left for the next kernel
+constexpr double kStreamBytes = 512.0 * (1 << 20);
 constexpr int kMaxTiles = 256;   // of a sort: a workgroup reads the counts of all of them
 constexpr int kMinTile = 1024;   // tokens
 constexpr int kMaxDigit = 9;     // bits
@@ -27,35 +29,34 @@ constexpr int kChunk = 64;       // sorted tokens of one piece of a long row
 
 // ---- lookup ----
 
-// `tr` threads of 8 columns per row, `rpb` rows per workgroup (whole waves
-// beyond one row of a wave); kRows rows per thread and step, so that their
-// loads overlap.
-constexpr int kRows = 4;
-
-template <typename E, typename X, bool R>
+// A workgroup takes one row (ONE: its id is the same for all threads and its
+// addresses need no vector arithmetic), or, of narrow rows, `rpb` rows of `tr`
+// threads. There is a workgroup for every row: a grid that keeps the card
+// full and strides over the rows measured 470 us on 131072 bf16 rows of 2560
+// into fp32 where this one takes 290 (1.52 GB: 5.3 TB/s), since rows that run
+// at the same time then lie side by side in memory. STREAM: x is too large to
+// be found in the caches later; its rows are written past them (362 us without;
+// at 168 MB 60 us with it and 42 without).
+template <typename E, typename X, bool R, bool ONE, bool STREAM>
 __global__ __launch_bounds__(1024) void k_embed(EmbedArgs A, int tr, int rpb) {
-  const int sub = threadIdx.x / tr, d = A.d;
-  const long long step = (long long)gridDim.x * rpb * kRows;
-  for (int c8 = threadIdx.x % tr; c8 * 8 < d; c8 += tr) {
+  const int sub = ONE ? 0 : threadIdx.x / tr, d = A.d;
+  const long long row = group_index() * rpb + sub;
+  if (row >= A.ids.n) return;
+  const int id = A.ids.at((unsigned)row);
+  const bool on = id >= 0 && id < A.vocab;
+  const E *src = reinterpret_cast<const E *>(A.E) + (long long)(on ? id : 0) * d;
+  X *dst = reinterpret_cast<X *>(A.x) + row * d;
+  for (int c8 = ONE ? threadIdx.x : threadIdx.x % tr; c8 * 8 < d; c8 += tr) {
     // the last columns of a ragged row: its last eight, some of which the neighbour writes too, to the same values
     const int c = R && c8 * 8 + 8 > d ? d - 8 : c8 * 8;
-    for (long long row0 = (long long)blockIdx.x * rpb * kRows; row0 < A.ids.n; row0 += step) {
-      float v[kRows][8];
+    float v[8];
+    load_w(src + c, on, v);
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const long long row = row0 + k * rpb + sub;
-        const int id = row < A.ids.n ? A.ids.at((unsigned)row) : -1;
-        const bool on = id >= 0 && id < A.vocab;
-        load_w(reinterpret_cast<const E *>(A.E) + (long long)(on ? id : 0) * d + c, on, v[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const long long row = row0 + k * rpb + sub;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] *= A.scale;
-        store_w(reinterpret_cast<X *>(A.x) + row * d + c, row < A.ids.n, v[k]);
-      }
-    }
+    for (int j = 0; j < 8; ++j) v[j] *= A.scale;
+    if (STREAM)
+      stream_w(dst + c, true, v);
+    else
+      store_w(dst + c, true, v);
   }
 }
 
@@ -377,6 +378,15 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_join(SumArgs S) {
 
 // ---- which instance ----
 
+template <typename E, typename X, bool R, bool ONE>
+void embed_form(const EmbedArgs &a, dim3 grid, int tr, int rpb, hipStream_t s) {
+  // not ragged rows: parts of cache lines written past the caches cost more (491 MB: 187 us, 129 through them)
+  if (!R && (double)a.ids.n * a.d * sizeof(X) > kStreamBytes)
+    hipLaunchKernelGGL((k_embed<E, X, R, ONE, !R>), grid, dim3(tr * rpb), 0, s, a, tr, rpb);
+  else
+    hipLaunchKernelGGL((k_embed<E, X, R, ONE, false>), grid, dim3(tr * rpb), 0, s, a, tr, rpb);
+}
+
 template <typename E, typename X>
 hipError_t embed(const EmbedArgs &a, hipStream_t s) {
   const int v = (a.d + 7) / 8;
@@ -384,14 +394,11 @@ hipError_t embed(const EmbedArgs &a, hipStream_t s) {
   while (tr < v && tr < 64) tr *= 2;
   if (v > 64) tr = v >= 1024 ? 1024 : (v + 63) / 64 * 64;
   const int rpb = tr <= 64 ? 256 / tr : 1;
-  const long long per = (long long)rpb * kRows;
-  long long grid = (a.ids.n + per - 1) / per;
-  const long long most = (long long)kCUs * (2048 / (tr * rpb));
-  if (grid > most) grid = most;
-  if (a.d % 8)
-    hipLaunchKernelGGL((k_embed<E, X, true>), dim3((unsigned)grid), dim3(tr * rpb), 0, s, a, tr, rpb);
+  const dim3 grid = group_grid((a.ids.n + rpb - 1LL) / rpb);
+  if (rpb > 1)
+    a.d % 8 ? embed_form<E, X, true, false>(a, grid, tr, rpb, s) : embed_form<E, X, false, false>(a, grid, tr, rpb, s);
   else
-    hipLaunchKernelGGL((k_embed<E, X, false>), dim3((unsigned)grid), dim3(tr * rpb), 0, s, a, tr, rpb);
+    a.d % 8 ? embed_form<E, X, true, true>(a, grid, tr, rpb, s) : embed_form<E, X, false, true>(a, grid, tr, rpb, s);
   return hipGetLastError();
 }
 

@@ -16,8 +16,8 @@
 namespace {
 
 constexpr int kCUs = 256;
-// threads a launch keeps on each CU
-constexpr int kFwdPerCu = 2048, kBwdPerCu = 2048;
+// bytes of rows that a gradient launch keeps under way on each CU
+constexpr int kBwdBytes = 48 * 1024;
 constexpr int kMaxNarrow = 8192;  // widest row whose elements stay in registers: 1024 threads of 8
 
 // How rows lie on threads: `tr` threads own a row, 8 elements each (a power
@@ -43,11 +43,50 @@ Map row_map(int d) {
   return m;
 }
 
-// workgroups of a launch that keeps `per_cu` threads on each CU
-unsigned grid_rows(long long rows, const Map &m, int per_cu) {
+// Workgroups of a gradient launch: each takes rows until none are left and
+// writes one partial sum per column. `elem`: bytes of a row's inputs per
+// column. Each workgroup has one step's rows under way while it works on the
+// step before. As many of them as have 48 KiB under way on a CU measured
+// best: at 32768 rows of 2560 (o, dh_in fp32; dx, y bf16: 30 KiB a row) one per
+// CU takes 272 us and two 294; at 1024 columns in bf16 (6 KiB a row) eight take
+// 58 us, five 65, ten 60 and sixteen 66. More of them only read from more
+// places at once, and leave more partial sums.
+unsigned bwd_grid(long long rows, const Map &m, int elem) {
   const long long want = (rows + m.rpb - 1) / m.rpb;
-  long long most = (long long)kCUs * (per_cu / m.threads > 0 ? per_cu / m.threads : 1);
-  return (unsigned)(want < most ? want : most);
+  long long per_cu = kBwdBytes / (m.threads * 8 * elem), most = 2048 / m.threads;
+  if (per_cu > most) per_cu = most;
+  if (per_cu < 1) per_cu = 1;
+  return (unsigned)(want < kCUs * per_cu ? want : kCUs * per_cu);
+}
+
+// elements between partial sums: whole cache lines
+__host__ __device__ __forceinline__ int part_ld(int d) { return (d + 31) / 32 * 32; }
+
+// v plus the value `CTRL` of the DPP controls brings from another lane
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// The sum over `width` lanes (8, 16, 32 or 64), in all of them, without the
+// LDS: within a quad by permutation, then each half of 8 and of 16 lanes from
+// the other by mirroring (its lanes hold the same sum), then by swapping rows
+// of 16 and halves of 32. Through the LDS crossbar the six sums of a gradient
+// row cost 36 passes per wave.
+__device__ __forceinline__ float wave_sum(float v, int width) {
+  v = add_dpp<0xB1>(v);   // quad_perm [1,0,3,2]
+  v = add_dpp<0x4E>(v);   // quad_perm [2,3,0,1]
+  v = add_dpp<0x141>(v);  // row_half_mirror
+  if (width >= 16) v = add_dpp<0x140>(v);  // row_mirror
+  if (width >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (width >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
 }
 
 // Sums of NS values over the tr threads of a row, the result in every one of
@@ -56,11 +95,8 @@ unsigned grid_rows(long long rows, const Map &m, int per_cu) {
 // of the sum between, which every reader of the half has then passed.
 template <int NS>
 __device__ __forceinline__ void row_sum(float (&s)[NS], int tr, float (*red)[16][NS], int &turn) {
-  const int width = tr < 64 ? tr : 64;
-  for (int o = width / 2; o > 0; o >>= 1) {
 #pragma unroll
-    for (int k = 0; k < NS; ++k) s[k] += __shfl_xor(s[k], o);
-  }
+  for (int k = 0; k < NS; ++k) s[k] = wave_sum(s[k], tr < 64 ? tr : 64);
   if (tr <= 64) return;
   const int wave = threadIdx.x >> 6, nw = tr >> 6;
   if ((threadIdx.x & 63) == 0) {
@@ -109,57 +145,57 @@ struct Cols {
 };
 
 // ---- forward ----
-template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R>
+// One workgroup per row (ONE: the row's addresses are the same for all its
+// threads), or per rpb narrow rows. Bound by memory: 32768 rows of 2560 with an
+// fp32 stream, bf16 y and x (1.007 GB) take 195 us, 5.2 TB/s, where a copy of
+// those arrays in the same pattern takes 165 to 170; bf16 rows of 1024 before a
+// block 6.1 TB/s. Workgroups that stay and stride over the rows take 206 us,
+// and writing past the caches changes nothing.
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE, bool TOKEN>
 __global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs A, int tr, int rpb) {
   __shared__ float red[2][16][1];
   int turn = 0;
-  const int d = A.d, sub = threadIdx.x / tr;
-  const Cols<R> cols(threadIdx.x % tr, d);
-  const int c = cols.at;
-  const bool mine = cols.mine;
-  float w[8], wn[8], ga[8];
+  const int d = A.d, sub = ONE ? 0 : threadIdx.x / tr;
+  const Cols<R> cols(ONE ? threadIdx.x : threadIdx.x % tr, d);
+  const unsigned c = cols.at;
+  const long long row = group_index() * rpb + sub;
+  const bool on = cols.mine && row < A.rows;
+  float o[8];
+  const Raw8<H> ro = load_raw(row_of<H>(A.h, row, d) + c, on);
   if (POST) {
-    load_param(A.w, A.p_f32, c, mine, w);
-    load_param(A.token_gate ? nullptr : A.gate, A.p_f32, c, mine, ga);
+    const Raw8<Y> ry = load_raw(row_of<Y>(A.y, row, d) + c, on);
+    float y[8], w[8], t[8];
+    if (TOKEN)
+      load_w(row_of<Y>(A.gate, row, d) + c, on, t);
+    else
+      load_param(A.gate, A.p_f32, c, cols.mine, t);
+    load_param(A.w, A.p_f32, c, cols.mine, w);
+    expand(ry, y);
+    float s[1] = {0.f};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] *= A.beta * ga[j];
+    for (int j = 0; j < 8; ++j) s[0] += cols.own(j, y[j] * y[j]);
+    row_sum<1>(s, tr, red, turn);
+    const float q = row_rms(s[0], d, A.eps);
+    expand(ro, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = A.alpha * o[j] + A.beta * t[j] * w[j] * (y[j] * q);
+    store_w(row_of<H>(A.o, row, d) + c, on, o);
+  } else {
+    expand(ro, o);
   }
-  if (NEXT) load_param(A.w_next, A.p_f32, c, mine, wn);
-  for (long long row0 = (long long)blockIdx.x * rpb; row0 < A.rows; row0 += (long long)gridDim.x * rpb) {
-    const long long row = row0 + sub;
-    const bool on = mine && row < A.rows;
-    float o[8];
-    load_w(row_of<H>(A.h, row, d) + c, on, o);
-    if (POST) {
-      float y[8];
-      load_w(row_of<Y>(A.y, row, d) + c, on, y);
-      float t[8];
-      if (A.token_gate)
-        load_w(row_of<Y>(A.gate, row, d) + c, on, t);
-      else {
+  if (NEXT) {
+    float wn[8];
+    load_param(A.w_next, A.p_f32, c, cols.mine, wn);
+    float s[1] = {0.f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = 1.f;
-      }
-      float s[1] = {0.f};
+    for (int j = 0; j < 8; ++j) s[0] += cols.own(j, o[j] * o[j]);
+    row_sum<1>(s, tr, red, turn);
+    const float r = row_rms(s[0], d, A.eps);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] += cols.own(j, y[j] * y[j]);
-      row_sum<1>(s, tr, red, turn);
-      const float q = row_rms(s[0], d, A.eps);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = A.alpha * o[j] + w[j] * t[j] * (y[j] * q);
-      store_w(row_of<H>(A.o, row, d) + c, on, o);
-    }
-    if (NEXT) {
-      float s[1] = {0.f};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] += cols.own(j, o[j] * o[j]);
-      row_sum<1>(s, tr, red, turn);
-      const float r = row_rms(s[0], d, A.eps);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = wn[j] * (o[j] * r);
-      store_w(row_of<X>(A.x, row, d) + c, on, o);
-    }
+    for (int j = 0; j < 8; ++j) o[j] = wn[j] * (o[j] * r);
+    store_w(row_of<X>(A.x, row, d) + c, on, o);
   }
+  end_of_stores();
 }
 
 // Rows too wide for registers: the row is read again for each step (from the
@@ -170,58 +206,58 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormArgs A) {
   __shared__ float red[2][16][1];
   int turn = 0;
   const int d = A.d, v = d / W;
-  for (long long row = blockIdx.x; row < A.rows; row += gridDim.x) {
-    const H *h = row_of<H>(A.h, row, d);
-    const Y *y = row_of<Y>(A.y, row, d);
-    const Y *ta = row_of<Y>(A.gate, row, d);
-    float q = 0.f, r = 0.f;
-    auto after = [&](int c, float (&o)[W]) {  // o of W columns
-      load_w(h + c * W, true, o);
-      if (POST) {
-        float yy[W], w[W], a[W];
-        load_w(y + c * W, true, yy);
-        load_param(A.w, A.p_f32, c * W, true, w);
-        if (A.token_gate)
-          load_w(ta + c * W, true, a);
-        else
-          load_param(A.gate, A.p_f32, c * W, true, a);
-#pragma unroll
-        for (int j = 0; j < W; ++j) o[j] = A.alpha * o[j] + A.beta * a[j] * w[j] * (yy[j] * q);
-      }
-    };
+  const long long row = group_index();
+  if (row >= A.rows) return;
+  const H *h = row_of<H>(A.h, row, d);
+  const Y *y = row_of<Y>(A.y, row, d);
+  const Y *ta = row_of<Y>(A.gate, row, d);
+  float q = 0.f, r = 0.f;
+  auto after = [&](int c, float (&o)[W]) {  // o of W columns
+    load_w(h + c * W, true, o);
     if (POST) {
-      float s[1] = {0.f};
-      for (int c = threadIdx.x; c < v; c += 1024) {
-        float yy[W];
-        load_w(y + c * W, true, yy);
+      float yy[W], w[W], a[W];
+      load_w(y + c * W, true, yy);
+      load_param(A.w, A.p_f32, c * W, true, w);
+      if (A.token_gate)
+        load_w(ta + c * W, true, a);
+      else
+        load_param(A.gate, A.p_f32, c * W, true, a);
 #pragma unroll
-        for (int j = 0; j < W; ++j) s[0] += yy[j] * yy[j];
-      }
-      row_sum<1>(s, 1024, red, turn);
-      q = row_rms(s[0], d, A.eps);
+      for (int j = 0; j < W; ++j) o[j] = A.alpha * o[j] + A.beta * a[j] * w[j] * (yy[j] * q);
     }
-    if (NEXT) {
-      float s[1] = {0.f};
-      for (int c = threadIdx.x; c < v; c += 1024) {
-        float o[W];
-        after(c, o);
+  };
+  if (POST) {
+    float s[1] = {0.f};
+    for (int c = threadIdx.x; c < v; c += 1024) {
+      float yy[W];
+      load_w(y + c * W, true, yy);
 #pragma unroll
-        for (int j = 0; j < W; ++j) s[0] += o[j] * o[j];
-      }
-      row_sum<1>(s, 1024, red, turn);
-      r = row_rms(s[0], d, A.eps);
+      for (int j = 0; j < W; ++j) s[0] += yy[j] * yy[j];
     }
+    row_sum<1>(s, 1024, red, turn);
+    q = row_rms(s[0], d, A.eps);
+  }
+  if (NEXT) {
+    float s[1] = {0.f};
     for (int c = threadIdx.x; c < v; c += 1024) {
       float o[W];
       after(c, o);
-      if (POST) store_w(row_of<H>(A.o, row, d) + c * W, true, o);
-      if (NEXT) {
-        float wn[W];
-        load_param(A.w_next, A.p_f32, c * W, true, wn);
 #pragma unroll
-        for (int j = 0; j < W; ++j) o[j] = wn[j] * (o[j] * r);
-        store_w(row_of<X>(A.x, row, d) + c * W, true, o);
-      }
+      for (int j = 0; j < W; ++j) s[0] += o[j] * o[j];
+    }
+    row_sum<1>(s, 1024, red, turn);
+    r = row_rms(s[0], d, A.eps);
+  }
+  for (int c = threadIdx.x; c < v; c += 1024) {
+    float o[W];
+    after(c, o);
+    if (POST) store_w(row_of<H>(A.o, row, d) + c * W, true, o);
+    if (NEXT) {
+      float wn[W];
+      load_param(A.w_next, A.p_f32, c * W, true, wn);
+#pragma unroll
+      for (int j = 0; j < W; ++j) o[j] = wn[j] * (o[j] * r);
+      store_w(row_of<X>(A.x, row, d) + c * W, true, o);
     }
   }
 }
@@ -280,20 +316,43 @@ __device__ __forceinline__ void add_terms(float (&s)[6], float o, float g, float
   }
 }
 
-// partial sums of workgroup b: [b][2][d]: the gradient of w', then S
-template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R>
-__global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs A, int tr, int rpb) {
+// A row's inputs, as they lie in memory.
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool TOKEN>
+struct BwdRow {
+  Raw8<H> o, di;
+  Raw8<X> dx;
+  Raw8<Y> y, a;
+  __device__ __forceinline__ void load(const NormArgs &A, long long row, unsigned c, bool on) {
+    const int d = A.d;
+    if (NEXT) {
+      o = load_raw(row_of<H>(A.h, row, d) + c, on);
+      dx = load_raw(row_of<X>(A.dx, row, d) + c, on);
+    }
+    di = load_raw(row_of<H>(A.dh_in, row, d) + c, on && A.dh_in);
+    if (POST) y = load_raw(row_of<Y>(A.y, row, d) + c, on);
+    if (POST && TOKEN) a = load_raw(row_of<Y>(A.gate, row, d) + c, on);
+  }
+};
+
+// Partial sums of workgroup b, [b][2][part_ld(d)]: the gradient of w', then S.
+// Bound by memory: 32768 rows of 2560 as above (1.51 GB) take 272 us with the
+// sums over the workgroups, 5.5 TB/s; 32768 bf16 rows of 1024 (0.27 GB) 58 us.
+// The loads of a workgroup's next row are issued before this row's results are
+// stored: waits for memory operations are counted in their order, so loads
+// behind the stores would be waited for together with them.
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE, bool TOKEN, int MOST>
+__global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs A, int tr, int rpb) {
   __shared__ float red[2][16][6];
-  __shared__ float acc[2][256 * 8];  // workgroups of several rows (256 threads) add their rows' columns here
+  __shared__ float acc[2][ONE ? 1 : 256 * 8];  // workgroups of several rows (256 threads) add their rows' columns here
   int turn = 0;
-  const int d = A.d, sub = threadIdx.x / tr;
-  const Cols<R> cols(threadIdx.x % tr, d);
-  const int c = cols.at;
+  const int d = A.d, sub = ONE ? 0 : threadIdx.x / tr;
+  const Cols<R> cols(ONE ? threadIdx.x : threadIdx.x % tr, d);
+  const unsigned c = cols.at;
   const bool mine = cols.mine;
   float w[8], wn[8], k[8], dwn[8], ds[8];
   if (POST) {
     load_param(A.w, A.p_f32, c, mine, w);
-    load_param(A.token_gate ? nullptr : A.gate, A.p_f32, c, mine, k);
+    load_param(TOKEN ? nullptr : A.gate, A.p_f32, c, mine, k);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       w[j] *= A.beta;
@@ -304,29 +363,26 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs A, int tr, int rpb) 
 #pragma unroll
   for (int j = 0; j < 8; ++j) dwn[j] = ds[j] = 0.f;
 
-  for (long long row0 = (long long)blockIdx.x * rpb; row0 < A.rows; row0 += (long long)gridDim.x * rpb) {
-    const long long row = row0 + sub;
+  const long long step = (long long)gridDim.x * rpb;
+  long long row = (long long)blockIdx.x * rpb + sub;
+  BwdRow<H, Y, X, POST, NEXT, TOKEN> in;
+  in.load(A, row, c, mine && row < A.rows);
+  for (long long row0 = (long long)blockIdx.x * rpb; row0 < A.rows; row0 += step, row += step) {
     const bool on = mine && row < A.rows;
     float o[8], g[8], di[8], y[8], a[8];
     if (NEXT) {
-      load_w(row_of<H>(A.h, row, d) + c, on, o);
-      load_w(row_of<X>(A.dx, row, d) + c, on, g);
+      expand(in.o, o);
+      expand(in.dx, g);
     }
-    load_w(row_of<H>(A.dh_in, row, d) + c, on && A.dh_in, di);
-    if (POST) {
-      load_w(row_of<Y>(A.y, row, d) + c, on, y);
-      if (A.token_gate)
-        load_w(row_of<Y>(A.gate, row, d) + c, on, a);
-      else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = 1.f;
-      }
-    }
+    expand(in.di, di);
+    if (POST) expand(in.y, y);
+    if (POST && TOKEN) expand(in.a, a);
+    in.load(A, row + step, c, mine && row + step < A.rows);
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       add_terms<POST, NEXT>(s, NEXT ? cols.own(j, o[j]) : 0.f, NEXT ? g[j] * wn[j] : 0.f, di[j],
-                            POST ? cols.own(j, y[j]) : 0.f, POST ? k[j] * a[j] : 0.f);
+                            POST ? cols.own(j, y[j]) : 0.f, !POST ? 0.f : TOKEN ? k[j] * a[j] : k[j]);
     row_sum<6>(s, tr, red, turn);
     const RowStat t = row_stat<POST, NEXT>(s, d, A.eps);
     float dh[8], dy[8], da[8];
@@ -339,41 +395,42 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs A, int tr, int rpb) 
       }
       dh[j] = A.alpha * v;
       if (POST) {
-        const float yn = y[j] * t.q;
-        ds[j] += v * a[j] * yn;
+        const float yn = y[j] * t.q, ta = TOKEN ? a[j] : 1.f;
+        ds[j] += v * ta * yn;
         da[j] = v * w[j] * yn;
-        dy[j] = t.q * (k[j] * a[j] * v) - t.q2s * y[j];
+        dy[j] = t.q * (k[j] * ta * v) - t.q2s * y[j];
       }
     }
     store_w(row_of<H>(A.dh, row, d) + c, on, dh);
     if (POST) {
       store_w(row_of<Y>(A.dy, row, d) + c, on, dy);
-      if (A.token_gate) store_w(row_of<Y>(A.dgate_t, row, d) + c, on, da);
+      if (TOKEN) store_w(row_of<Y>(A.dgate_t, row, d) + c, on, da);
     }
   }
   if (!A.part) return;
-  float *part = A.part + (long long)blockIdx.x * 2 * d;
-  if (rpb == 1) {
+  const int ld = part_ld(d);
+  float *part = A.part + (long long)blockIdx.x * 2 * ld;
+  if (ONE) {
     if (NEXT) store_w(part + c, mine, dwn);
-    if (POST) store_w(part + d + c, mine, ds);
+    if (POST) store_w(part + ld + c, mine, ds);
     return;
   }
   if (mine) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      acc[0][sub * tr * 8 + c + j] = dwn[j];
-      acc[1][sub * tr * 8 + c + j] = ds[j];
+      acc[0][ONE ? 0 : sub * tr * 8 + c + j] = dwn[j];
+      acc[1][ONE ? 0 : sub * tr * 8 + c + j] = ds[j];
     }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < d; i += blockDim.x) {
     float s0 = 0.f, s1 = 0.f;
     for (int u = 0; u < rpb; ++u) {
-      s0 += acc[0][u * tr * 8 + i];
-      s1 += acc[1][u * tr * 8 + i];
+      s0 += acc[0][ONE ? 0 : u * tr * 8 + i];
+      s1 += acc[1][ONE ? 0 : u * tr * 8 + i];
     }
     if (NEXT) part[i] = s0;
-    if (POST) part[d + i] = s1;
+    if (POST) part[ld + i] = s1;
   }
 }
 
@@ -385,7 +442,8 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormArgs A) {
   __shared__ float red[2][16][6];
   int turn = 0;
   const int d = A.d, v = d / W;
-  float *part = A.part ? A.part + (long long)blockIdx.x * 2 * d : nullptr;
+  const int ld = part_ld(d);
+  float *part = A.part ? A.part + (long long)blockIdx.x * 2 * ld : nullptr;
   bool first = true;
   for (long long row = blockIdx.x; row < A.rows; row += gridDim.x) {
     float o[W], g[W], di[W], y[W], a[W], w[W], k[W], dxv[W];
@@ -458,10 +516,10 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormArgs A) {
           store_w(part + c * W, true, old);
         }
         if (POST) {
-          load_w(part + d + c * W, !first, old);
+          load_w(part + ld + c * W, !first, old);
 #pragma unroll
           for (int j = 0; j < W; ++j) old[j] += ds[j];
-          store_w(part + d + c * W, true, old);
+          store_w(part + ld + c * W, true, old);
         }
       }
     }
@@ -470,28 +528,27 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormArgs A) {
 }
 
 // The parameters' gradients from the workgroups' partial sums (nparts of
-// them; none for a call without rows). 64 columns per workgroup, 16 threads
-// across them with 4 columns each and 16 slices of the partial sums.
-__global__ __launch_bounds__(256) void k_norm_params(NormArgs A, int nparts) {
-  __shared__ float sum[16][64];
-  const int d = A.d, which = blockIdx.y;
+// them; none for a call without rows). A workgroup takes 32 columns, a cache
+// line of each partial sum: 8 threads across it, 128 down the partial sums.
+constexpr int kDown = 128;
+__global__ __launch_bounds__(kDown * 8) void k_norm_params(NormArgs A, int nparts) {
+  __shared__ f32x4 sum[kDown][8];
+  const int d = A.d, which = blockIdx.y, ld = part_ld(d);
   if (which == 0 ? !A.dw_next : (!A.dw && !A.dgate_c)) return;
-  const int lane = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int c = blockIdx.x * 64 + lane * 4;
-  const float *p = A.part + (long long)which * d;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int b = slice; b < nparts; b += 16) {
-    const float *q = p + (long long)b * 2 * d + c;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] += c + j < d ? q[j] : 0.f;
+  const int across = threadIdx.x & 7, down = threadIdx.x >> 3;
+  const float *p = A.part + (long long)which * ld + blockIdx.x * 32 + across * 4;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int b = down; b < nparts; b += kDown) s += *reinterpret_cast<const f32x4 *>(p + (long long)b * 2 * ld);
+  sum[down][across] = s;
+  for (int half = kDown / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (down < half) sum[down][across] += sum[down + half][across];
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) sum[slice][lane * 4 + j] = s[j];
   __syncthreads();
-  const int i = blockIdx.x * 64 + threadIdx.x;
-  if (threadIdx.x >= 64 || i >= d) return;
-  float t = 0.f;
-  for (int k = 0; k < 16; ++k) t += sum[k][threadIdx.x];
+  const int i = blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x >= 32 || i >= d) return;
+  const float t = sum[0][threadIdx.x / 4][threadIdx.x % 4];
   if (which == 0) {
     A.dw_next[i] = t;
     return;
@@ -504,46 +561,79 @@ __global__ __launch_bounds__(256) void k_norm_params(NormArgs A, int nparts) {
 }
 
 // ---- which instance ----
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE>
+void fwd_form(const NormArgs &a, const Map &m, dim3 grid, hipStream_t s) {
+  if (POST && a.token_gate)
+    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, POST>), grid, dim3(m.threads), 0, s, a, m.tr, m.rpb);
+  else
+    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, false>), grid, dim3(m.threads), 0, s, a, m.tr, m.rpb);
+}
+
 template <typename H, typename Y, typename X, bool POST, bool NEXT>
 hipError_t fwd(const NormArgs &a, hipStream_t s) {
   const Map m = row_map(a.d);
-  const dim3 grid(grid_rows(a.rows, m, kFwdPerCu)), block(m.threads);
+  const dim3 grid = group_grid((a.rows + m.rpb - 1) / m.rpb);
   if (a.d > kMaxNarrow && a.d % 8)
-    hipLaunchKernelGGL((k_norm_fwd_wide<H, Y, X, POST, NEXT, 1>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_norm_fwd_wide<H, Y, X, POST, NEXT, 1>), grid, dim3(1024), 0, s, a);
   else if (a.d > kMaxNarrow)
-    hipLaunchKernelGGL((k_norm_fwd_wide<H, Y, X, POST, NEXT, 8>), grid, block, 0, s, a);
-  else if (a.d % 8)
-    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, true>), grid, block, 0, s, a, m.tr, m.rpb);
+    hipLaunchKernelGGL((k_norm_fwd_wide<H, Y, X, POST, NEXT, 8>), grid, dim3(1024), 0, s, a);
+  else if (m.rpb == 1)
+    a.d % 8 ? fwd_form<H, Y, X, POST, NEXT, true, true>(a, m, grid, s)
+            : fwd_form<H, Y, X, POST, NEXT, false, true>(a, m, grid, s);
   else
-    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, false>), grid, block, 0, s, a, m.tr, m.rpb);
+    a.d % 8 ? fwd_form<H, Y, X, POST, NEXT, true, false>(a, m, grid, s)
+            : fwd_form<H, Y, X, POST, NEXT, false, false>(a, m, grid, s);
   return hipGetLastError();
+}
+
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE, bool TOKEN>
+void bwd_launch(const NormArgs &a, const Map &m, unsigned grid, hipStream_t s) {
+  // up to 512 threads a kernel may hold 256 registers each and spills none (340 us and more at 32768 rows of 2560 with
+  // the 128 that 1024 threads allow)
+  if (!ONE || m.threads <= 512)
+    hipLaunchKernelGGL((k_norm_bwd<H, Y, X, POST, NEXT, R, ONE, TOKEN, 512>), dim3(grid), dim3(m.threads), 0, s, a,
+                       m.tr, m.rpb);
+  else
+    hipLaunchKernelGGL((k_norm_bwd<H, Y, X, POST, NEXT, R, ONE, TOKEN, ONE ? 1024 : 512>), dim3(grid),
+                       dim3(m.threads), 0, s, a, m.tr, m.rpb);
+}
+
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE>
+void bwd_form(const NormArgs &a, const Map &m, unsigned grid, hipStream_t s) {
+  if (POST && a.token_gate)
+    bwd_launch<H, Y, X, POST, NEXT, R, ONE, POST>(a, m, grid, s);
+  else
+    bwd_launch<H, Y, X, POST, NEXT, R, ONE, false>(a, m, grid, s);
 }
 
 template <typename H, typename Y, typename X, bool POST, bool NEXT>
 hipError_t bwd(const NormArgs &a, hipStream_t s) {
   const Map m = row_map(a.d);
-  const unsigned grid = grid_rows(a.rows, m, kBwdPerCu);
+  constexpr int elem = (NEXT ? sizeof(H) + sizeof(X) : 0) + sizeof(H) + (POST ? sizeof(Y) : 0);
+  const unsigned grid = bwd_grid(a.rows, m, elem);
   if (grid > 0) {
     if (a.d > kMaxNarrow && a.d % 8)
       hipLaunchKernelGGL((k_norm_bwd_wide<H, Y, X, POST, NEXT, 1>), dim3(grid), dim3(1024), 0, s, a);
     else if (a.d > kMaxNarrow)
       hipLaunchKernelGGL((k_norm_bwd_wide<H, Y, X, POST, NEXT, 8>), dim3(grid), dim3(1024), 0, s, a);
-    else if (a.d % 8)
-      hipLaunchKernelGGL((k_norm_bwd<H, Y, X, POST, NEXT, true>), dim3(grid), dim3(m.threads), 0, s, a, m.tr, m.rpb);
+    else if (m.rpb == 1)
+      a.d % 8 ? bwd_form<H, Y, X, POST, NEXT, true, true>(a, m, grid, s)
+              : bwd_form<H, Y, X, POST, NEXT, false, true>(a, m, grid, s);
     else
-      hipLaunchKernelGGL((k_norm_bwd<H, Y, X, POST, NEXT, false>), dim3(grid), dim3(m.threads), 0, s, a, m.tr, m.rpb);
+      a.d % 8 ? bwd_form<H, Y, X, POST, NEXT, true, false>(a, m, grid, s)
+              : bwd_form<H, Y, X, POST, NEXT, false, false>(a, m, grid, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.part) hipLaunchKernelGGL(k_norm_params, dim3((a.d + 63) / 64, 2), dim3(256), 0, s, a, (int)grid);
+  if (a.part) hipLaunchKernelGGL(k_norm_params, dim3((a.d + 31) / 32, 2), dim3(kDown * 8), 0, s, a, (int)grid);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t norm_ws_bytes(long long rows, int d) {
-  const unsigned grid = grid_rows(rows, row_map(d), kBwdPerCu);
-  return (size_t)(grid > 0 ? grid : 1) * 2 * d * sizeof(float);
+  const unsigned grid = bwd_grid(rows, row_map(d), 4);  // the least of any types
+  return (size_t)(grid > 0 ? grid : 1) * 2 * part_ld(d) * sizeof(float);
 }
 
 #define NORM_CASES(CALL)                                                                                  \

@@ -9,39 +9,51 @@
 
 #include "common.h"
 
-struct Raw8b {
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16_t> {
   uint32_t u[4];
 };
-struct Raw8f {
+template <>
+struct Raw8<float> {
   float f[8];
 };
 
-__device__ __forceinline__ void load_w(const bf16_t *p, bool on, float (&v)[8]) {
-  Raw8b r = {{0, 0, 0, 0}};
-  if (on) __builtin_memcpy(&r, p, 16);
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T *p, bool on) {
+  Raw8<T> r = {};
+  if (on) __builtin_memcpy(&r, p, sizeof r);
+  return r;
+}
+__device__ __forceinline__ void expand(const Raw8<bf16_t> &r, float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     v[2 * j] = __uint_as_float(r.u[j] << 16);
     v[2 * j + 1] = __uint_as_float(r.u[j] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load_w(const float *p, bool on, float (&v)[8]) {
-  Raw8f r = {{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}};
-  if (on) __builtin_memcpy(&r, p, 32);
+__device__ __forceinline__ void expand(const Raw8<float> &r, float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = r.f[j];
+}
+
+template <typename T>
+__device__ __forceinline__ void load_w(const T *p, bool on, float (&v)[8]) {
+  expand(load_raw(p, on), v);
 }
 __device__ __forceinline__ void load_w(const bf16_t *p, bool on, float (&v)[1]) { v[0] = on ? bf16_to_f32(*p) : 0.f; }
 __device__ __forceinline__ void load_w(const float *p, bool on, float (&v)[1]) { v[0] = on ? *p : 0.f; }
 
 __device__ __forceinline__ void store_w(bf16_t *p, bool on, const float (&v)[8]) {
-  Raw8b r;
+  Raw8<bf16_t> r;
 #pragma unroll
   for (int j = 0; j < 4; ++j) r.u[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
   if (on) __builtin_memcpy(p, &r, 16);
 }
 __device__ __forceinline__ void store_w(float *p, bool on, const float (&v)[8]) {
-  Raw8f r;
+  Raw8<float> r;
 #pragma unroll
   for (int j = 0; j < 8; ++j) r.f[j] = v[j];
   if (on) __builtin_memcpy(p, &r, 32);
@@ -52,6 +64,42 @@ __device__ __forceinline__ void store_w(bf16_t *p, bool on, const float (&v)[1])
 __device__ __forceinline__ void store_w(float *p, bool on, const float (&v)[1]) {
   if (on) *p = v[0];
 }
+
+// Behind a kernel's last wide store: the store reads its data registers after
+// it issues, and two wait states must pass before an instruction writes one of
+// them. No instruction follows at the kernel's end, but in the listing, which
+// is checked for this hazard line by line, the code of another branch may.
+__device__ __forceinline__ void end_of_stores() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 1");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Eight elements past the caches' keeping (the `nt` bit), for arrays too large
+// for the next kernel to find them there.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ void stream_w(bf16_t *p, bool on, const float (&v)[8]) {
+  const u32x4_any r = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7])};
+  if (on) __builtin_nontemporal_store(r, reinterpret_cast<u32x4_any *>(p));
+}
+__device__ __forceinline__ void stream_w(float *p, bool on, const float (&v)[8]) {
+  u32x4_any r[2];
+  __builtin_memcpy(r, v, 32);
+  if (on) {
+    __builtin_nontemporal_store(r[0], reinterpret_cast<u32x4_any *>(p));
+    __builtin_nontemporal_store(r[1], reinterpret_cast<u32x4_any *>(p) + 1);
+  }
+}
+
+// A launch of one workgroup per row or more: threads of a grid's side are
+// counted in 32 bits, so many rows take a second side. group_index() is the
+// workgroup's number; the last ones may lie past `groups`.
+constexpr long long kGridSide = 1 << 20;
+inline dim3 group_grid(long long groups) {
+  return groups <= kGridSide ? dim3((unsigned)groups) : dim3((unsigned)kGridSide, (unsigned)((groups + kGridSide - 1) / kGridSide));
+}
+__device__ __forceinline__ long long group_index() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
 
 // The same of a parameter that is fp32 or bf16 as the caller has it (a branch
 // all threads take alike); a NULL parameter reads as ones.

@@ -231,3 +231,14 @@ def test_refusals_of_the_binding():
         ttt.ttt_embed_grad(torch.zeros(4, 6, 64, device="cuda"), ids, 10, accumulate=True)
     with pytest.raises(ValueError, match="shape"):
         ttt.ttt_embed_grad(torch.zeros(4, 6, 64, device="cuda"), ids, 10, dE=torch.zeros(9, 64, device="cuda"))
+
+
+@gpu
+def test_more_rows_than_a_grid_side_counts():
+    """2^22 + 3 rows of 8192: at 1024 threads a row they pass 2^32."""
+    n, d = 2 ** 22 + 3, 8192
+    E = torch.arange(1, 4, device="cuda", dtype=torch.float32)[:, None].expand(3, d).contiguous().to(B16)
+    ids = (torch.arange(n, device="cuda") % 3).int()
+    x = ttt.ttt_embed(E, ids)
+    assert torch.equal(x[:, 0], E[:, 0][ids.long()]) and torch.equal(x[-5:], E[ids[-5:].long()])
+    assert torch.equal(x[:, -1], x[:, 0])

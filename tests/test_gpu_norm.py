@@ -8,7 +8,10 @@ relative. The longest chain of a gradient, r^2 m with m = r sum(g o) / d, holds
 r three times and one more sum, and enters a last sum: 3 (N/2 + 4) + 2 N and a
 few products, under (4 N + 40) u of the magnitudes. On top comes the rounding
 of the result to its type. A gradient of a gain sums over the rows: the rows
-of one workgroup, then the workgroups in 16 slices, then the slices.
+of one workgroup (at least 256 of them share the rows) and the up to 32 rows it
+takes at a time, then the workgroups in 128 slices, then the slices in seven
+steps. The bound below counts the workgroups at their most, and 48 additions
+besides, which also covers the 5 rows of a workgroup at these sizes.
 """
 import pytest
 import torch
@@ -390,3 +393,15 @@ def test_refusals_of_the_binding():
         ttt.ttt_norm_pre(h, x=h)
     with pytest.raises(ttt.TTTError, match="d must be"):
         ttt.ttt_norm_pre(torch.zeros(4, 7, device="cuda"))
+
+
+@gpu
+def test_more_rows_than_a_grid_side_counts():
+    """2^29 + 3 rows of 8: their threads, one per row of eight columns, pass 2^32 in eights of lanes."""
+    rows, d = 2 ** 29 + 3, 8
+    h = torch.ones((rows, d), dtype=B, device="cuda")
+    h[-1] = torch.arange(1, 9, device="cuda").to(B)
+    x = ttt.ttt_norm_pre(h, eps=EPS)
+    want = ttt.ttt_norm_pre(h[-2:].clone(), eps=EPS)
+    assert torch.equal(x[-2:], want)
+    assert bool((x[:-1] == 1).all())
