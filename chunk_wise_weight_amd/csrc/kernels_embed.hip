@@ -23,9 +23,11 @@ constexpr int kMaxTiles = 256;   // of a sort: a workgroup reads the counts of a
 constexpr int kMinTile = 1024;   // tokens
 constexpr int kMaxDigit = 9;     // bits
 constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
-constexpr long long kMaxGroups = 1 << 22;  // of a launch: threads of a grid are counted in 32 bits
 constexpr int kClearPerGroup = 2048;  // table rows whose segments one workgroup clears
-constexpr int kChunk = 64;       // sorted tokens of one piece of a long row
+constexpr int kRounds = kMinTile / kSortThreads;  // tokens of a thread that it holds at once
+constexpr int kSmallThreads = 1024, kSmall = kSmallThreads * kRounds;  // tokens that one workgroup sorts
+constexpr int kSmallClear = 16384;  // table rows whose segments one workgroup clears in passing
+constexpr int kChunk = 32;       // sorted tokens of one piece of a long row
 
 // ---- lookup ----
 
@@ -50,6 +52,15 @@ __global__ __launch_bounds__(1024) void k_embed(EmbedArgs A, int tr, int rpb) {
     // the last columns of a ragged row: its last eight, some of which the neighbour writes too, to the same values
     const int c = R && c8 * 8 + 8 > d ? d - 8 : c8 * 8;
     float v[8];
+    if (!R && sizeof(X) == 4) {
+      // four columns of each half of an fp32 row: each store of a wave then covers whole cache lines (5% on rows
+      // that stay in the caches)
+      expand(load_halves(src + c8 * 4, d / 2, on), v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= A.scale;
+      store_halves<STREAM>(dst + c8 * 4, d / 2, v);
+      continue;
+    }
     load_w(src + c, on, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= A.scale;
@@ -99,51 +110,99 @@ struct SortArgs {
   }
 };
 
+// seg of a table from `at` on, in steps
+__device__ __forceinline__ void clear_runs(Run *seg, int vocab, long long at, long long step) {
+  for (long long v = at; v < vocab; v += step) seg[v] = Run{0, 0};
+}
+__global__ __launch_bounds__(256) void k_clear_runs(Run *seg, int vocab) {
+  clear_runs(seg, vocab, (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
+}
+
 // hist[tile][digit]: how often each digit occurs in the tile
 __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs S) {
   __shared__ uint32_t cnt[1 << kMaxDigit];
   for (int i = threadIdx.x; i < S.bins; i += kSortThreads) cnt[i] = 0;
-  if (!S.key_in) {
-    for (long long v = (long long)blockIdx.x * kSortThreads + threadIdx.x; v < S.vocab;
-         v += (long long)gridDim.x * kSortThreads)
-      S.seg[v] = Run{0, 0};
-  }
+  if (!S.key_in)
+    clear_runs(S.seg, S.vocab, (long long)blockIdx.x * kSortThreads + threadIdx.x, (long long)gridDim.x * kSortThreads);
   if ((int)blockIdx.x >= S.tiles) return;  // here to clear only
   __syncthreads();
   const long long t0 = (long long)blockIdx.x * S.tile;
   const int hi = (int)(t0 + S.tile < S.ids.n ? t0 + S.tile : S.ids.n);
-  for (int i = (int)t0 + threadIdx.x; i < hi; i += kSortThreads)
-    atomicAdd(&cnt[(S.key(i) >> S.shift) & (S.bins - 1)], 1u);
+  for (int i = (int)t0 + threadIdx.x; i < hi; i += kSortThreads * kRounds) {
+    uint32_t key[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) key[r] = i + r * kSortThreads < hi ? S.key(i + r * kSortThreads) : 0;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+      if (i + r * kSortThreads < hi) atomicAdd(&cnt[(key[r] >> S.shift) & (S.bins - 1)], 1u);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < S.bins; i += kSortThreads) S.hist[(long long)blockIdx.x * S.bins + i] = cnt[i];
 }
 
+// The place of a lane's token among the wave's: `next` holds where the wave's
+// next token of each digit goes, and moves on. Tokens of one digit keep the
+// order of their lanes.
+__device__ __forceinline__ uint32_t place_of(uint32_t *next, int dg, int bins, bool in) {
+  const int lane = threadIdx.x & 63;
+  uint64_t same = __ballot(in);  // the lanes with the same digit
+  for (int bit = 1; bit < bins; bit <<= 1) {
+    const uint64_t one = __ballot(in && (dg & bit));
+    same &= (dg & bit) ? one : ~one;
+  }
+  uint32_t at = 0;
+  if (in) {
+    const int first = __ffsll((unsigned long long)same) - 1;
+    if (lane == first) at = atomicAdd(&next[dg], (uint32_t)__popcll(same));
+    at = __shfl(at, first) + __popcll(same & ((1ull << lane) - 1));
+  }
+  return at;
+}
+
 // Places the tile's tokens: behind all tokens of a smaller digit, and those of
 // the same digit in earlier tiles, earlier waves' parts of the tile (each wave
-// owns a run of it) and earlier steps of the wave.
+// owns a run of it) and earlier steps of the wave. ONCE: a wave's run is
+// kRounds steps, all in registers (tiles of kMinTile).
+template <bool ONCE>
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs S) {
   __shared__ uint32_t next[kSortWaves][1 << kMaxDigit];  // where a wave's next token of a digit goes
   __shared__ uint32_t wsum[kSortWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int i = threadIdx.x; i < kSortWaves * S.bins; i += kSortThreads) next[i / S.bins][i % S.bins] = 0;
-  __syncthreads();
   const long long t0 = (long long)blockIdx.x * S.tile;
   const int run = S.tile / kSortWaves;
   const long long w0 = t0 + (long long)wave * run;
   const int lo = (int)(w0 < S.ids.n ? w0 : S.ids.n), hi = (int)(w0 + run < S.ids.n ? w0 + run : S.ids.n);
-  for (int i = lo + lane; i < hi; i += 64) atomicAdd(&next[wave][(S.key(i) >> S.shift) & (S.bins - 1)], 1u);
-  __syncthreads();
+  uint32_t key[kRounds], pos[kRounds];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int i = i0 + r * 64 + lane;
+      key[r] = i < hi ? S.key(i) : 0;
+      pos[r] = i < hi && S.pos_in ? S.pos_in[i] : (uint32_t)i;
+    }
+  };
+  auto digit = [&](int r) { return (int)((key[r] >> S.shift) & (S.bins - 1)); };
+  if (ONCE) load(lo);
+  for (int i = threadIdx.x; i < kSortWaves * S.bins; i += kSortThreads) next[i / S.bins][i % S.bins] = 0;
   // two neighbouring digits per thread (at most 512 of them): their totals, and the part before this tile
   uint32_t total[2] = {0, 0}, before[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int b = threadIdx.x * 2 + k;
-    if (b >= S.bins) break;
+  if ((int)threadIdx.x * 2 < S.bins) {
+    const uint2 *h2 = reinterpret_cast<const uint2 *>(S.hist) + threadIdx.x;
+#pragma unroll 16  // as many loads at once, or each would wait for the one before it
     for (int t = 0; t < S.tiles; ++t) {
-      const uint32_t h = S.hist[(long long)t * S.bins + b];
-      total[k] += h;
-      before[k] += t < (int)blockIdx.x ? h : 0;
+      const uint2 h = h2[(long long)t * (S.bins / 2)];
+      total[0] += h.x;
+      total[1] += h.y;
+      before[0] += t < (int)blockIdx.x ? h.x : 0;
+      before[1] += t < (int)blockIdx.x ? h.y : 0;
     }
+  }
+  __syncthreads();
+  for (int i0 = lo; i0 < hi; i0 += 64 * kRounds) {
+    if (!ONCE) load(i0);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+      if (i0 + r * 64 + lane < hi) atomicAdd(&next[wave][digit(r)], 1u);
   }
   // exclusive sum of the totals over the digits
   uint32_t inc = total[0] + total[1];
@@ -168,37 +227,145 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs S) {
     base += total[k];
   }
   __syncthreads();
-  for (int i0 = lo; i0 < hi; i0 += 64) {
-    const int i = i0 + lane;
-    const bool in = i < hi;
-    const uint32_t key = in ? S.key(i) : 0;
-    const int dg = (int)((key >> S.shift) & (S.bins - 1));
-    // the lanes with the same digit
-    uint64_t same = __ballot(in);
-    for (int bit = 1; bit < S.bins; bit <<= 1) {
-      const uint64_t one = __ballot(in && (dg & bit));
-      same &= (dg & bit) ? one : ~one;
-    }
-    if (in) {
-      const int rank = __popcll(same & ((1ull << lane) - 1));
-      const int first = __ffsll((unsigned long long)same) - 1;
-      uint32_t at = 0;
-      if (lane == first) at = atomicAdd(&next[wave][dg], (uint32_t)__popcll(same));
-      at = __shfl(at, first) + rank;
-      S.key_out[at] = key;
-      S.pos_out[at] = S.pos_in ? S.pos_in[i] : (uint32_t)i;
+  for (int i0 = lo; i0 < hi; i0 += 64 * kRounds) {
+    if (!ONCE) load(i0);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const bool in = i0 + r * 64 + lane < hi;
+      const uint32_t at = place_of(next[wave], digit(r), S.bins, in);
+      if (in) {
+        S.key_out[at] = key[r];
+        S.pos_out[at] = pos[r];
+      }
     }
   }
 }
 
-// seg[v]: the sorted tokens of table row v
-__global__ __launch_bounds__(256) void k_segments(const uint32_t *key, int n, int vocab, Run *seg) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const uint32_t k = key[i];
-  if (k >= (uint32_t)vocab) return;
-  if (i == 0 || key[i - 1] != k) seg[k].start = (int)i;
-  if (i == n - 1 || key[i + 1] != k) seg[k].end = (int)i + 1;
+// What a chunk of kChunk sorted tokens holds of long rows (of more than kChunk
+// tokens): the one it opens with, which may have begun earlier, and the one it
+// closes with if that is another. A long row cannot lie inside a chunk, so
+// there are no others.
+struct Chunk {
+  int v0, end0, starts0;  // table row (-1: none), end of its tokens in the chunk, and whether it begins with the chunk
+  int v1, lo1;            // table row (-1: none) and the first of its tokens
+};
+
+// The runs that begin or end with sorted token i, and, in the first lane of
+// each chunk, the chunk. A lane per token; `key` may lie in any memory.
+static_assert(kChunk == 32, "half a wave's lanes are a chunk's tokens");
+__device__ __forceinline__ void segment(const uint32_t *key, int n, int vocab, long long i, Run *seg, Chunk *chunks) {
+  const bool in = i < n;
+  const uint32_t k = in ? key[i] : 0;
+  const bool head = in && (i == 0 || key[i - 1] != k);
+  const bool tail = in && (i == n - 1 || key[i + 1] != k);
+  if (head && k < (uint32_t)vocab) seg[k].start = (int)i;
+  if (tail && k < (uint32_t)vocab) seg[k].end = (int)i + 1;
+  const int half = threadIdx.x & 32;
+  const uint32_t heads = (uint32_t)(__ballot(head) >> half), tails = (uint32_t)(__ballot(tail) >> half);
+  if (!in || (threadIdx.x & 31)) return;
+  const int a = (int)i, b = a + kChunk < n ? a + kChunk : n;
+  Chunk c;
+  c.starts0 = (int)(heads & 1);
+  // the row the chunk opens with either goes on behind it, which takes more than kChunk tokens, or ends here, and is
+  // long if the token kChunk before its last is its own
+  c.end0 = tails ? a + __ffs((int)tails) : b;
+  const bool long0 = !tails || (c.end0 > kChunk && key[c.end0 - 1 - kChunk] == k);
+  c.v0 = k < (uint32_t)vocab && long0 ? (int)k : -1;
+  c.v1 = -1;
+  c.lo1 = 0;
+  const uint32_t later = heads & ~1u;
+  if (later) {
+    const int lo = a + 31 - __clz((int)later);  // the row the chunk closes with
+    const uint32_t k1 = key[lo];
+    c.lo1 = lo;
+    if (k1 < (uint32_t)vocab && lo + kChunk < n && key[lo + kChunk] == k1) c.v1 = (int)k1;
+  }
+  chunks[a / kChunk] = c;
+}
+
+__global__ __launch_bounds__(256) void k_segments(const uint32_t *key, int n, int vocab, Run *seg, Chunk *chunks) {
+  segment(key, n, vocab, (long long)blockIdx.x * 256 + threadIdx.x, seg, chunks);
+}
+
+// The whole sort of up to kSmall tokens, and their segments, in one workgroup:
+// five launches less, which is what a short batch's sort would cost. CLEAR: it
+// also clears seg, of a table that one workgroup clears sooner than a launch.
+template <bool CLEAR>
+__global__ __launch_bounds__(kSmallThreads) void k_sort_small(SortArgs S, int passes, int digit, Chunk *chunks) {
+  constexpr int kWaves = kSmallThreads / 64;
+  __shared__ uint32_t skey[kSmall], spos[kSmall];
+  __shared__ uint32_t next[kWaves][1 << kMaxDigit];
+  __shared__ uint32_t wsum[kWaves];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = S.ids.n;
+  if (CLEAR) clear_runs(S.seg, S.vocab, threadIdx.x, kSmallThreads);
+  const int run = (n + kWaves * 64 - 1) / (kWaves * 64) * 64, lo = wave * run;  // of a wave: up to kRounds steps
+  uint32_t key[kRounds], pos[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int i = lo + r * 64 + lane;
+    key[r] = r * 64 < run && i < n ? S.key(i) : 0;
+    pos[r] = (uint32_t)i;
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * digit;
+    for (int i = threadIdx.x; i < kWaves * S.bins; i += kSmallThreads) next[i / S.bins][i % S.bins] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+      if (r * 64 < run && lo + r * 64 + lane < n) atomicAdd(&next[wave][(key[r] >> shift) & (S.bins - 1)], 1u);
+    __syncthreads();
+    // exclusive sum over (digit, wave): a digit per thread
+    const int b = threadIdx.x;
+    uint32_t total = 0;
+    if (b < S.bins)
+      for (int w = 0; w < kWaves; ++w) total += next[w][b];
+    uint32_t inc = total;
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t up = __shfl_up(inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (lane == 63) wsum[wave] = inc;
+    __syncthreads();
+    uint32_t at = inc - total;
+    for (int w = 0; w < wave; ++w) at += wsum[w];
+    if (b < S.bins) {
+      for (int w = 0; w < kWaves; ++w) {
+        const uint32_t c = next[w][b];
+        next[w][b] = at;
+        at += c;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      if (r * 64 >= run) break;
+      const bool in = lo + r * 64 + lane < n;
+      const uint32_t to = place_of(next[wave], (int)((key[r] >> shift) & (S.bins - 1)), S.bins, in);
+      if (in) {
+        skey[to] = key[r];
+        spos[to] = pos[r];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int i = lo + r * 64 + lane;
+      if (r * 64 < run && i < n) {
+        key[r] = skey[i];
+        pos[r] = spos[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    if (r * 64 >= run) break;
+    const int i = lo + r * 64 + lane;
+    if (i < n) {
+      S.key_out[i] = key[r];
+      S.pos_out[i] = pos[r];
+    }
+    segment(skey, n, S.vocab, i, S.seg, chunks);
+  }
 }
 
 // ---- sums ----
@@ -208,14 +375,16 @@ struct SumArgs {
   void *dE;
   const uint32_t *key, *pos;  // sorted
   const Run *seg;
+  const Chunk *chunks;
   float *part;  // [chunks][2][d]
   int n, vocab, d, accumulate;
+  int nchunks;  // 0 where no row can be long
   float scale;
 };
 
 // The scaled sum of eight columns into the table's gradient. `first`: a
 // thread at the end of a ragged row owns its columns from there on only.
-template <typename G>
+template <bool STREAM, typename G>
 __device__ __forceinline__ void put(G *p, int first, int accumulate, float scale, float (&s)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) s[j] *= scale;
@@ -235,102 +404,94 @@ __device__ __forceinline__ void put(G *p, int first, int accumulate, float scale
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] += old[j];
   }
-  store_w(p, true, s);
+  if (STREAM)
+    stream_w(p, true, s);
+  else
+    store_w(p, true, s);
 }
 
-// A table row's tokens, in order, into NV vectors of 8 columns per lane of a
-// wave. An item is a table row, or, when the sums are added to dE, a sorted
-// token, which counts if it is the first of its row. Rows of more than kChunk
-// tokens are left to k_long.
-template <typename D, typename G, int NV, bool R>
-__device__ __forceinline__ void row_item(const SumArgs &S, long long item, int part) {
-  const int lane = threadIdx.x & 63, d = S.d;
-  const int c0 = part * (NV * 512) + lane * 8;
-  long long v = item;
-  if (S.accumulate) {
-    v = S.key[item];
-    if (v >= S.vocab || (item > 0 && S.key[item - 1] == (uint32_t)v)) return;
-  }
-  const Run g = S.seg[v];
-  if (g.end - g.start > kChunk) return;
-  float acc[NV][8];
-  int at[NV], first[NV];
+// Adds eight columns of the sorted tokens lo .. hi-1, in order; the loads of
+// eight tokens run at once.
+template <typename D, bool HALVES>
+__device__ __forceinline__ void add_rows(const SumArgs &S, int c, int lo, int hi, float (&acc)[8]) {
+  const D *dx = reinterpret_cast<const D *>(S.dx) + c;
+  for (int t = lo; t < hi; t += 8) {
+    Raw8<D> r[8];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = c0 + k * 512;
-    at[k] = R && c + 8 > d ? d - 8 : c;
-    first[k] = c >= d ? 8 : c - at[k];  // 8: no columns here
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[k][j] = 0.f;
-  }
-  for (int i = g.start; i < g.end; ++i) {
-    const D *row = reinterpret_cast<const D *>(S.dx) + (long long)S.pos[i] * d;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      float t[8];
-      load_w(row + at[k], first[k] < 8, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[k][j] += t[j];
+    for (int k = 0; k < 8; ++k) {
+      const bool on = t + k < hi;
+      const D *q = dx + (long long)S.pos[on ? t + k : lo] * S.d;
+      r[k] = HALVES ? load_halves(q, S.d / 2, on) : load_raw(q, on);
     }
-  }
-  G *out = reinterpret_cast<G *>(S.dE) + v * d;
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-    if (first[k] < 8) put(out + at[k], R ? first[k] : 0, S.accumulate, S.scale, acc[k]);
-}
-
-// one wave per (item, part of the columns)
-template <typename D, typename G, int NV, bool R>
-__global__ __launch_bounds__(256) void k_rows(SumArgs S, long long items, int parts) {
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  for (long long i = w; i < items * parts; i += (long long)gridDim.x * 4)
-    row_item<D, G, NV, R>(S, i / parts, (int)(i % parts));
-}
-
-// The long rows with tokens in a chunk: the one the chunk opens with (which may
-// have begun earlier), and the one it closes with if that is another. A long
-// row cannot lie inside a chunk, so there are no others.
-struct ChunkRows {
-  int v[2], lo[2], hi[2];  // table row (-1: none) and its sorted tokens in this chunk
-  Run seg[2];
-  __device__ __forceinline__ ChunkRows(const SumArgs &S, int chunk) {
-    const int a = chunk * kChunk, b = a + kChunk < S.n ? a + kChunk : S.n;
-    const uint32_t k0 = S.key[a], k1 = S.key[b - 1];
-    take(S, 0, k0, a, b);
-    v[1] = -1;
-    if (k1 != k0) take(S, 1, k1, a, b);
-  }
-  __device__ __forceinline__ void take(const SumArgs &S, int i, uint32_t k, int a, int b) {
-    v[i] = -1;
-    if (k >= (uint32_t)S.vocab) return;
-    seg[i] = S.seg[k];
-    if (seg[i].end - seg[i].start <= kChunk) return;
-    v[i] = (int)k;
-    lo[i] = seg[i].start > a ? seg[i].start : a;
-    hi[i] = seg[i].end < b ? seg[i].end : b;
-  }
-};
-
-// part[chunk][i]: the sum of a long row's tokens in this chunk
-template <typename D, bool R>
-__global__ __launch_bounds__(256) void k_long(SumArgs S) {
-  const ChunkRows r(S, blockIdx.x);
-  const int d = S.d;
-  const int c = (blockIdx.y * 256 + threadIdx.x) * 8;
-  if (c >= d) return;
-  const int at = R && c + 8 > d ? d - 8 : c;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (r.v[i] < 0) continue;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int t = r.lo[i]; t < r.hi[i]; ++t) {
+    for (int k = 0; k < 8; ++k) {
       float v[8];
-      load_w(reinterpret_cast<const D *>(S.dx) + (long long)S.pos[t] * d + at, true, v);
+      expand(r[k], v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += v[j];
     }
-    store_w(S.part + ((long long)blockIdx.x * 2 + i) * d + at, true, acc);
+  }
+}
+
+// Items: first the chunks, whose long rows' sums go to part[chunk][0 or 1];
+// then the table rows, or, when the sums are added to dE, the sorted tokens,
+// which count if they are the first of their row. A table row's tokens are
+// summed in order; long rows are left to their chunks and k_join. A workgroup
+// takes an item (ONE: what it reads to find its tokens is the same for all
+// threads), or, of narrow rows, rpb items of tr threads.
+//
+// Most rows of a large table do not occur and only take zeros, so the launch is
+// bound by writing: 151936 fp32 rows of 2560 (1.56 GB) from 32768 bf16 tokens
+// take 325 us (5.3 TB/s; a fill alone takes 227). Two things matter. HALVES: a
+// thread has four columns of each half of an fp32 row, so that each store of a
+// wave covers whole cache lines (with eight in a row, written past the caches:
+// 620 us). And STREAM, as in the lookup (400 us without). Several rows per
+// workgroup, side by side or apart, gain nothing.
+template <typename D, typename G, bool R, bool ONE, bool STREAM, bool HALVES>
+__global__ __launch_bounds__(1024) void k_sums(SumArgs S, long long items, int tr, int rpb) {
+  const int sub = ONE ? 0 : threadIdx.x / tr, d = S.d;
+  const int t0 = ONE ? threadIdx.x : threadIdx.x % tr;
+  const long long g = group_index() * rpb + sub;
+  if (g < S.nchunks) {
+    const Chunk k = S.chunks[g];
+    for (int c8 = t0; c8 * 8 < d; c8 += tr) {
+      const int at = R && c8 * 8 + 8 > d ? d - 8 : c8 * 8;
+      if (k.v0 >= 0) {
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        add_rows<D, false>(S, at, (int)g * kChunk, k.end0, acc);
+        store_w(S.part + g * 2 * d + at, true, acc);
+      }
+      if (k.v1 >= 0) {
+        const int b = ((int)g + 1) * kChunk;
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        add_rows<D, false>(S, at, k.lo1, b < S.n ? b : S.n, acc);
+        store_w(S.part + (g * 2 + 1) * d + at, true, acc);
+      }
+    }
+    return;
+  }
+  long long v = g - S.nchunks;
+  if (v >= items) return;
+  if (S.accumulate) {
+    const long long i = v;
+    v = S.key[i];
+    if (v >= S.vocab || (i > 0 && S.key[i - 1] == (uint32_t)v)) return;
+  }
+  const Run run = S.seg[v];
+  if (run.end - run.start > kChunk) return;
+  G *out = reinterpret_cast<G *>(S.dE) + v * d;
+  for (int c8 = t0; c8 * 8 < d; c8 += tr) {
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (HALVES) {
+      add_rows<D, true>(S, c8 * 4, run.start, run.end, acc);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] *= S.scale;
+      store_halves<STREAM>(out + c8 * 4, d / 2, acc);
+    } else {
+      const int at = R && c8 * 8 + 8 > d ? d - 8 : c8 * 8;
+      add_rows<D, false>(S, at, run.start, run.end, acc);
+      put<STREAM>(out + at, R ? c8 * 8 - at : 0, S.accumulate, S.scale, acc);
+    }
   }
 }
 
@@ -341,28 +502,24 @@ constexpr int kJoinWaves = 8;
 template <typename G, bool R>
 __global__ __launch_bounds__(kJoinWaves * 64) void k_join(SumArgs S) {
   __shared__ float sum[kJoinWaves][64][9];
-  const ChunkRows r(S, blockIdx.x);
-  const int a = blockIdx.x * kChunk, d = S.d;
-  int i = -1;
-  if (r.v[1] >= 0)
-    i = 1;
-  else if (r.v[0] >= 0 && r.seg[0].start >= a)
-    i = 0;
-  if (i < 0) return;
+  const Chunk k = S.chunks[blockIdx.x];
+  const int d = S.d, i = k.v1 >= 0 ? 1 : 0;
+  const int v = i ? k.v1 : k.starts0 ? k.v0 : -1;
+  if (v < 0) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int c = (blockIdx.y * 64 + lane) * 8;
   const int at = R && c + 8 > d ? d - 8 : c;
-  const int last = (r.seg[i].end - 1) / kChunk;  // pieces: (blockIdx.x, i), then (j, 0) up to the last chunk
+  const int last = (S.seg[v].end - 1) / kChunk;  // pieces: (blockIdx.x, i), then (j, 0) up to the last chunk
   const int pieces = last - (int)blockIdx.x + 1, run = (pieces + kJoinWaves - 1) / kJoinWaves;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (c < d) {
     const int p0 = wave * run, p1 = p0 + run < pieces ? p0 + run : pieces;
 #pragma unroll 8
     for (int p = p0; p < p1; ++p) {
-      float v[8];
-      load_w(S.part + (((long long)blockIdx.x + p) * 2 + (p == 0 ? i : 0)) * d + at, true, v);
+      float x[8];
+      load_w(S.part + (((long long)blockIdx.x + p) * 2 + (p == 0 ? i : 0)) * d + at, true, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += v[j];
+      for (int j = 0; j < 8; ++j) acc[j] += x[j];
     }
   }
 #pragma unroll
@@ -373,10 +530,22 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_join(SumArgs S) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] += sum[w][lane][j];
   }
-  put(reinterpret_cast<G *>(S.dE) + (long long)r.v[i] * d + at, R ? c - at : 0, S.accumulate, S.scale, acc);
+  put<false>(reinterpret_cast<G *>(S.dE) + (long long)v * d + at, R ? c - at : 0, S.accumulate, S.scale, acc);
 }
 
 // ---- which instance ----
+
+// threads of a row of d, and rows of a workgroup
+struct RowThreads {
+  int tr, rpb;
+};
+RowThreads row_threads(int d) {
+  const int v = (d + 7) / 8;
+  int tr = 8;
+  while (tr < v && tr < 64) tr *= 2;
+  if (v > 64) tr = v >= 1024 ? 1024 : (v + 63) / 64 * 64;
+  return {tr, tr <= 64 ? 256 / tr : 1};
+}
 
 template <typename E, typename X, bool R, bool ONE>
 void embed_form(const EmbedArgs &a, dim3 grid, int tr, int rpb, hipStream_t s) {
@@ -389,11 +558,7 @@ void embed_form(const EmbedArgs &a, dim3 grid, int tr, int rpb, hipStream_t s) {
 
 template <typename E, typename X>
 hipError_t embed(const EmbedArgs &a, hipStream_t s) {
-  const int v = (a.d + 7) / 8;
-  int tr = 8;
-  while (tr < v && tr < 64) tr *= 2;
-  if (v > 64) tr = v >= 1024 ? 1024 : (v + 63) / 64 * 64;
-  const int rpb = tr <= 64 ? 256 / tr : 1;
+  const auto [tr, rpb] = row_threads(a.d);
   const dim3 grid = group_grid((a.ids.n + rpb - 1LL) / rpb);
   if (rpb > 1)
     a.d % 8 ? embed_form<E, X, true, false>(a, grid, tr, rpb, s) : embed_form<E, X, false, false>(a, grid, tr, rpb, s);
@@ -402,49 +567,39 @@ hipError_t embed(const EmbedArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename D, typename G, int NV>
-void rows_nv(const SumArgs &S, long long items, int parts, hipStream_t s) {
-  const long long groups = (items * parts + 3) / 4;
-  const dim3 grid((unsigned)(groups < kMaxGroups ? groups : kMaxGroups));
-  if (S.d % 8)
-    hipLaunchKernelGGL((k_rows<D, G, NV, true>), grid, dim3(256), 0, s, S, items, parts);
+template <typename D, typename G, bool R, bool ONE>
+void sums_form(const SumArgs &S, int tr, int rpb, hipStream_t s) {
+  const long long items = S.accumulate ? (long long)S.n : S.vocab;
+  const dim3 grid = group_grid((S.nchunks + items + rpb - 1) / rpb), block(tr * rpb);
+  constexpr bool halves = !R && sizeof(G) == 4;
+  if (!R && !S.accumulate && (double)S.vocab * S.d * sizeof(G) > kStreamBytes)
+    hipLaunchKernelGGL((k_sums<D, G, R, ONE, !R, halves>), grid, block, 0, s, S, items, tr, rpb);
+  else if (halves && !S.accumulate)
+    hipLaunchKernelGGL((k_sums<D, G, R, ONE, false, halves>), grid, block, 0, s, S, items, tr, rpb);
   else
-    hipLaunchKernelGGL((k_rows<D, G, NV, false>), grid, dim3(256), 0, s, S, items, parts);
+    hipLaunchKernelGGL((k_sums<D, G, R, ONE, false, false>), grid, block, 0, s, S, items, tr, rpb);
 }
 
 template <typename D, typename G>
 hipError_t sums(const SumArgs &S, hipStream_t s) {
-  const int v = (S.d + 7) / 8;
-  const int parts = (v + 319) / 320;  // of a row, over at most five vectors of 8 columns per lane
-  const int nv = (v + 64 * parts - 1) / (64 * parts);
-  const long long items = S.accumulate ? S.n : S.vocab;
-  if (items > 0) {
-    switch (nv) {
-      case 1: rows_nv<D, G, 1>(S, items, parts, s); break;
-      case 2: rows_nv<D, G, 2>(S, items, parts, s); break;
-      case 3: rows_nv<D, G, 3>(S, items, parts, s); break;
-      case 4: rows_nv<D, G, 4>(S, items, parts, s); break;
-      default: rows_nv<D, G, 5>(S, items, parts, s); break;
-    }
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (S.n <= kChunk) return hipSuccess;  // no row can be long
-  const unsigned chunks = (unsigned)((S.n + kChunk - 1) / kChunk);
-  const dim3 g1(chunks, (unsigned)((v + 255) / 256)), g2(chunks, (unsigned)((v + 63) / 64));
-  if (S.d % 8) {
-    hipLaunchKernelGGL((k_long<D, true>), g1, dim3(256), 0, s, S);
-    hipLaunchKernelGGL((k_join<G, true>), g2, dim3(kJoinWaves * 64), 0, s, S);
-  } else {
-    hipLaunchKernelGGL((k_long<D, false>), g1, dim3(256), 0, s, S);
-    hipLaunchKernelGGL((k_join<G, false>), g2, dim3(kJoinWaves * 64), 0, s, S);
-  }
+  const RowThreads m = row_threads(S.d);
+  if (m.rpb > 1)
+    S.d % 8 ? sums_form<D, G, true, false>(S, m.tr, m.rpb, s) : sums_form<D, G, false, false>(S, m.tr, m.rpb, s);
+  else
+    S.d % 8 ? sums_form<D, G, true, true>(S, m.tr, m.rpb, s) : sums_form<D, G, false, true>(S, m.tr, m.rpb, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !S.nchunks) return e;
+  const dim3 grid((unsigned)S.nchunks, (unsigned)((S.d + 511) / 512));
+  if (S.d % 8)
+    hipLaunchKernelGGL((k_join<G, true>), grid, dim3(kJoinWaves * 64), 0, s, S);
+  else
+    hipLaunchKernelGGL((k_join<G, false>), grid, dim3(kJoinWaves * 64), 0, s, S);
   return hipGetLastError();
 }
 
 // The workspace of a gradient call, by offset.
 struct GradWs {
-  size_t key[2], pos[2], hist, seg, part, total;
+  size_t key[2], pos[2], hist, seg, chunks, part, total;
 };
 
 GradWs grad_ws(long long n, int vocab, int d) {
@@ -461,7 +616,9 @@ GradWs grad_ws(long long n, int vocab, int d) {
   }
   take(w.hist, ((size_t)p.tiles << p.digit) * 4);
   take(w.seg, (size_t)vocab * sizeof(Run));
-  take(w.part, n > kChunk ? (size_t)((n + kChunk - 1) / kChunk) * 2 * d * 4 : 0);
+  const size_t chunks = (size_t)((n + kChunk - 1) / kChunk);
+  take(w.chunks, chunks * sizeof(Chunk));
+  take(w.part, n > kChunk ? chunks * 2 * d * 4 : 0);
   w.total = off;
   return w;
 }
@@ -490,7 +647,20 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, int dx_f32, int dE_f32, hip
   S.tiles = p.tiles;
   S.hist = (uint32_t *)(ws + w.hist);
   S.seg = (Run *)(ws + w.seg);
-  for (int k = 0; k < p.passes; ++k) {
+  const bool small = n > 0 && n <= kSmall;
+  if (small) {
+    S.key_out = (uint32_t *)(ws + w.key[0]);
+    S.pos_out = (uint32_t *)(ws + w.pos[0]);
+    Chunk *chunks = (Chunk *)(ws + w.chunks);
+    if (a.vocab <= kSmallClear) {
+      hipLaunchKernelGGL(k_sort_small<true>, dim3(1), dim3(kSmallThreads), 0, s, S, p.passes, p.digit, chunks);
+    } else {
+      const int clear = (a.vocab + kClearPerGroup - 1) / kClearPerGroup;
+      hipLaunchKernelGGL(k_clear_runs, dim3(clear < kMaxTiles ? clear : kMaxTiles), dim3(256), 0, s, S.seg, a.vocab);
+      hipLaunchKernelGGL(k_sort_small<false>, dim3(1), dim3(kSmallThreads), 0, s, S, p.passes, p.digit, chunks);
+    }
+  }
+  for (int k = 0; k < p.passes && !small; ++k) {
     S.shift = k * p.digit;
     S.key_in = k ? (const uint32_t *)(ws + w.key[(k - 1) & 1]) : nullptr;
     S.pos_in = k ? (const uint32_t *)(ws + w.pos[(k - 1) & 1]) : nullptr;
@@ -502,7 +672,10 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, int dx_f32, int dE_f32, hip
     if (k == 0 && clear > grid) grid = clear < kMaxTiles ? clear : kMaxTiles > grid ? kMaxTiles : grid;
     hipLaunchKernelGGL(k_sort_count, dim3(grid), dim3(kSortThreads), 0, s, S);
     if (!p.tiles) break;
-    hipLaunchKernelGGL(k_sort_place, dim3(p.tiles), dim3(kSortThreads), 0, s, S);
+    if (p.tile == kMinTile)
+      hipLaunchKernelGGL(k_sort_place<true>, dim3(p.tiles), dim3(kSortThreads), 0, s, S);
+    else
+      hipLaunchKernelGGL(k_sort_place<false>, dim3(p.tiles), dim3(kSortThreads), 0, s, S);
   }
   SumArgs G{};
   G.dx = a.dx;
@@ -510,14 +683,17 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, int dx_f32, int dE_f32, hip
   G.key = S.key_out;
   G.pos = S.pos_out;
   G.seg = S.seg;
+  G.chunks = (const Chunk *)(ws + w.chunks);
+  G.nchunks = n > kChunk ? (n + kChunk - 1) / kChunk : 0;
   G.part = (float *)(ws + w.part);
   G.n = n;
   G.vocab = a.vocab;
   G.d = a.d;
   G.accumulate = a.accumulate;
   G.scale = a.scale;
-  if (n > 0)
-    hipLaunchKernelGGL(k_segments, dim3((unsigned)((n + 255LL) / 256)), dim3(256), 0, s, G.key, n, a.vocab, S.seg);
+  if (n > 0 && !small)
+    hipLaunchKernelGGL(k_segments, dim3((unsigned)((n + 255LL) / 256)), dim3(256), 0, s, G.key, n, a.vocab, S.seg,
+                       (Chunk *)(ws + w.chunks));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (dx_f32) return dE_f32 ? sums<float, float>(G, s) : sums<float, bf16_t>(G, s);

@@ -101,6 +101,50 @@ inline dim3 group_grid(long long groups) {
 }
 __device__ __forceinline__ long long group_index() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
 
+// Eight columns of a row as two runs of four, at p and `gap` elements behind
+// (half a row): the fp32 runs of neighbouring threads then lie side by side,
+// and each access of a wave covers whole cache lines.
+__device__ __forceinline__ Raw8<bf16_t> load_halves(const bf16_t *p, int gap, bool on) {
+  Raw8<bf16_t> r = {};
+  if (on) {
+    __builtin_memcpy(r.u, p, 8);
+    __builtin_memcpy(r.u + 2, p + gap, 8);
+  }
+  return r;
+}
+__device__ __forceinline__ Raw8<float> load_halves(const float *p, int gap, bool on) {
+  Raw8<float> r = {};
+  if (on) {
+    __builtin_memcpy(r.f, p, 16);
+    __builtin_memcpy(r.f + 4, p + gap, 16);
+  }
+  return r;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_halves(float *p, int gap, const float (&v)[8]) {
+  const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+  typedef f32x4 __attribute__((aligned(4))) any;
+  if (STREAM) {
+    __builtin_nontemporal_store(a, reinterpret_cast<any *>(p));
+    __builtin_nontemporal_store(b, reinterpret_cast<any *>(p + gap));
+  } else {
+    *reinterpret_cast<any *>(p) = a;
+    *reinterpret_cast<any *>(p + gap) = b;
+  }
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_halves(bf16_t *p, int gap, const float (&v)[8]) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
+  const u2 a = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, b = {pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  if (STREAM) {
+    __builtin_nontemporal_store(a, reinterpret_cast<u2 *>(p));
+    __builtin_nontemporal_store(b, reinterpret_cast<u2 *>(p + gap));
+  } else {
+    *reinterpret_cast<u2 *>(p) = a;
+    *reinterpret_cast<u2 *>(p + gap) = b;
+  }
+}
+
 // The same of a parameter that is fp32 or bf16 as the caller has it (a branch
 // all threads take alike); a NULL parameter reads as ones.
 template <int W>

@@ -393,9 +393,9 @@ int ttt_norm_post_grad(const void *dh_in, const void *dx, ttt_dtype x_dt, const 
  *   scale : finite.
  *
  * The gradient sorts the tokens by id and sums each row's in the order of
- * their positions, a long row's in pieces of 64: the same call gives the same
+ * their positions, a long row's in pieces of 32: the same call gives the same
  * bits. ws: see ttt_embed_grad_ws_bytes (about 16 bytes per token, 8 per table
- * row and d / 8 bytes per token for the pieces).
+ * row and d / 4 bytes per token for the pieces).
  */
 int ttt_embed(const void *E, ttt_dtype E_dt, int vocab, int d, const int32_t *ids, int64_t ids_ld, int B, int T,
               float scale, void *x, ttt_dtype x_dt, void *hip_stream);

@@ -2,8 +2,8 @@
 
 Bounds. The lookup is one product in fp32 and one rounding: u + half a step of
 the type. The gradient of a table row sums its c tokens in fp32, the longest
-way through a piece of 64, then a run of an eighth of the pieces, then eight
-sums: at most 63 + ceil(c / 64 / 8) + 1 + 8 additions, then the scale and, when
+way through a piece of 32, then a run of an eighth of the pieces, then eight
+sums: at most 31 + ceil(c / 32 / 8) + 1 + 8 additions, then the scale and, when
 accumulating, one more addition.
 """
 import pytest
@@ -37,7 +37,8 @@ CASES = [  # B, T, vocab, d, kind
     (1, 1, 1, 8, "uniform"), (3, 5, 7, 9, "holes"), (2, 64, 513, 64, "same"), (1, 65, 100, 72, "same"),
     (2, 1000, 50, 100, "skewed"), (3, 411, 512, 1024, "skewed"), (1, 4000, 3, 257, "uniform"),
     (4, 1025, 70001, 40, "skewed"), (1, 2049, 151936, 8, "uniform"), (5, 300, 1000, 2568, "holes"),
-    (1, 130, 9, 8200, "skewed"), (2, 33, 20, 20011, "uniform"), (1, 9000, 40, 16, "same"), (7, 3, 12, 2560, "uniform"),
+    (1, 32, 3, 64, "same"), (1, 33, 3, 64, "same"), (1, 96, 2, 64, "uniform"), (1, 4096, 20000, 24, "skewed"),
+    (1, 4097, 20000, 24, "skewed"), (3, 100001, 1000, 16, "skewed"), (1, 130, 9, 8200, "skewed"), (2, 33, 20, 20011, "uniform"), (1, 9000, 40, 16, "same"), (7, 3, 12, 2560, "uniform"),
 ]
 
 
@@ -78,7 +79,7 @@ def test_embed_grad(B, T, vocab, d, kind, tx, tE):
     ref = torch.zeros(vocab, d, dtype=torch.float64).index_add_(0, at, rows[known]) * scale
     mag = torch.zeros(vocab, d, dtype=torch.float64).index_add_(0, at, rows[known].abs()) * scale
     count = torch.bincount(at, minlength=vocab).double()
-    adds = torch.minimum(count, 64 + torch.ceil(count / 512) + 9)[:, None] + 2
+    adds = torch.minimum(count, 31 + torch.ceil(count / 256) + 9)[:, None] + 2
     bound = adds * U32 * mag
     dx_dev = dx.cuda()
     # rows of dx whose id is no row of the table are not read
