@@ -632,9 +632,13 @@ class _Many:
         self.n = len(grads)
         self.sizes = array("q", map(torch.Tensor.numel, grads))
         self.dtypes = list(map(self._dtype, grads))
-        if not _DT.keys() >= set(self.dtypes):
+        found = set(self.dtypes)
+        if not _DT.keys() >= found:
             raise ValueError("grads must be float32 or bfloat16")
-        kinds = array("i", map(_DT.__getitem__, self.dtypes))
+        if len(found) == 1:
+            kinds = array("i", [_DT[found.pop()]]) * self.n
+        else:
+            kinds = array("i", map(_DT.__getitem__, self.dtypes))
         self._keep = (self._addresses(c, grads, "grads"), self.sizes, kinds)
         self.args = tuple(a.buffer_info()[0] for a in self._keep) + (self.n,)
 

@@ -112,9 +112,12 @@ size_t ids_bytes(int B, int T, int64_t ids_ld) {
 // ---- many tensors ----
 
 constexpr int kMaxTensors = 1 << 20;
-constexpr long long kMaxNumel = 1LL << 40;  // of all tensors: their chunks of 32768 count in 32 bits
+constexpr long long kMaxNumel = 1LL << 40;  // of all tensors: their chunks count in 32 bits
+// gradients of more bytes than this are read and written past the caches, of which the last level holds 256 MiB
+constexpr long long kStreamGrads = 512LL << 20;
 
-size_t grad_ws(int n) { return ((size_t)kGradGroups + n / kGradTable + 1) * sizeof(double); }
+// the workgroups' sums and, before them, the factor
+size_t grad_ws(int n) { return ((size_t)kGradGroups + n / kGradTable + 2) * sizeof(double); }
 
 int check_grads(const char *where, const void *const *grads, const int64_t *numel, const int32_t *dt, int n,
                 const float *norm, const void *ws, size_t ws_bytes) {
@@ -154,8 +157,7 @@ int check_extents(const char *where, std::vector<Extent> &e) {
 }
 
 // The tables of a call, empty tensors left out and tensors that follow one
-// another in memory (views of one buffer) taken as one. Chunks are as small as
-// gives every workgroup of the norm one, between 2048 and 32768 elements.
+// another in memory (views of one buffer) taken as one.
 std::vector<GradTable> grad_tables(const void *const *grads, const int64_t *numel, const int32_t *dt, int n,
                                    void *const *out) {
   struct One {
@@ -166,12 +168,10 @@ std::vector<GradTable> grad_tables(const void *const *grads, const int64_t *nume
   };
   std::vector<One> all;
   all.reserve(n);
-  long long total = 0;
   for (int i = 0; i < n; ++i) {
     if (numel[i] == 0) continue;
     const int f32 = dt[i] == TTT_F32;
     const One x{(const char *)grads[i], out ? (char *)out[i] : (char *)grads[i], (long long)numel[i], f32};
-    total += x.n;
     if (!all.empty()) {
       One &p = all.back();
       const long long bytes = p.n * (p.f32 ? 4 : 2);
@@ -182,21 +182,18 @@ std::vector<GradTable> grad_tables(const void *const *grads, const int64_t *nume
     }
     all.push_back(x);
   }
-  long long chunk = (total / kGradGroups + 2047) / 2048 * 2048;
-  chunk = std::min(std::max(chunk, 2048LL), 32768LL);
   std::vector<GradTable> tables;
   for (size_t i = 0; i < all.size(); ++i) {
     if (tables.empty() || tables.back().n == kGradTable) {
       tables.emplace_back();
       tables.back().n = 0;
       tables.back().first[0] = 0;
-      tables.back().chunk = (uint32_t)chunk;
     }
     GradTable &t = tables.back();
-    const long long chunks = (all[i].n + chunk - 1) / chunk;
+    const long long chunks = (all[i].n + kGradChunk - 1) / kGradChunk;
     t.g[t.n] = all[i].g;
     t.out[t.n] = all[i].o;
-    t.tail[t.n] = (uint32_t)(all[i].n - (chunks - 1) * chunk);
+    t.tail[t.n] = (uint32_t)(all[i].n - (chunks - 1) * kGradChunk);
     t.f32[t.n] = (uint8_t)all[i].f32;
     t.first[t.n + 1] = t.first[t.n] + (uint32_t)chunks;
     ++t.n;
@@ -205,27 +202,31 @@ std::vector<GradTable> grad_tables(const void *const *grads, const int64_t *nume
 }
 
 // Norm of the tables and, with `clip`, the scaling by it.
-int run_grads(const char *where, const std::vector<GradTable> &tables, bool clip, float tau, float *norm, double *part,
+int run_grads(const char *where, const std::vector<GradTable> &tables, bool clip, float tau, float *norm, void *ws,
               hipStream_t s) {
-  long long chunks = 0;
-  for (const GradTable &t : tables) chunks += t.first[t.n];
-  // workgroups of a table: its share of kGradGroups
-  auto groups = [&](const GradTable &t) {
-    const long long c = t.first[t.n], most = std::max(1LL, kGradGroups * c / std::max(1LL, chunks));
-    return (int)std::min(c, most);
-  };
+  float *factor = (float *)ws;
+  double *part = (double *)ws + 1;
+  long long chunks = 0, bytes = 0;
+  for (const GradTable &t : tables) {
+    chunks += t.first[t.n];
+    for (int i = 0; i < t.n; ++i) bytes += (long long)(t.first[i + 1] - t.first[i]) * kGradChunk * (t.f32[i] ? 4 : 2);
+  }
+  const bool stream = bytes > kStreamGrads;
   int n = 0;
   for (const GradTable &t : tables) {
-    const int rc = ttt_launched(launch_grad_squares(t, part + n, groups(t), s), where);
+    // its share of kGradGroups
+    const long long c = t.first[t.n], most = std::max(1LL, kGradGroups * c / chunks);
+    const int groups = (int)std::min(c, most);
+    const int rc = ttt_launched(launch_grad_squares(t, part + n, groups, stream, s), where);
     if (rc) return rc;
-    n += groups(t);
+    n += groups;
   }
-  if (!clip || tables.empty()) return ttt_launched(launch_grad_norm(part, n, norm, s), where);
+  int rc = ttt_launched(launch_grad_norm(part, n, tau, norm, clip ? factor : nullptr, s), where);
   for (const GradTable &t : tables) {
-    const int rc = ttt_launched(launch_grad_scale(t, part, n, tau, &t == &tables[0] ? norm : nullptr, groups(t), s), where);
-    if (rc) return rc;
+    if (rc || !clip) break;
+    rc = ttt_launched(launch_grad_scale(t, factor, stream, s), where);
   }
-  return TTT_OK;
+  return rc;
 }
 
 }  // namespace
@@ -489,7 +490,7 @@ int ttt_grad_norm(const void *const *grads, const int64_t *numel, const int32_t 
     rc = check_extents(kWhere, e);
     if (!rc) rc = ttt_check_device();
     if (rc) return rc;
-    return run_grads(kWhere, grad_tables(grads, numel, dt, n, nullptr), false, 0.f, norm, (double *)ws,
+    return run_grads(kWhere, grad_tables(grads, numel, dt, n, nullptr), false, 0.f, norm, ws,
                      (hipStream_t)hip_stream);
   } catch (...) {
     return ttt_fail(TTT_E_NOMEM, "%s: out of host memory", kWhere);
@@ -518,8 +519,7 @@ int ttt_clip_grads(const void *const *grads, const int64_t *numel, const int32_t
     rc = check_extents(kWhere, e);
     if (!rc) rc = ttt_check_device();
     if (rc) return rc;
-    return run_grads(kWhere, grad_tables(grads, numel, dt, n, out), true, tau, norm, (double *)ws,
-                     (hipStream_t)hip_stream);
+    return run_grads(kWhere, grad_tables(grads, numel, dt, n, out), true, tau, norm, ws, (hipStream_t)hip_stream);
   } catch (...) {
     return ttt_fail(TTT_E_NOMEM, "%s: out of host memory", kWhere);
   }

@@ -3,11 +3,11 @@
 
 #include "common.h"
 
-// Up to kGradTable tensors, cut into chunks of `chunk` elements (the last one
-// of each tensor shorter). As a kernel argument it needs no device copy, so a
-// call reads nothing that could change or be freed behind it; 152 of them stay
-// within the 4 KiB that every launch may pass.
-constexpr int kGradTable = 152;
+// Up to kGradTable tensors, cut into chunks of kGradChunk elements (the last
+// one of each tensor shorter). As a kernel argument it needs no device copy, so
+// a call reads nothing that could change or be freed behind it; 152 of them
+// stay within the 4 KiB that every launch may pass.
+constexpr int kGradTable = 152, kGradChunk = 4096;
 struct GradTable {
   const void *g[kGradTable];
   void *out[kGradTable];
@@ -15,16 +15,14 @@ struct GradTable {
   uint32_t tail[kGradTable];       // elements of its last chunk
   uint8_t f32[kGradTable];
   int n;
-  uint32_t chunk;
 };
 
 // Workgroups of all norm launches of a call together (besides one per further table): one partial sum each.
 constexpr int kGradGroups = 2048;
 
-// part[blockIdx.x] = sum of squares of its chunks
-hipError_t launch_grad_squares(const GradTable &t, double *part, int groups, hipStream_t s);
-// *norm = sqrt(sum of part[0 .. n))
-hipError_t launch_grad_norm(const double *part, int n, float *norm, hipStream_t s);
-// out = g * min(1, tau / norm) (g as it is where the norm is not finite); norm (nullable) receives the norm
-hipError_t launch_grad_scale(const GradTable &t, const double *part, int n, float tau, float *norm, int groups,
-                             hipStream_t s);
+// part[blockIdx.x] = sum of squares of its chunks. stream: the gradients are more than the caches hold.
+hipError_t launch_grad_squares(const GradTable &t, double *part, int groups, bool stream, hipStream_t s);
+// *norm = sqrt(sum of part[0 .. n)); *factor (nullable) = min(1, tau / norm), 1 where the norm is not finite
+hipError_t launch_grad_norm(const double *part, int n, float tau, float *norm, float *factor, hipStream_t s);
+// out = g * *factor
+hipError_t launch_grad_scale(const GradTable &t, const float *factor, bool stream, hipStream_t s);

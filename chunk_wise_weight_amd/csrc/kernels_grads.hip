@@ -5,10 +5,10 @@
 // |g| > 1e19 or < 1e-19 (clipped updates of the layer are 1e-9 and less), and
 // the sums run over up to billions of terms. The conversions cost vector
 // instructions, not time: the kernels are bound by reading the gradients. Each
-// workgroup adds its chunks in a fixed order, and everyone who needs the norm
-// adds the workgroups' sums in a fixed order, so a call's bits do not change.
+// workgroup adds its chunks in a fixed order, and one workgroup adds the
+// workgroups' sums in a fixed order, so a call's bits do not change.
 #include "grads.h"
-#include "vec8.h"
+#include "grid.h"
 
 namespace {
 
@@ -19,19 +19,135 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// the sum over the workgroup, in every thread
-__device__ __forceinline__ double group_sum(double v, double *red) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
+// 16 bytes as they lie in memory, at any element: four fp32 or eight bf16.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <bool NT>
+__device__ __forceinline__ u32x4_any load16(const void *p) {
+  const u32x4_any *q = reinterpret_cast<const u32x4_any *>(p);
+  return NT ? __builtin_nontemporal_load(q) : *q;
+}
+template <bool NT>
+__device__ __forceinline__ void store16(void *p, u32x4_any v) {
+  u32x4_any *q = reinterpret_cast<u32x4_any *>(p);
+  if (NT)
+    __builtin_nontemporal_store(v, q);
+  else
+    *q = v;
+}
+
+__device__ __forceinline__ double square(float v) { return (double)v * (double)v; }
+__device__ __forceinline__ float lower(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float upper(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v); }
+
+template <typename T>
+__device__ __forceinline__ double squares16(u32x4_any v) {
   double s = 0.0;
-  for (int w = 0; w < kThreads / 64; ++w) s += red[w];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s += sizeof(T) == 4 ? square(__uint_as_float(v[j])) : square(lower(v[j])) + square(upper(v[j]));
+  return s;
+}
+template <typename T>
+__device__ __forceinline__ u32x4_any scaled16(u32x4_any v, float c) {
+  u32x4_any r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    r[j] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(v[j]) * c) : pack_bf16x2(lower(v[j]) * c, upper(v[j]) * c);
+  return r;
+}
+
+// 16-byte pieces of a full chunk per thread
+template <typename T>
+constexpr int kPieces = kGradChunk * sizeof(T) / 16 / kThreads;
+
+// the sum of squares of up to a chunk
+template <typename T, bool NT>
+__device__ __forceinline__ double chunk_squares(const T *p, int n) {
+  constexpr int E = 16 / sizeof(T), P = kPieces<T>;
+  double s = 0.0;
+  if (n == kGradChunk) {
+    u32x4_any v[P];
+#pragma unroll
+    for (int k = 0; k < P; ++k) v[k] = load16<NT>(p + (k * kThreads + threadIdx.x) * E);
+#pragma unroll
+    for (int k = 0; k < P; ++k) s += squares16<T>(v[k]);
+    return s;
+  }
+  for (int i = threadIdx.x * E; i + E <= n; i += kThreads * E) s += squares16<T>(load16<NT>(p + i));
+  if ((int)threadIdx.x < n % E) s += square(to_f32(p[n / E * E + threadIdx.x]));
   return s;
 }
 
-// the tensor that chunk c belongs to
-__device__ __forceinline__ int tensor_of(const GradTable &t, uint32_t c) {
-  int lo = 0, hi = t.n - 1;
+__device__ __forceinline__ void put1(float *q, float v) { *q = v; }
+__device__ __forceinline__ void put1(bf16_t *q, float v) { *q = f32_to_bf16(v); }
+
+template <typename T, bool NT>
+__device__ __forceinline__ void chunk_scale(const T *p, T *q, int n, float c) {
+  constexpr int E = 16 / sizeof(T), P = kPieces<T>;
+  if (n == kGradChunk) {
+    u32x4_any v[P];
+#pragma unroll
+    for (int k = 0; k < P; ++k) v[k] = load16<NT>(p + (k * kThreads + threadIdx.x) * E);
+#pragma unroll
+    for (int k = 0; k < P; ++k) store16<NT>(q + (k * kThreads + threadIdx.x) * E, scaled16<T>(v[k], c));
+    return;
+  }
+  for (int i = threadIdx.x * E; i + E <= n; i += kThreads * E) store16<NT>(q + i, scaled16<T>(load16<NT>(p + i), c));
+  if ((int)threadIdx.x < n % E) put1(q + n / E * E + threadIdx.x, to_f32(p[n / E * E + threadIdx.x]) * c);
+}
+
+// part[blockIdx.x]: the sum of squares of chunks blockIdx.x, + gridDim.x, ...
+// 539M fp32 values (2.16 GB) take 315 us, 6.9 TB/s, which is what reading alone
+// reaches here (425 us in chunks of 128 KiB and through the caches).
+template <bool NT>
+__global__ __launch_bounds__(kThreads) void k_squares(GradTable t, double *part) {
+  __shared__ double red[kThreads / 64];
+  double s = 0.0;
+  int i = 0;  // the chunk's tensor: chunks only go up
+  for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
+    while (c >= t.first[i + 1]) ++i;
+    const int n = c + 1 == t.first[i + 1] ? (int)t.tail[i] : kGradChunk;
+    const long long at = (long long)(c - t.first[i]) * kGradChunk;
+    s += t.f32[i] ? chunk_squares<float, NT>(reinterpret_cast<const float *>(t.g[i]) + at, n)
+                  : chunk_squares<bf16_t, NT>(reinterpret_cast<const bf16_t *>(t.g[i]) + at, n);
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < kThreads / 64; ++w) s += red[w];
+  part[blockIdx.x] = s;
+}
+
+// The norm from the workgroups' sums, and the factor min(1, tau / norm): 1
+// where the norm is not finite.
+__global__ __launch_bounds__(1024) void k_norm(const double *part, int n, float tau, float *norm, float *factor) {
+  __shared__ double red[16];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += 1024) s += part[i];
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 16; ++w) s += red[w];
+  const double v = sqrt(s);
+  *norm = (float)v;
+  if (factor) *factor = v > (double)tau && v <= 1.7e308 ? (float)((double)tau / v) : 1.f;
+}
+
+// A workgroup per chunk: ones that stay and stride over the chunks take 850 us
+// where these take 700 (539M fp32 values, 4.3 GB: 6.2 TB/s; a copy reaches
+// 6.6), since a wave's loads would wait behind its own stores. Through the
+// caches 760. Taking the chunks in the opposite order, to find the last ones
+// read still cached, gains nothing at any size.
+template <bool NT>
+__global__ __launch_bounds__(kThreads) void k_scale(GradTable t, const float *factor) {
+  const long long g = group_index();
+  if (g >= t.first[t.n]) return;
+  const uint32_t c = (uint32_t)g;
+  int lo = 0, hi = t.n - 1;  // the tensor of the chunk
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
     if (t.first[mid] <= c)
@@ -39,104 +155,36 @@ __device__ __forceinline__ int tensor_of(const GradTable &t, uint32_t c) {
     else
       hi = mid - 1;
   }
-  return lo;
-}
-
-template <typename T>
-__device__ __forceinline__ double squares(const T *p, uint32_t n) {
-  double s = 0.0;
-#pragma unroll 4
-  for (uint32_t i = threadIdx.x * 8; i + 8 <= n; i += kThreads * 8) {
-    float v[8];
-    load_w(p + i, true, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s += (double)v[j] * (double)v[j];
-  }
-  if (threadIdx.x < n % 8) {
-    float v[1];
-    load_w(p + n / 8 * 8 + threadIdx.x, true, v);
-    s += (double)v[0] * (double)v[0];
-  }
-  return s;
-}
-
-template <typename T>
-__device__ __forceinline__ void scale(const T *p, T *q, uint32_t n, float c) {
-#pragma unroll 4
-  for (uint32_t i = threadIdx.x * 8; i + 8 <= n; i += kThreads * 8) {
-    float v[8];
-    load_w(p + i, true, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= c;
-    store_w(q + i, true, v);
-  }
-  if (threadIdx.x < n % 8) {
-    const uint32_t i = n / 8 * 8 + threadIdx.x;
-    float v[1];
-    load_w(p + i, true, v);
-    v[0] *= c;
-    store_w(q + i, true, v);
-  }
-}
-
-__global__ __launch_bounds__(kThreads) void k_squares(GradTable t, double *part) {
-  __shared__ double red[kThreads / 64];
-  double s = 0.0;
-  for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    const uint32_t n = c + 1 == t.first[i + 1] ? t.tail[i] : t.chunk;
-    const long long at = (long long)(c - t.first[i]) * t.chunk;
-    s += t.f32[i] ? squares(reinterpret_cast<const float *>(t.g[i]) + at, n)
-                  : squares(reinterpret_cast<const bf16_t *>(t.g[i]) + at, n);
-  }
-  s = group_sum(s, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
-}
-
-__device__ __forceinline__ double total_norm(const double *part, int n, double *red) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) s += part[i];
-  return sqrt(group_sum(s, red));
-}
-
-__global__ __launch_bounds__(kThreads) void k_norm(const double *part, int n, float *norm) {
-  __shared__ double red[kThreads / 64];
-  const double v = total_norm(part, n, red);
-  if (threadIdx.x == 0) *norm = (float)v;
-}
-
-__global__ __launch_bounds__(kThreads) void k_scale(GradTable t, const double *part, int n, float tau, float *norm) {
-  __shared__ double red[kThreads / 64];
-  const double v = total_norm(part, n, red);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
-  const bool clip = v > (double)tau && v <= 1.7e308;
-  const float f = clip ? (float)((double)tau / v) : 1.f;
-  for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    if (!clip && t.out[i] == t.g[i]) continue;
-    const uint32_t m = c + 1 == t.first[i + 1] ? t.tail[i] : t.chunk;
-    const long long at = (long long)(c - t.first[i]) * t.chunk;
-    if (t.f32[i])
-      scale(reinterpret_cast<const float *>(t.g[i]) + at, reinterpret_cast<float *>(t.out[i]) + at, m, f);
-    else
-      scale(reinterpret_cast<const bf16_t *>(t.g[i]) + at, reinterpret_cast<bf16_t *>(t.out[i]) + at, m, f);
-  }
+  const float f = *factor;
+  if (f == 1.f && t.out[lo] == t.g[lo]) return;  // in place, and not clipped
+  const int n = c + 1 == t.first[lo + 1] ? (int)t.tail[lo] : kGradChunk;
+  const long long at = (long long)(c - t.first[lo]) * kGradChunk;
+  if (t.f32[lo])
+    chunk_scale<float, NT>(reinterpret_cast<const float *>(t.g[lo]) + at, reinterpret_cast<float *>(t.out[lo]) + at, n, f);
+  else
+    chunk_scale<bf16_t, NT>(reinterpret_cast<const bf16_t *>(t.g[lo]) + at, reinterpret_cast<bf16_t *>(t.out[lo]) + at, n, f);
 }
 
 }  // namespace
 
-hipError_t launch_grad_squares(const GradTable &t, double *part, int groups, hipStream_t s) {
-  hipLaunchKernelGGL(k_squares, dim3(groups), dim3(kThreads), 0, s, t, part);
+hipError_t launch_grad_squares(const GradTable &t, double *part, int groups, bool stream, hipStream_t s) {
+  if (stream)
+    hipLaunchKernelGGL(k_squares<true>, dim3(groups), dim3(kThreads), 0, s, t, part);
+  else
+    hipLaunchKernelGGL(k_squares<false>, dim3(groups), dim3(kThreads), 0, s, t, part);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_norm(const double *part, int n, float *norm, hipStream_t s) {
-  hipLaunchKernelGGL(k_norm, dim3(1), dim3(kThreads), 0, s, part, n, norm);
+hipError_t launch_grad_norm(const double *part, int n, float tau, float *norm, float *factor, hipStream_t s) {
+  hipLaunchKernelGGL(k_norm, dim3(1), dim3(1024), 0, s, part, n, tau, norm, factor);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_scale(const GradTable &t, const double *part, int n, float tau, float *norm, int groups,
-                             hipStream_t s) {
-  hipLaunchKernelGGL(k_scale, dim3(groups), dim3(kThreads), 0, s, t, part, n, tau, norm);
+hipError_t launch_grad_scale(const GradTable &t, const float *factor, bool stream, hipStream_t s) {
+  const dim3 grid = group_grid(t.first[t.n]);
+  if (stream)
+    hipLaunchKernelGGL(k_scale<true>, grid, dim3(kThreads), 0, s, t, factor);
+  else
+    hipLaunchKernelGGL(k_scale<false>, grid, dim3(kThreads), 0, s, t, factor);
   return hipGetLastError();
 }

@@ -8,6 +8,7 @@
 #pragma once
 
 #include "common.h"
+#include "grid.h"
 
 // Eight elements as they lie in memory.
 template <typename T>
@@ -91,15 +92,6 @@ __device__ __forceinline__ void stream_w(float *p, bool on, const float (&v)[8])
     __builtin_nontemporal_store(r[1], reinterpret_cast<u32x4_any *>(p) + 1);
   }
 }
-
-// A launch of one workgroup per row or more: threads of a grid's side are
-// counted in 32 bits, so many rows take a second side. group_index() is the
-// workgroup's number; the last ones may lie past `groups`.
-constexpr long long kGridSide = 1 << 20;
-inline dim3 group_grid(long long groups) {
-  return groups <= kGridSide ? dim3((unsigned)groups) : dim3((unsigned)kGridSide, (unsigned)((groups + kGridSide - 1) / kGridSide));
-}
-__device__ __forceinline__ long long group_index() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
 
 // Eight columns of a row as two runs of four, at p and `gap` elements behind
 // (half a row): the fp32 runs of neighbouring threads then lie side by side,
