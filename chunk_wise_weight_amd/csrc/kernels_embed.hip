@@ -433,6 +433,16 @@ __device__ __forceinline__ void add_rows(const SumArgs &S, int c, int lo, int hi
   }
 }
 
+// Neighbouring workgroups run on different dies, and cache lines and pages that
+// two of them write cost; here each die takes 64 neighbours at a time (of n).
+__device__ __forceinline__ long long beside(long long w, long long n) {
+  constexpr int kDies = 8, kRun = 64;
+  const long long base = w / (kDies * kRun) * (kDies * kRun);
+  if (base + kDies * kRun > n) return w;
+  const int k = (int)(w - base);
+  return base + k % kDies * kRun + k / kDies;
+}
+
 // Items: first the chunks, whose long rows' sums go to part[chunk][0 or 1];
 // then the table rows, or, when the sums are added to dE, the sorted tokens,
 // which count if they are the first of their row. A table row's tokens are
@@ -442,16 +452,20 @@ __device__ __forceinline__ void add_rows(const SumArgs &S, int c, int lo, int hi
 //
 // Most rows of a large table do not occur and only take zeros, so the launch is
 // bound by writing: 151936 fp32 rows of 2560 (1.56 GB) from 32768 bf16 tokens
-// take 325 us (5.3 TB/s; a fill alone takes 227). Two things matter. HALVES: a
-// thread has four columns of each half of an fp32 row, so that each store of a
-// wave covers whole cache lines (with eight in a row, written past the caches:
-// 620 us). And STREAM, as in the lookup (400 us without). Several rows per
-// workgroup, side by side or apart, gain nothing.
+// take 307 us (5.6 TB/s). A fill in the same rows takes 285, one in pages of
+// 4 KiB 227, but sums by pages, where each thread has to find its row, 395.
+// What matters is HALVES: a thread has four columns of each half of an fp32
+// row, so that each store of a wave covers whole cache lines (with eight in a
+// row, written past the caches: 620 us); STREAM, as in the lookup (355 us
+// without); and the order (325 us without). Several rows per workgroup, side
+// by side or apart, gain nothing.
 template <typename D, typename G, bool R, bool ONE, bool STREAM, bool HALVES>
 __global__ __launch_bounds__(1024) void k_sums(SumArgs S, long long items, int tr, int rpb) {
   const int sub = ONE ? 0 : threadIdx.x / tr, d = S.d;
   const int t0 = ONE ? threadIdx.x : threadIdx.x % tr;
-  const long long g = group_index() * rpb + sub;
+  long long w = group_index();
+  if (STREAM) w = beside(w, (long long)gridDim.x * gridDim.y);
+  const long long g = w * rpb + sub;
   if (g < S.nchunks) {
     const Chunk k = S.chunks[g];
     for (int c8 = t0; c8 * 8 < d; c8 += tr) {
