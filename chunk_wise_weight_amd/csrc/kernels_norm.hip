@@ -18,6 +18,7 @@ namespace {
 constexpr int kCUs = 256;
 // bytes of rows that a gradient launch keeps under way on each CU
 constexpr int kBwdBytes = 48 * 1024;
+constexpr int kTwoRows = 8192;    // rows from which a workgroup after a block takes two: still several for every CU
 constexpr int kMaxNarrow = 8192;  // widest row whose elements stay in registers: 1024 threads of 8
 
 // How rows lie on threads: `tr` threads own a row, 8 elements each (a power
@@ -145,55 +146,79 @@ struct Cols {
 };
 
 // ---- forward ----
-// One workgroup per row (ONE: the row's addresses are the same for all its
-// threads), or per rpb narrow rows. Bound by memory: 32768 rows of 2560 with an
-// fp32 stream, bf16 y and x (1.007 GB) take 195 us, 5.2 TB/s, where a copy of
-// those arrays in the same pattern takes 165 to 170; bf16 rows of 1024 before a
-// block 6.1 TB/s. Workgroups that stay and stride over the rows take 206 us,
-// and writing past the caches changes nothing.
-template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE, bool TOKEN>
+// One workgroup per ROWS neighbouring rows (ONE: their addresses are the same
+// for all its threads), or per rpb narrow rows. Bound by memory: 32768 rows of
+// 2560 with an fp32 stream, bf16 y and x (1.007 GB) take 180 us, 5.6 TB/s, where
+// a copy of those arrays in the same pattern takes 165 to 170; bf16 rows of
+// 1024 before a block 6.1 TB/s. After a block, with its two sums one behind the
+// other, two rows at a time share the barriers and have their loads under way
+// together (one row 195 us, four 194); before a block one row is enough (88 us
+// at 131072 bf16 rows of 1024, two 92). Workgroups that stay and stride over
+// the rows take 206 us, and writing past the caches changes nothing.
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE, bool TOKEN, int ROWS>
 __global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs A, int tr, int rpb) {
-  __shared__ float red[2][16][1];
+  __shared__ float red[2][16][ROWS];
   int turn = 0;
   const int d = A.d, sub = ONE ? 0 : threadIdx.x / tr;
   const Cols<R> cols(ONE ? threadIdx.x : threadIdx.x % tr, d);
   const unsigned c = cols.at;
-  const long long row = group_index() * rpb + sub;
-  const bool on = cols.mine && row < A.rows;
-  float o[8];
-  const Raw8<H> ro = load_raw(row_of<H>(A.h, row, d) + c, on);
+  const long long row0 = group_index() * rpb * ROWS + sub;
+  float o[ROWS][8];
+  Raw8<H> ro[ROWS];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) ro[k] = load_raw(row_of<H>(A.h, row0 + k, d) + c, cols.mine && row0 + k < A.rows);
   if (POST) {
-    const Raw8<Y> ry = load_raw(row_of<Y>(A.y, row, d) + c, on);
+    Raw8<Y> ry[ROWS], ra[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const bool on = cols.mine && row0 + k < A.rows;
+      ry[k] = load_raw(row_of<Y>(A.y, row0 + k, d) + c, on);
+      if (TOKEN) ra[k] = load_raw(row_of<Y>(A.gate, row0 + k, d) + c, on);
+    }
     float y[8], w[8], t[8];
-    if (TOKEN)
-      load_w(row_of<Y>(A.gate, row, d) + c, on, t);
-    else
-      load_param(A.gate, A.p_f32, c, cols.mine, t);
+    if (!TOKEN) load_param(A.gate, A.p_f32, c, cols.mine, t);
     load_param(A.w, A.p_f32, c, cols.mine, w);
-    expand(ry, y);
-    float s[1] = {0.f};
+    float s[ROWS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[0] += cols.own(j, y[j] * y[j]);
-    row_sum<1>(s, tr, red, turn);
-    const float q = row_rms(s[0], d, A.eps);
-    expand(ro, o);
+    for (int k = 0; k < ROWS; ++k) {
+      expand(ry[k], y);
+      s[k] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = A.alpha * o[j] + A.beta * t[j] * w[j] * (y[j] * q);
-    store_w(row_of<H>(A.o, row, d) + c, on, o);
+      for (int j = 0; j < 8; ++j) s[k] += cols.own(j, y[j] * y[j]);
+    }
+    row_sum<ROWS>(s, tr, red, turn);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const float q = row_rms(s[k], d, A.eps);
+      expand(ro[k], o[k]);
+      expand(ry[k], y);
+      if (TOKEN) expand(ra[k], t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[k][j] = A.alpha * o[k][j] + A.beta * t[j] * w[j] * (y[j] * q);
+      store_w(row_of<H>(A.o, row0 + k, d) + c, cols.mine && row0 + k < A.rows, o[k]);
+    }
   } else {
-    expand(ro, o);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) expand(ro[k], o[k]);
   }
   if (NEXT) {
     float wn[8];
     load_param(A.w_next, A.p_f32, c, cols.mine, wn);
-    float s[1] = {0.f};
+    float s[ROWS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[0] += cols.own(j, o[j] * o[j]);
-    row_sum<1>(s, tr, red, turn);
-    const float r = row_rms(s[0], d, A.eps);
+    for (int k = 0; k < ROWS; ++k) {
+      s[k] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = wn[j] * (o[j] * r);
-    store_w(row_of<X>(A.x, row, d) + c, on, o);
+      for (int j = 0; j < 8; ++j) s[k] += cols.own(j, o[k][j] * o[k][j]);
+    }
+    row_sum<ROWS>(s, tr, red, turn);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const float r = row_rms(s[k], d, A.eps);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[k][j] = wn[j] * (o[k][j] * r);
+      store_w(row_of<X>(A.x, row0 + k, d) + c, cols.mine && row0 + k < A.rows, o[k]);
+    }
   }
   end_of_stores();
 }
@@ -561,28 +586,36 @@ __global__ __launch_bounds__(kDown * 8) void k_norm_params(NormArgs A, int npart
 }
 
 // ---- which instance ----
-template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE>
-void fwd_form(const NormArgs &a, const Map &m, dim3 grid, hipStream_t s) {
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE, int ROWS>
+void fwd_rows(const NormArgs &a, const Map &m, hipStream_t s) {
+  const dim3 grid = group_grid((a.rows + m.rpb * ROWS - 1) / (m.rpb * ROWS));
   if (POST && a.token_gate)
-    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, POST>), grid, dim3(m.threads), 0, s, a, m.tr, m.rpb);
+    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, POST, ROWS>), grid, dim3(m.threads), 0, s, a, m.tr, m.rpb);
   else
-    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, false>), grid, dim3(m.threads), 0, s, a, m.tr, m.rpb);
+    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, false, ROWS>), grid, dim3(m.threads), 0, s, a, m.tr, m.rpb);
+}
+
+template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE>
+void fwd_form(const NormArgs &a, const Map &m, hipStream_t s) {
+  if (ONE && POST && a.rows >= kTwoRows)
+    fwd_rows<H, Y, X, POST, NEXT, R, ONE, ONE && POST ? 2 : 1>(a, m, s);
+  else
+    fwd_rows<H, Y, X, POST, NEXT, R, ONE, 1>(a, m, s);
 }
 
 template <typename H, typename Y, typename X, bool POST, bool NEXT>
 hipError_t fwd(const NormArgs &a, hipStream_t s) {
   const Map m = row_map(a.d);
-  const dim3 grid = group_grid((a.rows + m.rpb - 1) / m.rpb);
+  const dim3 grid = group_grid(a.rows);
   if (a.d > kMaxNarrow && a.d % 8)
     hipLaunchKernelGGL((k_norm_fwd_wide<H, Y, X, POST, NEXT, 1>), grid, dim3(1024), 0, s, a);
   else if (a.d > kMaxNarrow)
     hipLaunchKernelGGL((k_norm_fwd_wide<H, Y, X, POST, NEXT, 8>), grid, dim3(1024), 0, s, a);
   else if (m.rpb == 1)
-    a.d % 8 ? fwd_form<H, Y, X, POST, NEXT, true, true>(a, m, grid, s)
-            : fwd_form<H, Y, X, POST, NEXT, false, true>(a, m, grid, s);
+    a.d % 8 ? fwd_form<H, Y, X, POST, NEXT, true, true>(a, m, s) : fwd_form<H, Y, X, POST, NEXT, false, true>(a, m, s);
   else
-    a.d % 8 ? fwd_form<H, Y, X, POST, NEXT, true, false>(a, m, grid, s)
-            : fwd_form<H, Y, X, POST, NEXT, false, false>(a, m, grid, s);
+    a.d % 8 ? fwd_form<H, Y, X, POST, NEXT, true, false>(a, m, s)
+            : fwd_form<H, Y, X, POST, NEXT, false, false>(a, m, s);
   return hipGetLastError();
 }
 

@@ -11,7 +11,7 @@ of the result to its type. A gradient of a gain sums over the rows: the rows
 of one workgroup (at least 256 of them share the rows) and the up to 32 rows it
 takes at a time, then the workgroups in 128 slices, then the slices in seven
 steps. The bound below counts the workgroups at their most, and 48 additions
-besides, which also covers the 5 rows of a workgroup at these sizes.
+besides, which also covers the up to 11 rows of a workgroup at these sizes.
 """
 import pytest
 import torch
@@ -106,7 +106,7 @@ def parts_of(rows, d):
     return binding._norm_ws(rows, d) // (8 * d)
 
 
-SIZES = [(1, 8), (5, 9), (257, 64), (33, 100), (1031, 256), (7, 257), (130, 511), (12, 520), (61, 1023), (700, 2560),
+SIZES = [(1, 8), (5, 9), (257, 64), (33, 100), (1031, 256), (7, 257), (130, 511), (12, 520), (61, 1023), (700, 2560), (8193, 520),
          (3, 4097), (5, 8192), (2, 8200), (3, 9001), (1, 65536)]
 
 
