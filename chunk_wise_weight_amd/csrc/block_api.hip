@@ -204,7 +204,7 @@ std::vector<GradTable> grad_tables(const void *const *grads, const int64_t *nume
 // Norm of the tables and, with `clip`, the scaling by it.
 int run_grads(const char *where, const std::vector<GradTable> &tables, bool clip, float tau, float *norm, void *ws,
               hipStream_t s) {
-  float *factor = (float *)ws;
+  GradFactor *factor = (GradFactor *)ws;
   double *part = (double *)ws + 1;
   long long chunks = 0, bytes = 0;
   for (const GradTable &t : tables) {

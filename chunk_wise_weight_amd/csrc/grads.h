@@ -17,12 +17,18 @@ struct GradTable {
   int n;
 };
 
+// What gradients are multiplied by, mantissa * 2^exponent.
+struct GradFactor {
+  float mantissa;
+  int exponent;
+};
+
 // Workgroups of all norm launches of a call together (besides one per further table): one partial sum each.
 constexpr int kGradGroups = 2048;
 
 // part[blockIdx.x] = sum of squares of its chunks. stream: the gradients are more than the caches hold.
 hipError_t launch_grad_squares(const GradTable &t, double *part, int groups, bool stream, hipStream_t s);
 // *norm = sqrt(sum of part[0 .. n)); *factor (nullable) = min(1, tau / norm), 1 where the norm is not finite
-hipError_t launch_grad_norm(const double *part, int n, float tau, float *norm, float *factor, hipStream_t s);
+hipError_t launch_grad_norm(const double *part, int n, float tau, float *norm, GradFactor *factor, hipStream_t s);
 // out = g * *factor
-hipError_t launch_grad_scale(const GradTable &t, const float *factor, bool stream, hipStream_t s);
+hipError_t launch_grad_scale(const GradTable &t, const GradFactor *factor, bool stream, hipStream_t s);

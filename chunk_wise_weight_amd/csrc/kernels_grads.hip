@@ -49,12 +49,17 @@ __device__ __forceinline__ double squares16(u32x4_any v) {
   for (int j = 0; j < 4; ++j) s += sizeof(T) == 4 ? square(__uint_as_float(v[j])) : square(lower(v[j])) + square(upper(v[j]));
   return s;
 }
+// v tau / N with the factor as mantissa and exponent: as one fp32 number it
+// would lose its bits below 1e-38, where tau is small and N large.
+__device__ __forceinline__ float scaled(float v, GradFactor f) { return ldexpf(v * f.mantissa, f.exponent); }
+
 template <typename T>
-__device__ __forceinline__ u32x4_any scaled16(u32x4_any v, float c) {
+__device__ __forceinline__ u32x4_any scaled16(u32x4_any v, GradFactor f) {
   u32x4_any r;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    r[j] = sizeof(T) == 4 ? __float_as_uint(__uint_as_float(v[j]) * c) : pack_bf16x2(lower(v[j]) * c, upper(v[j]) * c);
+    r[j] = sizeof(T) == 4 ? __float_as_uint(scaled(__uint_as_float(v[j]), f))
+                          : pack_bf16x2(scaled(lower(v[j]), f), scaled(upper(v[j]), f));
   return r;
 }
 
@@ -84,18 +89,18 @@ __device__ __forceinline__ void put1(float *q, float v) { *q = v; }
 __device__ __forceinline__ void put1(bf16_t *q, float v) { *q = f32_to_bf16(v); }
 
 template <typename T, bool NT>
-__device__ __forceinline__ void chunk_scale(const T *p, T *q, int n, float c) {
+__device__ __forceinline__ void chunk_scale(const T *p, T *q, int n, GradFactor f) {
   constexpr int E = 16 / sizeof(T), P = kPieces<T>;
   if (n == kGradChunk) {
     u32x4_any v[P];
 #pragma unroll
     for (int k = 0; k < P; ++k) v[k] = load16<NT>(p + (k * kThreads + threadIdx.x) * E);
 #pragma unroll
-    for (int k = 0; k < P; ++k) store16<NT>(q + (k * kThreads + threadIdx.x) * E, scaled16<T>(v[k], c));
+    for (int k = 0; k < P; ++k) store16<NT>(q + (k * kThreads + threadIdx.x) * E, scaled16<T>(v[k], f));
     return;
   }
-  for (int i = threadIdx.x * E; i + E <= n; i += kThreads * E) store16<NT>(q + i, scaled16<T>(load16<NT>(p + i), c));
-  if ((int)threadIdx.x < n % E) put1(q + n / E * E + threadIdx.x, to_f32(p[n / E * E + threadIdx.x]) * c);
+  for (int i = threadIdx.x * E; i + E <= n; i += kThreads * E) store16<NT>(q + i, scaled16<T>(load16<NT>(p + i), f));
+  if ((int)threadIdx.x < n % E) put1(q + n / E * E + threadIdx.x, scaled(to_f32(p[n / E * E + threadIdx.x]), f));
 }
 
 // part[blockIdx.x]: the sum of squares of chunks blockIdx.x, + gridDim.x, ...
@@ -122,8 +127,9 @@ __global__ __launch_bounds__(kThreads) void k_squares(GradTable t, double *part)
 }
 
 // The norm from the workgroups' sums, and the factor min(1, tau / norm): 1
-// where the norm is not finite.
-__global__ __launch_bounds__(1024) void k_norm(const double *part, int n, float tau, float *norm, float *factor) {
+// where the norm is not finite (a factor below 1 has a mantissa below 1 or a
+// negative exponent).
+__global__ __launch_bounds__(1024) void k_norm(const double *part, int n, float tau, float *norm, GradFactor *factor) {
   __shared__ double red[16];
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += 1024) s += part[i];
@@ -134,7 +140,13 @@ __global__ __launch_bounds__(1024) void k_norm(const double *part, int n, float 
   for (int w = 1; w < 16; ++w) s += red[w];
   const double v = sqrt(s);
   *norm = (float)v;
-  if (factor) *factor = v > (double)tau && v <= 1.7e308 ? (float)((double)tau / v) : 1.f;
+  if (!factor) return;
+  GradFactor f{1.f, 0};
+  if (v > (double)tau && v <= 1.7e308) {
+    const double m = frexp((double)tau / v, &f.exponent);
+    f.mantissa = (float)m;
+  }
+  *factor = f;
 }
 
 // A workgroup per chunk: ones that stay and stride over the chunks take 850 us
@@ -143,7 +155,7 @@ __global__ __launch_bounds__(1024) void k_norm(const double *part, int n, float 
 // caches 760. Taking the chunks in the opposite order, to find the last ones
 // read still cached, gains nothing at any size.
 template <bool NT>
-__global__ __launch_bounds__(kThreads) void k_scale(GradTable t, const float *factor) {
+__global__ __launch_bounds__(kThreads) void k_scale(GradTable t, const GradFactor *factor) {
   const long long g = group_index();
   if (g >= t.first[t.n]) return;
   const uint32_t c = (uint32_t)g;
@@ -155,8 +167,8 @@ __global__ __launch_bounds__(kThreads) void k_scale(GradTable t, const float *fa
     else
       hi = mid - 1;
   }
-  const float f = *factor;
-  if (f == 1.f && t.out[lo] == t.g[lo]) return;  // in place, and not clipped
+  const GradFactor f = *factor;
+  if (f.mantissa == 1.f && f.exponent == 0 && t.out[lo] == t.g[lo]) return;  // in place, and not clipped
   const int n = c + 1 == t.first[lo + 1] ? (int)t.tail[lo] : kGradChunk;
   const long long at = (long long)(c - t.first[lo]) * kGradChunk;
   if (t.f32[lo])
@@ -175,12 +187,12 @@ hipError_t launch_grad_squares(const GradTable &t, double *part, int groups, boo
   return hipGetLastError();
 }
 
-hipError_t launch_grad_norm(const double *part, int n, float tau, float *norm, float *factor, hipStream_t s) {
+hipError_t launch_grad_norm(const double *part, int n, float tau, float *norm, GradFactor *factor, hipStream_t s) {
   hipLaunchKernelGGL(k_norm, dim3(1), dim3(1024), 0, s, part, n, tau, norm, factor);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_scale(const GradTable &t, const float *factor, bool stream, hipStream_t s) {
+hipError_t launch_grad_scale(const GradTable &t, const GradFactor *factor, bool stream, hipStream_t s) {
   const dim3 grid = group_grid(t.first[t.n]);
   if (stream)
     hipLaunchKernelGGL(k_scale<true>, grid, dim3(kThreads), 0, s, t, factor);

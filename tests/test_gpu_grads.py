@@ -117,6 +117,40 @@ def test_squares_that_leave_fp32(std):
 
 
 @gpu
+def test_factor_below_fp32():
+    """tau / N past the smallest fp32 number, with results well inside it."""
+    _, g = make([5000, 77], [F, B16], std=1e30)
+    n64 = norm64(g)
+    tau = 1e-10
+    out = [torch.empty_like(t) for t in g]
+    ttt.ttt_clip_grads(g, tau, out=out)
+    c = float(torch.tensor(tau, dtype=F)) / n64
+    assert c < 1e-41
+    for a, b in zip(out, g):
+        ref = b.double().cpu() * c
+        assert_close(a, ref, (2.02 * U32 + 1.01 * half_step(a.dtype)) * ref.abs(), "out")
+
+
+@gpu
+def test_more_than_the_caches_hold_unaligned():
+    """600 MB, which is read and written past the caches, from odd addresses."""
+    n = 300_000_001
+    buf = torch.full((n + 3,), 77.0, dtype=B16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    g = buf[1:1 + n]
+    g.copy_(torch.randn(n, generator=gen, device="cuda"))
+    n64 = float(torch.linalg.vector_norm(g, dtype=torch.float64))
+    out = torch.full((n + 6,), 77.0, dtype=B16, device="cuda")
+    norm = ttt.ttt_clip_grads([g], 0.5 * n64, out=[out[3:3 + n]])
+    assert abs(float(norm) - n64) <= 1.01 * U32 * n64
+    # the factor is a half but for its rounding, so a value may end one step off where it lies between two steps
+    ref = (g.float() * 0.5)
+    assert bool(((out[3:3 + n].float() - ref).abs() <= ref.abs() * 2.0 ** -7).all())
+    assert bool((out[:3] == 77).all()) and bool((out[3 + n:] == 77).all())
+    assert bool((buf[:1] == 77).all()) and bool((buf[1 + n:] == 77).all())
+
+
+@gpu
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
 def test_a_norm_that_is_not_finite_leaves_the_gradients(bad):
     _, g = make([5000, 77], [F, B16])

@@ -189,6 +189,50 @@ def test_post_gradient(rows, d, types, gate, use):
 
 
 @gpu
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+@pytest.mark.parametrize("rows,d", [(33, 100), (130, 511), (700, 2560), (3, 9001)])
+def test_without_gains(rows, d, gate):
+    """No gain on either norm: ones in the formulas, and no gradients of them."""
+    alpha, beta = 1.0, -0.5
+    p = inputs(rows, d, (F, B, B), gate, seed=d, gains=False)
+    o64, x64, bo, bx = post64(p, alpha, beta, True)
+    v = {k: dev(t) for k, t in p.items()}
+    o, x = ttt.ttt_norm_post(v["h"], v["y"], gate=v["gate"], alpha=alpha, beta=beta, eps=EPS, next_norm=True)
+    assert_close(o, o64, bo + half_step(F) * (o64.abs() + bo), "o")
+    assert_close(x, x64, bx + half_step(B) * (x64.abs() + bx), "x")
+    want = grads64(p, alpha, beta, True, True, parts_of(rows, d))
+    got = ttt.ttt_norm_post_grad(v["dh"], v["dx"], v["h"], v["y"], gate=v["gate"], alpha=alpha, beta=beta, eps=EPS)
+    have = {k: t for k, t in got._asdict().items() if t is not None}
+    assert set(have) == set(want) == {"dh", "dy"} | ({"dgate"} if gate != "none" else set())
+    for k, t in have.items():
+        val, bound = want[k]
+        assert_close(t, val, bound + half_step(t.dtype) * (val.abs() + bound), k)
+    dh, dw = ttt.ttt_norm_pre_grad(v["dx"], v["h"], eps=EPS)
+    assert dw is None and dh.dtype == F
+
+
+@gpu
+def test_two_streams_at_once():
+    """Calls that run at the same time keep to their own workspaces and outputs."""
+    cases = []
+    for k, (rows, d) in enumerate([(3000, 1024), (2500, 2560)]):
+        p = inputs(rows, d, (F, B, B), "channel", seed=k)
+        v = {n: dev(t) for n, t in p.items()}
+        args = (v["dh"], v["dx"], v["h"], v["y"], v["w"], v["gate"])
+        cases.append((args, v["w_next"], ttt.ttt_norm_post_grad(*args, w_next=v["w_next"])))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for k, (args, wn, _) in enumerate(cases):
+            got[k].append(ttt.ttt_norm_post_grad(*args, w_next=wn, stream=streams[k]))
+    torch.cuda.synchronize()
+    for k, (_, _, want) in enumerate(cases):
+        for g in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+@gpu
 def test_gradients_against_autograd_and_differences():
     """The gradient along a random direction: formula by autograd in 64 bits, and central differences of the forward
     kernel in fp32. The difference's own error is that of the same difference in 64 bits plus the forward's rounding
