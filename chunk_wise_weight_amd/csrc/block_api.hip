@@ -190,10 +190,10 @@ std::vector<GradTable> grad_tables(const void *const *grads, const int64_t *nume
       tables.back().first[0] = 0;
     }
     GradTable &t = tables.back();
-    const long long chunks = (all[i].n + kGradChunk - 1) / kGradChunk;
+    const long long chunk = kGradBytes / (all[i].f32 ? 4 : 2), chunks = (all[i].n + chunk - 1) / chunk;
     t.g[t.n] = all[i].g;
     t.out[t.n] = all[i].o;
-    t.tail[t.n] = (uint32_t)(all[i].n - (chunks - 1) * kGradChunk);
+    t.tail[t.n] = (uint32_t)(all[i].n - (chunks - 1) * chunk);
     t.f32[t.n] = (uint8_t)all[i].f32;
     t.first[t.n + 1] = t.first[t.n] + (uint32_t)chunks;
     ++t.n;
@@ -206,12 +206,9 @@ int run_grads(const char *where, const std::vector<GradTable> &tables, bool clip
               hipStream_t s) {
   GradFactor *factor = (GradFactor *)ws;
   double *part = (double *)ws + 1;
-  long long chunks = 0, bytes = 0;
-  for (const GradTable &t : tables) {
-    chunks += t.first[t.n];
-    for (int i = 0; i < t.n; ++i) bytes += (long long)(t.first[i + 1] - t.first[i]) * kGradChunk * (t.f32[i] ? 4 : 2);
-  }
-  const bool stream = bytes > kStreamGrads;
+  long long chunks = 0;
+  for (const GradTable &t : tables) chunks += t.first[t.n];
+  const bool stream = chunks * kGradBytes > kStreamGrads;
   int n = 0;
   for (const GradTable &t : tables) {
     // its share of kGradGroups

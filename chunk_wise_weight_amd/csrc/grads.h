@@ -3,11 +3,11 @@
 
 #include "common.h"
 
-// Up to kGradTable tensors, cut into chunks of kGradChunk elements (the last
-// one of each tensor shorter). As a kernel argument it needs no device copy, so
+// Up to kGradTable tensors, cut into chunks of kGradBytes (the last one of
+// each tensor shorter). As a kernel argument it needs no device copy, so
 // a call reads nothing that could change or be freed behind it; 152 of them
 // stay within the 4 KiB that every launch may pass.
-constexpr int kGradTable = 152, kGradChunk = 4096;
+constexpr int kGradTable = 152, kGradBytes = 16384;
 struct GradTable {
   const void *g[kGradTable];
   void *out[kGradTable];

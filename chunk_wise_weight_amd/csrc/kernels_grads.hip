@@ -63,16 +63,17 @@ __device__ __forceinline__ u32x4_any scaled16(u32x4_any v, GradFactor f) {
   return r;
 }
 
-// 16-byte pieces of a full chunk per thread
+// 16-byte pieces of a full chunk per thread, and elements of a chunk
+constexpr int kPieces = kGradBytes / 16 / kThreads;
 template <typename T>
-constexpr int kPieces = kGradChunk * sizeof(T) / 16 / kThreads;
+constexpr int kChunk = kGradBytes / sizeof(T);
 
 // the sum of squares of up to a chunk
 template <typename T, bool NT>
 __device__ __forceinline__ double chunk_squares(const T *p, int n) {
-  constexpr int E = 16 / sizeof(T), P = kPieces<T>;
+  constexpr int E = 16 / sizeof(T), P = kPieces;
   double s = 0.0;
-  if (n == kGradChunk) {
+  if (n == kChunk<T>) {
     u32x4_any v[P];
 #pragma unroll
     for (int k = 0; k < P; ++k) v[k] = load16<NT>(p + (k * kThreads + threadIdx.x) * E);
@@ -88,19 +89,27 @@ __device__ __forceinline__ double chunk_squares(const T *p, int n) {
 __device__ __forceinline__ void put1(float *q, float v) { *q = v; }
 __device__ __forceinline__ void put1(bf16_t *q, float v) { *q = f32_to_bf16(v); }
 
-template <typename T, bool NT>
-__device__ __forceinline__ void chunk_scale(const T *p, T *q, int n, GradFactor f) {
-  constexpr int E = 16 / sizeof(T), P = kPieces<T>;
-  if (n == kGradChunk) {
-    u32x4_any v[P];
+template <bool NT>
+constexpr int kScaleParts = NT ? 4 : 1;
+
+// one of PARTS parts of up to a chunk, scaled
+template <typename T, bool NT, int PARTS>
+__device__ __forceinline__ void chunk_scale(const T *p, T *q, int n, int part, GradFactor f) {
+  constexpr int E = 16 / sizeof(T), N = kChunk<T> / PARTS;  // elements of a part
+  const int lo = part * N, hi = lo + N < n ? lo + N : n;
+  if (hi - lo == N) {
+    u32x4_any v[kPieces / PARTS];
 #pragma unroll
-    for (int k = 0; k < P; ++k) v[k] = load16<NT>(p + (k * kThreads + threadIdx.x) * E);
+    for (int k = 0; k < kPieces / PARTS; ++k) v[k] = load16<NT>(p + lo + (k * kThreads + threadIdx.x) * E);
 #pragma unroll
-    for (int k = 0; k < P; ++k) store16<NT>(q + (k * kThreads + threadIdx.x) * E, scaled16<T>(v[k], f));
+    for (int k = 0; k < kPieces / PARTS; ++k) store16<NT>(q + lo + (k * kThreads + threadIdx.x) * E, scaled16<T>(v[k], f));
     return;
   }
-  for (int i = threadIdx.x * E; i + E <= n; i += kThreads * E) store16<NT>(q + i, scaled16<T>(load16<NT>(p + i), f));
-  if ((int)threadIdx.x < n % E) put1(q + n / E * E + threadIdx.x, scaled(to_f32(p[n / E * E + threadIdx.x]), f));
+  for (int i = lo + threadIdx.x * E; i + E <= hi; i += kThreads * E)
+    store16<NT>(q + i, scaled16<T>(load16<NT>(p + i), f));
+  if (hi <= lo) return;  // a part past the tensor's end
+  const int rest = hi - (hi - lo) % E + threadIdx.x;
+  if (rest < hi) put1(q + rest, scaled(to_f32(p[rest]), f));
 }
 
 // part[blockIdx.x]: the sum of squares of chunks blockIdx.x, + gridDim.x, ...
@@ -113,10 +122,14 @@ __global__ __launch_bounds__(kThreads) void k_squares(GradTable t, double *part)
   int i = 0;  // the chunk's tensor: chunks only go up
   for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
     while (c >= t.first[i + 1]) ++i;
-    const int n = c + 1 == t.first[i + 1] ? (int)t.tail[i] : kGradChunk;
-    const long long at = (long long)(c - t.first[i]) * kGradChunk;
-    s += t.f32[i] ? chunk_squares<float, NT>(reinterpret_cast<const float *>(t.g[i]) + at, n)
-                  : chunk_squares<bf16_t, NT>(reinterpret_cast<const bf16_t *>(t.g[i]) + at, n);
+    const bool last = c + 1 == t.first[i + 1];
+    const long long at = (long long)(c - t.first[i]) * kGradBytes;
+    if (t.f32[i])
+      s += chunk_squares<float, NT>(reinterpret_cast<const float *>((const char *)t.g[i] + at),
+                                    last ? (int)t.tail[i] : kChunk<float>);
+    else
+      s += chunk_squares<bf16_t, NT>(reinterpret_cast<const bf16_t *>((const char *)t.g[i] + at),
+                                     last ? (int)t.tail[i] : kChunk<bf16_t>);
   }
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
@@ -149,16 +162,21 @@ __global__ __launch_bounds__(1024) void k_norm(const double *part, int n, float 
   *factor = f;
 }
 
-// A workgroup per chunk: ones that stay and stride over the chunks take 850 us
-// where these take 700 (539M fp32 values, 4.3 GB: 6.2 TB/s; a copy reaches
-// 6.6), since a wave's loads would wait behind its own stores. Through the
-// caches 760. Taking the chunks in the opposite order, to find the last ones
-// read still cached, gains nothing at any size.
+// A workgroup per chunk, or, of gradients past the caches (NT), per page of 4
+// KiB, which workgroups on different dies should not share: 539M fp32 values
+// (4.3 GB) take 650 us, 6.6 TB/s, as a copy does; 715 by chunks, 850 with
+// workgroups that stay and stride over the chunks (a wave's loads would wait
+// behind its own stores), 760 through the caches. Taking the chunks in the
+// opposite order, to find the last ones read still cached, gains nothing at
+// any size. Where most calls clip nothing and only look, smaller steps cost:
+// 70M bf16 values in place take 33 us by chunks and 38 by pages.
 template <bool NT>
 __global__ __launch_bounds__(kThreads) void k_scale(GradTable t, const GradFactor *factor) {
+  constexpr int PARTS = kScaleParts<NT>;
   const long long g = group_index();
-  if (g >= t.first[t.n]) return;
-  const uint32_t c = (uint32_t)g;
+  if (g >= (long long)t.first[t.n] * PARTS) return;
+  const uint32_t c = (uint32_t)(g / PARTS);
+  const int part = (int)(g % PARTS);
   int lo = 0, hi = t.n - 1;  // the tensor of the chunk
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -169,12 +187,16 @@ __global__ __launch_bounds__(kThreads) void k_scale(GradTable t, const GradFacto
   }
   const GradFactor f = *factor;
   if (f.mantissa == 1.f && f.exponent == 0 && t.out[lo] == t.g[lo]) return;  // in place, and not clipped
-  const int n = c + 1 == t.first[lo + 1] ? (int)t.tail[lo] : kGradChunk;
-  const long long at = (long long)(c - t.first[lo]) * kGradChunk;
+  const bool last = c + 1 == t.first[lo + 1];
+  const long long at = (long long)(c - t.first[lo]) * kGradBytes;
+  const char *p = (const char *)t.g[lo] + at;
+  char *q = (char *)t.out[lo] + at;
   if (t.f32[lo])
-    chunk_scale<float, NT>(reinterpret_cast<const float *>(t.g[lo]) + at, reinterpret_cast<float *>(t.out[lo]) + at, n, f);
+    chunk_scale<float, NT, PARTS>(reinterpret_cast<const float *>(p), reinterpret_cast<float *>(q),
+                           last ? (int)t.tail[lo] : kChunk<float>, part, f);
   else
-    chunk_scale<bf16_t, NT>(reinterpret_cast<const bf16_t *>(t.g[lo]) + at, reinterpret_cast<bf16_t *>(t.out[lo]) + at, n, f);
+    chunk_scale<bf16_t, NT, PARTS>(reinterpret_cast<const bf16_t *>(p), reinterpret_cast<bf16_t *>(q),
+                            last ? (int)t.tail[lo] : kChunk<bf16_t>, part, f);
 }
 
 }  // namespace
@@ -193,7 +215,7 @@ hipError_t launch_grad_norm(const double *part, int n, float tau, float *norm, G
 }
 
 hipError_t launch_grad_scale(const GradTable &t, const GradFactor *factor, bool stream, hipStream_t s) {
-  const dim3 grid = group_grid(t.first[t.n]);
+  const dim3 grid = group_grid((long long)t.first[t.n] * (stream ? kScaleParts<true> : kScaleParts<false>));
   if (stream)
     hipLaunchKernelGGL(k_scale<true>, grid, dim3(kThreads), 0, s, t, factor);
   else
