@@ -31,43 +31,58 @@ constexpr int kChunk = 32;       // sorted tokens of one piece of a long row
 
 // ---- lookup ----
 
-// A workgroup takes one row (ONE: its id is the same for all threads and its
-// addresses need no vector arithmetic), or, of narrow rows, `rpb` rows of `tr`
-// threads. There is a workgroup for every row: a grid that keeps the card
-// full and strides over the rows measured 470 us on 131072 bf16 rows of 2560
-// into fp32 where this one takes 290 (1.52 GB: 5.3 TB/s), since rows that run
-// at the same time then lie side by side in memory. STREAM: x is too large to
-// be found in the caches later; its rows are written past them (362 us without;
-// at 168 MB 60 us with it and 42 without).
+template <bool ONE, bool STREAM>
+constexpr int kEmbedRows = ONE && STREAM ? 2 : 1;
+
+// A workgroup takes one row or two neighbouring ones (ONE: their ids are the
+// same for all threads and their addresses need no vector arithmetic), or, of
+// narrow rows, `rpb` rows of `tr` threads. There is a workgroup for every row or
+// two: a grid that keeps the card full and strides over the rows measured 470
+// us on 131072 bf16 rows of 2560 into fp32 where this one takes 265 (1.52 GB:
+// 5.7 TB/s), since rows that run at the same time then lie side by side in
+// memory. STREAM: x is too large to be found in the caches later; its rows are
+// written past them (342 us without; at 168 MB 60 us with it and 39 without),
+// two at a time, so that their loads overlap (295 us one at a time, 332 four;
+// within the caches one is as good or better). Writing x in pages of 4 KiB by
+// threads that each find their row: 375 us and more.
 template <typename E, typename X, bool R, bool ONE, bool STREAM>
 __global__ __launch_bounds__(1024) void k_embed(EmbedArgs A, int tr, int rpb) {
   const int sub = ONE ? 0 : threadIdx.x / tr, d = A.d;
-  const long long row = group_index() * rpb + sub;
-  if (row >= A.ids.n) return;
-  const int id = A.ids.at((unsigned)row);
-  const bool on = id >= 0 && id < A.vocab;
-  const E *src = reinterpret_cast<const E *>(A.E) + (long long)(on ? id : 0) * d;
-  X *dst = reinterpret_cast<X *>(A.x) + row * d;
+  // four columns of each half of an fp32 row: each store of a wave then covers whole cache lines (5% on rows that
+  // stay in the caches)
+  constexpr bool HALVES = !R && sizeof(X) == 4;
+  constexpr int ROWS = kEmbedRows<ONE, STREAM>;
+  const long long row0 = group_index() * rpb * ROWS + sub;
+  const E *src[ROWS];
+  bool on[ROWS];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const int id = row0 + k < A.ids.n ? A.ids.at((unsigned)(row0 + k)) : -1;
+    on[k] = id >= 0 && id < A.vocab;
+    src[k] = reinterpret_cast<const E *>(A.E) + (long long)(on[k] ? id : 0) * d;
+  }
   for (int c8 = ONE ? threadIdx.x : threadIdx.x % tr; c8 * 8 < d; c8 += tr) {
     // the last columns of a ragged row: its last eight, some of which the neighbour writes too, to the same values
     const int c = R && c8 * 8 + 8 > d ? d - 8 : c8 * 8;
-    float v[8];
-    if (!R && sizeof(X) == 4) {
-      // four columns of each half of an fp32 row: each store of a wave then covers whole cache lines (5% on rows
-      // that stay in the caches)
-      expand(load_halves(src + c8 * 4, d / 2, on), v);
+    Raw8<E> r[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k)
+      r[k] = HALVES ? load_halves(src[k] + c8 * 4, d / 2, on[k]) : load_raw(src[k] + c, on[k]);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      if (row0 + k >= A.ids.n) break;
+      X *dst = reinterpret_cast<X *>(A.x) + (row0 + k) * d;
+      float v[8];
+      expand(r[k], v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= A.scale;
-      store_halves<STREAM>(dst + c8 * 4, d / 2, v);
-      continue;
+      if (HALVES)
+        store_halves<STREAM>(dst + c8 * 4, d / 2, v);
+      else if (STREAM)
+        stream_w(dst + c, true, v);
+      else
+        store_w(dst + c, true, v);
     }
-    load_w(src + c, on, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= A.scale;
-    if (STREAM)
-      stream_w(dst + c, true, v);
-    else
-      store_w(dst + c, true, v);
   }
 }
 
@@ -561,23 +576,29 @@ RowThreads row_threads(int d) {
   return {tr, tr <= 64 ? 256 / tr : 1};
 }
 
+template <typename E, typename X, bool R, bool ONE, bool STREAM>
+void embed_launch(const EmbedArgs &a, int tr, int rpb, hipStream_t s) {
+  const int rows = rpb * kEmbedRows<ONE, STREAM>;
+  hipLaunchKernelGGL((k_embed<E, X, R, ONE, STREAM>), group_grid((a.ids.n + rows - 1LL) / rows), dim3(tr * rpb), 0, s, a,
+                     tr, rpb);
+}
+
 template <typename E, typename X, bool R, bool ONE>
-void embed_form(const EmbedArgs &a, dim3 grid, int tr, int rpb, hipStream_t s) {
+void embed_form(const EmbedArgs &a, int tr, int rpb, hipStream_t s) {
   // not ragged rows: parts of cache lines written past the caches cost more (491 MB: 187 us, 129 through them)
   if (!R && (double)a.ids.n * a.d * sizeof(X) > kStreamBytes)
-    hipLaunchKernelGGL((k_embed<E, X, R, ONE, !R>), grid, dim3(tr * rpb), 0, s, a, tr, rpb);
+    embed_launch<E, X, R, ONE, !R>(a, tr, rpb, s);
   else
-    hipLaunchKernelGGL((k_embed<E, X, R, ONE, false>), grid, dim3(tr * rpb), 0, s, a, tr, rpb);
+    embed_launch<E, X, R, ONE, false>(a, tr, rpb, s);
 }
 
 template <typename E, typename X>
 hipError_t embed(const EmbedArgs &a, hipStream_t s) {
   const auto [tr, rpb] = row_threads(a.d);
-  const dim3 grid = group_grid((a.ids.n + rpb - 1LL) / rpb);
   if (rpb > 1)
-    a.d % 8 ? embed_form<E, X, true, false>(a, grid, tr, rpb, s) : embed_form<E, X, false, false>(a, grid, tr, rpb, s);
+    a.d % 8 ? embed_form<E, X, true, false>(a, tr, rpb, s) : embed_form<E, X, false, false>(a, tr, rpb, s);
   else
-    a.d % 8 ? embed_form<E, X, true, true>(a, grid, tr, rpb, s) : embed_form<E, X, false, true>(a, grid, tr, rpb, s);
+    a.d % 8 ? embed_form<E, X, true, true>(a, tr, rpb, s) : embed_form<E, X, false, true>(a, tr, rpb, s);
   return hipGetLastError();
 }
 

@@ -159,6 +159,39 @@ def test_table_past_32_bit_offsets():
 
 
 @gpu
+@pytest.mark.parametrize("tx", [F, B16], ids=["x32", "x16"])
+def test_more_than_the_caches_hold(tx):
+    """Outputs over half a GiB, which are written past the caches, two rows at a time: an odd number of them."""
+    vocab, d = 70001, 1032
+    n = 600 * 2 ** 20 // (d * (4 if tx == F else 2)) | 1
+    E = torch.randn((vocab, d), device="cuda").to(B16)
+    ids = torch.randint(-1, vocab + 1, (n,), device="cuda").int()
+    x = ttt.ttt_embed(E, ids, scale=3.0, dtype=tx)
+    known = (ids >= 0) & (ids < vocab)
+    want = (E[ids.long().clamp(0, vocab - 1)].float() * 3.0 * known[:, None]).to(tx)
+    assert torch.equal(x, want)  # 3 e is exact in fp32, so both round the same number once
+
+
+@gpu
+@pytest.mark.parametrize("tE", [F, B16], ids=["dE32", "dE16"])
+def test_gradient_of_a_table_past_the_caches(tE):
+    """Over half a GiB of gradient, whose rows are written past the caches and dealt to the dies in runs: each row that
+    occurs against 64 bits, and all others zero."""
+    vocab, d, n = (70001, 2056, 6001) if tE == F else (70001, 4104, 6001)
+    ids = make_ids(1, n, vocab, "skewed", seed=4)[0]
+    g = torch.Generator().manual_seed(8)
+    dx = torch.randn((n, d), generator=g).to(B16)
+    dE = ttt.ttt_embed_grad(dx.cuda(), ids.cuda(), vocab, dE=torch.full((vocab, d), 7.0, dtype=tE, device="cuda"))
+    rows, inverse, count = torch.unique(ids.long(), return_inverse=True, return_counts=True)
+    ref = torch.zeros((len(rows), d), dtype=torch.float64).index_add_(0, inverse, dx.double())
+    mag = torch.zeros((len(rows), d), dtype=torch.float64).index_add_(0, inverse, dx.double().abs())
+    bound = (torch.minimum(count, 31 + torch.ceil(count / 256) + 9)[:, None] + 2) * U32 * mag
+    assert_close(dE[rows.cuda()], ref, bound + half_step(tE) * (ref.abs() + bound), "dE")
+    dE[rows.cuda()] = 0
+    assert int(torch.count_nonzero(dE)) == 0
+
+
+@gpu
 def test_another_stream_and_graph_replays():
     vocab, d = 5000, 520
     ids = make_ids(2, 700, vocab, "skewed").cuda().contiguous()
