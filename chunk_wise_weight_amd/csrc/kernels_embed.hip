@@ -22,10 +22,10 @@ constexpr double kStreamBytes = 512.0 * (1 << 20);
 constexpr int kMaxTiles = 256;   // of a sort: a workgroup reads the counts of all of them
 constexpr int kMinTile = 1024;   // tokens
 constexpr int kMaxDigit = 9;     // bits
-constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kClearPerGroup = 2048;  // table rows whose segments one workgroup clears
-constexpr int kRounds = kMinTile / kSortThreads;  // tokens of a thread that it holds at once
-constexpr int kSmallThreads = 1024, kSmall = kSmallThreads * kRounds;  // tokens that one workgroup sorts
+static_assert(kMinTile == kSortThreads, "a token per thread");
+constexpr int kSmallRounds = 4, kSmall = kSortThreads * kSmallRounds;  // tokens that one workgroup sorts by itself
 constexpr int kSmallClear = 16384;  // table rows whose segments one workgroup clears in passing
 constexpr int kChunk = 32;       // sorted tokens of one piece of a long row
 
@@ -143,14 +143,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs S) {
   __syncthreads();
   const long long t0 = (long long)blockIdx.x * S.tile;
   const int hi = (int)(t0 + S.tile < S.ids.n ? t0 + S.tile : S.ids.n);
-  for (int i = (int)t0 + threadIdx.x; i < hi; i += kSortThreads * kRounds) {
-    uint32_t key[kRounds];
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) key[r] = i + r * kSortThreads < hi ? S.key(i + r * kSortThreads) : 0;
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r)
-      if (i + r * kSortThreads < hi) atomicAdd(&cnt[(key[r] >> S.shift) & (S.bins - 1)], 1u);
-  }
+  for (int i = (int)t0 + threadIdx.x; i < hi; i += kSortThreads)
+    atomicAdd(&cnt[(S.key(i) >> S.shift) & (S.bins - 1)], 1u);
   __syncthreads();
   for (int i = threadIdx.x; i < S.bins; i += kSortThreads) S.hist[(long long)blockIdx.x * S.bins + i] = cnt[i];
 }
@@ -174,84 +168,90 @@ __device__ __forceinline__ uint32_t place_of(uint32_t *next, int dg, int bins, b
   return at;
 }
 
-// Places the tile's tokens: behind all tokens of a smaller digit, and those of
-// the same digit in earlier tiles, earlier waves' parts of the tile (each wave
-// owns a run of it) and earlier steps of the wave. ONCE: a wave's run is
-// kRounds steps, all in registers (tiles of kMinTile).
-template <bool ONCE>
-__global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs S) {
-  __shared__ uint32_t next[kSortWaves][1 << kMaxDigit];  // where a wave's next token of a digit goes
-  __shared__ uint32_t wsum[kSortWaves];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const long long t0 = (long long)blockIdx.x * S.tile;
-  const int run = S.tile / kSortWaves;
-  const long long w0 = t0 + (long long)wave * run;
-  const int lo = (int)(w0 < S.ids.n ? w0 : S.ids.n), hi = (int)(w0 + run < S.ids.n ? w0 + run : S.ids.n);
-  uint32_t key[kRounds], pos[kRounds];
-  auto load = [&](int i0) {
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const int i = i0 + r * 64 + lane;
-      key[r] = i < hi ? S.key(i) : 0;
-      pos[r] = i < hi && S.pos_in ? S.pos_in[i] : (uint32_t)i;
-    }
-  };
-  auto digit = [&](int r) { return (int)((key[r] >> S.shift) & (S.bins - 1)); };
-  if (ONCE) load(lo);
-  for (int i = threadIdx.x; i < kSortWaves * S.bins; i += kSortThreads) next[i / S.bins][i % S.bins] = 0;
-  // two neighbouring digits per thread (at most 512 of them): their totals, and the part before this tile
-  uint32_t total[2] = {0, 0}, before[2] = {0, 0};
-  if ((int)threadIdx.x * 2 < S.bins) {
-    const uint2 *h2 = reinterpret_cast<const uint2 *>(S.hist) + threadIdx.x;
-#pragma unroll 16  // as many loads at once, or each would wait for the one before it
-    for (int t = 0; t < S.tiles; ++t) {
-      const uint2 h = h2[(long long)t * (S.bins / 2)];
-      total[0] += h.x;
-      total[1] += h.y;
-      before[0] += t < (int)blockIdx.x ? h.x : 0;
-      before[1] += t < (int)blockIdx.x ? h.y : 0;
-    }
-  }
-  __syncthreads();
-  for (int i0 = lo; i0 < hi; i0 += 64 * kRounds) {
-    if (!ONCE) load(i0);
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r)
-      if (i0 + r * 64 + lane < hi) atomicAdd(&next[wave][digit(r)], 1u);
-  }
-  // exclusive sum of the totals over the digits
-  uint32_t inc = total[0] + total[1];
+// Turns next[wave][digit], how many tokens of each digit the waves have, into
+// where their first ones go: behind the tokens of smaller digits and those of
+// earlier waves. total: how many tokens of digit threadIdx.x there are in all,
+// before: how many of them lie in front of this workgroup's.
+__device__ __forceinline__ void first_places(uint32_t (*next)[1 << kMaxDigit], uint32_t *wsum, int bins, uint32_t total,
+                                             uint32_t before) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, b = threadIdx.x;
+  uint32_t inc = total;
   for (int o = 1; o < 64; o <<= 1) {
     const uint32_t up = __shfl_up(inc, o);
     if (lane >= o) inc += up;
   }
   if (lane == 63) wsum[wave] = inc;
   __syncthreads();
-  uint32_t base = inc - total[0] - total[1];
-  for (int w = 0; w < wave; ++w) base += wsum[w];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int b = threadIdx.x * 2 + k;
-    if (b >= S.bins) break;
-    uint32_t at = base + before[k];
+  if (b < bins) {
+    uint32_t at = inc - total + before;
+    for (int w = 0; w < wave; ++w) at += wsum[w];
     for (int w = 0; w < kSortWaves; ++w) {
       const uint32_t c = next[w][b];
       next[w][b] = at;
       at += c;
     }
-    base += total[k];
   }
   __syncthreads();
-  for (int i0 = lo; i0 < hi; i0 += 64 * kRounds) {
-    if (!ONCE) load(i0);
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const bool in = i0 + r * 64 + lane < hi;
-      const uint32_t at = place_of(next[wave], digit(r), S.bins, in);
-      if (in) {
-        S.key_out[at] = key[r];
-        S.pos_out[at] = pos[r];
-      }
+}
+
+// Places the tile's tokens: behind all tokens of a smaller digit, and those of
+// the same digit in earlier tiles, earlier waves' parts of the tile (each wave
+// owns a run of it) and earlier steps of the wave. ONCE: tiles of kMinTile, a
+// token per thread, kept in registers. The counts of the tiles are the longest
+// wait (they come from other dies): they are loaded many at a time, even and
+// odd tiles by half the threads. 32768 tokens, 32 tiles: 7 us (with a quarter
+// of the threads and four tokens each 11; with tiles of 4096 9).
+template <bool ONCE>
+__global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs S) {
+  __shared__ uint32_t next[kSortWaves][1 << kMaxDigit];  // where a wave's next token of a digit goes
+  __shared__ uint32_t odd[2][1 << kMaxDigit];            // totals and counts before this tile, of odd tiles
+  __shared__ uint32_t wsum[kSortWaves];
+  static_assert(kSortThreads == 2 << kMaxDigit, "a thread per digit and half of the tiles");
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const long long t0 = (long long)blockIdx.x * S.tile;
+  const int run = S.tile / kSortWaves;
+  const long long w0 = t0 + (long long)wave * run;
+  const int lo = (int)(w0 < S.ids.n ? w0 : S.ids.n), hi = (int)(w0 + run < S.ids.n ? w0 + run : S.ids.n);
+  uint32_t key = 0, pos = 0;
+  auto load = [&](int i) {
+    key = i < hi ? S.key(i) : 0;
+    pos = i < hi && S.pos_in ? S.pos_in[i] : (uint32_t)i;
+  };
+  auto digit = [&]() { return (int)((key >> S.shift) & (S.bins - 1)); };
+  if (ONCE) load(lo + lane);
+  uint32_t total = 0, before = 0;
+  const int b = threadIdx.x & ((1 << kMaxDigit) - 1), half = threadIdx.x >> kMaxDigit;
+  if (b < S.bins) {
+#pragma unroll 16
+    for (int t = half; t < S.tiles; t += 2) {
+      const uint32_t h = S.hist[(long long)t * S.bins + b];
+      total += h;
+      before += t < (int)blockIdx.x ? h : 0;
+    }
+  }
+  for (int i = threadIdx.x; i < kSortWaves * S.bins; i += kSortThreads) next[i / S.bins][i % S.bins] = 0;
+  if (half) {
+    odd[0][b] = total;
+    odd[1][b] = before;
+    total = before = 0;
+  }
+  __syncthreads();
+  if (!half) {
+    total += odd[0][b];
+    before += odd[1][b];
+  }
+  for (int i0 = lo; i0 < hi; i0 += 64) {
+    if (!ONCE) load(i0 + lane);
+    if (i0 + lane < hi) atomicAdd(&next[wave][digit()], 1u);
+  }
+  first_places(next, wsum, S.bins, total, before);
+  for (int i0 = lo; i0 < hi; i0 += 64) {
+    if (!ONCE) load(i0 + lane);
+    const bool in = i0 + lane < hi;
+    const uint32_t at = place_of(next[wave], digit(), S.bins, in);
+    if (in) {
+      S.key_out[at] = key;
+      S.pos_out[at] = pos;
     }
   }
 }
@@ -306,53 +306,34 @@ __global__ __launch_bounds__(256) void k_segments(const uint32_t *key, int n, in
 // five launches less, which is what a short batch's sort would cost. CLEAR: it
 // also clears seg, of a table that one workgroup clears sooner than a launch.
 template <bool CLEAR>
-__global__ __launch_bounds__(kSmallThreads) void k_sort_small(SortArgs S, int passes, int digit, Chunk *chunks) {
-  constexpr int kWaves = kSmallThreads / 64;
+__global__ __launch_bounds__(kSortThreads) void k_sort_small(SortArgs S, int passes, int digit, Chunk *chunks) {
   __shared__ uint32_t skey[kSmall], spos[kSmall];
-  __shared__ uint32_t next[kWaves][1 << kMaxDigit];
-  __shared__ uint32_t wsum[kWaves];
+  __shared__ uint32_t next[kSortWaves][1 << kMaxDigit];
+  __shared__ uint32_t wsum[kSortWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = S.ids.n;
-  if (CLEAR) clear_runs(S.seg, S.vocab, threadIdx.x, kSmallThreads);
-  const int run = (n + kWaves * 64 - 1) / (kWaves * 64) * 64, lo = wave * run;  // of a wave: up to kRounds steps
-  uint32_t key[kRounds], pos[kRounds];
+  if (CLEAR) clear_runs(S.seg, S.vocab, threadIdx.x, kSortThreads);
+  const int run = (n + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64, lo = wave * run;  // of a wave: up to kSmallRounds steps
+  uint32_t key[kSmallRounds], pos[kSmallRounds];
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
+  for (int r = 0; r < kSmallRounds; ++r) {
     const int i = lo + r * 64 + lane;
     key[r] = r * 64 < run && i < n ? S.key(i) : 0;
     pos[r] = (uint32_t)i;
   }
   for (int p = 0; p < passes; ++p) {
     const int shift = p * digit;
-    for (int i = threadIdx.x; i < kWaves * S.bins; i += kSmallThreads) next[i / S.bins][i % S.bins] = 0;
+    for (int i = threadIdx.x; i < kSortWaves * S.bins; i += kSortThreads) next[i / S.bins][i % S.bins] = 0;
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r)
+    for (int r = 0; r < kSmallRounds; ++r)
       if (r * 64 < run && lo + r * 64 + lane < n) atomicAdd(&next[wave][(key[r] >> shift) & (S.bins - 1)], 1u);
     __syncthreads();
-    // exclusive sum over (digit, wave): a digit per thread
-    const int b = threadIdx.x;
     uint32_t total = 0;
-    if (b < S.bins)
-      for (int w = 0; w < kWaves; ++w) total += next[w][b];
-    uint32_t inc = total;
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t up = __shfl_up(inc, o);
-      if (lane >= o) inc += up;
-    }
-    if (lane == 63) wsum[wave] = inc;
-    __syncthreads();
-    uint32_t at = inc - total;
-    for (int w = 0; w < wave; ++w) at += wsum[w];
-    if (b < S.bins) {
-      for (int w = 0; w < kWaves; ++w) {
-        const uint32_t c = next[w][b];
-        next[w][b] = at;
-        at += c;
-      }
-    }
-    __syncthreads();
+    if ((int)threadIdx.x < S.bins)
+      for (int w = 0; w < kSortWaves; ++w) total += next[w][threadIdx.x];
+    first_places(next, wsum, S.bins, total, 0);
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
+    for (int r = 0; r < kSmallRounds; ++r) {
       if (r * 64 >= run) break;
       const bool in = lo + r * 64 + lane < n;
       const uint32_t to = place_of(next[wave], (int)((key[r] >> shift) & (S.bins - 1)), S.bins, in);
@@ -363,7 +344,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_sort_small(SortArgs S, int pa
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
+    for (int r = 0; r < kSmallRounds; ++r) {
       const int i = lo + r * 64 + lane;
       if (r * 64 < run && i < n) {
         key[r] = skey[i];
@@ -372,7 +353,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_sort_small(SortArgs S, int pa
     }
   }
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
+  for (int r = 0; r < kSmallRounds; ++r) {
     if (r * 64 >= run) break;
     const int i = lo + r * 64 + lane;
     if (i < n) {
@@ -688,11 +669,11 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, int dx_f32, int dE_f32, hip
     S.pos_out = (uint32_t *)(ws + w.pos[0]);
     Chunk *chunks = (Chunk *)(ws + w.chunks);
     if (a.vocab <= kSmallClear) {
-      hipLaunchKernelGGL(k_sort_small<true>, dim3(1), dim3(kSmallThreads), 0, s, S, p.passes, p.digit, chunks);
+      hipLaunchKernelGGL(k_sort_small<true>, dim3(1), dim3(kSortThreads), 0, s, S, p.passes, p.digit, chunks);
     } else {
       const int clear = (a.vocab + kClearPerGroup - 1) / kClearPerGroup;
       hipLaunchKernelGGL(k_clear_runs, dim3(clear < kMaxTiles ? clear : kMaxTiles), dim3(256), 0, s, S.seg, a.vocab);
-      hipLaunchKernelGGL(k_sort_small<false>, dim3(1), dim3(kSmallThreads), 0, s, S, p.passes, p.digit, chunks);
+      hipLaunchKernelGGL(k_sort_small<false>, dim3(1), dim3(kSortThreads), 0, s, S, p.passes, p.digit, chunks);
     }
   }
   for (int k = 0; k < p.passes && !small; ++k) {
