@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from array import array
+from functools import lru_cache
 from operator import attrgetter
 from typing import Dict, List, NamedTuple, Optional, Tuple
 
@@ -25,7 +26,8 @@ EXPORTS = ("ttt_init", "ttt_forward_chunked", "ttt_forward_docs", "ttt_reset", "
            "ttt_set_group_chunks", "ttt_set_clip", "ttt_set_target_conv", "ttt_plan", "ttt_set_profiling", "ttt_phase_times",
            "ttt_workspace_bytes", "ttt_set_output_f32", "ttt_state_delta", "ttt_forward_chunked_noalloc",
            "ttt_norm_pre", "ttt_norm_post", "ttt_norm_ws_bytes", "ttt_norm_pre_grad", "ttt_norm_post_grad",
-           "ttt_embed", "ttt_embed_grad_ws_bytes", "ttt_embed_grad", "ttt_grad_ws_bytes", "ttt_grad_norm", "ttt_clip_grads")
+           "ttt_embed", "ttt_embed_grad_ws_bytes", "ttt_embed_grad", "ttt_grad_ws_bytes", "ttt_grad_norm",
+           "ttt_clip_grads")
 
 _lib = None
 
@@ -91,8 +93,9 @@ def lib() -> ctypes.CDLL:
     L.ttt_grad_ws_bytes.argtypes = [i32, ctypes.POINTER(sz)]
     L.ttt_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, sz, vp]
     L.ttt_clip_grads.argtypes = [vp, vp, vp, i32, f32, vp, vp, vp, sz, vp]
-    for fn in (L.ttt_grad_ws_bytes, L.ttt_grad_norm, L.ttt_clip_grads, L.ttt_norm_pre, L.ttt_norm_post, L.ttt_norm_ws_bytes, L.ttt_norm_pre_grad, L.ttt_norm_post_grad,
-               L.ttt_embed, L.ttt_embed_grad_ws_bytes, L.ttt_embed_grad):
+    for fn in (L.ttt_norm_pre, L.ttt_norm_post, L.ttt_norm_ws_bytes, L.ttt_norm_pre_grad, L.ttt_norm_post_grad,
+               L.ttt_embed, L.ttt_embed_grad_ws_bytes, L.ttt_embed_grad, L.ttt_grad_ws_bytes, L.ttt_grad_norm,
+               L.ttt_clip_grads):
         fn.restype = i32
     _lib = L
     return L
@@ -365,7 +368,7 @@ class _Call:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         if t.get_device() != self.device or self.device < 0:  # -1: a host tensor
-            raise ValueError(f"{name} must be a device tensor" if not t.is_cuda else f"{name} must be on the current device")
+            raise ValueError(f"{name} must be {'on the current device' if t.is_cuda else 'a device tensor'}")
         if self.stream is not None:
             t.record_stream(self.stream)
         return t.data_ptr()
@@ -429,6 +432,7 @@ def _gate_kind(gate, y: torch.Tensor, d: int) -> int:
     raise ValueError(f"gate must have shape ({d},) or that of y, got {tuple(gate.shape)}")
 
 
+@lru_cache(maxsize=1024)  # sizes alone decide it
 def _norm_ws(rows: int, d: int) -> int:
     n = ctypes.c_size_t()
     _check(lib().ttt_norm_ws_bytes(rows, d, ctypes.byref(n)), "ttt_norm_ws_bytes")
@@ -448,7 +452,8 @@ def ttt_norm_pre(h: torch.Tensor, w: Optional[torch.Tensor] = None, eps: float =
     if x is None:
         x = c.like(h, dtype or h.dtype)
     px = c.arg(x, "x", dtype, h.shape)
-    _check(lib().ttt_norm_pre(ph, _DT[h.dtype], pw, _DT[wdt], eps, rows, d, px, _DT[x.dtype], c.on()), "ttt_norm_pre")
+    _check(lib().ttt_norm_pre(ph, _DT[h.dtype], pw, _DT[wdt], float(eps), rows, d, px, _DT[x.dtype], c.on()),
+           "ttt_norm_pre")
     return x
 
 
@@ -476,8 +481,9 @@ def ttt_norm_post(h: torch.Tensor, y: torch.Tensor, w: Optional[torch.Tensor] = 
     if x is None and (next_norm or w_next is not None):
         x = c.like(h, dtype or y.dtype)
     px = c.arg(x, "x", dtype, h.shape)
-    _check(lib().ttt_norm_post(ph, _DT[h.dtype], py, _DT[y.dtype], pw, pg, kind, pn, _DT[wdt], alpha, beta, eps, rows,
-                               d, po, px, _DT[y.dtype if x is None else x.dtype], c.on()), "ttt_norm_post")
+    _check(lib().ttt_norm_post(ph, _DT[h.dtype], py, _DT[y.dtype], pw, pg, kind, pn, _DT[wdt], float(alpha),
+                               float(beta), float(eps), rows, d, po, px, _DT[y.dtype if x is None else x.dtype],
+                               c.on()), "ttt_norm_post")
     return o, x
 
 
@@ -500,7 +506,7 @@ def ttt_norm_pre_grad(dx: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tenso
         dw = c.empty((d,), torch.float32)
         nws = _norm_ws(rows, d)
         ws = c.scratch(nws)
-    _check(lib().ttt_norm_pre_grad(pdx, _DT[dx.dtype], ph, _DT[h.dtype], pw, _DT[wdt], pin, eps, rows, d, pdh,
+    _check(lib().ttt_norm_pre_grad(pdx, _DT[dx.dtype], ph, _DT[h.dtype], pw, _DT[wdt], pin, float(eps), rows, d, pdh,
                                    dw.data_ptr() if dw is not None else None, ws.data_ptr() if ws is not None else None,
                                    nws, c.on()), "ttt_norm_pre_grad")
     return dh, dw
@@ -557,8 +563,8 @@ def ttt_norm_post_grad(dh_in: Optional[torch.Tensor], dx: Optional[torch.Tensor]
         ws = c.scratch(nws)
     out = [None if t is None else t.data_ptr() for t in (dw, dg, dn, ws)]
     _check(lib().ttt_norm_post_grad(pin, pdx, _DT[y.dtype if dx is None else dx.dtype], po, _DT[hdt], py, _DT[y.dtype],
-                                    pw, pg, kind, pn, _DT[wdt], alpha, beta, eps, rows, d, pdh, pdy, out[0], out[1],
-                                    out[2], out[3], nws, c.on()), "ttt_norm_post_grad")
+                                    pw, pg, kind, pn, _DT[wdt], float(alpha), float(beta), float(eps), rows, d, pdh,
+                                    pdy, out[0], out[1], out[2], out[3], nws, c.on()), "ttt_norm_post_grad")
     return NormGrads(dh, dy, dw, dg, dn)
 
 
@@ -584,6 +590,20 @@ def _ids_arg(c: _Call, ids: torch.Tensor) -> Tuple[int, int, int, int]:
     return ids.data_ptr(), n, 1, n
 
 
+@lru_cache(maxsize=1024)
+def _embed_ws(B: int, T: int, vocab: int, d: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().ttt_embed_grad_ws_bytes(B, T, vocab, d, ctypes.byref(n)), "ttt_embed_grad_ws_bytes")
+    return n.value
+
+
+@lru_cache(maxsize=1024)
+def _grad_ws(n: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().ttt_grad_ws_bytes(n, ctypes.byref(b)), "ttt_grad_ws_bytes")
+    return b.value
+
+
 def ttt_embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, x: Optional[torch.Tensor] = None,
               dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
     """Token embedding: x[t] = scale * E[ids[t]], a zero row for an id outside [0, vocab).
@@ -600,7 +620,8 @@ def ttt_embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, x: Optiona
     if x is None:
         x = c.empty(shape, dtype or E.dtype)
     px = c.arg(x, "x", dtype, shape)
-    _check(lib().ttt_embed(pE, _DT[E.dtype], vocab, d, pi, ld, B, T, scale, px, _DT[x.dtype], c.on()), "ttt_embed")
+    _check(lib().ttt_embed(pE, _DT[E.dtype], vocab, d, pi, ld, B, T, float(scale), px, _DT[x.dtype], c.on()),
+           "ttt_embed")
     return x
 
 
@@ -613,18 +634,17 @@ def ttt_embed_grad(dx: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float
     pi, ld, B, T = _ids_arg(c, ids)
     if dx.dim() != ids.dim() + 1 or dx.shape[:-1] != ids.shape:
         raise ValueError(f"dx must be ids' shape and d, got {tuple(dx.shape)} for ids {tuple(ids.shape)}")
-    d = dx.shape[-1]
+    d, vocab = dx.shape[-1], int(vocab)
     pdx = c.arg(dx, "dx")
     if dE is None:
         if accumulate:
             raise ValueError("dE must be given to accumulate into")
         dE = c.empty((vocab, d), dtype)
     pE = c.arg(dE, "dE", None, (vocab, d))
-    n = ctypes.c_size_t()
-    _check(lib().ttt_embed_grad_ws_bytes(B, T, vocab, d, ctypes.byref(n)), "ttt_embed_grad_ws_bytes")
-    ws = c.scratch(n.value)
-    _check(lib().ttt_embed_grad(pdx, _DT[dx.dtype], pi, ld, B, T, scale, vocab, d, pE, _DT[dE.dtype],
-                                1 if accumulate else 0, ws.data_ptr(), n.value, c.on()), "ttt_embed_grad")
+    nws = _embed_ws(B, T, vocab, d)
+    ws = c.scratch(nws)
+    _check(lib().ttt_embed_grad(pdx, _DT[dx.dtype], pi, ld, B, T, float(scale), vocab, d, pE, _DT[dE.dtype],
+                                1 if accumulate else 0, ws.data_ptr(), nws, c.on()), "ttt_embed_grad")
     return dE
 
 
@@ -679,9 +699,8 @@ def _grads_call(grads, norm, stream):
     if norm is None:
         norm = c.empty((1,), torch.float32)
     pn = c.arg(norm, "norm", torch.float32, (1,))
-    n = ctypes.c_size_t()
-    _check(lib().ttt_grad_ws_bytes(m.n, ctypes.byref(n)), "ttt_grad_ws_bytes")
-    return c, m, norm, pn, c.scratch(n.value), n.value
+    nws = _grad_ws(m.n)
+    return c, m, norm, pn, c.scratch(nws), nws
 
 
 def ttt_grad_norm(grads, norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -698,6 +717,6 @@ def ttt_clip_grads(grads, tau: float, out=None, norm: Optional[torch.Tensor] = N
     stay as they are."""
     c, m, norm, pn, ws, nws = _grads_call(grads, norm, stream)
     po = None if out is None else m.outputs(c, out)
-    _check(lib().ttt_clip_grads(*m.args, tau, None if po is None else po.buffer_info()[0], pn, ws.data_ptr(), nws,
-                                c.on()), "ttt_clip_grads")
+    _check(lib().ttt_clip_grads(*m.args, float(tau), None if po is None else po.buffer_info()[0], pn, ws.data_ptr(),
+                                nws, c.on()), "ttt_clip_grads")
     return norm

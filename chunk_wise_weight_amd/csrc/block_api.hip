@@ -68,8 +68,10 @@ int check_norm(const char *where, ttt_dtype h, ttt_dtype y, ttt_dtype x, ttt_dty
   if (d < 8 || d > kMaxWidth) return ttt_fail(TTT_E_SHAPE, "%s: d must be in [8, %d], got %d", where, kMaxWidth, d);
   if (rows < 0 || rows > kMaxRows)
     return ttt_fail(TTT_E_SHAPE, "%s: rows must be in [0, 2^31), got %lld", where, (long long)rows);
-  if (!(eps >= 1e-30f) || !std::isfinite(eps)) return ttt_fail(TTT_E_ARG, "%s: eps must be finite, at least 1e-30", where);
-  if (!std::isfinite(alpha) || !std::isfinite(beta)) return ttt_fail(TTT_E_ARG, "%s: alpha, beta must be finite", where);
+  if (!(eps >= 1e-30f) || !std::isfinite(eps))
+    return ttt_fail(TTT_E_ARG, "%s: eps must be finite, at least 1e-30", where);
+  if (!std::isfinite(alpha) || !std::isfinite(beta))
+    return ttt_fail(TTT_E_ARG, "%s: alpha, beta must be finite", where);
   return TTT_OK;
 }
 
@@ -296,7 +298,8 @@ int ttt_norm_post(const void *h, ttt_dtype h_dt, const void *y, ttt_dtype y_dt, 
 
 int ttt_norm_ws_bytes(int64_t rows, int d, size_t *bytes) {
   if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_norm_ws_bytes: bytes is NULL");
-  const int rc = check_norm("ttt_norm_ws_bytes", TTT_F32, TTT_F32, TTT_F32, TTT_F32, true, true, 1.f, 1.f, 1.f, rows, d);
+  const int rc =
+      check_norm("ttt_norm_ws_bytes", TTT_F32, TTT_F32, TTT_F32, TTT_F32, true, true, 1.f, 1.f, 1.f, rows, d);
   if (rc) return rc;
   *bytes = norm_ws_bytes(rows, d);
   return TTT_OK;
@@ -411,7 +414,8 @@ int ttt_embed(const void *E, ttt_dtype E_dt, int vocab, int d, const int32_t *id
   const long long n = (long long)B * T;
   if (n > 0 && (!E || !ids || !x)) return ttt_fail(TTT_E_NULL, "%s: E, ids or x is NULL", kWhere);
   rc = check_spans(kWhere,
-                   {{"E", E, (size_t)vocab * d * size_of(E_dt), size_of(E_dt)}, {"ids", ids, ids_bytes(B, T, ids_ld), 4}},
+                   {{"E", E, (size_t)vocab * d * size_of(E_dt), size_of(E_dt)},
+                    {"ids", ids, ids_bytes(B, T, ids_ld), 4}},
                    {{"x", x, (size_t)n * d * size_of(x_dt), size_of(x_dt)}}, {});
   if (rc) return rc;
   rc = ttt_check_device();
@@ -448,7 +452,8 @@ int ttt_embed_grad(const void *dx, ttt_dtype dx_dt, const int32_t *ids, int64_t 
   rc = check_ws(kWhere, ws, ws_bytes, need);
   if (rc) return rc;
   rc = check_spans(kWhere,
-                   {{"dx", dx, (size_t)n * d * size_of(dx_dt), size_of(dx_dt)}, {"ids", ids, ids_bytes(B, T, ids_ld), 4}},
+                   {{"dx", dx, (size_t)n * d * size_of(dx_dt), size_of(dx_dt)},
+                    {"ids", ids, ids_bytes(B, T, ids_ld), 4}},
                    {{"dE", dE, (size_t)vocab * d * size_of(dE_dt), size_of(dE_dt)}, {"ws", ws, need, 4}}, {});
   if (rc) return rc;
   rc = ttt_check_device();

@@ -8,6 +8,7 @@
 // workgroup's number; the last ones may lie past `groups`.
 constexpr long long kGridSide = 1 << 20;
 inline dim3 group_grid(long long groups) {
-  return groups <= kGridSide ? dim3((unsigned)groups) : dim3((unsigned)kGridSide, (unsigned)((groups + kGridSide - 1) / kGridSide));
+  if (groups <= kGridSide) return dim3((unsigned)groups);
+  return dim3((unsigned)kGridSide, (unsigned)((groups + kGridSide - 1) / kGridSide));
 }
 __device__ __forceinline__ long long group_index() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }

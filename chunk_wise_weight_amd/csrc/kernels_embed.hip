@@ -76,9 +76,9 @@ __global__ __launch_bounds__(1024) void k_embed(EmbedArgs A, int tr, int rpb) {
       expand(r[k], v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= A.scale;
-      if (HALVES)
+      if constexpr (HALVES)
         store_halves<STREAM>(dst + c8 * 4, d / 2, v);
-      else if (STREAM)
+      else if constexpr (STREAM)
         stream_w(dst + c, true, v);
       else
         store_w(dst + c, true, v);
@@ -312,7 +312,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(SortArgs S, int pas
   __shared__ uint32_t wsum[kSortWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = S.ids.n;
   if (CLEAR) clear_runs(S.seg, S.vocab, threadIdx.x, kSortThreads);
-  const int run = (n + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64, lo = wave * run;  // of a wave: up to kSmallRounds steps
+  // of a wave: up to kSmallRounds steps
+  const int run = (n + kSortWaves * 64 - 1) / (kSortWaves * 64) * 64, lo = wave * run;
   uint32_t key[kSmallRounds], pos[kSmallRounds];
 #pragma unroll
   for (int r = 0; r < kSmallRounds; ++r) {
@@ -400,7 +401,7 @@ __device__ __forceinline__ void put(G *p, int first, int accumulate, float scale
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] += old[j];
   }
-  if (STREAM)
+  if constexpr (STREAM)
     stream_w(p, true, s);
   else
     store_w(p, true, s);
@@ -492,7 +493,7 @@ __global__ __launch_bounds__(1024) void k_sums(SumArgs S, long long items, int t
   G *out = reinterpret_cast<G *>(S.dE) + v * d;
   for (int c8 = t0; c8 * 8 < d; c8 += tr) {
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (HALVES) {
+    if constexpr (HALVES) {
       add_rows<D, true>(S, c8 * 4, run.start, run.end, acc);
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] *= S.scale;
@@ -560,8 +561,8 @@ RowThreads row_threads(int d) {
 template <typename E, typename X, bool R, bool ONE, bool STREAM>
 void embed_launch(const EmbedArgs &a, int tr, int rpb, hipStream_t s) {
   const int rows = rpb * kEmbedRows<ONE, STREAM>;
-  hipLaunchKernelGGL((k_embed<E, X, R, ONE, STREAM>), group_grid((a.ids.n + rows - 1LL) / rows), dim3(tr * rpb), 0, s, a,
-                     tr, rpb);
+  const dim3 grid = group_grid((a.ids.n + rows - 1LL) / rows);
+  hipLaunchKernelGGL((k_embed<E, X, R, ONE, STREAM>), grid, dim3(tr * rpb), 0, s, a, tr, rpb);
 }
 
 template <typename E, typename X, bool R, bool ONE>

@@ -46,7 +46,8 @@ template <typename T>
 __device__ __forceinline__ double squares16(u32x4_any v) {
   double s = 0.0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) s += sizeof(T) == 4 ? square(__uint_as_float(v[j])) : square(lower(v[j])) + square(upper(v[j]));
+  for (int j = 0; j < 4; ++j)
+    s += sizeof(T) == 4 ? square(__uint_as_float(v[j])) : square(lower(v[j])) + square(upper(v[j]));
   return s;
 }
 // v tau / N with the factor as mantissa and exponent: as one fp32 number it
@@ -102,7 +103,8 @@ __device__ __forceinline__ void chunk_scale(const T *p, T *q, int n, int part, G
 #pragma unroll
     for (int k = 0; k < kPieces / PARTS; ++k) v[k] = load16<NT>(p + lo + (k * kThreads + threadIdx.x) * E);
 #pragma unroll
-    for (int k = 0; k < kPieces / PARTS; ++k) store16<NT>(q + lo + (k * kThreads + threadIdx.x) * E, scaled16<T>(v[k], f));
+    for (int k = 0; k < kPieces / PARTS; ++k)
+      store16<NT>(q + lo + (k * kThreads + threadIdx.x) * E, scaled16<T>(v[k], f));
     return;
   }
   for (int i = lo + threadIdx.x * E; i + E <= hi; i += kThreads * E)

@@ -579,7 +579,8 @@ __global__ __launch_bounds__(kDown * 8) void k_norm_params(NormArgs A, int npart
     return;
   }
   auto param = [&](const void *q) {
-    return !q ? 1.f : A.p_f32 ? reinterpret_cast<const float *>(q)[i] : bf16_to_f32(reinterpret_cast<const bf16_t *>(q)[i]);
+    if (!q) return 1.f;
+    return A.p_f32 ? reinterpret_cast<const float *>(q)[i] : bf16_to_f32(reinterpret_cast<const bf16_t *>(q)[i]);
   };
   if (A.dw) A.dw[i] = A.beta * (A.token_gate ? 1.f : param(A.gate)) * t;
   if (A.dgate_c) A.dgate_c[i] = A.beta * param(A.w) * t;
@@ -588,11 +589,11 @@ __global__ __launch_bounds__(kDown * 8) void k_norm_params(NormArgs A, int npart
 // ---- which instance ----
 template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE, int ROWS>
 void fwd_rows(const NormArgs &a, const Map &m, hipStream_t s) {
-  const dim3 grid = group_grid((a.rows + m.rpb * ROWS - 1) / (m.rpb * ROWS));
+  const dim3 grid = group_grid((a.rows + m.rpb * ROWS - 1) / (m.rpb * ROWS)), block(m.threads);
   if (POST && a.token_gate)
-    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, POST, ROWS>), grid, dim3(m.threads), 0, s, a, m.tr, m.rpb);
+    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, POST, ROWS>), grid, block, 0, s, a, m.tr, m.rpb);
   else
-    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, false, ROWS>), grid, dim3(m.threads), 0, s, a, m.tr, m.rpb);
+    hipLaunchKernelGGL((k_norm_fwd<H, Y, X, POST, NEXT, R, ONE, false, ROWS>), grid, block, 0, s, a, m.tr, m.rpb);
 }
 
 template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE>

@@ -84,14 +84,6 @@ __device__ __forceinline__ void stream_w(bf16_t *p, bool on, const float (&v)[8]
                        pack_bf16x2(v[6], v[7])};
   if (on) __builtin_nontemporal_store(r, reinterpret_cast<u32x4_any *>(p));
 }
-__device__ __forceinline__ void stream_w(float *p, bool on, const float (&v)[8]) {
-  u32x4_any r[2];
-  __builtin_memcpy(r, v, 32);
-  if (on) {
-    __builtin_nontemporal_store(r[0], reinterpret_cast<u32x4_any *>(p));
-    __builtin_nontemporal_store(r[1], reinterpret_cast<u32x4_any *>(p) + 1);
-  }
-}
 
 // Eight columns of a row as two runs of four, at p and `gap` elements behind
 // (half a row): the fp32 runs of neighbouring threads then lie side by side,
@@ -122,18 +114,6 @@ __device__ __forceinline__ void store_halves(float *p, int gap, const float (&v)
   } else {
     *reinterpret_cast<any *>(p) = a;
     *reinterpret_cast<any *>(p + gap) = b;
-  }
-}
-template <bool STREAM>
-__device__ __forceinline__ void store_halves(bf16_t *p, int gap, const float (&v)[8]) {
-  typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
-  const u2 a = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, b = {pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-  if (STREAM) {
-    __builtin_nontemporal_store(a, reinterpret_cast<u2 *>(p));
-    __builtin_nontemporal_store(b, reinterpret_cast<u2 *>(p + gap));
-  } else {
-    *reinterpret_cast<u2 *>(p) = a;
-    *reinterpret_cast<u2 *>(p + gap) = b;
   }
 }
 

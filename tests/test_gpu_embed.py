@@ -38,7 +38,8 @@ CASES = [  # B, T, vocab, d, kind
     (2, 1000, 50, 100, "skewed"), (3, 411, 512, 1024, "skewed"), (1, 4000, 3, 257, "uniform"),
     (4, 1025, 70001, 40, "skewed"), (1, 2049, 151936, 8, "uniform"), (5, 300, 1000, 2568, "holes"),
     (1, 32, 3, 64, "same"), (1, 33, 3, 64, "same"), (1, 96, 2, 64, "uniform"), (1, 4096, 20000, 24, "skewed"),
-    (1, 4097, 20000, 24, "skewed"), (3, 100001, 1000, 16, "skewed"), (1, 130, 9, 8200, "skewed"), (2, 33, 20, 20011, "uniform"), (1, 9000, 40, 16, "same"), (7, 3, 12, 2560, "uniform"),
+    (1, 4097, 20000, 24, "skewed"), (3, 100001, 1000, 16, "skewed"), (1, 130, 9, 8200, "skewed"),
+    (2, 33, 20, 20011, "uniform"), (1, 9000, 40, 16, "same"), (7, 3, 12, 2560, "uniform"),
 ]
 
 

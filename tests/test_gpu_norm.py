@@ -106,8 +106,8 @@ def parts_of(rows, d):
     return binding._norm_ws(rows, d) // (8 * d)
 
 
-SIZES = [(1, 8), (5, 9), (257, 64), (33, 100), (1031, 256), (7, 257), (130, 511), (12, 520), (61, 1023), (700, 2560), (8193, 520),
-         (3, 4097), (5, 8192), (2, 8200), (3, 9001), (1, 65536)]
+SIZES = [(1, 8), (5, 9), (257, 64), (33, 100), (1031, 256), (7, 257), (130, 511), (12, 520), (61, 1023), (700, 2560),
+         (8193, 520), (3, 4097), (5, 8192), (2, 8200), (3, 9001), (1, 65536)]
 
 
 @gpu
