@@ -114,8 +114,9 @@ struct Run {
 struct SortArgs {
   TokenIds ids;
   int vocab, shift, bins, tile, tiles;
-  const uint32_t *key_in, *pos_in;  // NULL in the first pass: the ids themselves
+  const uint32_t *key_in, *pos_in;  // NULL in the first pass: its counts read the ids, its positions are the tokens' own
   uint32_t *key_out, *pos_out;
+  uint32_t *key_first;  // where the first pass's counts leave the keys: the ids are read once, so counts and places agree
   uint32_t *hist;  // [tiles][bins]
   Run *seg;        // [vocab], cleared by the first pass's counts
   __device__ __forceinline__ uint32_t key(int i) const {
@@ -143,8 +144,11 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs S) {
   __syncthreads();
   const long long t0 = (long long)blockIdx.x * S.tile;
   const int hi = (int)(t0 + S.tile < S.ids.n ? t0 + S.tile : S.ids.n);
-  for (int i = (int)t0 + threadIdx.x; i < hi; i += kSortThreads)
-    atomicAdd(&cnt[(S.key(i) >> S.shift) & (S.bins - 1)], 1u);
+  for (int i = (int)t0 + threadIdx.x; i < hi; i += kSortThreads) {
+    const uint32_t key = S.key(i);
+    if (!S.key_in) S.key_first[i] = key;
+    atomicAdd(&cnt[(key >> S.shift) & (S.bins - 1)], 1u);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < S.bins; i += kSortThreads) S.hist[(long long)blockIdx.x * S.bins + i] = cnt[i];
 }
@@ -683,12 +687,14 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, int dx_f32, int dE_f32, hip
     S.pos_in = k ? (const uint32_t *)(ws + w.pos[(k - 1) & 1]) : nullptr;
     S.key_out = (uint32_t *)(ws + w.key[k & 1]);
     S.pos_out = (uint32_t *)(ws + w.pos[k & 1]);
+    S.key_first = (uint32_t *)(ws + w.key[1]);
     // the first pass also clears seg, with workgroups beyond the tiles' where the table is large
     int grid = p.tiles;
     const int clear = (a.vocab + kClearPerGroup - 1) / kClearPerGroup;
     if (k == 0 && clear > grid) grid = clear < kMaxTiles ? clear : kMaxTiles > grid ? kMaxTiles : grid;
     hipLaunchKernelGGL(k_sort_count, dim3(grid), dim3(kSortThreads), 0, s, S);
     if (!p.tiles) break;
+    if (k == 0) S.key_in = S.key_first;
     if (p.tile == kMinTile)
       hipLaunchKernelGGL(k_sort_place<true>, dim3(p.tiles), dim3(kSortThreads), 0, s, S);
     else

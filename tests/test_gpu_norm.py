@@ -427,6 +427,8 @@ def test_refusals_of_the_binding():
         ttt.ttt_norm_post(b, h)
     with pytest.raises(ValueError, match="gate"):
         ttt.ttt_norm_post(h, h.clone(), gate=torch.ones(4, 1, device="cuda"))
+    with pytest.raises(ValueError, match="row dimension"):
+        ttt.ttt_norm_post(w, w.clone(), gate=w)
     with pytest.raises(ValueError, match="one dtype"):
         ttt.ttt_norm_post(h, h.clone(), w, w_next=w.bfloat16())
     with pytest.raises(ValueError, match="gate must be"):
