@@ -399,6 +399,14 @@ def _tensor(t, name: str) -> torch.Tensor:
     return t
 
 
+def _out_dtype(dtype: Optional[torch.dtype], default: torch.dtype) -> torch.dtype:
+    if dtype is None:
+        return default
+    if dtype not in _DT:
+        raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+    return dtype
+
+
 def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
     if _tensor(t, name).dim() < 1:
         raise ValueError(f"{name} must have at least one dimension")
@@ -450,8 +458,10 @@ def ttt_norm_pre(h: torch.Tensor, w: Optional[torch.Tensor] = None, eps: float =
     ph, pw = c.arg(h, "h"), c.arg(w, "w", None, (d,))
     wdt = _params_dtype(("w", w))
     if x is None:
-        x = c.like(h, dtype or h.dtype)
-    px = c.arg(x, "x", dtype, h.shape)
+        x = c.like(h, _out_dtype(dtype, h.dtype))
+        px = x.data_ptr()
+    else:
+        px = c.arg(x, "x", dtype, h.shape)
     _check(lib().ttt_norm_pre(ph, _DT[h.dtype], pw, _DT[wdt], float(eps), rows, d, px, _DT[x.dtype], c.on()),
            "ttt_norm_pre")
     return x
@@ -477,10 +487,14 @@ def ttt_norm_post(h: torch.Tensor, y: torch.Tensor, w: Optional[torch.Tensor] = 
     wdt = _params_dtype(("w", w), ("w_next", w_next), ("gate", gate if kind == GATE_CHANNEL else None))
     if o is None:
         o = c.like(h, h.dtype)
-    po = c.arg(o, "o", h.dtype, h.shape)
+        po = o.data_ptr()
+    else:
+        po = c.arg(o, "o", h.dtype, h.shape)
     if x is None and (next_norm or w_next is not None):
-        x = c.like(h, dtype or y.dtype)
-    px = c.arg(x, "x", dtype, h.shape)
+        x = c.like(h, _out_dtype(dtype, y.dtype))
+        px = x.data_ptr()
+    else:
+        px = c.arg(x, "x", dtype, h.shape)
     _check(lib().ttt_norm_post(ph, _DT[h.dtype], py, _DT[y.dtype], pw, pg, kind, pn, _DT[wdt], float(alpha),
                                float(beta), float(eps), rows, d, po, px, _DT[y.dtype if x is None else x.dtype],
                                c.on()), "ttt_norm_post")
@@ -499,7 +513,9 @@ def ttt_norm_pre_grad(dx: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tenso
     wdt = _params_dtype(("w", w))
     if dh is None:
         dh = c.like(h, h.dtype)
-    pdh = c.arg(dh, "dh", h.dtype, h.shape)
+        pdh = dh.data_ptr()
+    else:
+        pdh = c.arg(dh, "dh", h.dtype, h.shape)
     dw = ws = None
     nws = 0
     if w is not None:
@@ -547,9 +563,14 @@ def ttt_norm_post_grad(dh_in: Optional[torch.Tensor], dx: Optional[torch.Tensor]
     wdt = _params_dtype(("w", w), ("w_next", w_next), ("gate", gate if kind == GATE_CHANNEL else None))
     if dh is None:
         dh = c.like(y, hdt)
+        pdh = dh.data_ptr()
+    else:
+        pdh = c.arg(dh, "dh", hdt, y.shape)
     if dy is None:
         dy = c.like(y, y.dtype)
-    pdh, pdy = c.arg(dh, "dh", hdt, y.shape), c.arg(dy, "dy", y.dtype, y.shape)
+        pdy = dy.data_ptr()
+    else:
+        pdy = c.arg(dy, "dy", y.dtype, y.shape)
     dw = c.empty((d,), torch.float32) if w is not None else None
     dn = c.empty((d,), torch.float32) if w_next is not None and dx is not None else None
     dg = None
@@ -618,8 +639,10 @@ def ttt_embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, x: Optiona
     pi, ld, B, T = _ids_arg(c, ids)
     shape = ids.shape + (d,)
     if x is None:
-        x = c.empty(shape, dtype or E.dtype)
-    px = c.arg(x, "x", dtype, shape)
+        x = c.empty(shape, _out_dtype(dtype, E.dtype))
+        px = x.data_ptr()
+    else:
+        px = c.arg(x, "x", dtype, shape)
     _check(lib().ttt_embed(pE, _DT[E.dtype], vocab, d, pi, ld, B, T, float(scale), px, _DT[x.dtype], c.on()),
            "ttt_embed")
     return x
@@ -639,8 +662,10 @@ def ttt_embed_grad(dx: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float
     if dE is None:
         if accumulate:
             raise ValueError("dE must be given to accumulate into")
-        dE = c.empty((vocab, d), dtype)
-    pE = c.arg(dE, "dE", None, (vocab, d))
+        dE = c.empty((vocab, d), _out_dtype(dtype, torch.float32))
+        pE = dE.data_ptr()
+    else:
+        pE = c.arg(dE, "dE", None, (vocab, d))
     nws = _embed_ws(B, T, vocab, d)
     ws = c.scratch(nws)
     _check(lib().ttt_embed_grad(pdx, _DT[dx.dtype], pi, ld, B, T, float(scale), vocab, d, pE, _DT[dE.dtype],
@@ -698,7 +723,9 @@ def _grads_call(grads, norm, stream):
     m = _Many(c, grads)
     if norm is None:
         norm = c.empty((1,), torch.float32)
-    pn = c.arg(norm, "norm", torch.float32, (1,))
+        pn = norm.data_ptr()
+    else:
+        pn = c.arg(norm, "norm", torch.float32, (1,))
     nws = _grad_ws(m.n)
     return c, m, norm, pn, c.scratch(nws), nws
 

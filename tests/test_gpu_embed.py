@@ -262,6 +262,10 @@ def test_refusals_of_the_binding():
         ttt.ttt_embed(E, ids, x=torch.zeros(24, 64, device="cuda"))
     with pytest.raises(ValueError, match="dx must be"):
         ttt.ttt_embed_grad(torch.zeros(4, 64, device="cuda"), ids, 10)
+    with pytest.raises(ValueError, match="dtype must be"):
+        ttt.ttt_embed(E, ids, dtype=torch.float16)
+    with pytest.raises(ValueError, match="dtype must be"):
+        ttt.ttt_embed_grad(torch.zeros(4, 6, 64, device="cuda"), ids, 10, dtype=torch.int32)
     with pytest.raises(ValueError, match="dE must be given"):
         ttt.ttt_embed_grad(torch.zeros(4, 6, 64, device="cuda"), ids, 10, accumulate=True)
     with pytest.raises(ValueError, match="shape"):

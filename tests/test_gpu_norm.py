@@ -439,6 +439,10 @@ def test_refusals_of_the_binding():
         ttt.ttt_norm_pre(h, x=h)
     with pytest.raises(ttt.TTTError, match="d must be"):
         ttt.ttt_norm_pre(torch.zeros(4, 7, device="cuda"))
+    for call in (lambda: ttt.ttt_norm_pre(h, dtype=torch.float16),
+                 lambda: ttt.ttt_norm_post(h, h.clone(), next_norm=True, dtype=torch.float64)):
+        with pytest.raises(ValueError, match="dtype must be"):
+            call()
 
 
 @gpu
