@@ -309,9 +309,11 @@ __global__ __launch_bounds__(256) void k_segments(const uint32_t *key, int n, in
 // The whole sort of up to kSmall tokens, and their segments, in one workgroup:
 // one launch in place of five, which would be most of a short batch's time.
 // CLEAR: it also clears seg, of a table that one workgroup clears sooner than a
-// launch. 1233 tokens take 9 us (and their whole gradient 19, 52 by tiles);
-// with twice the tokens per thread, for up to 8192, it is slower than tiles are
-// from 4097 on (50 us against 41 at 6216 tokens).
+// launch. Gradient calls of 64, 1233 and 4096 tokens, d 1024: 14.1, 14.1 and
+// 21.0 us against 23.3, 22.9 and 22.7 by tiles with a table of 512 rows; 30.0,
+// 33.3 and 42.9 against 33.3, 36.7 and 39.6 with 32000 rows (and their clear). With
+// eight tokens per thread, 6216 tokens take 29.8 us against 25.8 by tiles, and
+// 50.5 against 42.0 with 32000 rows.
 template <bool CLEAR>
 __global__ __launch_bounds__(kSortThreads) void k_sort_small(SortArgs S, int passes, int digit, Chunk *chunks) {
   __shared__ uint32_t skey[kSmall], spos[kSmall];
