@@ -146,6 +146,16 @@ struct Cols {
 };
 
 // ---- forward ----
+//
+// Which product joins a sum unrounded is written out here. Left to the
+// compiler it differs from form to form of a kernel, and with it the last bit
+// of a row: with the number of rows, say, or without a next norm.
+__device__ __forceinline__ float add_square(float s, float v) { return __builtin_fmaf(v, v, s); }
+// alpha h + beta a w n
+__device__ __forceinline__ float after_block(const NormArgs &A, float h, float a, float w, float n) {
+  return __builtin_fmaf(A.alpha, h, A.beta * a * w * n);
+}
+
 // One workgroup per ROWS neighbouring rows (ONE: their addresses are the same
 // for all its threads), or per rpb narrow rows. Bound by memory: 32768 rows of
 // 2560 with an fp32 stream, bf16 y and x (1.007 GB) take 180 us, 5.6 TB/s, where
@@ -184,7 +194,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs A, int tr, int rpb) 
       expand(ry[k], y);
       s[k] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[k] += cols.own(j, y[j] * y[j]);
+      for (int j = 0; j < 8; ++j) s[k] = add_square(s[k], cols.own(j, y[j]));
     }
     row_sum<ROWS>(s, tr, red, turn);
 #pragma unroll
@@ -194,7 +204,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs A, int tr, int rpb) 
       expand(ry[k], y);
       if (TOKEN) expand(ra[k], t);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[k][j] = A.alpha * o[k][j] + A.beta * t[j] * w[j] * (y[j] * q);
+      for (int j = 0; j < 8; ++j) o[k][j] = after_block(A, o[k][j], t[j], w[j], y[j] * q);
       store_w(row_of<H>(A.o, row0 + k, d) + c, cols.mine && row0 + k < A.rows, o[k]);
     }
   } else {
@@ -209,7 +219,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs A, int tr, int rpb) 
     for (int k = 0; k < ROWS; ++k) {
       s[k] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[k] += cols.own(j, o[k][j] * o[k][j]);
+      for (int j = 0; j < 8; ++j) s[k] = add_square(s[k], cols.own(j, o[k][j]));
     }
     row_sum<ROWS>(s, tr, red, turn);
 #pragma unroll
@@ -248,7 +258,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormArgs A) {
       else
         load_param(A.gate, A.p_f32, c * W, true, a);
 #pragma unroll
-      for (int j = 0; j < W; ++j) o[j] = A.alpha * o[j] + A.beta * a[j] * w[j] * (yy[j] * q);
+      for (int j = 0; j < W; ++j) o[j] = after_block(A, o[j], a[j], w[j], yy[j] * q);
     }
   };
   if (POST) {
@@ -257,7 +267,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormArgs A) {
       float yy[W];
       load_w(y + c * W, true, yy);
 #pragma unroll
-      for (int j = 0; j < W; ++j) s[0] += yy[j] * yy[j];
+      for (int j = 0; j < W; ++j) s[0] = add_square(s[0], yy[j]);
     }
     row_sum<1>(s, 1024, red, turn);
     q = row_rms(s[0], d, A.eps);
@@ -268,7 +278,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormArgs A) {
       float o[W];
       after(c, o);
 #pragma unroll
-      for (int j = 0; j < W; ++j) s[0] += o[j] * o[j];
+      for (int j = 0; j < W; ++j) s[0] = add_square(s[0], o[j]);
     }
     row_sum<1>(s, 1024, red, turn);
     r = row_rms(s[0], d, A.eps);

@@ -455,3 +455,23 @@ def test_more_rows_than_a_grid_side_counts():
     want = ttt.ttt_norm_pre(h[-2:].clone(), eps=EPS)
     assert torch.equal(x[-2:], want)
     assert bool((x[:-1] == 1).all())
+
+
+@gpu
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+@pytest.mark.parametrize("types", TYPES, ids=["fff", "fbb", "ffb", "bbb"])
+@pytest.mark.parametrize("d", [64, 511, 520, 1023, 2560, 8200])
+def test_a_row_does_not_depend_on_how_many_there_are(d, types, gate):
+    """The same bits in a batch long enough for two rows per workgroup, in a short one, and without the next norm."""
+    rows, kw = 8195, dict(alpha=0.75, beta=1.5, eps=EPS)
+    p = inputs(rows, d, types, gate, seed=d)
+    v = {k: dev(t) for k, t in p.items()}
+    o, x = ttt.ttt_norm_post(v["h"], v["y"], v["w"], gate=v["gate"], w_next=v["w_next"], dtype=types[2], **kw)
+    first = ttt.ttt_norm_pre(v["h"], v["w_next"], eps=EPS, dtype=types[2])
+    for lo, hi in ((0, 1), (4000, 4101), (rows - 2, rows)):
+        h, y = v["h"][lo:hi].clone(), v["y"][lo:hi].clone()
+        a = v["gate"][lo:hi].clone() if gate == "token" else v["gate"]
+        o2, x2 = ttt.ttt_norm_post(h, y, v["w"], gate=a, w_next=v["w_next"], dtype=types[2], **kw)
+        assert torch.equal(o2, o[lo:hi]) and torch.equal(x2, x[lo:hi])
+        assert torch.equal(ttt.ttt_norm_pre(h, v["w_next"], eps=EPS, dtype=types[2]), first[lo:hi])
+    assert torch.equal(ttt.ttt_norm_post(v["h"], v["y"], v["w"], gate=v["gate"], **kw)[0], o)
