@@ -115,8 +115,23 @@ __device__ __forceinline__ void row_sum(float (&s)[NS], int tr, float (*red)[16]
   turn ^= 1;
 }
 
-// r of a row from its sum of squares
-__device__ __forceinline__ float row_rms(float sumsq, int d, float eps) { return rsqrtf(sumsq / (float)d + eps); }
+// A row's sums of squares and of products are formed as if of elements times A.shrink = 2^-k, with 4^k >= d, so that a
+// sum is no larger than the largest of its terms and leaves fp32 only where a term itself would (the squares of d
+// elements of 1e18 pass 3.4e38 from d = 340 on). A thread's own eight terms are added first and then shrunk: one or two
+// products per sum, where shrinking each element took 1% more time in all (32768x2560 bf16). A power of two costs the
+// sums no bits; what it moves below fp32 is nothing beside eps, which is 1e-30 at least. The launch passes the powers:
+// as arguments they take scalar registers, computed by the threads they took three to six vector registers.
+NormArgs scaled(NormArgs a) {
+  int k = 0;
+  while (1LL << 2 * k < a.d) ++k;
+  a.shrink = ldexpf(1.f, -k);
+  a.grow = ldexpf(1.f, k);
+  a.mean = ldexpf((float)a.d, -2 * k);
+  return a;
+}
+
+// r of a row from its sum of shrunk squares
+__device__ __forceinline__ float row_rms(float sumsq, const NormArgs &A) { return rsqrtf(sumsq / A.mean + A.eps); }
 
 template <typename T>
 __device__ __forceinline__ const T *row_of(const void *p, long long row, int d) {
@@ -195,11 +210,12 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs A, int tr, int rpb) 
       s[k] = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[k] = add_square(s[k], cols.own(j, y[j]));
+      s[k] *= A.shrink * A.shrink;
     }
     row_sum<ROWS>(s, tr, red, turn);
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-      const float q = row_rms(s[k], d, A.eps);
+      const float q = row_rms(s[k], A);
       expand(ro[k], o[k]);
       expand(ry[k], y);
       if (TOKEN) expand(ra[k], t);
@@ -220,11 +236,12 @@ __global__ __launch_bounds__(1024) void k_norm_fwd(NormArgs A, int tr, int rpb) 
       s[k] = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[k] = add_square(s[k], cols.own(j, o[k][j]));
+      s[k] *= A.shrink * A.shrink;
     }
     row_sum<ROWS>(s, tr, red, turn);
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
-      const float r = row_rms(s[k], d, A.eps);
+      const float r = row_rms(s[k], A);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[k][j] = wn[j] * (o[k][j] * r);
       store_w(row_of<X>(A.x, row0 + k, d) + c, cols.mine && row0 + k < A.rows, o[k]);
@@ -267,10 +284,10 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormArgs A) {
       float yy[W];
       load_w(y + c * W, true, yy);
 #pragma unroll
-      for (int j = 0; j < W; ++j) s[0] = add_square(s[0], yy[j]);
+      for (int j = 0; j < W; ++j) s[0] = add_square(s[0], yy[j] * A.shrink);
     }
     row_sum<1>(s, 1024, red, turn);
-    q = row_rms(s[0], d, A.eps);
+    q = row_rms(s[0], A);
   }
   if (NEXT) {
     float s[1] = {0.f};
@@ -278,10 +295,10 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormArgs A) {
       float o[W];
       after(c, o);
 #pragma unroll
-      for (int j = 0; j < W; ++j) s[0] = add_square(s[0], o[j]);
+      for (int j = 0; j < W; ++j) s[0] = add_square(s[0], o[j] * A.shrink);
     }
     row_sum<1>(s, 1024, red, turn);
-    r = row_rms(s[0], d, A.eps);
+    r = row_rms(s[0], A);
   }
   for (int c = threadIdx.x; c < v; c += 1024) {
     float o[W];
@@ -307,28 +324,30 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(NormArgs A) {
 //
 // mean(p y q) needs do, which needs r and m. Put in, sum(p y) is a sum of
 // three products that do not: with k = beta a w,
-//   sum(k do y) = sum(k dh_in y) + r sum(k g y) - r^2 m sum(k o y),
+//   sum(k do y) = sum(k dh_in y) + r sum(k g y) - r m (r sum(k o y)),
 // so one pass over the registers and one exchange between the waves gives all
-// the row's sums.
+// the row's sums. r and m meet o and y as n = o r and y q only: r^2 by itself
+// would lose its bits below 1e-38, where o is large.
 
 // What a gradient call keeps of one row after its sums.
 struct RowStat {
-  float r, r2m, q, q2s;
+  float r, rm, q, qs;  // m = mean(g n), s = mean(p y q)
 };
 
 template <bool POST, bool NEXT>
-__device__ __forceinline__ RowStat row_stat(const float (&s)[6], int d, float eps) {
+__device__ __forceinline__ RowStat row_stat(const float (&s)[6], const NormArgs &A) {
   RowStat t{0.f, 0.f, 0.f, 0.f};
-  const float inv = 1.f / (float)d;
-  float py = s[3];
+  const float inv = 1.f / (float)A.d;
+  float py = s[3];  // shrunk
   if (NEXT) {
-    t.r = row_rms(s[0], d, eps);
-    t.r2m = t.r * t.r * (s[1] * t.r * inv);
-    py += t.r * s[4] - t.r2m * s[5];
+    t.r = row_rms(s[0], A);
+    const float grown = t.r * A.grow;
+    t.rm = t.r * (s[1] * grown * inv);
+    py += t.r * s[4] - t.rm * (grown * s[5]);
   }
   if (POST) {
-    t.q = row_rms(s[2], d, eps);
-    t.q2s = t.q * t.q * (py * t.q * inv);
+    t.q = row_rms(s[2], A);
+    t.qs = t.q * (py * (t.q * A.grow) * inv);
   }
   return t;
 }
@@ -374,7 +393,11 @@ struct BwdRow {
 // sums over the workgroups, 5.5 TB/s; 32768 bf16 rows of 1024 (0.27 GB) 58 us.
 // The loads of a workgroup's next row are issued before this row's results are
 // stored: waits for memory operations are counted in their order, so loads
-// behind the stores would be waited for together with them.
+// behind the stores would be waited for together with them. AHEAD: not where
+// a thread of 1024, with 128 registers, would have to spill for it (13 to 75 of
+// them): 8192 rows of 5120 with an fp32 stream take 156 us so against 174, with
+// a gate per token 184 against 409. bf16 rows without that gate spill none and
+// gain from it (119 us without, 111 with), as a first norm's do (125, 120).
 template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE, bool TOKEN, int MOST>
 __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs A, int tr, int rpb) {
   __shared__ float red[2][16][6];
@@ -401,10 +424,12 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs A, int tr, int rpb) 
   const long long step = (long long)gridDim.x * rpb;
   long long row = (long long)blockIdx.x * rpb + sub;
   BwdRow<H, Y, X, POST, NEXT, TOKEN> in;
-  in.load(A, row, c, mine && row < A.rows);
+  constexpr bool AHEAD = MOST <= 512 || !POST || !NEXT || (!TOKEN && sizeof(H) == 2);
+  if (AHEAD) in.load(A, row, c, mine && row < A.rows);
   for (long long row0 = (long long)blockIdx.x * rpb; row0 < A.rows; row0 += step, row += step) {
     const bool on = mine && row < A.rows;
     float o[8], g[8], di[8], y[8], a[8];
+    if (!AHEAD) in.load(A, row, c, on);
     if (NEXT) {
       expand(in.o, o);
       expand(in.dx, g);
@@ -412,28 +437,41 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs A, int tr, int rpb) 
     expand(in.di, di);
     if (POST) expand(in.y, y);
     if (POST && TOKEN) expand(in.a, a);
-    in.load(A, row + step, c, mine && row + step < A.rows);
+    if (AHEAD) in.load(A, row + step, c, mine && row + step < A.rows);
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       add_terms<POST, NEXT>(s, NEXT ? cols.own(j, o[j]) : 0.f, NEXT ? g[j] * wn[j] : 0.f, di[j],
                             POST ? cols.own(j, y[j]) : 0.f, !POST ? 0.f : TOKEN ? k[j] * a[j] : k[j]);
+    if (NEXT) {
+      s[0] *= A.shrink * A.shrink;
+      s[1] *= A.shrink;
+    }
+    if (POST) {
+      s[2] *= A.shrink * A.shrink;
+      s[3] *= A.shrink;
+    }
+    if (POST && NEXT) {
+      s[4] *= A.shrink;
+      s[5] *= A.shrink * A.shrink;
+    }
     row_sum<6>(s, tr, red, turn);
-    const RowStat t = row_stat<POST, NEXT>(s, d, A.eps);
+    const RowStat t = row_stat<POST, NEXT>(s, A);
     float dh[8], dy[8], da[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float v = di[j];
       if (NEXT) {
-        v += t.r * (g[j] * wn[j]) - t.r2m * o[j];
-        dwn[j] += g[j] * (o[j] * t.r);
+        const float n = o[j] * t.r;
+        v += t.r * (g[j] * wn[j]) - t.rm * n;
+        dwn[j] += g[j] * n;
       }
       dh[j] = A.alpha * v;
       if (POST) {
         const float yn = y[j] * t.q, ta = TOKEN ? a[j] : 1.f;
         ds[j] += v * ta * yn;
         da[j] = v * w[j] * yn;
-        dy[j] = t.q * (k[j] * ta * v) - t.q2s * y[j];
+        dy[j] = t.q * (k[j] * ta * v) - t.qs * yn;
       }
     }
     store_w(row_of<H>(A.dh, row, d) + c, on, dh);
@@ -515,10 +553,11 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormArgs A) {
       read(c);
 #pragma unroll
       for (int j = 0; j < W; ++j)
-        add_terms<POST, NEXT>(s, NEXT ? o[j] : 0.f, NEXT ? g[j] : 0.f, di[j], POST ? y[j] : 0.f, POST ? k[j] : 0.f);
+        add_terms<POST, NEXT>(s, NEXT ? o[j] * A.shrink : 0.f, NEXT ? g[j] : 0.f, di[j], POST ? y[j] * A.shrink : 0.f,
+                              POST ? k[j] : 0.f);
     }
     row_sum<6>(s, 1024, red, turn);
-    const RowStat t = row_stat<POST, NEXT>(s, d, A.eps);
+    const RowStat t = row_stat<POST, NEXT>(s, A);
     for (int c = threadIdx.x; c < v; c += 1024) {
       read(c);
       float dh[W], dy[W], da[W], dwn[W], ds[W];
@@ -526,15 +565,16 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_wide(NormArgs A) {
       for (int j = 0; j < W; ++j) {
         float u = di[j];
         if (NEXT) {
-          u += t.r * g[j] - t.r2m * o[j];
-          dwn[j] = dxv[j] * (o[j] * t.r);
+          const float n = o[j] * t.r;
+          u += t.r * g[j] - t.rm * n;
+          dwn[j] = dxv[j] * n;
         }
         dh[j] = A.alpha * u;
         if (POST) {
           const float yn = y[j] * t.q;
           ds[j] = u * a[j] * yn;
           da[j] = u * w[j] * yn;
-          dy[j] = t.q * (k[j] * u) - t.q2s * y[j];
+          dy[j] = t.q * (k[j] * u) - t.qs * yn;
         }
       }
       store_w(row_of<H>(A.dh, row, d) + c * W, true, dh);
@@ -697,12 +737,14 @@ size_t norm_ws_bytes(long long rows, int d) {
   }                                                                                                       \
   return hipErrorInvalidValue
 
-hipError_t launch_norm_fwd(const NormArgs &a, NormTypes t, hipStream_t s) {
-  if (a.rows <= 0) return hipSuccess;
+hipError_t launch_norm_fwd(const NormArgs &args, NormTypes t, hipStream_t s) {
+  if (args.rows <= 0) return hipSuccess;
+  const NormArgs a = scaled(args);
   const bool post = a.y != nullptr, next = a.x != nullptr;
   NORM_CASES(fwd);
 }
 
-hipError_t launch_norm_bwd(const NormArgs &a, NormTypes t, bool post, bool next, hipStream_t s) {
+hipError_t launch_norm_bwd(const NormArgs &args, NormTypes t, bool post, bool next, hipStream_t s) {
+  const NormArgs a = scaled(args);
   NORM_CASES(bwd);
 }

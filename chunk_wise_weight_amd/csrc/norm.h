@@ -23,6 +23,8 @@ struct NormArgs {
   void *dh, *dy, *dgate_t;  // gradients of h, y and a gate per token
   float *dw, *dgate_c, *dw_next;  // gradients of the parameters, or NULL
   float *part;              // workspace
+  float shrink, grow, mean;  // of a row's sums: 2^-k, 2^k, and what a sum of shrunk squares is divided by for their
+                             // mean, 4^-k d; set by the launchers
 };
 
 // Types of one call: residual stream, block output, block input (1: fp32, 0: bf16).

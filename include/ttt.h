@@ -320,7 +320,8 @@ int ttt_workspace_bytes(ttt_handle *h, size_t *bytes);
  *
  * With w = NULL the rows are normalised without a gain (the layer's
  * RMS-normalised input rows). Sums are fp32, and each result is rounded once:
- * |elements| past 1e18, whose squares leave fp32, are not supported.
+ * |elements| of h, y and o past 1e18, whose squares leave fp32, are not
+ * supported (a row's sum of squares may leave it).
  *
  *   rows    : 0 .. 2^31-1.
  *   h, o    : [rows][d] residual stream, h_dt. o may be h (in place).
@@ -357,6 +358,9 @@ int ttt_norm_post(const void *h, ttt_dtype h_dt, const void *y, ttt_dtype y_dt, 
  *                        token. dw, dw_next and dgate per channel may be NULL;
  *                        dgate per token may not. dw_next is not written
  *                        without dx.
+ *
+ * Rows as large as above are taken where |beta * gate * w| is at most 32 (the
+ * formulas hold products beta * gate * w * y * o).
  *
  * dh has h_dt and may be dh_in (in place); dy has y_dt and may be y. The sums
  * over the rows are fp32, in an order fixed by (rows, d): the same call gives

@@ -475,3 +475,42 @@ def test_a_row_does_not_depend_on_how_many_there_are(d, types, gate):
         assert torch.equal(o2, o[lo:hi]) and torch.equal(x2, x[lo:hi])
         assert torch.equal(ttt.ttt_norm_pre(h, v["w_next"], eps=EPS, dtype=types[2]), first[lo:hi])
     assert torch.equal(ttt.ttt_norm_post(v["h"], v["y"], v["w"], gate=v["gate"], **kw)[0], o)
+
+
+@gpu
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+@pytest.mark.parametrize("types", TYPES, ids=["fff", "fbb", "ffb", "bbb"])
+@pytest.mark.parametrize("rows,d", [(3, 8), (35, 100), (9, 511), (5, 2560), (3, 4097), (2, 8200), (2, 9001), (1, 65536)])
+def test_elements_of_1e18(rows, d, types, gate):
+    """The largest elements that are supported: rows whose sums of squares leave fp32 (from a width of about 340 on), and
+    whose r^2 lies at the end of its range. The bounds are those of any other row."""
+    alpha, beta = 0.75, 1.5
+    p = inputs(rows, d, types, gate, seed=d, w=F if types[2] == F or d % 2 else B)
+    gen = torch.Generator().manual_seed(d)
+    for k in ("h", "y"):
+        sign = torch.randint(0, 2, (rows, d), generator=gen) * 2.0 - 1.0
+        p[k] = (sign * (0.5e18 + 0.49e18 * torch.rand((rows, d), generator=gen))).to(p[k].dtype)
+    v = {k: dev(t) for k, t in p.items()}
+    o64, x64, bo, bx = post64(p, alpha, beta, True)
+    o, x = ttt.ttt_norm_post(v["h"], v["y"], v["w"], gate=v["gate"], alpha=alpha, beta=beta, eps=EPS,
+                             w_next=v["w_next"], dtype=types[2])
+    assert_close(o, o64, bo + half_step(types[0]) * (o64.abs() + bo), "o")
+    assert_close(x, x64, bx + half_step(types[2]) * (x64.abs() + bx), "x")
+    want = grads64(p, alpha, beta, True, True, parts_of(rows, d))
+    got = ttt.ttt_norm_post_grad(v["dh"], v["dx"], v["h"], v["y"], v["w"], gate=v["gate"], alpha=alpha, beta=beta,
+                                 eps=EPS, w_next=v["w_next"])
+    for k, t in got._asdict().items():
+        if t is not None:
+            val, bound = want[k]
+            assert_close(t, val, bound + half_step(t.dtype) * (val.abs() + bound), k)
+    h, w, dx = p["h"].double(), p["w_next"].double(), p["dx"].double()
+    r, c = rms64(h, EPS), chain(d)
+    assert_close(ttt.ttt_norm_pre(v["h"], v["w_next"], eps=EPS, dtype=types[2]), w * h * r,
+                 (c + 2 * half_step(types[2])) * (w * h * r).abs(), "first norm")
+    g = dx * w
+    want = p["dh"].double() * 2.0 ** -60 + r * (g - h * r * (g * h * r).mean(-1, keepdim=True))
+    bound = 2 * c * (p["dh"].double().abs() * 2.0 ** -60 +
+                     r * (g.abs() + h.abs() * r * (g * h * r).abs().mean(-1, keepdim=True)))
+    # a residual path's gradient as small as this one's share
+    dh, _ = ttt.ttt_norm_pre_grad(v["dx"], v["h"], v["w_next"], eps=EPS, dh_in=v["dh"] * 2.0 ** -60)
+    assert_close(dh, want, bound + half_step(types[0]) * (want.abs() + bound), "dh")
