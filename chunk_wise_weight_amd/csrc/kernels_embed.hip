@@ -6,11 +6,11 @@
 // The gradient does not add with atomics, whose order would change its bits:
 // the tokens are sorted by id, stably, so that each table row's tokens lie
 // together in the order of their positions, and each row's columns are summed
-// in fp32 in that order, by one thread each. Ids are skewed in real text, so a row of more than
-// kChunk tokens is cut at multiples of kChunk sorted tokens; the pieces are
-// summed side by side and joined in order. The sort is a radix sort of (id,
-// position) by counting: per pass, each workgroup counts its tile's digits,
-// and then places its tokens from the counts of all tiles.
+// in fp32 in that order, by one thread each. Ids are skewed in real text, so a
+// row of more than kChunk tokens is cut at multiples of kChunk sorted tokens;
+// the pieces are summed side by side and joined in order, in fp64. The sort is
+// a radix sort of (id, position) by counting: per pass, each workgroup counts
+// its tile's digits, and then places its tokens from the counts of all tiles.
 #include "embed.h"
 #include "vec8.h"
 
@@ -517,29 +517,50 @@ __global__ __launch_bounds__(1024) void k_sums(SumArgs S, long long items, int t
 
 // A long row from its pieces: workgroup (chunk, 512 columns) for the long row
 // that begins in the chunk, each wave a run of the pieces, the waves' sums
-// joined in order.
-constexpr int kJoinWaves = 8;
+// joined in order. Eight pieces are added in fp32 and their sums in fp64, since
+// a batch may hold one id (a padding, say) in most of its up to 2^27 tokens: so
+// many pieces one behind the other in fp32 lose up to half of a piece's last
+// place each, together 2e-4 of the row at 2^22 tokens and some percent at 2^27.
+// Each eight pieces are under way at once: a padding id in 131072 bf16 tokens of
+// 2560 takes 389 us with its sort and sums (pieces as the compiler orders their
+// loads 557, all in fp64 420 and more, all in fp32 450).
+constexpr int kJoinWaves = 8, kJoinStep = 8;  // waves, and pieces of a step
 template <typename G, bool R>
 __global__ __launch_bounds__(kJoinWaves * 64) void k_join(SumArgs S) {
-  __shared__ float sum[kJoinWaves][64][9];
-  const Chunk k = S.chunks[blockIdx.x];
-  const int d = S.d, i = k.v1 >= 0 ? 1 : 0;
-  const int v = i ? k.v1 : k.starts0 ? k.v0 : -1;
+  __shared__ double sum[kJoinWaves][64][9];
+  const Chunk chunk = S.chunks[blockIdx.x];
+  const int d = S.d, i = chunk.v1 >= 0 ? 1 : 0;
+  const int v = i ? chunk.v1 : chunk.starts0 ? chunk.v0 : -1;
   if (v < 0) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int c = (blockIdx.y * 64 + lane) * 8;
   const int at = R && c + 8 > d ? d - 8 : c;
   const int last = (S.seg[v].end - 1) / kChunk;  // pieces: (blockIdx.x, i), then (j, 0) up to the last chunk
   const int pieces = last - (int)blockIdx.x + 1, run = (pieces + kJoinWaves - 1) / kJoinWaves;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  double acc[8] = {0., 0., 0., 0., 0., 0., 0., 0.};
   if (c < d) {
     const int p0 = wave * run, p1 = p0 + run < pieces ? p0 + run : pieces;
-#pragma unroll 8
-    for (int p = p0; p < p1; ++p) {
-      float x[8];
-      load_w(S.part + (((long long)blockIdx.x + p) * 2 + (p == 0 ? i : 0)) * d + at, true, x);
+    auto piece = [&](int p) {
+      return load_raw(S.part + (((long long)blockIdx.x + p) * 2 + (p == 0 ? i : 0)) * d + at, true);
+    };
+    int p = p0;
+    for (; p + kJoinStep <= p1; p += kJoinStep) {
+      Raw8<float> r[kJoinStep];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += x[j];
+      for (int k = 0; k < kJoinStep; ++k) r[k] = piece(p + k);
+      __builtin_amdgcn_sched_barrier(0);  // all of them under way before the first is waited for
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float x = r[0].f[j];
+#pragma unroll
+        for (int k = 1; k < kJoinStep; ++k) x += r[k].f[j];
+        acc[j] += (double)x;
+      }
+    }
+    for (; p < p1; ++p) {
+      const Raw8<float> r = piece(p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += (double)r.f[j];
     }
   }
 #pragma unroll
@@ -550,7 +571,10 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_join(SumArgs S) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] += sum[w][lane][j];
   }
-  put<false>(reinterpret_cast<G *>(S.dE) + (long long)v * d + at, R ? c - at : 0, S.accumulate, S.scale, acc);
+  float s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = (float)acc[j];
+  put<false>(reinterpret_cast<G *>(S.dE) + (long long)v * d + at, R ? c - at : 0, S.accumulate, S.scale, s);
 }
 
 // ---- which instance ----

@@ -381,7 +381,7 @@ int ttt_norm_post_grad(const void *dh_in, const void *dx, ttt_dtype x_dt, const 
  *
  *   ttt_embed      : x[t] = scale * E[ids[t]], rounded once
  *   ttt_embed_grad : dE[v] = scale * sum of dx[t] over the tokens t with
- *                    ids[t] = v, summed in fp32, rounded once. With
+ *                    ids[t] = v, summed in fp32, scaled and rounded. With
  *                    accumulate = 0 all of dE is written (zero rows for ids
  *                    that do not occur); otherwise the sums are added to the
  *                    rows that occur and the others are left alone.
@@ -397,8 +397,8 @@ int ttt_norm_post_grad(const void *dh_in, const void *dx, ttt_dtype x_dt, const 
  *   scale : finite.
  *
  * The gradient sorts the tokens by id and sums each row's in the order of
- * their positions, a long row's in pieces of 32: the same call gives the same
- * bits. ws: see ttt_embed_grad_ws_bytes (about 16 bytes per token, 8 per table
+ * their positions, a long row's in pieces of 32 that join in fp64 by eights:
+ * the same call gives the same bits. ws: see ttt_embed_grad_ws_bytes (about 16 bytes per token, 8 per table
  * row and d / 4 bytes per token for the pieces).
  */
 int ttt_embed(const void *E, ttt_dtype E_dt, int vocab, int d, const int32_t *ids, int64_t ids_ld, int B, int T,

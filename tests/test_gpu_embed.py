@@ -281,3 +281,23 @@ def test_more_rows_than_a_grid_side_counts():
     x = ttt.ttt_embed(E, ids)
     assert torch.equal(x[:, 0], E[:, 0][ids.long()]) and torch.equal(x[-5:], E[ids[-5:].long()])
     assert torch.equal(x[:, -1], x[:, 0])
+
+
+@gpu
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,d", [(2 ** 17 + 5, 72), (2 ** 22, 8), (2 ** 22 - 17, 9)])
+def test_one_id_in_a_long_batch(n, d, accumulate):
+    """A padding id that takes most of a batch: the pieces of 32 tokens are summed in fp32 (31 additions), eight
+    pieces again (7), and those sums in fp64, so the error's bound does not grow with the tokens. All gradients are the
+    same number, chosen so that a running fp32 sum of the pieces would lose up to half of a piece's last place with each
+    of them, always downwards."""
+    value = (1 + 501 * 2.0 ** -20) / 32
+    dx = torch.full((n, d), value, device="cuda")
+    ids = torch.full((n,), 1, dtype=torch.int32, device="cuda")
+    ids[::1000] = 0
+    dE = torch.ones((3, d), device="cuda") if accumulate else None
+    got = ttt.ttt_embed_grad(dx, ids, 3, dE=dE, accumulate=accumulate)
+    count = torch.bincount(ids.long(), minlength=3).double().cpu()[:, None]
+    ref = count * value + (1.0 if accumulate else 0.0)
+    # 31 + 7 additions, and a rounding each of the joined sum, its scaling and the accumulation
+    assert_close(got, ref.expand(3, d), (41 * U32 * ref).expand(3, d), "dE")
