@@ -158,8 +158,11 @@ int check_extents(const char *where, std::vector<Extent> &e) {
   return TTT_OK;
 }
 
-// The tables of a call, empty tensors left out and tensors that follow one
-// another in memory (views of one buffer) taken as one.
+// The tables of a launch, empty tensors left out and tensors that follow one
+// another in memory (views of one buffer), with their outputs, taken as one:
+// 2000 gradients of 1000 values in one buffer take 5 us so and 97 one by one.
+// The norm's are made without outputs (NULL), so that its sum, which follows
+// the cuts, does not change its last bit with where the outputs lie.
 std::vector<GradTable> grad_tables(const void *const *grads, const int64_t *numel, const int32_t *dt, int n,
                                    void *const *out) {
   struct One {
@@ -203,9 +206,9 @@ std::vector<GradTable> grad_tables(const void *const *grads, const int64_t *nume
   return tables;
 }
 
-// Norm of the tables and, with `clip`, the scaling by it.
-int run_grads(const char *where, const std::vector<GradTable> &tables, bool clip, float tau, float *norm, void *ws,
-              hipStream_t s) {
+// Norm of the tables and, with `clip`, the scaling of its tables by it.
+int run_grads(const char *where, const std::vector<GradTable> &tables, const std::vector<GradTable> *clip, float tau,
+              float *norm, void *ws, hipStream_t s) {
   GradFactor *factor = (GradFactor *)ws;
   double *part = (double *)ws + 1;
   long long chunks = 0;
@@ -221,8 +224,9 @@ int run_grads(const char *where, const std::vector<GradTable> &tables, bool clip
     n += groups;
   }
   int rc = ttt_launched(launch_grad_norm(part, n, tau, norm, clip ? factor : nullptr, s), where);
-  for (const GradTable &t : tables) {
-    if (rc || !clip) break;
+  if (!clip) return rc;
+  for (const GradTable &t : *clip) {
+    if (rc) break;
     rc = ttt_launched(launch_grad_scale(t, factor, stream, s), where);
   }
   return rc;
@@ -492,7 +496,7 @@ int ttt_grad_norm(const void *const *grads, const int64_t *numel, const int32_t 
     rc = check_extents(kWhere, e);
     if (!rc) rc = ttt_check_device();
     if (rc) return rc;
-    return run_grads(kWhere, grad_tables(grads, numel, dt, n, nullptr), false, 0.f, norm, ws,
+    return run_grads(kWhere, grad_tables(grads, numel, dt, n, nullptr), nullptr, 0.f, norm, ws,
                      (hipStream_t)hip_stream);
   } catch (...) {
     return ttt_fail(TTT_E_NOMEM, "%s: out of host memory", kWhere);
@@ -521,7 +525,10 @@ int ttt_clip_grads(const void *const *grads, const int64_t *numel, const int32_t
     rc = check_extents(kWhere, e);
     if (!rc) rc = ttt_check_device();
     if (rc) return rc;
-    return run_grads(kWhere, grad_tables(grads, numel, dt, n, out), true, tau, norm, ws, (hipStream_t)hip_stream);
+    const std::vector<GradTable> tables = grad_tables(grads, numel, dt, n, nullptr);
+    if (!out) return run_grads(kWhere, tables, &tables, tau, norm, ws, (hipStream_t)hip_stream);
+    const std::vector<GradTable> copies = grad_tables(grads, numel, dt, n, out);
+    return run_grads(kWhere, tables, &copies, tau, norm, ws, (hipStream_t)hip_stream);
   } catch (...) {
     return ttt_fail(TTT_E_NOMEM, "%s: out of host memory", kWhere);
   }

@@ -415,10 +415,12 @@ int ttt_embed_grad(const void *dx, ttt_dtype dx_dt, const int32_t *ids, int64_t 
  *   ttt_clip_grads : the same, and out[i] = g[i] * min(1, tau / N)
  *
  * (The layer's own updates are clipped by ttt_set_clip.) Squares are summed in
- * fp64, in an order fixed by the sizes: the same call gives the same bits. A
- * norm that is not finite (a gradient holds an infinity or NaN) clips nothing:
- * the gradients come out as they are, and *norm says so. The host learns of
- * nothing and waits for nothing.
+ * fp64, in an order fixed by the sizes and types of the list and by which of
+ * its neighbours adjoin in memory too (those are taken as one): the same call
+ * gives the same bits, and both entry points the same norm, wherever outputs
+ * lie. A norm that is not finite (a gradient holds an infinity or NaN) clips
+ * nothing: the gradients come out as they are, and *norm says so. The host
+ * learns of nothing and waits for nothing.
  *
  *   grads : host array of n device pointers; numel, dt: host arrays of their
  *           element counts (together at most 2^40) and types (ttt_dtype). The

@@ -258,3 +258,35 @@ def test_refusals_of_the_binding():
         ttt.ttt_clip_grads([torch.zeros(8, 8, device="cuda").t()], 1.0)
     with pytest.raises(ValueError, match="shape"):
         ttt.ttt_grad_norm(g, norm=torch.zeros((), device="cuda"))
+
+
+def at_a_tie():
+    """Two tensors whose norm tells the order of its sum. The first one's squares add to 1 + 2^-23 + 5 s, s = 2^-52 the
+    step of a sum near 1; a square of the second is b^2 = s / 20, 252 of them 12.6 s. Added apart and then at once they
+    move the sum by 13 s; added by fours, eights, ... 128 (a wave whose first lane holds the first tensor) by
+    0 + 0 + 1 + 2 + 3 + 6 = 12. The root of the sum with 12 s is the tie 1 + 2^-24, which fp32 rounds to 1, with 13 s
+    it lies past it."""
+    first = torch.tensor([1.0, 2.0 ** -12, 2.0 ** -12, math.sqrt(5.0) * 2.0 ** -26])
+    return first, torch.full((252,), math.sqrt(0.05) * 2.0 ** -26)
+
+
+@gpu
+@pytest.mark.parametrize("gap,want", [(0, 1.0), (1, 1.0 + 2.0 ** -23), (1000, 1.0 + 2.0 ** -23)])
+def test_the_norm_does_not_depend_on_where_outputs_lie(gap, want):
+    """Gradients that adjoin in memory are summed as one, others apart, whichever call it is and wherever it writes."""
+    first, second = at_a_tie()
+    buf = torch.full((4 + gap + 252,), 77.0, device="cuda")
+    g = [buf[:4], buf[4 + gap:]]
+    g[0].copy_(first), g[1].copy_(second)
+    norms = [float(ttt.ttt_grad_norm(g))]
+    for apart in (0, 3):
+        obuf = torch.full((4 + apart + 252,), 77.0, device="cuda")
+        out = [obuf[:4], obuf[4 + apart:]]
+        norms.append(float(ttt.ttt_clip_grads(g, 0.5, out=out)))
+        # the factor is 1/2 (1 - 2^-24 or so), rounded once, as is each product
+        for a, b in zip(out, (first, second)):
+            assert_close(a, b.double() * 0.5, 4 * U32 * b.double(), "out")
+        assert bool((obuf[4:4 + apart] == 77).all())
+        norms.append(float(ttt.ttt_clip_grads(g, 0.5, out=[g[0].clone(), out[1]])))
+    norms.append(float(ttt.ttt_clip_grads(g, 2.0)))
+    assert norms == [want] * len(norms)
