@@ -358,10 +358,9 @@ class _Call:
             return None
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-        if dtype is None:
-            if t.dtype not in _DT:
-                raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-        elif t.dtype != dtype:
+        if t.dtype not in _DT:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+        if dtype is not None and t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")

@@ -514,3 +514,16 @@ def test_elements_of_1e18(rows, d, types, gate):
     # a residual path's gradient as small as this one's share
     dh, _ = ttt.ttt_norm_pre_grad(v["dx"], v["h"], v["w_next"], eps=EPS, dh_in=v["dh"] * 2.0 ** -60)
     assert_close(dh, want, bound + half_step(types[0]) * (want.abs() + bound), "dh")
+
+
+@gpu
+def test_an_output_of_another_type_is_refused_by_name():
+    h = torch.zeros(4, 64, device="cuda")
+    for dt in (torch.float64, torch.float16):
+        x = h.to(dt)
+        with pytest.raises(ValueError, match="x must be float32 or bfloat16"):
+            ttt.ttt_norm_pre(h, x=x, dtype=dt)
+        with pytest.raises(ValueError, match="x must be float32 or bfloat16"):
+            ttt.ttt_norm_post(h, h.clone(), x=x, dtype=dt)
+        with pytest.raises(ValueError, match="x must be float32 or bfloat16"):
+            ttt.ttt_embed(h, torch.zeros(4, dtype=torch.int32, device="cuda"), x=x, dtype=dt)
