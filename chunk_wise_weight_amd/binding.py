@@ -398,6 +398,15 @@ def _tensor(t, name: str) -> torch.Tensor:
     return t
 
 
+# Sizes from this on are refused here: ctypes passes the low bits of a number that a C int does not hold without a word.
+# (Compared where they come up: a call of about 10 us has no fraction of one for a function around it.)
+_INT = 2 ** 31
+
+
+def _too_large(n: int, name: str) -> ValueError:
+    return ValueError(f"{name} must be below 2^31, got {n}")
+
+
 def _out_dtype(dtype: Optional[torch.dtype], default: torch.dtype) -> torch.dtype:
     if dtype is None:
         return default
@@ -410,6 +419,8 @@ def _rows(t: torch.Tensor, name: str) -> Tuple[int, int]:
     if _tensor(t, name).dim() < 1:
         raise ValueError(f"{name} must have at least one dimension")
     d = t.shape[-1]
+    if d >= _INT:
+        raise _too_large(d, f"the last dimension of {name}")
     return (t.numel() // d if d else 0), d
 
 
@@ -593,6 +604,9 @@ def _ids_arg(c: _Call, ids: torch.Tensor) -> Tuple[int, int, int, int]:
     [:, :T] view of the layer's [B][T+1] ids)."""
     if _tensor(ids, "ids").dtype != torch.int32:
         raise ValueError(f"ids must be {torch.int32}, got {ids.dtype}")
+    n = ids.numel()
+    if n >= _INT:
+        raise _too_large(n, "the number of ids")
     if not ids.is_cuda:
         raise ValueError("ids must be a device tensor")
     if ids.get_device() != c.device:
@@ -606,7 +620,6 @@ def _ids_arg(c: _Call, ids: torch.Tensor) -> Tuple[int, int, int, int]:
         return ids.data_ptr(), ids.stride(0), B, T
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous or a 2-D view of contiguous rows")
-    n = ids.numel()
     return ids.data_ptr(), n, 1, n
 
 
@@ -632,8 +645,10 @@ def ttt_embed(E: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, x: Optiona
     the table's)."""
     if _tensor(E, "E").dim() != 2:
         raise ValueError("E must be [vocab][d]")
-    c = _Call(E.device, stream)
     vocab, d = E.shape
+    if vocab >= _INT or d >= _INT:
+        raise _too_large(max(vocab, d), "each dimension of E")
+    c = _Call(E.device, stream)
     pE = c.arg(E, "E")
     pi, ld, B, T = _ids_arg(c, ids)
     shape = ids.shape + (d,)
@@ -653,10 +668,14 @@ def ttt_embed_grad(dx: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float
     """Gradient of ttt_embed's table: dE[v] = scale * sum of dx[t] over ids[t] = v, [vocab][d] in `dtype` (or that of
     a given dE). With accumulate the sums are added to dE, which must then be given."""
     c = _Call(_tensor(dx, "dx").device, stream)
+    vocab, d = int(vocab), dx.shape[-1] if dx.dim() else 0
+    if not -_INT < vocab < _INT:
+        raise _too_large(vocab, "vocab")
+    if d >= _INT:
+        raise _too_large(d, "the last dimension of dx")
     pi, ld, B, T = _ids_arg(c, ids)
     if dx.dim() != ids.dim() + 1 or dx.shape[:-1] != ids.shape:
         raise ValueError(f"dx must be ids' shape and d, got {tuple(dx.shape)} for ids {tuple(ids.shape)}")
-    d, vocab = dx.shape[-1], int(vocab)
     pdx = c.arg(dx, "dx")
     if dE is None:
         if accumulate:

@@ -301,3 +301,22 @@ def test_one_id_in_a_long_batch(n, d, accumulate):
     ref = count * value + (1.0 if accumulate else 0.0)
     # 31 + 7 additions, and a rounding each of the joined sum, its scaling and the accumulation
     assert_close(got, ref.expand(3, d), (41 * U32 * ref).expand(3, d), "dE")
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Sizes that a 32-bit int would hold the low bits of only (meta tensors: no memory behind them)."""
+    def ids(*shape):
+        return torch.empty(shape, dtype=torch.int32, device="meta")
+
+    def dx(*shape):
+        return torch.empty(shape, device="meta")
+
+    big = 2 ** 32 + 64
+    for call in (lambda: ttt.ttt_embed(dx(big, 64), ids(4)), lambda: ttt.ttt_embed(dx(10, big), ids(4)),
+                 lambda: ttt.ttt_embed_grad(dx(4, 64), ids(4), big),
+                 lambda: ttt.ttt_embed_grad(dx(4, 64), ids(4), 64 - 2 ** 32),
+                 lambda: ttt.ttt_embed_grad(dx(4, big), ids(4), 10),
+                 lambda: ttt.ttt_embed_grad(dx(big, 64), ids(big), 10),
+                 lambda: ttt.ttt_embed_grad(dx(2, big, 64), ids(2, big + 1)[:, :big], 10)):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            call()

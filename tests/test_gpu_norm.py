@@ -527,3 +527,12 @@ def test_an_output_of_another_type_is_refused_by_name():
             ttt.ttt_norm_post(h, h.clone(), x=x, dtype=dt)
         with pytest.raises(ValueError, match="x must be float32 or bfloat16"):
             ttt.ttt_embed(h, torch.zeros(4, dtype=torch.int32, device="cuda"), x=x, dtype=dt)
+
+
+def test_widths_past_32_bits_are_refused():
+    """A width that a 32-bit int would hold the low bits of only (meta tensors: no memory behind them)."""
+    wide = torch.empty((1, 2 ** 32 + 64), device="meta")
+    for call in (lambda: ttt.ttt_norm_pre(wide), lambda: ttt.ttt_norm_post(wide, wide),
+                 lambda: ttt.ttt_norm_pre_grad(wide, wide), lambda: ttt.ttt_norm_post_grad(wide, wide, wide, wide)):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            call()
