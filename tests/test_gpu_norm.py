@@ -536,3 +536,81 @@ def test_widths_past_32_bits_are_refused():
                  lambda: ttt.ttt_norm_pre_grad(wide, wide), lambda: ttt.ttt_norm_post_grad(wide, wide, wide, wide)):
         with pytest.raises(ValueError, match=r"2\^31"):
             call()
+
+
+# Workgroups of a gradient launch take rows in steps. Sizes where every form takes several: narrow rows side by side,
+# ragged rows, rows of more than 512 threads, and rows too wide for registers; the last step not full. (8195, 1023) is
+# also the forward with two ragged rows per workgroup, and an odd number of them.
+STEPS = [(40000, 64), (9001, 256), (5003, 511), (8195, 1023), (601, 4097), (600, 8192), (600, 8200), (601, 9001)]
+
+
+@gpu
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+@pytest.mark.parametrize("types", TYPES, ids=["fff", "fbb", "ffb", "bbb"])
+@pytest.mark.parametrize("rows,d", STEPS)
+def test_gradients_of_several_steps(rows, d, types, gate):
+    """Bounds as above, the sums over the rows counted at their longest: a launch has 256 workgroups at least, each of
+    which takes ceil(rows / 256) rows at most one after another and joins 32 rows side by side at most; of the at most
+    2048 partial sums 16 follow one another, and seven steps join the slices: under ceil(rows / 256) + 16 + 48."""
+    alpha, beta = 0.75, 1.5
+    p = inputs(rows, d, types, gate, seed=rows, w=F if types[2] == F or d % 2 else B)
+    v = {k: dev(t) for k, t in p.items()}
+    with torch.device("cuda"):  # the formulas in 64 bits, computed there for speed
+        o64, x64, bo, bx = post64(v, alpha, beta, True)
+        want = grads64(v, alpha, beta, True, True, 256)
+    o, x = ttt.ttt_norm_post(v["h"], v["y"], v["w"], gate=v["gate"], alpha=alpha, beta=beta, eps=EPS,
+                             w_next=v["w_next"], dtype=types[2])
+    assert_close(o, o64.cpu(), (bo + half_step(types[0]) * (o64.abs() + bo)).cpu(), "o")
+    assert_close(x, x64.cpu(), (bx + half_step(types[2]) * (x64.abs() + bx)).cpu(), "x")
+    keep = [v[k].clone() for k in ("dx", "h")]
+    dh, dy = Guarded((rows, d), types[0]), Guarded((rows, d), types[1], off=1)
+    got = ttt.ttt_norm_post_grad(v["dh"], v["dx"], v["h"], v["y"], v["w"], gate=v["gate"], alpha=alpha, beta=beta,
+                                 eps=EPS, w_next=v["w_next"], dh=dh.t, dy=dy.t)
+    torch.cuda.synchronize()
+    dh.check(), dy.check()
+    have = {k: t for k, t in got._asdict().items() if t is not None}
+    assert set(have) == set(want)
+    for k, t in have.items():
+        val, bound = want[k]
+        assert_close(t, val.cpu(), (bound + half_step(t.dtype) * (val.abs() + bound)).cpu(), k)
+    # without the residual path's gradient, and without the next norm's: the same forms with fewer inputs
+    with torch.device("cuda"):
+        some = [(None, v["dx"], grads64(v, alpha, beta, True, False, 256)),
+                (v["dh"], None, grads64(v, alpha, beta, False, True, 256))]
+    for dh_in, dx, want in some:
+        part = ttt.ttt_norm_post_grad(dh_in, dx, v["h"], v["y"], v["w"], gate=v["gate"], alpha=alpha, beta=beta,
+                                      eps=EPS, w_next=v["w_next"])
+        for k, t in part._asdict().items():
+            if t is not None:
+                val, bound = want[k]
+                assert_close(t, val.cpu(), (bound + half_step(t.dtype) * (val.abs() + bound)).cpu(), k)
+    # in place: the same bits, and the inputs as they were
+    again = ttt.ttt_norm_post_grad(v["dh"], v["dx"], v["h"], v["y"], v["w"], gate=v["gate"], alpha=alpha, beta=beta,
+                                   eps=EPS, w_next=v["w_next"], dh=v["dh"], dy=v["y"])
+    assert again.dh is v["dh"] and again.dy is v["y"]
+    for k, t in have.items():
+        assert torch.equal(getattr(again, k), t), k
+    assert torch.equal(v["dx"], keep[0]) and torch.equal(v["h"], keep[1])
+
+
+@gpu
+@pytest.mark.parametrize("types", TYPES, ids=["fff", "fbb", "ffb", "bbb"])
+@pytest.mark.parametrize("rows,d", STEPS)
+def test_first_norm_gradient_of_several_steps(rows, d, types):
+    p = inputs(rows, d, types, "none", seed=rows + 1, w=F)
+    v = {k: dev(t) for k, t in p.items()}
+    c, adds = chain(d), (-(-rows // 256) + 16 + 48) * U32
+    h, w, dx, din = (v[k].double() for k in ("h", "w_next", "dx", "dh"))
+    r = rms64(h, EPS)
+    g = dx * w
+    want = din + r * (g - h * r * (g * h * r).mean(-1, keepdim=True))
+    bound = 2 * c * (din.abs() + r * (g.abs() + h.abs() * r * (g * h * r).abs().mean(-1, keepdim=True)))
+    t = dx * h * r
+    dh, dw = ttt.ttt_norm_pre_grad(v["dx"], v["h"], v["w_next"], eps=EPS, dh_in=v["dh"])
+    assert_close(dh, want.cpu(), (bound + half_step(types[0]) * (want.abs() + bound)).cpu(), "dh")
+    assert_close(dw, t.sum(0).cpu(), ((adds + c) * t.abs().sum(0)).cpu(), "dw")
+    again, dw2 = ttt.ttt_norm_pre_grad(v["dx"], v["h"], v["w_next"], eps=EPS, dh_in=v["dh"], dh=v["dh"])
+    assert again is v["dh"] and torch.equal(again, dh) and torch.equal(dw2, dw)
+    ref = w * h * r
+    x = ttt.ttt_norm_pre(v["h"], v["w_next"], eps=EPS, dtype=types[2])
+    assert_close(x, ref.cpu(), ((c + 2 * half_step(types[2])) * ref.abs()).cpu(), "x")
