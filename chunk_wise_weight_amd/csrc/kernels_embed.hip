@@ -26,6 +26,7 @@ constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kClearPerGroup = 2048;  // table rows whose segments one workgroup clears
 static_assert(kMinTile == kSortThreads, "a token per thread");
 constexpr int kSmallRounds = 4, kSmall = kSortThreads * kSmallRounds;  // tokens that one workgroup sorts by itself
+constexpr int kSmallRows = 8191, kSmallWide = 3000;  // and of tables of more rows than kSmallRows
 constexpr int kSmallClear = 16384;  // table rows whose segments one workgroup clears in passing
 constexpr int kChunk = 32;       // sorted tokens of one piece of a long row
 
@@ -309,11 +310,16 @@ __global__ __launch_bounds__(256) void k_segments(const uint32_t *key, int n, in
 // The whole sort of up to kSmall tokens, and their segments, in one workgroup:
 // one launch in place of five, which would be most of a short batch's time.
 // CLEAR: it also clears seg, of a table that one workgroup clears sooner than a
-// launch. Gradient calls of 64, 1233 and 4096 tokens, d 1024: 14.1, 14.1 and
-// 21.0 us against 23.3, 22.9 and 22.7 by tiles with a table of 512 rows; 30.0,
-// 33.3 and 42.9 against 33.3, 36.7 and 39.6 with 32000 rows (and their clear). With
-// eight tokens per thread, 6216 tokens take 29.8 us against 25.8 by tiles, and
-// 50.5 against 42.0 with 32000 rows.
+// launch. Accumulating gradient calls in a captured graph, 256 columns, ids
+// drawn with a share of 1 / rank, this way and by tiles: 512 rows, 2560 tokens
+// 26.4 and 30.0 us, 4096 29.7 and 30.5; 4000 rows, 4096 tokens 30.2 both ways;
+// 8000 rows, 3200 tokens 30.8 and 31.7, 4096 32.5 and 31.9. The keys of more
+// rows than that have 14 bits or more, and placing them takes two more steps a
+// pass: 16000 rows, 3000 tokens 31.0 and 31.8, 3500 32.9 and 32.0; 32000 rows,
+// 2560 tokens 31.2 and 31.7, 3000 32.0 both ways, 4096 35.7 and 33.3; 151936
+// rows, 3000 tokens 33.9 and 34.2, 3200 34.3 and 33.6. Eight tokens per thread
+// are too many for any table: 6216 tokens, 1024 columns, 29.8 and 25.8 us with
+// 512 rows, 50.5 and 42.0 with 32000.
 template <bool CLEAR>
 __global__ __launch_bounds__(kSortThreads) void k_sort_small(SortArgs S, int passes, int digit, Chunk *chunks) {
   __shared__ uint32_t skey[kSmall], spos[kSmall];
@@ -697,7 +703,7 @@ hipError_t launch_embed_grad(const EmbedGradArgs &a, int dx_f32, int dE_f32, hip
   S.tiles = p.tiles;
   S.hist = (uint32_t *)(ws + w.hist);
   S.seg = (Run *)(ws + w.seg);
-  const bool small = n > 0 && n <= kSmall;
+  const bool small = n > 0 && n <= (a.vocab <= kSmallRows ? kSmall : kSmallWide);
   if (small) {
     S.key_out = (uint32_t *)(ws + w.key[0]);
     S.pos_out = (uint32_t *)(ws + w.pos[0]);

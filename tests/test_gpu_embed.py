@@ -320,3 +320,12 @@ def test_sizes_past_32_bits_are_refused():
                  lambda: ttt.ttt_embed_grad(dx(2, big, 64), ids(2, big + 1)[:, :big], 10)):
         with pytest.raises(ValueError, match=r"2\^31"):
             call()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["skewed", "holes"])
+@pytest.mark.parametrize("T,vocab", [(2999, 8192), (3000, 8192), (3001, 8192), (4095, 8191), (4096, 8191), (4097, 8191),
+                                     (4096, 8192), (3001, 151936), (1025, 8191), (1024, 8192)])
+def test_gradient_where_the_sort_changes(T, vocab, kind):
+    """One workgroup sorts up to 4096 tokens of a table of up to 8191 rows, 3000 of larger ones; more go by tiles."""
+    test_embed_grad(1, T, vocab, 24, kind, F, F)
