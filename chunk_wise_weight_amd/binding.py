@@ -328,7 +328,9 @@ def ttt_workspace_bytes(h: Handle) -> int:
 # output that is not given is allocated. With `stream` the work, and the
 # outputs made here, belong to that stream, as under torch.cuda.stream(stream);
 # what the tensors hold must be ready on it. They record no autograd graph:
-# each gradient is a call of its own.
+# each gradient is a call of its own. Nor does autograd see what a call writes
+# into a tensor it was given (no version is counted), so one that a graph has
+# saved for its backward must not be given for an output.
 
 _DT = {torch.float32: TTT_F32, torch.bfloat16: TTT_BF16}
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2

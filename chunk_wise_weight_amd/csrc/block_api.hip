@@ -116,6 +116,7 @@ size_t ids_bytes(int B, int T, int64_t ids_ld) {
 constexpr int kMaxTensors = 1 << 20;
 constexpr long long kMaxNumel = 1LL << 40;  // of all tensors: their chunks count in 32 bits
 // gradients of more bytes than this are read and written past the caches, of which the last level holds 256 MiB
+// (measured at 140 MB and 2.1 GB, with nothing between)
 constexpr long long kStreamGrads = 512LL << 20;
 
 // the workgroups' sums and, before them, the factor

@@ -18,7 +18,8 @@ namespace {
 constexpr int kCUs = 256;
 // bytes of rows that a gradient launch keeps under way on each CU
 constexpr int kBwdBytes = 48 * 1024;
-constexpr int kTwoRows = 8192;    // rows from which a workgroup after a block takes two: still several for every CU
+// rows from which a workgroup after a block takes two: still several for every CU (measured at 32768 rows of 2560)
+constexpr int kTwoRows = 8192;
 constexpr int kMaxNarrow = 8192;  // widest row whose elements stay in registers: 1024 threads of 8
 
 // How rows lie on threads: `tr` threads own a row, 8 elements each (a power
@@ -173,7 +174,7 @@ __device__ __forceinline__ float after_block(const NormArgs &A, float h, float a
 
 // One workgroup per ROWS neighbouring rows (ONE: their addresses are the same
 // for all its threads), or per rpb narrow rows. Bound by memory: 32768 rows of
-// 2560 with an fp32 stream, bf16 y and x (1.007 GB) take 180 us, 5.6 TB/s, where
+// 2560 with an fp32 stream, bf16 y and x (1.007 GB) take 177 us, 5.7 TB/s, where
 // a copy of those arrays in the same pattern takes 165 to 170; bf16 rows of
 // 1024 before a block 6.1 TB/s. After a block, with its two sums one behind the
 // other, two rows at a time share the barriers and have their loads under way
@@ -389,8 +390,9 @@ struct BwdRow {
 };
 
 // Partial sums of workgroup b, [b][2][part_ld(d)]: the gradient of w', then S.
-// Bound by memory: 32768 rows of 2560 as above (1.51 GB) take 272 us with the
-// sums over the workgroups, 5.5 TB/s; 32768 bf16 rows of 1024 (0.27 GB) 58 us.
+// Bound by memory: 32768 rows of 2560 as above (1.51 GB) take 269 us with the
+// sums over the workgroups, 5.6 TB/s (up to a fifth more in the first 20 ms of a
+// load); 32768 bf16 rows of 1024 (0.27 GB) 57 us.
 // The loads of a workgroup's next row are issued before this row's results are
 // stored: waits for memory operations are counted in their order, so loads
 // behind the stores would be waited for together with them. AHEAD: not where
@@ -673,7 +675,7 @@ hipError_t fwd(const NormArgs &a, hipStream_t s) {
 template <typename H, typename Y, typename X, bool POST, bool NEXT, bool R, bool ONE, bool TOKEN>
 void bwd_launch(const NormArgs &a, const Map &m, unsigned grid, hipStream_t s) {
   // up to 512 threads a kernel may hold 256 registers each and spills none (340 us and more at 32768 rows of 2560 with
-  // the 128 that 1024 threads allow)
+  // the 128 that 1024 threads allow, where it loads ahead)
   if (!ONE || m.threads <= 512)
     hipLaunchKernelGGL((k_norm_bwd<H, Y, X, POST, NEXT, R, ONE, TOKEN, 512>), dim3(grid), dim3(m.threads), 0, s, a,
                        m.tr, m.rpb);

@@ -363,8 +363,8 @@ int ttt_norm_post(const void *h, ttt_dtype h_dt, const void *y, ttt_dtype y_dt, 
  * formulas hold products beta * gate * w * y * o).
  *
  * dh has h_dt and may be dh_in (in place); dy has y_dt and may be y. The sums
- * over the rows are fp32, in an order fixed by (rows, d): the same call gives
- * the same bits. With rows = 0 the parameters' gradients are written as zero.
+ * over the rows are fp32, in an order fixed by rows, d and the types: the same
+ * call gives the same bits. With rows = 0 the parameters' gradients are written as zero.
  * ws is needed when a parameter's gradient is wanted.
  */
 int ttt_norm_ws_bytes(int64_t rows, int d, size_t *bytes);

@@ -480,10 +480,11 @@ def test_a_row_does_not_depend_on_how_many_there_are(d, types, gate):
 @gpu
 @pytest.mark.parametrize("gate", ["none", "channel", "token"])
 @pytest.mark.parametrize("types", TYPES, ids=["fff", "fbb", "ffb", "bbb"])
-@pytest.mark.parametrize("rows,d", [(3, 8), (35, 100), (9, 511), (5, 2560), (3, 4097), (2, 8200), (2, 9001), (1, 65536)])
+@pytest.mark.parametrize("rows,d", [(3, 8), (35, 100), (9, 511), (5, 2560), (3, 4097), (2, 8200), (2, 9001),
+                                    (1, 65536)])
 def test_elements_of_1e18(rows, d, types, gate):
-    """The largest elements that are supported: rows whose sums of squares leave fp32 (from a width of about 340 on), and
-    whose r^2 lies at the end of its range. The bounds are those of any other row."""
+    """The largest elements that are supported: rows whose sums of squares leave fp32 (from a width of about 340 on),
+    and whose r^2 lies at the end of its range. The bounds are those of any other row."""
     alpha, beta = 0.75, 1.5
     p = inputs(rows, d, types, gate, seed=d, w=F if types[2] == F or d % 2 else B)
     gen = torch.Generator().manual_seed(d)
