@@ -27,7 +27,9 @@ EXPORTS = ("ttt_init", "ttt_forward_chunked", "ttt_forward_docs", "ttt_reset", "
            "ttt_workspace_bytes", "ttt_set_output_f32", "ttt_state_delta", "ttt_forward_chunked_noalloc",
            "ttt_norm_pre", "ttt_norm_post", "ttt_norm_ws_bytes", "ttt_norm_pre_grad", "ttt_norm_post_grad",
            "ttt_embed", "ttt_embed_grad_ws_bytes", "ttt_embed_grad", "ttt_grad_ws_bytes", "ttt_grad_norm",
-           "ttt_clip_grads")
+           "ttt_clip_grads", "ttt_linear_ws_bytes", "ttt_linear", "ttt_gated_ws_bytes", "ttt_gated",
+           "ttt_linear_grad_ws_bytes", "ttt_linear_grad", "ttt_gated_grad_ws_bytes", "ttt_gated_grad", "ttt_adamw",
+           "ttt_adamw_values")
 
 _lib = None
 
@@ -93,6 +95,19 @@ def lib() -> ctypes.CDLL:
     L.ttt_grad_ws_bytes.argtypes = [i32, ctypes.POINTER(sz)]
     L.ttt_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, sz, vp]
     L.ttt_clip_grads.argtypes = [vp, vp, vp, i32, f32, vp, vp, vp, sz, vp]
+    psz, f64 = ctypes.POINTER(sz), ctypes.c_double
+    for fn in (L.ttt_linear_ws_bytes, L.ttt_gated_ws_bytes, L.ttt_linear_grad_ws_bytes, L.ttt_gated_grad_ws_bytes):
+        fn.argtypes = [i64, i32, i32, i32, psz]
+        fn.restype = i32
+    L.ttt_linear.argtypes = [vp, vp, i32, vp, i32, f32, vp, i64, i32, i32, vp, vp, i32, vp, sz, vp]
+    L.ttt_gated.argtypes = [vp, vp, vp, i32, vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.ttt_linear_grad.argtypes = [vp, i32, vp, vp, i32, vp, i32, f32, i64, i32, i32, vp, vp, vp, i32, vp, sz, vp]
+    L.ttt_gated_grad.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+    L.ttt_adamw.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i64, vp, f64, vp, f64, f64, f64, f64, vp,
+                            f64, ctypes.c_uint32, vp]
+    L.ttt_adamw_values.argtypes = [vp, vp, i32, vp, vp, i32, vp]
+    for fn in (L.ttt_linear, L.ttt_gated, L.ttt_linear_grad, L.ttt_gated_grad, L.ttt_adamw, L.ttt_adamw_values):
+        fn.restype = i32
     for fn in (L.ttt_norm_pre, L.ttt_norm_post, L.ttt_norm_ws_bytes, L.ttt_norm_pre_grad, L.ttt_norm_post_grad,
                L.ttt_embed, L.ttt_embed_grad_ws_bytes, L.ttt_embed_grad, L.ttt_grad_ws_bytes, L.ttt_grad_norm,
                L.ttt_clip_grads):
@@ -767,3 +782,279 @@ def ttt_clip_grads(grads, tau: float, out=None, norm: Optional[torch.Tensor] = N
     _check(lib().ttt_clip_grads(*m.args, float(tau), None if po is None else po.buffer_info()[0], pn, ws.data_ptr(),
                                 nws, c.on()), "ttt_clip_grads")
     return norm
+
+
+# ---- the plain layers and the step ----
+
+_ACT = {None: 0, "silu": 1, "gelu": 2, "relu": 3}  # TTT_ACT_* in include/ttt.h
+
+
+def _act(act: Optional[str], gated: bool = False) -> int:
+    if act not in _ACT or (gated and act is None):
+        names = [a for a in _ACT if a is not None or not gated]
+        raise ValueError(f"act must be one of {names}, got {act!r}")
+    return _ACT[act]
+
+
+@lru_cache(maxsize=1024)
+def _dense_ws(name: str, rows: int, n_in: int, n_out: int, dt: int) -> int:
+    n = ctypes.c_size_t()
+    _check(getattr(lib(), name)(rows, n_in, n_out, dt, ctypes.byref(n)), name)
+    return n.value
+
+
+def _weight_shape(w: torch.Tensor, name: str, n_in: int) -> int:
+    """The rows of a weight [out][in]."""
+    if _tensor(w, name).dim() != 2 or w.shape[1] != n_in:
+        raise ValueError(f"{name} must be [out][{n_in}], got {tuple(w.shape)}")
+    if w.shape[0] >= _INT:
+        raise _too_large(w.shape[0], f"the first dimension of {name}")
+    return w.shape[0]
+
+
+def ttt_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: Optional[str] = None,
+               residual: Optional[torch.Tensor] = None, scale: float = 1.0, keep: bool = False,
+               y: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None, stream=None):
+    """y = residual + scale * act(x w^T + bias); act None, "silu", "gelu" (tanh form) or "relu".
+
+    x [...][in], w [out][in], bias [out], all of one dtype; y [...][out] in `dtype` (default: the residual's, else x's;
+    a bfloat16 x may give a float32 y), the residual in y's dtype. y may be the residual. With keep returns (y, pre),
+    pre = x w^T + bias in x's dtype, which ttt_linear_grad takes where there is an activation."""
+    rows, n = _rows(x, "x")
+    out = _weight_shape(w, "w", n)
+    c = _Call(x.device, stream)
+    dt = x.dtype
+    px, pw, pb = c.arg(x, "x"), c.arg(w, "w", dt), c.arg(bias, "bias", dt, (out,))
+    shape = x.shape[:-1] + (out,)
+    if y is None:
+        y = c.empty(shape, _out_dtype(dtype, dt if residual is None else _tensor(residual, "residual").dtype))
+        py = y.data_ptr()
+    else:
+        py = c.arg(y, "y", dtype, shape)
+    pr = c.arg(residual, "residual", y.dtype, shape)
+    pre = c.empty(shape, dt) if keep else None
+    nws = _dense_ws("ttt_linear_ws_bytes", rows, n, out, _DT[dt])
+    ws = c.scratch(nws) if nws else None
+    _check(lib().ttt_linear(px, pw, _DT[dt], pb, _act(act), float(scale), pr, rows, n, out,
+                            None if pre is None else pre.data_ptr(), py, _DT[y.dtype],
+                            None if ws is None else ws.data_ptr(), nws, c.on()), "ttt_linear")
+    return (y, pre) if keep else y
+
+
+def ttt_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, b_gate: Optional[torch.Tensor] = None,
+              b_up: Optional[torch.Tensor] = None, act: str = "silu", keep: bool = False,
+              z: Optional[torch.Tensor] = None, stream=None):
+    """The gated projections of a feed-forward block: z = act(g) * u, g = x w_gate^T + b_gate, u = x w_up^T + b_up.
+
+    x [...][in], weights [f][in], biases [f] (both or neither), z [...][f], all of one dtype; act "silu", "gelu" (tanh
+    form) or "relu". With keep returns (z, g, u) for ttt_gated_grad."""
+    rows, n = _rows(x, "x")
+    f = _weight_shape(w_gate, "w_gate", n)
+    c = _Call(x.device, stream)
+    dt = x.dtype
+    px, pg, pu = c.arg(x, "x"), c.arg(w_gate, "w_gate", dt), c.arg(_tensor(w_up, "w_up"), "w_up", dt, (f, n))
+    pbg, pbu = c.arg(b_gate, "b_gate", dt, (f,)), c.arg(b_up, "b_up", dt, (f,))
+    shape = x.shape[:-1] + (f,)
+    if z is None:
+        z = c.empty(shape, dt)
+        pz = z.data_ptr()
+    else:
+        pz = c.arg(z, "z", dt, shape)
+    g, u = (c.empty(shape, dt), c.empty(shape, dt)) if keep else (None, None)
+    nws = _dense_ws("ttt_gated_ws_bytes", rows, n, f, _DT[dt])
+    ws = c.scratch(nws) if nws else None
+    _check(lib().ttt_gated(px, pg, pu, _DT[dt], pbg, pbu, _act(act, True), rows, n, f,
+                           None if g is None else g.data_ptr(), None if u is None else u.data_ptr(), pz,
+                           None if ws is None else ws.data_ptr(), nws, c.on()), "ttt_gated")
+    return (z, g, u) if keep else z
+
+
+class LinearGrads(NamedTuple):
+    """What ttt_linear_grad gives; None where it was not asked for."""
+
+    dx: Optional[torch.Tensor]
+    dw: Optional[torch.Tensor]
+    dbias: Optional[torch.Tensor]
+
+
+class GatedGrads(NamedTuple):
+    """What ttt_gated_grad gives; None where it was not asked for."""
+
+    dx: Optional[torch.Tensor]
+    dw_gate: Optional[torch.Tensor]
+    dw_up: Optional[torch.Tensor]
+    db_gate: Optional[torch.Tensor]
+    db_up: Optional[torch.Tensor]
+
+
+def _grad_out(c: _Call, given, name: str, wanted: bool, accumulate: bool, shape, dtype):
+    """(tensor, address) of a gradient: given, made here, or not wanted."""
+    if given is not None:
+        return given, c.arg(given, name, dtype, shape)
+    if not wanted:
+        return None, None
+    if accumulate:
+        raise ValueError(f"{name} must be given to accumulate into")
+    t = c.empty(shape, dtype)
+    return t, t.data_ptr()
+
+
+def ttt_linear_grad(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: Optional[str] = None,
+                    pre: Optional[torch.Tensor] = None, scale: float = 1.0, bias: bool = False,
+                    dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                    dbias: Optional[torch.Tensor] = None, need_dx: bool = True, need_dw: bool = True,
+                    accumulate: bool = False, stream=None) -> LinearGrads:
+    """Gradients of ttt_linear: with q = scale * dy * act'(pre), dx = q w, dw = q^T x and, with bias, dbias = sum q.
+
+    dy [...][out] in the dtype y had; pre as ttt_linear kept it (needed with an activation). dx and dw have x's dtype,
+    dbias is float32. With accumulate, dw and dbias are added to the tensors given for them."""
+    rows, n = _rows(x, "x")
+    out = _weight_shape(w, "w", n)
+    c = _Call(x.device, stream)
+    dt, kind = x.dtype, _act(act)
+    px, pw = c.arg(x, "x"), c.arg(w, "w", dt)
+    shape = x.shape[:-1] + (out,)
+    pdy = c.arg(_tensor(dy, "dy"), "dy", None, shape)
+    if kind and pre is None:
+        raise ValueError("pre must be given with an activation")
+    pp = c.arg(pre if kind else None, "pre", dt, shape)
+    dx, pdx = _grad_out(c, dx, "dx", need_dx, False, x.shape, dt)
+    dw, pdw = _grad_out(c, dw, "dw", need_dw, accumulate, (out, n), dt)
+    dbias, pdb = _grad_out(c, dbias, "dbias", bias, accumulate, (out,), torch.float32)
+    nws = _dense_ws("ttt_linear_grad_ws_bytes", rows, n, out, _DT[dt])
+    ws = c.scratch(nws)
+    _check(lib().ttt_linear_grad(pdy, _DT[dy.dtype], px, pw, _DT[dt], pp, kind, float(scale), rows, n, out, pdx, pdw,
+                                 pdb, 1 if accumulate else 0, ws.data_ptr(), nws, c.on()), "ttt_linear_grad")
+    return LinearGrads(dx, dw, dbias)
+
+
+def ttt_gated_grad(dz: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, g: torch.Tensor,
+                   u: torch.Tensor, act: str = "silu", bias: bool = False, dx: Optional[torch.Tensor] = None,
+                   dw_gate: Optional[torch.Tensor] = None, dw_up: Optional[torch.Tensor] = None,
+                   db_gate: Optional[torch.Tensor] = None, db_up: Optional[torch.Tensor] = None, need_dx: bool = True,
+                   need_dw: bool = True, accumulate: bool = False, stream=None) -> GatedGrads:
+    """Gradients of ttt_gated: with dg = dz * u * act'(g) and du = dz * act(g), dx = dg w_gate + du w_up,
+    dw_gate = dg^T x, dw_up = du^T x and, with bias, db_gate = sum dg, db_up = sum du.
+
+    g, u as ttt_gated kept them. dx and the weights' gradients have x's dtype, the biases' are float32. With accumulate
+    the weights' and biases' gradients are added to the tensors given for them."""
+    rows, n = _rows(x, "x")
+    f = _weight_shape(w_gate, "w_gate", n)
+    c = _Call(x.device, stream)
+    dt, kind = x.dtype, _act(act, True)
+    px, pg, pu = c.arg(x, "x"), c.arg(w_gate, "w_gate", dt), c.arg(_tensor(w_up, "w_up"), "w_up", dt, (f, n))
+    shape = x.shape[:-1] + (f,)
+    pdz = c.arg(_tensor(dz, "dz"), "dz", dt, shape)
+    pkg, pku = c.arg(_tensor(g, "g"), "g", dt, shape), c.arg(_tensor(u, "u"), "u", dt, shape)
+    dx, pdx = _grad_out(c, dx, "dx", need_dx, False, x.shape, dt)
+    dw_gate, pdg = _grad_out(c, dw_gate, "dw_gate", need_dw, accumulate, (f, n), dt)
+    dw_up, pdu = _grad_out(c, dw_up, "dw_up", need_dw, accumulate, (f, n), dt)
+    db_gate, pbg = _grad_out(c, db_gate, "db_gate", bias, accumulate, (f,), torch.float32)
+    db_up, pbu = _grad_out(c, db_up, "db_up", bias, accumulate, (f,), torch.float32)
+    nws = _dense_ws("ttt_gated_grad_ws_bytes", rows, n, f, _DT[dt])
+    ws = c.scratch(nws)
+    _check(lib().ttt_gated_grad(pdz, px, pg, pu, _DT[dt], pkg, pku, kind, rows, n, f, pdx, pdg, pdu, pbg, pbu,
+                                1 if accumulate else 0, ws.data_ptr(), nws, c.on()), "ttt_gated_grad")
+    return GatedGrads(dx, dw_gate, dw_up, db_gate, db_up)
+
+
+class _List:
+    """Lists of tensors of one call, as arrays of addresses that live as long as it does (the library copies them)."""
+
+    def __init__(self, c: _Call, first):
+        self.c, self.n, self.keep = c, len(first), []
+        self.sizes = array("q", map(torch.Tensor.numel, first))
+        self.numel = self._put(self.sizes)
+
+    def _put(self, a: array) -> int:
+        self.keep.append(a)
+        return a.buffer_info()[0]
+
+    def kinds(self, ts, name: str) -> int:
+        found = set(map(_Many._dtype, ts))
+        if not _DT.keys() >= found:
+            raise ValueError(f"{name} must be float32 or bfloat16")
+        if len(found) == 1:
+            return self._put(array("i", [_DT[found.pop()]]) * self.n)
+        return self._put(array("i", [_DT[t.dtype] for t in ts]))
+
+    def like(self, ts, name: str, dtype=None) -> int:
+        """The addresses of tensors of the first list's sizes."""
+        if len(ts) != self.n:
+            raise ValueError(f"{name} must have one tensor per parameter, got {len(ts)} for {self.n}")
+        if array("q", map(torch.Tensor.numel, ts)) != self.sizes:
+            raise ValueError(f"{name} must have the parameters' sizes")
+        return self.of(ts, name, dtype)
+
+    def of(self, ts, name: str, dtype=None) -> int:
+        if dtype is not None and not set(map(_Many._dtype, ts)) <= {dtype}:
+            raise ValueError(f"{name} must be {dtype}")
+        return self._put(_Many._addresses(self.c, ts, name))
+
+    def tops(self, ts) -> int:
+        want = [(2, -(-n // 256)) for n in self.sizes]
+        if [tuple(t.shape) for t in ts] != want:
+            raise ValueError("tops must have one tensor [2][ceil(numel / 256)] per parameter")
+        return self.of(ts, "tops", torch.int16)
+
+
+def _list_call(ts, stream) -> _Call:
+    return _Call(ts[0].device if ts and isinstance(ts[0], torch.Tensor) else torch.device("cuda"), stream)
+
+
+def _number(c: _Call, v, name: str, dtype) -> Tuple[object, Optional[int]]:
+    """A number, or a device tensor of one element: (the number, the tensor's address)."""
+    if not isinstance(v, torch.Tensor):
+        return v, None
+    if v.dtype != dtype or v.numel() != 1:
+        raise ValueError(f"{name} must be a number or a {dtype} tensor of one element")
+    return 0, _Many._addresses(c, [v], name)[0]
+
+
+def ttt_adamw(params, grads, m, v, step, lr, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+              weight_decay: float = 0.01, copies=None, norm: Optional[torch.Tensor] = None, tau: float = float("inf"),
+              tops=None, seed: int = 0, stream=None) -> None:
+    """One AdamW step over lists of contiguous tensors, in place:
+
+        g' = g min(1, tau / norm);  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
+        w = w (1 - lr weight_decay) - lr (m / (1 - b1^step)) / (sqrt(v / (1 - b2^step)) + eps)
+
+    params and grads are float32 or bfloat16, each tensor its own. The moments m and v are float32, or uint8 codes with
+    `tops`, int16 [2][ceil(numel / 256)] per parameter (all zeros at the start, as the codes): see include/ttt.h for
+    what a code stands for, ttt_adamw_values for its values. They are rounded at random, by `seed`, the step and the
+    place. copies: bfloat16 tensors that receive the rounded parameters. norm: what ttt_grad_norm gave for the
+    gradients; one that is not finite clips nothing. step (1, 2, ...) and lr are numbers, or device tensors of one
+    element (int64, float32) that a captured call reads anew at each replay."""
+    params, grads, m, v = list(params), list(grads), list(m), list(v)
+    c = _list_call(params, stream)
+    a = _List(c, params)
+    bits8 = bool(m) and _tensor(m[0], "m").dtype == torch.uint8
+    state = torch.uint8 if bits8 else torch.float32
+    if bits8 and tops is None:
+        raise ValueError("tops must be given with codes")
+    if not 0 <= seed < 2 ** 32:
+        raise ValueError(f"seed must be in [0, 2^32), got {seed}")
+    step, step_dev = _number(c, step, "step", torch.int64)
+    lr, lr_dev = _number(c, lr, "lr", torch.float32)
+    if not -2 ** 63 <= step < 2 ** 63:
+        raise ValueError(f"step must be below 2^63, got {step}")
+    args = (a.of(params, "params"), a.kinds(params, "params"), a.like(grads, "grads"), a.kinds(grads, "grads"),
+            a.like(m, "m", state), a.like(v, "v", state), 8 if bits8 else 32, a.tops(list(tops)) if bits8 else None,
+            None if copies is None else a.like(list(copies), "copies", torch.bfloat16), a.numel, a.n)
+    _check(lib().ttt_adamw(*args, int(step), step_dev, float(lr), lr_dev, float(betas[0]), float(betas[1]), float(eps),
+                           float(weight_decay), c.arg(norm, "norm", torch.float32, (1,)), float(tau), int(seed),
+                           c.on()), "ttt_adamw")
+
+
+def ttt_adamw_values(codes, tops, moment: int, out=None, stream=None) -> List[torch.Tensor]:
+    """The float32 values of ttt_adamw's 8-bit moments: moment 1 (codes m) or 2 (codes v), a tensor of each one's shape
+    (or into `out`)."""
+    codes = list(codes)
+    c = _list_call(codes, stream)
+    a = _List(c, codes)
+    pc = a.of(codes, "codes", torch.uint8)
+    pt = a.tops(list(tops))
+    out = [c.like(t, torch.float32) for t in codes] if out is None else list(out)
+    po = a.like(out, "out", torch.float32)
+    _check(lib().ttt_adamw_values(pc, pt, int(moment), po, a.numel, a.n, c.on()), "ttt_adamw_values")
+    return out

@@ -1,0 +1,416 @@
+// The matrix products of the plain layers: p = x W^T with bias, activation and
+// residual, the two gated projections, and the products of their gradients.
+//
+// D[i][j] = sum_k A(i, k) B(j, k); the results lie in memory with i running
+// fastest, so i is the weights' side (their rows forward, their columns
+// backward) and j the tokens' (or, in a weight's gradient, its rows).
+//
+// MFMA 16x16 register layout (lane l, accumulator register r): A row i = l % 16
+// and B row j = l % 16, with k = 8 (l / 16) .. +7 (bf16, 16x16x32) or k = l / 16
+// (fp32, 16x16x4); D: j = l % 16, i = 4 (l / 16) + r.
+#include "act.h"
+#include "grid.h"
+#include "linear.h"
+#include "vec8.h"
+
+namespace {
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+
+// ---------------------------------------------------------------------------
+// Any size, any alignment: tiles of 128 x 128, four waves of 64 x 64, staged
+// through registers. fp32 products run on the fp32 MFMA, whose products and
+// sums are those of fp32 FMAs.
+
+constexpr int kTile = 128, kThreads = 256;
+
+template <typename T>
+constexpr int kBK = sizeof(T) == 2 ? 32 : 16;  // k per step: 64 bytes of a row
+
+// n of 8 elements, the rest zero
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_some(const T *p, int n) {
+  Raw8<T> r = {};
+  if (n >= 8) {
+    __builtin_memcpy(&r, p, sizeof r);
+  } else if (n > 0) {
+    T v[8] = {};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) v[i] = p[i];
+    __builtin_memcpy(&r, v, sizeof r);
+  }
+  return r;
+}
+
+__device__ __forceinline__ int clamp8(long long n) { return n < 0 ? 0 : n > 8 ? 8 : (int)n; }
+
+// One operand's tile: 128 rows of kBK, in LDS [row][k] where it lies by rows,
+// [k][row] where it lies transposed.
+template <typename T, bool TRANS>
+struct Tile {
+  static constexpr int BK = kBK<T>, PAD = 16 / (int)sizeof(T);
+  static constexpr int PITCH = TRANS ? kTile + PAD : BK + PAD;
+  static constexpr int SIZE = TRANS ? BK * PITCH : kTile * PITCH;
+  static constexpr int N = kTile * BK / 8 / kThreads;
+  Raw8<T> v[N];
+
+  // row(r): the operand's row of tile row r, and its matrix in m; -1 if none
+  template <class Row>
+  __device__ __forceinline__ void load(const void *const (&m)[2], long long ld, long long row0, long long rows,
+                                       long long k0, long long nk, Row &&row) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int q = threadIdx.x + n * kThreads;
+      if constexpr (TRANS) {
+        const long long k = k0 + q / (kTile / 8), r = row0 + q % (kTile / 8) * 8;
+        v[n] = load_some(reinterpret_cast<const T *>(m[0]) + (k < nk ? k : 0) * ld + r, k < nk ? clamp8(rows - r) : 0);
+      } else {
+        int which = 0;
+        const long long r = row(q / (BK / 8), which), k = k0 + q % (BK / 8) * 8;
+        v[n] = load_some(reinterpret_cast<const T *>(m[which]) + (r < rows ? r : 0) * ld + k,
+                         r < rows ? clamp8(nk - k) : 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(T *lds) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int q = threadIdx.x + n * kThreads;
+      const int at = TRANS ? q / (kTile / 8) * PITCH + q % (kTile / 8) * 8 : q / (BK / 8) * PITCH + q % (BK / 8) * 8;
+      __builtin_memcpy(__builtin_assume_aligned(lds + at, 16), &v[n], sizeof v[n]);
+    }
+  }
+};
+
+// Fragment of rows r0 .. r0 + 15 of a step.
+template <bool TRANS>
+__device__ __forceinline__ bf16x8 fragment(const bf16_t *lds, int r0, int lane) {
+  constexpr int P = Tile<bf16_t, TRANS>::PITCH;
+  const int g = lane >> 4, t = lane & 15;
+  if constexpr (TRANS) {
+    // a transposing read takes, in each group of 16 lanes, a 4 x 16 block (lane t addresses row t/4, elements
+    // 4(t%4) ..) and gives lane t column t of it
+    const bf16_t *p = lds + (8 * g + (t >> 2)) * P + r0 + 4 * (t & 3);
+    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)p);
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)(p + 4 * P));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  } else {
+    return *reinterpret_cast<const bf16x8 *>(lds + (r0 + t) * P + 8 * g);
+  }
+}
+// k = 4 (l / 16) + s in MFMA s of the step's four: the sum over k may take
+// them in any order as long as A and B do alike.
+template <bool TRANS>
+__device__ __forceinline__ f32x4 fragment(const float *lds, int r0, int lane) {
+  constexpr int P = Tile<float, TRANS>::PITCH;
+  const int g = lane >> 4, t = lane & 15;
+  if constexpr (TRANS) {
+    f32x4 v;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = lds[(4 * g + s) * P + r0 + t];
+    return v;
+  } else {
+    return *reinterpret_cast<const f32x4 *>(lds + (r0 + t) * P + 4 * g);
+  }
+}
+__device__ __forceinline__ void mma(f32x4 &acc, const bf16x8 &a, const bf16x8 &b) {
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x4 &acc, const f32x4 &a, const f32x4 &b) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], acc, 0, 0, 0);
+}
+
+// ---- what becomes of W consecutive elements i of one j ----
+
+template <int W>
+__device__ __forceinline__ void get(const float *p, int n, float (&v)[W]) {
+  if (n >= W) {
+    __builtin_memcpy(v, p, W * 4);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = i < n ? p[i] : 0.f;
+}
+template <int W>
+__device__ __forceinline__ void get(const bf16_t *p, int n, float (&v)[W]) {
+  if (n >= W) {
+    uint32_t u[W / 2];
+    __builtin_memcpy(u, p, W * 2);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = i < n ? bf16_to_f32(p[i]) : 0.f;
+}
+template <int W>
+__device__ __forceinline__ void put(float *p, int n, const float (&v)[W]) {
+  if (n >= W) {
+    __builtin_memcpy(p, v, W * 4);
+    end_of_stores();  // the code of the other branch may follow
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (i < n) p[i] = v[i];
+}
+template <int W>
+__device__ __forceinline__ void put(bf16_t *p, int n, const float (&v)[W]) {
+  if (n >= W) {
+    uint32_t u[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) u[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    __builtin_memcpy(p, u, W * 2);
+    end_of_stores();
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (i < n) p[i] = f32_to_bf16(v[i]);
+}
+
+// n of the W elements from (i, j) on are there.
+template <typename T, typename O, int W>
+__device__ __forceinline__ void finish(const GemmArgs &g, int z, long long i, long long j, int n, float (&v)[W]) {
+  const long long at = j * g.ldo + i;
+  float w[W];
+  if (g.bias[0]) {
+    get(reinterpret_cast<const T *>(g.bias[0]) + i, n, w);
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] += w[e];
+  }
+  if (g.pre[0]) put(reinterpret_cast<T *>(g.pre[0]) + at, n, v);
+#pragma unroll
+  for (int e = 0; e < W; ++e) v[e] = g.scale * act_of(v[e], g.act);
+  if (g.res[z]) {
+    get(reinterpret_cast<const O *>(g.res[z]) + at, n, w);
+#pragma unroll
+    for (int e = 0; e < W; ++e) v[e] += w[e];
+  }
+  put(reinterpret_cast<O *>(g.out[z]) + at, n, v);
+}
+// the gated pair: a the gate's products, u the other's
+template <typename T, int W>
+__device__ __forceinline__ void finish_pair(const GemmArgs &g, long long i, long long j, int n, float (&a)[W],
+                                            float (&u)[W]) {
+  const long long at = j * g.ldo + i;
+  float w[W];
+  if (g.bias[0]) {
+    get(reinterpret_cast<const T *>(g.bias[0]) + i, n, w);
+#pragma unroll
+    for (int e = 0; e < W; ++e) a[e] += w[e];
+    get(reinterpret_cast<const T *>(g.bias[1]) + i, n, w);
+#pragma unroll
+    for (int e = 0; e < W; ++e) u[e] += w[e];
+  }
+  if (g.pre[0]) {
+    put(reinterpret_cast<T *>(g.pre[0]) + at, n, a);
+    put(reinterpret_cast<T *>(g.pre[1]) + at, n, u);
+  }
+#pragma unroll
+  for (int e = 0; e < W; ++e) w[e] = act_of(a[e], g.act) * u[e];
+  put(reinterpret_cast<T *>(g.out[0]) + at, n, w);
+}
+
+// grid: i tiles (128 rows of A; with a pair 64 of each matrix), times j tiles, times batch
+template <typename T, typename O, bool AT, bool BT, bool PAIR>
+__global__ __launch_bounds__(kThreads, 2) void k_gemm(GemmArgs g, long long ti, long long tj) {
+  using TA = Tile<T, AT>;
+  using TB = Tile<T, BT>;
+  __shared__ __attribute__((aligned(16))) T la[TA::SIZE];
+  __shared__ __attribute__((aligned(16))) T lb[TB::SIZE];
+  long long n = group_index();
+  if (n >= ti * tj * g.batch) return;
+  const int z = (int)(n / (ti * tj));
+  n -= z * ti * tj;
+  const long long j0 = n / ti * kTile, i0 = n % ti * (PAIR ? kTile / 2 : kTile);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wi = w & 1, wj = w >> 1;
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // with a pair, a wave's 64 rows of A are 32 of the first matrix and the matching 32 of the second
+  auto row_a = [&](int r, int &which) {
+    if constexpr (PAIR) {
+      which = (r >> 5) & 1;
+      return i0 + (r >> 6) * 32 + (r & 31);
+    }
+    return i0 + r;
+  };
+  auto row_b = [&](int r, int &) { return j0 + r; };
+  constexpr int BK = kBK<T>;
+  const long long per = (g.nk + BK - 1) / BK, steps = per * g.segments;
+  TA ta;
+  TB tb;
+  auto fetch = [&](long long st) {
+    const int sg = st >= per;
+    const long long k0 = (st - sg * per) * BK;
+    const void *const a[2] = {PAIR ? g.a[0] : g.a[sg], g.a[1]};
+    const void *const b[2] = {g.b[sg + z], nullptr};
+    ta.load(a, g.lda, i0, g.ni, k0, g.nk, row_a);
+    tb.load(b, g.ldb, j0, g.nj, k0, g.nk, row_b);
+  };
+  if (steps > 0) fetch(0);
+  for (long long st = 0; st < steps; ++st) {
+    ta.put(la);
+    tb.put(lb);
+    __syncthreads();
+    if (st + 1 < steps) fetch(st + 1);
+    decltype(fragment<AT>(la, 0, 0)) fa[4], fb[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) fa[x] = fragment<AT>(la, wi * 64 + x * 16, lane);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) fb[x] = fragment<BT>(lb, wj * 64 + x * 16, lane);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) mma(acc[x][y], fa[x], fb[y]);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const long long j = j0 + wj * 64 + y * 16 + (lane & 15);
+    if (j >= g.nj) continue;
+#pragma unroll
+    for (int x = 0; x < (PAIR ? 2 : 4); ++x) {
+      const long long i = i0 + wi * (PAIR ? 32 : 64) + x * 16 + 4 * (lane >> 4);
+      const int left = i < g.ni ? (int)(g.ni - i < 4 ? g.ni - i : 4) : 0;
+      if (left == 0) continue;
+      float v[4] = {acc[x][y][0], acc[x][y][1], acc[x][y][2], acc[x][y][3]};
+      if constexpr (PAIR) {
+        float u[4] = {acc[x + 2][y][0], acc[x + 2][y][1], acc[x + 2][y][2], acc[x + 2][y][3]};
+        finish_pair<T>(g, i, j, left, v, u);
+      } else {
+        finish<T, O>(g, z, i, j, left, v);
+      }
+    }
+  }
+  end_of_stores();
+}
+
+template <typename T, typename O, bool AT, bool BT, bool PAIR>
+hipError_t run_gemm(const GemmArgs &g, hipStream_t s) {
+  const long long ti = (g.ni + (PAIR ? kTile / 2 : kTile) - 1) / (PAIR ? kTile / 2 : kTile);
+  const long long tj = (g.nj + kTile - 1) / kTile;
+  if (ti * tj == 0) return hipSuccess;
+  hipLaunchKernelGGL((k_gemm<T, O, AT, BT, PAIR>), group_grid(ti * tj * g.batch), dim3(kThreads), 0, s, g, ti, tj);
+  return hipGetLastError();
+}
+
+template <typename T, typename O>
+hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
+  if (f.pair) return run_gemm<T, T, false, false, true>(g, s);
+  if (!f.a_trans) return run_gemm<T, O, false, false, false>(g, s);
+  // gradients come in the operands' type
+  return f.b_trans ? run_gemm<T, T, true, true, false>(g, s) : run_gemm<T, T, true, false, false>(g, s);
+}
+
+// ---------------------------------------------------------------------------
+// The gradient at the pre-activations, elementwise, and its sums over the rows
+// for the biases. A thread takes eight columns and a run of rows; the runs'
+// sums are added in a fixed order by k_column_sums.
+
+constexpr int kSumThreads = 256;
+// runs of rows: enough workgroups to fill the device, and at least 32 rows each where that many are there
+long long row_runs(long long rows, long long n) {
+  const long long groups = (n + kSumThreads * 8 - 1) / (kSumThreads * 8);
+  const long long most = (rows + 31) / 32, want = (2048 + groups - 1) / groups;
+  return most < want ? (most > 0 ? most : 1) : want;
+}
+
+template <typename D, typename T, bool GATED>
+__global__ __launch_bounds__(kSumThreads) void k_act_grad(ActGradArgs a, long long runs) {
+  const long long c = ((long long)blockIdx.x * kSumThreads + threadIdx.x) * 8;
+  const int left = clamp8(a.n - c);
+  if (left == 0) return;
+  const long long run = blockIdx.y, r0 = a.rows * run / runs, r1 = a.rows * (run + 1) / runs;
+  float s1[8] = {}, s2[8] = {};
+  for (long long r = r0; r < r1; ++r) {
+    const long long at = r * a.n + c;
+    float dy[8], q[8];
+    get(reinterpret_cast<const D *>(a.dy) + at, left, dy);
+    if constexpr (GATED) {
+      float p[8], u[8], q2[8];
+      get(reinterpret_cast<const T *>(a.p) + at, left, p);
+      get(reinterpret_cast<const T *>(a.u) + at, left, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float f, df;
+        act_grad_of(p[e], a.act, f, df);
+        q[e] = dy[e] * u[e] * df;
+        q2[e] = dy[e] * f;
+        s2[e] += q2[e];
+      }
+      put(reinterpret_cast<T *>(a.out2) + at, left, q2);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = a.scale * dy[e];
+      if (a.p) {
+        float p[8];
+        get(reinterpret_cast<const T *>(a.p) + at, left, p);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float f, df;
+          act_grad_of(p[e], a.act, f, df);
+          q[e] *= df;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s1[e] += q[e];
+    if (a.out) put(reinterpret_cast<T *>(a.out) + at, left, q);
+  }
+  if (a.sum) {
+    put(a.part + run * a.n + c, left, s1);
+    if constexpr (GATED) put(a.part + (runs + run) * a.n + c, left, s2);
+  }
+  end_of_stores();
+}
+
+__global__ __launch_bounds__(kSumThreads) void k_column_sums(const float *part, long long runs, long long n, float *sum,
+                                                             float *sum2, int accumulate) {
+  const long long c = (long long)blockIdx.x * kSumThreads + threadIdx.x;
+  if (c >= n) return;
+  float *out = blockIdx.y ? sum2 : sum;
+  const float *p = part + blockIdx.y * runs * n + c;
+  float s = 0.f;
+  for (long long r = 0; r < runs; ++r) s += p[r * n];
+  out[c] = accumulate ? out[c] + s : s;
+}
+
+template <typename D, typename T>
+hipError_t run_act_grad(const ActGradArgs &a, hipStream_t s) {
+  const long long runs = row_runs(a.rows, a.n);
+  const dim3 grid((unsigned)((a.n + kSumThreads * 8 - 1) / (kSumThreads * 8)), (unsigned)runs);
+  if (a.u)
+    hipLaunchKernelGGL((k_act_grad<D, T, true>), grid, dim3(kSumThreads), 0, s, a, runs);
+  else
+    hipLaunchKernelGGL((k_act_grad<D, T, false>), grid, dim3(kSumThreads), 0, s, a, runs);
+  if (a.sum)
+    hipLaunchKernelGGL(k_column_sums, dim3((unsigned)((a.n + kSumThreads - 1) / kSumThreads), a.u ? 2 : 1),
+                       dim3(kSumThreads), 0, s, a.part, runs, a.n, a.sum, a.sum2, a.accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
+  if (f.f32) return run_gemm<float, float>(g, f, s);
+  return f.out_f32 ? run_gemm<bf16_t, float>(g, f, s) : run_gemm<bf16_t, bf16_t>(g, f, s);
+}
+
+size_t act_grad_ws_bytes(long long rows, long long n, bool gated) {
+  return (size_t)row_runs(rows, n) * n * 4 * (gated ? 2 : 1);
+}
+
+hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t s) {
+  if (a.f32) return run_act_grad<float, float>(a, s);
+  return a.dy_f32 ? run_act_grad<float, bf16_t>(a, s) : run_act_grad<bf16_t, bf16_t>(a, s);
+}

@@ -1,0 +1,51 @@
+// The matrix products of the plain layers (kernels_linear.hip): launch arguments.
+#pragma once
+
+#include "common.h"
+
+// One product D[i][j] = sum_k A(i, k) B(j, k) and what becomes of it, element (i, j) at out[j * ldo + i]. An operand
+// is held by rows (element (i, k) at a[i * lda + k]) or transposed (at a[k * lda + i]).
+//
+//   segments : k runs through the two pairs a[0], b[0] and a[1], b[1] one after the other, nk each
+//   batch    : two products, a[0] with b[0] into out[0] and a[0] with b[1] into out[1]
+//   pair     : A's rows are those of two matrices a[0], a[1], products g and u: out[0] = act(g) u, and pre[0], pre[1]
+//              receive g and u
+//
+// Without pair: p = D + bias[0], pre[0] receives p, out = res + scale * act(p), res of out's type.
+struct GemmArgs {
+  const void *a[2], *b[2];
+  long long lda, ldb;
+  long long ni, nj, nk;
+  int segments, batch;
+  const void *bias[2];  // of the operands' type
+  const void *res[2];
+  void *out[2];
+  void *pre[2];  // of the operands' type, laid out like out
+  long long ldo;
+  float scale;
+  int act;  // TTT_ACT_*
+};
+
+struct GemmForm {
+  bool f32;               // the operands' type
+  bool a_trans, b_trans;  // held transposed
+  bool pair;
+  bool out_f32;
+};
+
+hipError_t launch_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s);
+
+// q = scale * dy * act'(p) (p NULL: scale * dy), rounded to out's type, and its column sums. dy, p, out: [rows][n].
+// gated (u not NULL): out2 = dy * act(p), out = dy * u * act'(p).
+struct ActGradArgs {
+  const void *dy, *p, *u;
+  void *out, *out2;  // nullable: only the sums are wanted
+  float *sum, *sum2;  // [n] fp32, nullable
+  float *part;        // act_grad_ws_bytes(rows, n, gated), with sum
+  long long rows, n;
+  float scale;
+  int act, accumulate;  // accumulate: the sums are added to sum, sum2
+  bool dy_f32, f32;     // types of dy; of p, u, out, out2
+};
+size_t act_grad_ws_bytes(long long rows, long long n, bool gated);
+hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t s);

@@ -441,6 +441,124 @@ int ttt_grad_norm(const void *const *grads, const int64_t *numel, const int32_t 
 int ttt_clip_grads(const void *const *grads, const int64_t *numel, const int32_t *dt, int n, float tau,
                    void *const *out, float *norm, void *ws, size_t ws_bytes, void *hip_stream);
 
+/*
+ * The plain layers of a stack, whose MLPs do not learn at test time: a gated
+ * feed-forward block is ttt_gated followed by ttt_linear with the residual
+ * stream (paperlayer sec. 4: the fast weights stand in every 6th MLP). Rows
+ * are tokens; x [rows][in], rows 0 .. 2^31-1, widths 1 .. 2^20.
+ *
+ *   a(p): TTT_ACT_NONE p; TTT_ACT_SILU p / (1 + e^-p); TTT_ACT_GELU the tanh
+ *         form, p / (1 + e^-2w) with w = sqrt(2 / pi) (p + 0.044715 p^3);
+ *         TTT_ACT_RELU max(p, 0).
+ *
+ *   ttt_linear : p = x W^T + bias,  y = residual + scale * a(p)
+ *   ttt_gated  : g = x W_gate^T + b_gate,  u = x W_up^T + b_up,  z = a(g) * u
+ *                (TTT_ACT_NONE is not taken)
+ *
+ *   W       : [out][in]; W_gate, W_up: [f][in].
+ *   bias    : [out]; b_gate, b_up: [f], both or neither. NULL: none.
+ *   residual: [rows][out] of y's type, or NULL. y may be the residual (in
+ *             place).
+ *   pre     : [rows][out], receives p; g, u: [rows][f], both or neither. NULL:
+ *             not kept. The gradients need them (pre only with an activation).
+ *   types   : dt is the type of x, the weights, the biases and what is kept
+ *             (and of z); y and residual are fp32, or bf16 where dt is.
+ *
+ * bf16 products run on bf16 MFMA, fp32 ones on fp32 MFMA; sums are fp32, and
+ * each result is rounded once, from fp32 values of what it depends on (y and z
+ * from p, g and u as they were before they are rounded to be kept).
+ */
+enum { TTT_ACT_NONE = 0, TTT_ACT_SILU = 1, TTT_ACT_GELU = 2, TTT_ACT_RELU = 3 };
+int ttt_linear_ws_bytes(int64_t rows, int in, int out, ttt_dtype dt, size_t *bytes);
+int ttt_linear(const void *x, const void *W, ttt_dtype dt, const void *bias, int act, float scale,
+               const void *residual, int64_t rows, int in, int out, void *pre, void *y, ttt_dtype y_dt, void *ws,
+               size_t ws_bytes, void *hip_stream);
+int ttt_gated_ws_bytes(int64_t rows, int in, int f, ttt_dtype dt, size_t *bytes);
+int ttt_gated(const void *x, const void *W_gate, const void *W_up, ttt_dtype dt, const void *b_gate, const void *b_up,
+              int act, int64_t rows, int in, int f, void *g, void *u, void *z, void *ws, size_t ws_bytes,
+              void *hip_stream);
+
+/*
+ * Their gradients.
+ *
+ *   ttt_linear_grad : q = scale * dy * a'(pre);  dx = q W,  dW = q^T x,
+ *                     dbias = the sum of q over the rows. (The residual's
+ *                     gradient is dy itself.)
+ *   ttt_gated_grad  : dg = dz * u * a'(g),  du = dz * a(g);
+ *                     dx = dg W_gate + du W_up,  dW_gate = dg^T x,
+ *                     dW_up = du^T x, db_gate, db_up the sums of dg, du
+ *
+ * dx, dW have dt; dbias, db_gate, db_up are fp32 ([out], [f]). Each may be
+ * NULL (not wanted; dW_gate and dW_up, db_gate and db_up come in pairs). pre
+ * is needed with an activation. With accumulate != 0 the weights' and biases'
+ * gradients are added to what is there (gradients of several batches), dx is
+ * always written. rows = 0 writes them as zero, or leaves them.
+ *
+ * The products of bf16 calls take q, dg and du as bf16 (one more rounding, half
+ * a step of each term; where q is dy, in bf16 and without an activation, there
+ * is none); the biases' gradients sum the unrounded ones. Every sum's order is
+ * fixed by the sizes and types: the same call gives the same bits.
+ */
+int ttt_linear_grad_ws_bytes(int64_t rows, int in, int out, ttt_dtype dt, size_t *bytes);
+int ttt_linear_grad(const void *dy, ttt_dtype y_dt, const void *x, const void *W, ttt_dtype dt, const void *pre,
+                    int act, float scale, int64_t rows, int in, int out, void *dx, void *dW, float *dbias,
+                    int accumulate, void *ws, size_t ws_bytes, void *hip_stream);
+int ttt_gated_grad_ws_bytes(int64_t rows, int in, int f, ttt_dtype dt, size_t *bytes);
+int ttt_gated_grad(const void *dz, const void *x, const void *W_gate, const void *W_up, ttt_dtype dt, const void *g,
+                   const void *u, int act, int64_t rows, int in, int f, void *dx, void *dW_gate, void *dW_up,
+                   float *db_gate, float *db_up, int accumulate, void *ws, size_t ws_bytes, void *hip_stream);
+
+/*
+ * ttt_adamw — one AdamW step over many tensors:
+ *
+ *   g' = g * min(1, tau / N)                    (norm not NULL: N = *norm)
+ *   m' = beta1 m + (1 - beta1) g',  v' = beta2 v + (1 - beta2) g'^2
+ *   w' = w (1 - lr weight_decay) - lr (m' / (1 - beta1^step)) / (sqrt(v' / (1 - beta2^step)) + eps)
+ *
+ *   w, g    : host arrays of n device pointers, w_dt, g_dt their types (fp32
+ *             or bf16, each its own), numel their element counts (together at
+ *             most 2^40). The arrays may be freed on return. n 0 .. 2^20.
+ *   m, v    : the moments, in place: fp32 (state_bits 32) or codes of 8 bits,
+ *             a byte each (state_bits 8). All bytes zero: moments of zero.
+ *   tops    : state_bits 8: per tensor [2][ceil(numel / 256)] int16 (m's row,
+ *             then v's), zero at the start. NULL with state_bits 32.
+ *   copies  : NULL, or n pointers to bf16 arrays (or NULL) that receive w'
+ *             rounded, for an fp32 w whose next forward pass runs in bf16.
+ *   step    : 1, 2, ...; read from step_dev (device, one int64) where that is
+ *             not NULL, as lr is from lr_dev (device, one float), so that a
+ *             captured call can be replayed with others.
+ *   norm    : device, one float, as ttt_grad_norm or ttt_clip_grads gives it,
+ *             or NULL. One that is not finite clips nothing. tau > 0.
+ *   beta1, beta2 : in [0, 1); eps, weight_decay: finite, not negative; lr:
+ *             finite.
+ *
+ * 8-bit moments. T, a block's top (256 elements from the tensor's start), is
+ * the least multiple of 2^20, in units of 2^20, that no |x| of the block passes
+ * as an fp32 bit pattern. m's code is a sign (bit 7) and c in 0 .. 127, v's is
+ * c in 0 .. 255; c > 0 stands for the fp32 number of pattern (T - most + c)
+ * << 20, most = 127 or 255 (0 where that is not positive), c = 0 for 0: three
+ * mantissa bits over the 16 (32) octaves under the block's largest. m' and v'
+ * are computed in fp64, rounded to fp32 and then to one of the two neighbouring
+ * codes at random, so that the expectation is kept: of |x|'s pattern P, (P +
+ * 16 r) >> 20 with 16 random bits r; below the smallest value s of the block m'
+ * becomes s where |m'| >= (r + 1/2) 2^-16 s and 0 otherwise, and a v' that is
+ * not 0 becomes s. r is the low half for m, the high half for v, of 32 bits
+ * made of seed, step, the tensor's number in the list and the element's number
+ * in the tensor (modulo 2^32): the same call gives the same codes. w' is
+ * computed from the moments before they become codes.
+ *
+ * Every array but g may be written; none may overlap another (TTT_E_ARG).
+ *
+ * ttt_adamw_values — the fp32 values of codes: moment 1 (codes m, first row of
+ * tops) or 2.
+ */
+int ttt_adamw(void *const *w, const int32_t *w_dt, const void *const *g, const int32_t *g_dt, void *const *m,
+              void *const *v, int state_bits, int16_t *const *tops, void *const *copies, const int64_t *numel, int n,
+              int64_t step, const int64_t *step_dev, double lr, const float *lr_dev, double beta1, double beta2,
+              double eps, double weight_decay, const float *norm, double tau, uint32_t seed, void *hip_stream);
+int ttt_adamw_values(const void *const *codes, const int16_t *const *tops, int moment, float *const *out,
+                     const int64_t *numel, int n, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
