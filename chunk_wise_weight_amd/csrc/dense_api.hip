@@ -40,15 +40,6 @@ int check_scratch(const char *where, const void *ws, size_t have, size_t need) {
 
 size_t padded(size_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// Workspace of the gradients: q (or dg and du), then the sums' parts.
-struct GradScratch {
-  size_t q, part;
-  size_t bytes() const { return q + part; }
-};
-GradScratch grad_scratch(int64_t rows, int out, ttt_dtype dt, bool gated) {
-  return {padded((size_t)rows * out * size_of(dt)) * (gated ? 2 : 1), padded(act_grad_ws_bytes(rows, out, gated))};
-}
-
 GemmForm form(ttt_dtype dt, bool a_trans, bool b_trans, bool pair, bool out_f32) {
   GemmForm f;
   f.f32 = dt == TTT_F32;
@@ -59,41 +50,80 @@ GemmForm form(ttt_dtype dt, bool a_trans, bool b_trans, bool pair, bool out_f32)
   return f;
 }
 
-// dx[rows][in] = scale * (q W) over one or two pairs of q [rows][out] and W [out][in].
-int run_dx(const char *where, const void *const *q, const void *const *W, int pairs, ttt_dtype dt, float scale,
-           int64_t rows, int in, int out, void *dx, hipStream_t s) {
+// The products by their sizes: y[rows][out] = x W^T (pair: of both weights), dx[rows][in] = q W over one or two pairs,
+// dW[out][in] = q^T x for one or two q.
+GemmArgs sizes_y(int64_t rows, int in, int out) {
   GemmArgs g{};
-  for (int i = 0; i < pairs; ++i) {
-    g.a[i] = W[i];
-    g.b[i] = q[i];
-  }
+  g.lda = g.ldb = g.nk = in;
+  g.ni = g.ldo = out;
+  g.nj = rows;
+  g.segments = g.batch = 1;
+  g.scale = 1.f;
+  return g;
+}
+GemmArgs sizes_dx(int64_t rows, int in, int out, int pairs) {
+  GemmArgs g{};
   g.lda = g.ldo = g.ni = in;
   g.ldb = g.nk = out;
   g.nj = rows;
   g.segments = pairs;
   g.batch = 1;
-  g.out[0] = dx;
-  g.scale = scale;
-  return ttt_launched(launch_gemm(g, form(dt, true, false, false, dt == TTT_F32), s), where);
+  g.scale = 1.f;
+  return g;
 }
-
-// dW[out][in] (+)= scale * (q^T x) for one or two q.
-int run_dw(const char *where, const void *const *q, const void *x, int count, ttt_dtype dt, float scale, int64_t rows,
-           int in, int out, void *const *dW, int accumulate, hipStream_t s) {
+GemmArgs sizes_dw(int64_t rows, int in, int out, int count) {
   GemmArgs g{};
-  g.a[0] = x;
   g.lda = g.ldo = g.ni = in;
   g.ldb = g.nj = out;
   g.nk = rows;
   g.segments = 1;
   g.batch = count;
+  g.scale = 1.f;
+  return g;
+}
+GemmForm form_y(ttt_dtype dt, bool pair, ttt_dtype y) { return form(dt, false, false, pair, y == TTT_F32); }
+GemmForm form_dx(ttt_dtype dt) { return form(dt, true, false, false, dt == TTT_F32); }
+GemmForm form_dw(ttt_dtype dt) { return form(dt, true, true, false, dt == TTT_F32); }
+
+// Workspace of the gradients: q (or dg and du), the biases' sums, the products' splits.
+struct GradScratch {
+  size_t q, part, gemm;
+  size_t bytes() const { return q + part + gemm; }
+};
+GradScratch grad_scratch(int64_t rows, int in, int out, ttt_dtype dt, int count) {
+  GradScratch s;
+  s.q = padded((size_t)rows * out * size_of(dt)) * count;
+  s.part = padded(act_grad_ws_bytes(rows, out, count == 2));
+  s.gemm = padded(std::max(gemm_ws_bytes(sizes_dx(rows, in, out, count), form_dx(dt)),
+                           gemm_ws_bytes(sizes_dw(rows, in, out, count), form_dw(dt))));
+  return s;
+}
+
+int run_dx(const char *where, const void *const *q, const void *const *W, int pairs, ttt_dtype dt, float scale,
+           int64_t rows, int in, int out, void *dx, void *ws, hipStream_t s) {
+  GemmArgs g = sizes_dx(rows, in, out, pairs);
+  for (int i = 0; i < pairs; ++i) {
+    g.a[i] = W[i];
+    g.b[i] = q[i];
+  }
+  g.out[0] = dx;
+  g.scale = scale;
+  g.ws = ws;
+  return ttt_launched(launch_gemm(g, form_dx(dt), s), where);
+}
+
+int run_dw(const char *where, const void *const *q, const void *x, int count, ttt_dtype dt, float scale, int64_t rows,
+           int in, int out, void *const *dW, int accumulate, void *ws, hipStream_t s) {
+  GemmArgs g = sizes_dw(rows, in, out, count);
+  g.a[0] = x;
   for (int i = 0; i < count; ++i) {
     g.b[i] = q[i];
     g.out[i] = dW[i];
     g.res[i] = accumulate ? dW[i] : nullptr;
   }
   g.scale = scale;
-  return ttt_launched(launch_gemm(g, form(dt, true, true, false, dt == TTT_F32), s), where);
+  g.ws = ws;
+  return ttt_launched(launch_gemm(g, form_dw(dt), s), where);
 }
 
 // ---- many tensors ----
@@ -199,7 +229,7 @@ int ttt_linear_ws_bytes(int64_t rows, int in, int out, ttt_dtype dt, size_t *byt
   if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_linear_ws_bytes: bytes is NULL");
   const int rc = check_dense("ttt_linear_ws_bytes", dt, rows, in, out);
   if (rc) return rc;
-  *bytes = 0;
+  *bytes = gemm_ws_bytes(sizes_y(rows, in, out), form_y(dt, false, dt));
   return TTT_OK;
 }
 
@@ -227,27 +257,24 @@ int ttt_linear(const void *x, const void *W, ttt_dtype dt, const void *bias, int
                    {{y, residual}});
   if (!rc) rc = ttt_check_device();
   if (rc || rows == 0) return rc;
-  GemmArgs g{};
+  GemmArgs g = sizes_y(rows, in, out);
   g.a[0] = W;
   g.b[0] = x;
-  g.lda = g.ldb = g.nk = in;
-  g.ni = g.ldo = out;
-  g.nj = rows;
-  g.segments = g.batch = 1;
   g.bias[0] = bias;
   g.res[0] = residual;
   g.pre[0] = pre;
   g.out[0] = y;
   g.scale = scale;
   g.act = act;
-  return ttt_launched(launch_gemm(g, form(dt, false, false, false, y_dt == TTT_F32), (hipStream_t)hip_stream), kWhere);
+  g.ws = ws;
+  return ttt_launched(launch_gemm(g, form_y(dt, false, y_dt), (hipStream_t)hip_stream), kWhere);
 }
 
 int ttt_gated_ws_bytes(int64_t rows, int in, int f, ttt_dtype dt, size_t *bytes) {
   if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_gated_ws_bytes: bytes is NULL");
   const int rc = check_dense("ttt_gated_ws_bytes", dt, rows, in, f);
   if (rc) return rc;
-  *bytes = 0;
+  *bytes = gemm_ws_bytes(sizes_y(rows, in, f), form_y(dt, true, dt));
   return TTT_OK;
 }
 
@@ -276,29 +303,25 @@ int ttt_gated(const void *x, const void *W_gate, const void *W_up, ttt_dtype dt,
                    {{"g", g, no, e}, {"u", u, no, e}, {"z", z, no, e}, {"ws", need ? ws : nullptr, need, 4}}, {});
   if (!rc) rc = ttt_check_device();
   if (rc || rows == 0) return rc;
-  GemmArgs a{};
+  GemmArgs a = sizes_y(rows, in, f);
   a.a[0] = W_gate;
   a.a[1] = W_up;
   a.b[0] = x;
-  a.lda = a.ldb = a.nk = in;
-  a.ni = a.ldo = f;
-  a.nj = rows;
-  a.segments = a.batch = 1;
   a.bias[0] = b_gate;
   a.bias[1] = b_up;
   a.pre[0] = g;
   a.pre[1] = u;
   a.out[0] = z;
-  a.scale = 1.f;
   a.act = act;
-  return ttt_launched(launch_gemm(a, form(dt, false, false, true, dt == TTT_F32), (hipStream_t)hip_stream), kWhere);
+  a.ws = ws;
+  return ttt_launched(launch_gemm(a, form_y(dt, true, dt), (hipStream_t)hip_stream), kWhere);
 }
 
 int ttt_linear_grad_ws_bytes(int64_t rows, int in, int out, ttt_dtype dt, size_t *bytes) {
   if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_linear_grad_ws_bytes: bytes is NULL");
   const int rc = check_dense("ttt_linear_grad_ws_bytes", dt, rows, in, out);
   if (rc) return rc;
-  *bytes = grad_scratch(rows, out, dt, false).bytes();
+  *bytes = grad_scratch(rows, in, out, dt, 1).bytes();
   return TTT_OK;
 }
 
@@ -314,7 +337,7 @@ int ttt_linear_grad(const void *dy, ttt_dtype y_dt, const void *x, const void *W
   if (act == TTT_ACT_NONE) pre = nullptr;
   if (rows > 0 && (!dy || (dW && !x) || (dx && !W) || (act != TTT_ACT_NONE && !pre)))
     return ttt_fail(TTT_E_NULL, "%s: dy, x, W or pre is NULL", kWhere);
-  const GradScratch sc = grad_scratch(rows, out, dt, false);
+  const GradScratch sc = grad_scratch(rows, in, out, dt, 1);
   rc = check_ws(kWhere, ws, ws_bytes, sc.bytes());
   if (rc) return rc;
   const size_t e = size_of(dt), ye = size_of(y_dt), no = (size_t)rows * out, ni = (size_t)rows * in;
@@ -350,8 +373,9 @@ int ttt_linear_grad(const void *dy, ttt_dtype y_dt, const void *x, const void *W
     if (rc) return rc;
   }
   const float left = pass ? 1.f : scale;
-  if (dx && rows > 0) rc = run_dx(kWhere, &q, &W, 1, dt, left, rows, in, out, dx, s);
-  if (dW && !rc) rc = run_dw(kWhere, &q, x, 1, dt, left, rows, in, out, &dW, accumulate, s);
+  void *split_ws = (char *)ws + sc.q + sc.part;
+  if (dx && rows > 0) rc = run_dx(kWhere, &q, &W, 1, dt, left, rows, in, out, dx, split_ws, s);
+  if (dW && !rc) rc = run_dw(kWhere, &q, x, 1, dt, left, rows, in, out, &dW, accumulate, split_ws, s);
   return rc;
 }
 
@@ -359,7 +383,7 @@ int ttt_gated_grad_ws_bytes(int64_t rows, int in, int f, ttt_dtype dt, size_t *b
   if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_gated_grad_ws_bytes: bytes is NULL");
   const int rc = check_dense("ttt_gated_grad_ws_bytes", dt, rows, in, f);
   if (rc) return rc;
-  *bytes = grad_scratch(rows, f, dt, true).bytes();
+  *bytes = grad_scratch(rows, in, f, dt, 2).bytes();
   return TTT_OK;
 }
 
@@ -374,7 +398,7 @@ int ttt_gated_grad(const void *dz, const void *x, const void *W_gate, const void
     return ttt_fail(TTT_E_NULL, "%s: one of dW_gate, dW_up or of db_gate, db_up is NULL", kWhere);
   if (rows > 0 && (!dz || !g || !u || (dW_gate && !x) || (dx && (!W_gate || !W_up))))
     return ttt_fail(TTT_E_NULL, "%s: dz, x, W_gate, W_up, g or u is NULL", kWhere);
-  const GradScratch sc = grad_scratch(rows, f, dt, true);
+  const GradScratch sc = grad_scratch(rows, in, f, dt, 2);
   rc = check_ws(kWhere, ws, ws_bytes, sc.bytes());
   if (rc) return rc;
   const size_t e = size_of(dt), no = (size_t)rows * f * e, ni = (size_t)rows * in * e, nw = (size_t)f * in * e;
@@ -412,8 +436,9 @@ int ttt_gated_grad(const void *dz, const void *x, const void *W_gate, const void
     rc = ttt_launched(launch_act_grad(a, s), kWhere);
     if (rc) return rc;
   }
-  if (dx && rows > 0) rc = run_dx(kWhere, q, W, 2, dt, 1.f, rows, in, f, dx, s);
-  if (dW_gate && !rc) rc = run_dw(kWhere, q, x, 2, dt, 1.f, rows, in, f, dW, accumulate, s);
+  void *split_ws = (char *)ws + sc.q + sc.part;
+  if (dx && rows > 0) rc = run_dx(kWhere, q, W, 2, dt, 1.f, rows, in, f, dx, split_ws, s);
+  if (dW_gate && !rc) rc = run_dw(kWhere, q, x, 2, dt, 1.f, rows, in, f, dW, accumulate, split_ws, s);
   return rc;
 }
 

@@ -1,0 +1,396 @@
+// The products of bf16 operands whose rows start on 16 bytes: tiles that go
+// from memory straight into LDS.
+//
+// A workgroup of WI x WJ waves computes a tile of D; each wave 16 FI x 16 FJ of
+// it with v_mfma_f32_16x16x32_bf16. Tiles of 256 x 256 take eight waves of 128 x
+// 64, one workgroup per CU; tiles of 128 x 128 four of 64 x 64, two workgroups
+// per CU. k runs in slabs of 64: a load instruction moves eight 128-byte lines
+// into LDS (16 bytes per lane), two slabs are held, and the loads of slab n + 2
+// are issued behind the MFMAs of slab n's second half, into the buffer that
+// half has just finished reading. The fragments of the next half and of the
+// second half of rows are read behind MFMAs already queued.
+//
+// An operand that lies by rows is held as [rows][64 k], the eight 16-byte
+// chunks of a row permuted by swz(row), which leaves the fragments' reads free
+// of bank conflicts. One that lies transposed is held as it lies, in blocks of
+// [64 k][64 rows] permuted by zsw(k), and its fragments come from transposing
+// reads (ds_read_b64_tr_b16). Rows, k and transposed rows past an operand's end
+// are addressed behind the end of its buffer descriptor, which reads zero;
+// columns past a transposed operand's row read the next row, and only reach
+// elements of D that are not stored.
+//
+// The epilogue takes a wave's sums through LDS, 32 j at a time, so that a lane
+// holds eight consecutive i and a row's stores cover whole lines.
+#include <type_traits>
+
+#include "linear_dev.h"
+
+namespace {
+
+constexpr int SK = 64;  // k per slab
+constexpr uint32_t kBufferFlags = 0x00020000u;  // raw buffer descriptor word 3 on the gfx9 family
+constexpr uint32_t kOutOfRange = 0x80000000u;   // past every descriptor's end
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int lds_off(int r, int c) { return r * SK + ((c ^ swz(r)) << 3); }
+// A transposing read covers rows r0 + 8g .. +3 of k (g: the group of 16 lanes) and a pair of adjacent chunks; this
+// gives the rows that are served at a time disjoint banks.
+__device__ __forceinline__ int zsw(int k) { return ((k & 3) ^ ((k >> 3) & 1)) << 1; }
+
+// A load the compiler does not track: tracked, it would wait for every load in
+// flight before each transposing read. The kernel's own counted waits and
+// barriers order them. No register outputs: the data goes to LDS at M0 + 16
+// bytes per lane. M0 is the compiler's register, saved and put back; one wait
+// state must pass between its write and the load.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, bf16_t *lds, uint32_t voff, uint32_t soff) {
+  const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
+  uint32_t keep;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+      : "=&s"(keep)
+      : "s"(base), "v"(voff), "s"(rs), "s"(soff)
+      : "memory");
+}
+
+__device__ __forceinline__ int clamp_bytes(long long n) { return n < 0 ? 0 : n > 0x7fffffffLL ? 0x7fffffff : (int)n; }
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, long long bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, clamp_bytes(bytes), kBufferFlags);
+}
+
+// The loads of one operand's tile by one wave: 32 of its rows (or, transposed, 32 of a block's 64 k), four at 1 KB.
+template <bool TRANS, int NW>
+struct Loads {
+  const bf16_t *seg[2];  // first row of this wave's matrix, per segment; transposed: first column of its block
+  long long ld, rows;    // rows of the matrix left from there; transposed: elements of a row left from there
+  long long nk;
+  uint32_t vo[4];
+  int chunk[4];  // k of the lane's piece in a slab (by rows), row of k (transposed)
+  int lds0;      // element offset of the wave's share
+
+  // by rows: row0 is the operand's row that the wave's first tile row w*32 holds
+  __device__ __forceinline__ void init(const void *s0, const void *s1, long long ld_, long long row0, long long nrows,
+                                       long long nk_, int w, int lane) {
+    ld = ld_;
+    nk = nk_;
+    if constexpr (TRANS) {
+      const int blk = w >> 1, k0 = (w & 1) * 32;
+      const long long col = row0 + blk * 64;
+      seg[0] = (const bf16_t *)s0 + col;
+      seg[1] = (const bf16_t *)s1 + col;
+      rows = col;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int k = k0 + 8 * n + (lane >> 3);
+        chunk[n] = k;
+        vo[n] = (uint32_t)(k * ld * 2 + (((lane & 7) ^ zsw(k)) << 4));
+      }
+      lds0 = (blk * 64 + k0) * 64;
+    } else {
+      seg[0] = (const bf16_t *)s0 + row0 * ld;
+      seg[1] = (const bf16_t *)s1 + row0 * ld;
+      rows = nrows - row0;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int r = 8 * n + (lane >> 3), c = (lane & 7) ^ swz(w * 32 + r);
+        chunk[n] = c * 8;
+        vo[n] = (uint32_t)(r * ld * 2 + c * 16);
+      }
+      lds0 = w * 32 * SK;
+    }
+  }
+  struct Pre {
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t soff;
+    int left;  // k left from the slab on
+  };
+  __device__ __forceinline__ Pre prep(int sg, long long k0) const {
+    Pre p;
+    const bf16_t *s = sg ? seg[1] : seg[0];
+    const long long left = nk - k0;
+    p.left = left > SK ? SK : (int)left;
+    if constexpr (TRANS) {
+      // from the slab's first row to the end of the array
+      p.rs = rsrc(s + k0 * ld, (left * ld - rows) * 2);
+      p.soff = 0;
+    } else {
+      p.rs = rsrc(s + k0, (rows * ld - k0) * 2);
+      p.soff = 0;
+    }
+    return p;
+  }
+  __device__ __forceinline__ void issue(const Pre &p, bf16_t *tile, int n) const {
+    // by rows the last slab's k past the end would read the next row
+    uint32_t v = vo[n];
+    if (chunk[n] >= p.left) v = kOutOfRange;
+    dma16(p.rs, tile + lds0 + n * 8 * SK, v, p.soff);
+  }
+};
+
+template <int FI_, int FJ_, int WI_, int WJ_>
+struct Shape {
+  static constexpr int FI = FI_, FJ = FJ_, WI = WI_, WJ = WJ_, NW = WI * WJ;
+  static constexpr int TI = 16 * FI * WI, TJ = 16 * FJ * WJ;
+  static_assert(TI == 32 * NW && TJ == 32 * NW, "each wave loads 32 rows of each operand");
+  static constexpr int THREADS = 64 * NW, PER_CU = NW == 8 ? 1 : 2;
+  static constexpr int SLAB = (TI + TJ) * SK;      // elements
+  static constexpr int PITCH = 16 * FI + 4;        // of the epilogue's rows, fp32
+  static constexpr int RING = 2 * SLAB * 2, OUT = NW * 32 * PITCH * 4;
+  static constexpr int SMEM = RING > OUT ? RING : OUT;
+};
+using Big = Shape<8, 4, 2, 4>;
+using Small = Shape<4, 4, 2, 2>;
+
+// s_waitcnt immediate (gfx9): vmcnt(n), expcnt unchanged, lgkmcnt(0)
+constexpr unsigned wait_imm(int n) { return (unsigned)((n & 15) | 0x70 | (((n >> 4) & 3) << 14)); }
+// Every wave's loads but the last `later` (8 or none) have landed, and its reads of LDS are done.
+template <int LATER>
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_s_waitcnt(wait_imm(LATER));
+  asm volatile("s_barrier" ::: "memory");
+}
+__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
+
+__device__ __forceinline__ int z_lane_off(int lane) {
+  const int t = lane & 15, k = 8 * (lane >> 4) + (t >> 2);
+  return k * 64 + (((t & 3) >> 1) ^ zsw(k)) * 8 + 4 * (t & 1);
+}
+// Fragments f0 .. f0 + N - 1 (16 rows each) of the tile rows from r0, half h of the slab.
+template <bool TRANS, int N>
+__device__ __forceinline__ void read(bf16x8 (&f)[N], const bf16_t *tile, int r0, int h, int lane) {
+  if constexpr (TRANS) {
+    const int lo = z_lane_off(lane);
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+      const int r = r0 + 16 * x;  // the lane's offset is even in 16-byte chunks, so fragment r / 16 of a block is a XOR
+      const bf16_t *p = tile + (r >> 6) * 4096 + h * 2048 + (lo ^ (((r >> 4) & 3) << 4));
+      const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)p);
+      const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4 *)(p + 256));
+      f[x] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  } else {
+    const int c = 4 * h + (lane >> 4);
+#pragma unroll
+    for (int x = 0; x < N; ++x)
+      f[x] = *reinterpret_cast<const bf16x8 *>(tile + lds_off(r0 + 16 * x + (lane & 15), c));
+  }
+}
+
+// Workgroups go to the 8 XCDs in turn, and each has an L2 of its own: XCD k
+// takes one contiguous range of the tiles' order (a bijection on [0, N)).
+constexpr int kXcds = 8;
+__device__ __forceinline__ int xcd_tile(int n, int N) {
+  const int xcd = n % kXcds, m = n / kXcds, q = N / kXcds, r = N % kXcds;
+  return xcd * q + (xcd < r ? xcd : r) + m;
+}
+// Tile t of nx by ny in bands of H along y, y fastest inside a band: neighbours share operands.
+__device__ __forceinline__ void band_tile(int t, int nx, int ny, int H, int &x, int &y) {
+  const int full = ny / H, per = H * nx, band = t / per, h = band < full ? H : ny - full * H, r = t - band * per;
+  x = r / h;
+  y = band * H + r % h;
+}
+
+template <class S, typename O, bool AT, bool BT, bool PAIR>
+__global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int nti, int ntj, Parts parts) {
+  __shared__ __attribute__((aligned(16))) char smem[S::SMEM];
+  bf16_t *ring = reinterpret_cast<bf16_t *>(smem);
+  constexpr int FI = S::FI, FJ = S::FJ, HF = FI / 2, HALF = 8 * FI;  // HALF: a pair's rows of one matrix in a wave
+  constexpr int WIDE = PAIR ? S::TI / 2 : S::TI;
+  const int per_split = nti * ntj * g.batch;
+  const int logical = xcd_tile(blockIdx.x, gridDim.x);
+  const int split = logical / per_split, rest = logical % per_split, z = rest / (nti * ntj);
+  int tx, ty;
+  band_tile(rest % (nti * ntj), nti, ntj, 8, tx, ty);
+  const long long i0 = (long long)tx * WIDE, j0 = (long long)ty * S::TJ;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wi = w % S::WI, wj = w / S::WI;
+
+  Loads<AT, S::NW> la;
+  Loads<BT, S::NW> lb;
+  if constexpr (PAIR) {
+    // rows 32 w .. of the tile: group w*32 / (2 HALF), matrix and row within it
+    const int q = w * 32 % (2 * HALF);
+    const long long row = i0 + w * 32 / (2 * HALF) * HALF + q % HALF;
+    la.init(g.a[q / HALF], g.a[q / HALF], g.lda, row, g.ni, g.nk, w, lane);
+  } else {
+    la.init(g.a[0], g.a[1], g.lda, AT ? i0 : i0 + w * 32, g.ni, g.nk, w, lane);
+  }
+  lb.init(g.b[z], g.b[1], g.ldb, BT ? j0 : j0 + w * 32, g.nj, g.nk, w, lane);
+
+  const int per = (int)((g.nk + SK - 1) / SK), slabs = per * g.segments;
+  const int first = (int)((long long)slabs * split / parts.splits);
+  const int end = (int)((long long)slabs * (split + 1) / parts.splits);
+
+  f32x4 acc[FI][FJ];
+#pragma unroll
+  for (int a = 0; a < FI; ++a)
+#pragma unroll
+    for (int b = 0; b < FJ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto tile_a = [&](int sl) { return ring + (sl & 1) * S::SLAB; };
+  auto tile_b = [&](int sl) { return ring + (sl & 1) * S::SLAB + S::TI * SK; };
+  struct Pre {
+    typename Loads<AT, S::NW>::Pre a;
+    typename Loads<BT, S::NW>::Pre b;
+  };
+  auto prep = [&](int sl) {
+    const int sg = sl >= per;
+    const long long k0 = (long long)(sl - sg * per) * SK;
+    return Pre{la.prep(sg, k0), lb.prep(sg, k0)};
+  };
+  auto issue = [&](const Pre &p, int sl, int n) {  // load n of 8
+    if (n < 4)
+      la.issue(p.a, tile_a(sl), n);
+    else
+      lb.issue(p.b, tile_b(sl), n - 4);
+  };
+  bf16x8 lo[HF], hi[HF], fb[2][FJ];
+  const int ra = wi * 16 * FI, rb = wj * 16 * FJ;
+
+  // Half H of slab sl. On entry lo and fb[H] hold its fragments of the first half of rows and of the columns; on exit
+  // those of the next half. REFILL: slab sl + 2 is there to be loaded.
+  auto stage = [&](int sl, auto half, auto refill) {
+    constexpr int H = decltype(half)::value;
+    constexpr bool REFILL = decltype(refill)::value;
+    read<AT, HF>(hi, tile_a(sl), ra + 16 * HF, H, lane);
+    pin();
+#pragma unroll
+    for (int y = 0; y < FJ; ++y) acc[0][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[0], fb[H][y], acc[0][y], 0, 0, 0);
+    pin();
+    Pre p;
+    if (H == 1) {
+      meet<0>();  // slab sl + 1 has landed, and no wave reads slab sl any more
+      if (REFILL) p = prep(sl + 2);
+    }
+    pin();
+#pragma unroll
+    for (int x = 1; x < FI; ++x) {
+#pragma unroll
+      for (int y = 0; y < FJ; ++y)
+        acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x < HF ? lo[x % HF] : hi[x % HF], fb[H][y], acc[x][y], 0, 0, 0);
+      if (x == HF) {
+        pin();
+        // past the last slab this reads what the other buffer holds, and nothing uses it
+        read<AT, HF>(lo, tile_a(H ? sl + 1 : sl), ra, H ^ 1, lane);
+        read<BT, FJ>(fb[H ^ 1], tile_b(H ? sl + 1 : sl), rb, H ^ 1, lane);
+      }
+      if (REFILL) {
+#pragma unroll
+        for (int n = (x - 1) * 8 / (FI - 1); n < x * 8 / (FI - 1); ++n) issue(p, sl + 2, n);
+      }
+      pin();
+    }
+  };
+  using T0 = std::integral_constant<int, 0>;
+  using T1 = std::integral_constant<int, 1>;
+  if (first < end) {
+    Pre p = prep(first);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) issue(p, first, n);
+    if (first + 1 < end) {
+      p = prep(first + 1);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) issue(p, first + 1, n);
+      meet<8>();
+    } else {
+      meet<0>();
+    }
+    read<AT, HF>(lo, tile_a(first), ra, 0, lane);
+    read<BT, FJ>(fb[0], tile_b(first), rb, 0, lane);
+    int sl = first;
+    for (; sl + 2 < end; ++sl) {
+      stage(sl, T0{}, std::false_type{});
+      stage(sl, T1{}, std::true_type{});
+    }
+    for (; sl < end; ++sl) {
+      stage(sl, T0{}, std::false_type{});
+      stage(sl, T1{}, std::false_type{});
+    }
+  }
+  __syncthreads();  // the ring is free
+
+  // Epilogue: the wave's sums of 32 j as [j][i], then eight i of one j per lane. A lane keeps its i throughout.
+  float *stg = reinterpret_cast<float *>(smem) + w * 32 * S::PITCH;
+  constexpr int LANES = (PAIR ? HALF : 2 * HALF) / 8;  // lanes to a row
+  constexpr int STEP = 64 / LANES;                     // rows at a time
+  const int ii = lane % LANES * 8;
+  const long long i = i0 + wi * (PAIR ? HALF : 2 * HALF) + ii;
+  const int left = clamp8(g.ni - i);
+#pragma unroll
+  for (int q = 0; q < FJ / 2; ++q) {
+#pragma unroll
+    for (int x = 0; x < FI; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        *reinterpret_cast<f32x4 *>(stg + (16 * y + (lane & 15)) * S::PITCH + 16 * x + 4 * (lane >> 4)) = acc[x][2 * q + y];
+    // the wave's own LDS writes and reads run in order
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+#pragma unroll 2
+    for (int r = 0; r < 32; r += STEP) {
+      const int row = r + lane / LANES;
+      const long long j = j0 + rb + 32 * q + row;
+      float v[8], u[8];
+      __builtin_memcpy(v, __builtin_assume_aligned(stg + row * S::PITCH + ii, 16), 32);
+      if constexpr (PAIR) __builtin_memcpy(u, __builtin_assume_aligned(stg + row * S::PITCH + HALF + ii, 16), 32);
+      if (parts.splits > 1) {
+        float *p = parts.at + (((long long)split * per_split + (long long)z * nti * ntj + (long long)ty * nti + tx) * S::TJ + rb + 32 * q + row) * S::TI +
+                   wi * 2 * HALF + ii;
+        __builtin_memcpy(__builtin_assume_aligned(p, 16), v, 32);
+        if constexpr (PAIR) __builtin_memcpy(__builtin_assume_aligned(p + HALF, 16), u, 32);
+      } else if (j < g.nj && left > 0) {
+        if constexpr (PAIR)
+          finish_pair<bf16_t>(g, i, j, left, v, u);
+        else
+          finish<bf16_t, O>(g, z, i, j, left, v);
+      }
+      end_of_stores();
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+template <class S, typename O, bool AT, bool BT, bool PAIR>
+hipError_t run(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) {
+  const int wide = PAIR ? S::TI / 2 : S::TI;
+  const long long ti = (g.ni + wide - 1) / wide, tj = (g.nj + S::TJ - 1) / S::TJ;
+  if (ti * tj == 0) return hipSuccess;
+  const Parts parts{(float *)g.ws, splits, S::TI, S::TJ, 8 * S::FI};
+  hipLaunchKernelGGL((k_dense<S, O, AT, BT, PAIR>), dim3((unsigned)(ti * tj * g.batch * splits)), dim3(S::THREADS), 0, s,
+                     g, (int)ti, (int)tj, parts);
+  return splits > 1 ? launch_join(g, f, ti, tj, parts, s) : hipGetLastError();
+}
+
+template <class S>
+hipError_t run(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) {
+  if (f.pair) return run<S, bf16_t, false, false, true>(g, f, splits, s);
+  if (!f.a_trans)
+    return f.out_f32 ? run<S, float, false, false, false>(g, f, splits, s)
+                     : run<S, bf16_t, false, false, false>(g, f, splits, s);
+  return f.b_trans ? run<S, bf16_t, true, true, false>(g, f, splits, s)
+                   : run<S, bf16_t, true, false, false>(g, f, splits, s);
+}
+
+}  // namespace
+
+long long dense_tiles(const GemmArgs &g, const GemmForm &f, int tile) {
+  const int wide = f.pair ? tile / 2 : tile;
+  return (g.ni + wide - 1) / wide * ((g.nj + tile - 1) / tile) * g.batch;
+}
+
+// Rows are whole 16-byte pieces; the tiles fit a launch (its threads count in 32 bits) with up to 32 splits, and k an int.
+bool dense_sizes(const GemmArgs &g, const GemmForm &f) {
+  return !f.f32 && g.lda % 8 == 0 && g.ldb % 8 == 0 && dense_tiles(g, f, 128) <= (1LL << 22) && g.nk > 0 &&
+         g.nk * g.segments <= (1LL << 34);
+}
+bool dense_aligned(const GemmArgs &g, const GemmForm &f) {
+  uintptr_t low = (uintptr_t)g.a[0] | (uintptr_t)g.b[0];
+  if (f.pair || g.segments > 1) low |= (uintptr_t)g.a[1];
+  if (g.batch > 1 || g.segments > 1) low |= (uintptr_t)g.b[1];
+  return low % 16 == 0;
+}
+
+hipError_t launch_dense(const GemmArgs &g, const GemmForm &f, int tile, int splits, hipStream_t s) {
+  return tile == 256 ? run<Big>(g, f, splits, s) : run<Small>(g, f, splits, s);
+}

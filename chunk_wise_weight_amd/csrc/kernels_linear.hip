@@ -8,10 +8,11 @@
 // MFMA 16x16 register layout (lane l, accumulator register r): A row i = l % 16
 // and B row j = l % 16, with k = 8 (l / 16) .. +7 (bf16, 16x16x32) or k = l / 16
 // (fp32, 16x16x4); D: j = l % 16, i = 4 (l / 16) + r.
-#include "act.h"
+#include <algorithm>
+#include <cmath>
+
 #include "grid.h"
-#include "linear.h"
-#include "vec8.h"
+#include "linear_dev.h"
 
 namespace {
 
@@ -43,8 +44,6 @@ __device__ __forceinline__ Raw8<T> load_some(const T *p, int n) {
   }
   return r;
 }
-
-__device__ __forceinline__ int clamp8(long long n) { return n < 0 ? 0 : n > 8 ? 8 : (int)n; }
 
 // One operand's tile: 128 rows of kBK, in LDS [row][k] where it lies by rows,
 // [k][row] where it lies transposed.
@@ -123,113 +122,18 @@ __device__ __forceinline__ void mma(f32x4 &acc, const f32x4 &a, const f32x4 &b) 
   for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], acc, 0, 0, 0);
 }
 
-// ---- what becomes of W consecutive elements i of one j ----
-
-template <int W>
-__device__ __forceinline__ void get(const float *p, int n, float (&v)[W]) {
-  if (n >= W) {
-    __builtin_memcpy(v, p, W * 4);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = i < n ? p[i] : 0.f;
-}
-template <int W>
-__device__ __forceinline__ void get(const bf16_t *p, int n, float (&v)[W]) {
-  if (n >= W) {
-    uint32_t u[W / 2];
-    __builtin_memcpy(u, p, W * 2);
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = i < n ? bf16_to_f32(p[i]) : 0.f;
-}
-template <int W>
-__device__ __forceinline__ void put(float *p, int n, const float (&v)[W]) {
-  if (n >= W) {
-    __builtin_memcpy(p, v, W * 4);
-    end_of_stores();  // the code of the other branch may follow
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i)
-    if (i < n) p[i] = v[i];
-}
-template <int W>
-__device__ __forceinline__ void put(bf16_t *p, int n, const float (&v)[W]) {
-  if (n >= W) {
-    uint32_t u[W / 2];
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) u[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    __builtin_memcpy(p, u, W * 2);
-    end_of_stores();
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i)
-    if (i < n) p[i] = f32_to_bf16(v[i]);
-}
-
-// n of the W elements from (i, j) on are there.
-template <typename T, typename O, int W>
-__device__ __forceinline__ void finish(const GemmArgs &g, int z, long long i, long long j, int n, float (&v)[W]) {
-  const long long at = j * g.ldo + i;
-  float w[W];
-  if (g.bias[0]) {
-    get(reinterpret_cast<const T *>(g.bias[0]) + i, n, w);
-#pragma unroll
-    for (int e = 0; e < W; ++e) v[e] += w[e];
-  }
-  if (g.pre[0]) put(reinterpret_cast<T *>(g.pre[0]) + at, n, v);
-#pragma unroll
-  for (int e = 0; e < W; ++e) v[e] = g.scale * act_of(v[e], g.act);
-  if (g.res[z]) {
-    get(reinterpret_cast<const O *>(g.res[z]) + at, n, w);
-#pragma unroll
-    for (int e = 0; e < W; ++e) v[e] += w[e];
-  }
-  put(reinterpret_cast<O *>(g.out[z]) + at, n, v);
-}
-// the gated pair: a the gate's products, u the other's
-template <typename T, int W>
-__device__ __forceinline__ void finish_pair(const GemmArgs &g, long long i, long long j, int n, float (&a)[W],
-                                            float (&u)[W]) {
-  const long long at = j * g.ldo + i;
-  float w[W];
-  if (g.bias[0]) {
-    get(reinterpret_cast<const T *>(g.bias[0]) + i, n, w);
-#pragma unroll
-    for (int e = 0; e < W; ++e) a[e] += w[e];
-    get(reinterpret_cast<const T *>(g.bias[1]) + i, n, w);
-#pragma unroll
-    for (int e = 0; e < W; ++e) u[e] += w[e];
-  }
-  if (g.pre[0]) {
-    put(reinterpret_cast<T *>(g.pre[0]) + at, n, a);
-    put(reinterpret_cast<T *>(g.pre[1]) + at, n, u);
-  }
-#pragma unroll
-  for (int e = 0; e < W; ++e) w[e] = act_of(a[e], g.act) * u[e];
-  put(reinterpret_cast<T *>(g.out[0]) + at, n, w);
-}
-
-// grid: i tiles (128 rows of A; with a pair 64 of each matrix), times j tiles, times batch
+// grid: i tiles (128 rows of A; with a pair 64 of each matrix), times j tiles, times batch, times splits of k
 template <typename T, typename O, bool AT, bool BT, bool PAIR>
-__global__ __launch_bounds__(kThreads, 2) void k_gemm(GemmArgs g, long long ti, long long tj) {
+__global__ __launch_bounds__(kThreads, 2) void k_gemm(GemmArgs g, long long ti, long long tj, Parts parts) {
   using TA = Tile<T, AT>;
   using TB = Tile<T, BT>;
   __shared__ __attribute__((aligned(16))) T la[TA::SIZE];
   __shared__ __attribute__((aligned(16))) T lb[TB::SIZE];
-  long long n = group_index();
-  if (n >= ti * tj * g.batch) return;
-  const int z = (int)(n / (ti * tj));
-  n -= z * ti * tj;
-  const long long j0 = n / ti * kTile, i0 = n % ti * (PAIR ? kTile / 2 : kTile);
+  const long long n = group_index();
+  if (n >= ti * tj * g.batch * parts.splits) return;
+  const long long tile = n % (ti * tj);
+  const int z = (int)(n / (ti * tj) % g.batch), split = (int)(n / (ti * tj * g.batch));
+  const long long j0 = tile / ti * kTile, i0 = tile % ti * (PAIR ? kTile / 2 : kTile);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wi = w & 1, wj = w >> 1;
   f32x4 acc[4][4];
 #pragma unroll
@@ -247,6 +151,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm(GemmArgs g, long long ti, 
   auto row_b = [&](int r, int &) { return j0 + r; };
   constexpr int BK = kBK<T>;
   const long long per = (g.nk + BK - 1) / BK, steps = per * g.segments;
+  const long long first = steps * split / parts.splits, end = steps * (split + 1) / parts.splits;
   TA ta;
   TB tb;
   auto fetch = [&](long long st) {
@@ -257,12 +162,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm(GemmArgs g, long long ti, 
     ta.load(a, g.lda, i0, g.ni, k0, g.nk, row_a);
     tb.load(b, g.ldb, j0, g.nj, k0, g.nk, row_b);
   };
-  if (steps > 0) fetch(0);
-  for (long long st = 0; st < steps; ++st) {
+  if (first < end) fetch(first);
+  for (long long st = first; st < end; ++st) {
     ta.put(la);
     tb.put(lb);
     __syncthreads();
-    if (st + 1 < steps) fetch(st + 1);
+    if (st + 1 < end) fetch(st + 1);
     decltype(fragment<AT>(la, 0, 0)) fa[4], fb[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) fa[x] = fragment<AT>(la, wi * 64 + x * 16, lane);
@@ -273,6 +178,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm(GemmArgs g, long long ti, 
 #pragma unroll
       for (int y = 0; y < 4; ++y) mma(acc[x][y], fa[x], fb[y]);
     __syncthreads();
+  }
+  if (parts.splits > 1) {
+    float *p = parts.at + (n * kTile + wj * 64) * kTile + wi * 64;
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        *reinterpret_cast<f32x4 *>(p + (y * 16 + (lane & 15)) * kTile + x * 16 + 4 * (lane >> 4)) = acc[x][y];
+    end_of_stores();
+    return;
   }
 #pragma unroll
   for (int y = 0; y < 4; ++y) {
@@ -295,21 +210,101 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm(GemmArgs g, long long ti, 
   end_of_stores();
 }
 
+// The splits' sums, added in their order, and what becomes of them. A thread
+// takes eight elements i of one j of one tile.
+template <typename T, typename O, bool PAIR>
+__global__ __launch_bounds__(kThreads) void k_join(GemmArgs g, long long ti, long long tj, Parts parts) {
+  const int wide = PAIR ? parts.ti / 2 : parts.ti;  // elements i of a tile
+  const long long q = group_index() * kThreads + threadIdx.x, per = (long long)parts.tj * (wide / 8);
+  const long long tiles = ti * tj * g.batch, n = q / per;
+  if (n >= tiles) return;
+  const int z = (int)(n / (ti * tj)), r = (int)(q % per), ii = r % (wide / 8) * 8, jj = r / (wide / 8);
+  const long long tile = n % (ti * tj), i = tile % ti * wide + ii, j = tile / ti * parts.tj + jj;
+  const int left = j < g.nj ? clamp8(g.ni - i) : 0;
+  if (left == 0) return;
+  const long long size = (long long)parts.ti * parts.tj;
+  const float *p = parts.at + n * size + (long long)jj * parts.ti + (PAIR ? ii / parts.half * 2 * parts.half + ii % parts.half : ii);
+  float v[8] = {}, u[8] = {};
+  for (int s = 0; s < parts.splits; ++s) {
+    float w[8];
+    __builtin_memcpy(w, __builtin_assume_aligned(p, 16), 32);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += w[e];
+    if constexpr (PAIR) {
+      __builtin_memcpy(w, __builtin_assume_aligned(p + parts.half, 16), 32);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] += w[e];
+    }
+    p += tiles * size;
+  }
+  if constexpr (PAIR)
+    finish_pair<T>(g, i, j, left, v, u);
+  else
+    finish<T, O>(g, z, i, j, left, v);
+  end_of_stores();
+}
+
 template <typename T, typename O, bool AT, bool BT, bool PAIR>
-hipError_t run_gemm(const GemmArgs &g, hipStream_t s) {
+hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) {
   const long long ti = (g.ni + (PAIR ? kTile / 2 : kTile) - 1) / (PAIR ? kTile / 2 : kTile);
   const long long tj = (g.nj + kTile - 1) / kTile;
   if (ti * tj == 0) return hipSuccess;
-  hipLaunchKernelGGL((k_gemm<T, O, AT, BT, PAIR>), group_grid(ti * tj * g.batch), dim3(kThreads), 0, s, g, ti, tj);
-  return hipGetLastError();
+  const Parts parts{(float *)g.ws, splits, kTile, kTile, kTile / 4};
+  hipLaunchKernelGGL((k_gemm<T, O, AT, BT, PAIR>), group_grid(ti * tj * g.batch * splits), dim3(kThreads), 0, s, g, ti,
+                     tj, parts);
+  return splits > 1 ? launch_join(g, f, ti, tj, parts, s) : hipGetLastError();
 }
 
 template <typename T, typename O>
-hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
-  if (f.pair) return run_gemm<T, T, false, false, true>(g, s);
-  if (!f.a_trans) return run_gemm<T, O, false, false, false>(g, s);
+hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) {
+  if (f.pair) return run_gemm<T, T, false, false, true>(g, f, splits, s);
+  if (!f.a_trans) return run_gemm<T, O, false, false, false>(g, f, splits, s);
   // gradients come in the operands' type
-  return f.b_trans ? run_gemm<T, T, true, true, false>(g, s) : run_gemm<T, T, true, false, false>(g, s);
+  return f.b_trans ? run_gemm<T, T, true, true, false>(g, f, splits, s)
+                   : run_gemm<T, T, true, false, false>(g, f, splits, s);
+}
+
+// ---- the choice of tile and splits ----
+//
+// By what a launch would take: rounds of tiles over the device's 256 CUs times
+// a tile's share of k, and for splits the fp32 sums written and read again and
+// the second launch.
+
+constexpr int kCus = 256;
+struct Choice {
+  int tile, splits;
+  double us;
+};
+
+// us_slab: one tile's 64 of k with `slots` tiles at once on the device
+Choice choose(const GemmArgs &g, const GemmForm &f, int tile, long long tiles, int slots, double us_slab) {
+  Choice best{tile, 1, 1e30};
+  const double slabs = (double)((g.nk + 63) / 64) * g.segments;
+  const double bytes = (double)tiles * tile * tile * 4;
+  for (int s = 1; s <= 32; ++s) {
+    if (s > 1 && (slabs / s < 4 || bytes * s > 512e6)) break;
+    const double rounds = (double)((tiles * s + slots - 1) / slots);
+    double us = rounds * std::ceil(slabs / s) * us_slab;
+    if (s > 1) us += 4.0 + 2.0 * bytes * s / 4.0e6;  // 4 TB/s
+    if (us < 0.95 * best.us) best = Choice{tile, s, us};
+  }
+  return best;
+}
+
+long long general_tiles(const GemmArgs &g, const GemmForm &f) {
+  const int wide = f.pair ? kTile / 2 : kTile;
+  return (g.ni + wide - 1) / wide * ((g.nj + kTile - 1) / kTile) * g.batch;
+}
+Choice choose_general(const GemmArgs &g, const GemmForm &f) {
+  return choose(g, f, kTile, general_tiles(g, f), 2 * kCus, f.f32 ? 10.5 : 1.7);
+}
+Choice choose_dense(const GemmArgs &g, const GemmForm &f) {
+  const Choice big = choose(g, f, 256, dense_tiles(g, f, 256), kCus, 1.7);
+  const Choice small = choose(g, f, 128, dense_tiles(g, f, 128), 2 * kCus, 1.1);
+  return small.us < big.us ? small : big;
+}
+size_t parts_bytes(long long tiles, const Choice &c) {
+  return c.splits > 1 ? (size_t)tiles * c.splits * c.tile * c.tile * 4 : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -399,11 +394,39 @@ hipError_t run_act_grad(const ActGradArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T, typename O>
+hipError_t run_join(const GemmArgs &g, bool pair, long long ti, long long tj, const Parts &p, hipStream_t s) {
+  const long long threads = ti * tj * g.batch * p.tj * ((pair ? p.ti / 2 : p.ti) / 8);
+  const dim3 grid = group_grid((threads + kThreads - 1) / kThreads);
+  if (pair)
+    hipLaunchKernelGGL((k_join<T, T, true>), grid, dim3(kThreads), 0, s, g, ti, tj, p);
+  else
+    hipLaunchKernelGGL((k_join<T, O, false>), grid, dim3(kThreads), 0, s, g, ti, tj, p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
+hipError_t launch_join(const GemmArgs &g, const GemmForm &f, long long ti, long long tj, const Parts &p, hipStream_t s) {
+  if (f.f32) return run_join<float, float>(g, f.pair, ti, tj, p, s);
+  return f.out_f32 ? run_join<bf16_t, float>(g, f.pair, ti, tj, p, s) : run_join<bf16_t, bf16_t>(g, f.pair, ti, tj, p, s);
+}
+
+size_t gemm_ws_bytes(const GemmArgs &g, const GemmForm &f) {
+  const size_t general = parts_bytes(general_tiles(g, f), choose_general(g, f));
+  if (!dense_sizes(g, f)) return general;
+  const Choice c = choose_dense(g, f);
+  return std::max(general, parts_bytes(dense_tiles(g, f, c.tile), c));
+}
+
 hipError_t launch_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
-  if (f.f32) return run_gemm<float, float>(g, f, s);
-  return f.out_f32 ? run_gemm<bf16_t, float>(g, f, s) : run_gemm<bf16_t, bf16_t>(g, f, s);
+  if (dense_sizes(g, f) && dense_aligned(g, f)) {
+    const Choice c = choose_dense(g, f);
+    return launch_dense(g, f, c.tile, c.splits, s);
+  }
+  const int splits = choose_general(g, f).splits;
+  if (f.f32) return run_gemm<float, float>(g, f, splits, s);
+  return f.out_f32 ? run_gemm<bf16_t, float>(g, f, splits, s) : run_gemm<bf16_t, bf16_t>(g, f, splits, s);
 }
 
 size_t act_grad_ws_bytes(long long rows, long long n, bool gated) {

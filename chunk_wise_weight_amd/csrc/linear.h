@@ -24,6 +24,7 @@ struct GemmArgs {
   long long ldo;
   float scale;
   int act;  // TTT_ACT_*
+  void *ws;  // gemm_ws_bytes
 };
 
 struct GemmForm {
@@ -33,7 +34,27 @@ struct GemmForm {
   bool out_f32;
 };
 
+// Workspace of a product by its sizes (ni, nj, nk, segments, batch) and form alone, wherever its arrays lie.
+size_t gemm_ws_bytes(const GemmArgs &g, const GemmForm &f);
 hipError_t launch_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s);
+
+// Sums of a part of k, fp32, for k_join: [splits][batch][tiles][tj][ti], tiles in the order j, i, of ti rows of A (with
+// a pair `half` of the first matrix, then the matching `half` of the second, and so on) and tj of B.
+struct Parts {
+  float *at;
+  int splits;  // 1: none, the product is finished at once
+  int ti, tj, half;
+};
+
+// The second launch of a split product (kernels_linear.hip); tiles: ti by tj of them per batch.
+hipError_t launch_join(const GemmArgs &g, const GemmForm &f, long long ti, long long tj, const Parts &p, hipStream_t s);
+
+// bf16 operands whose rows start on 16 bytes (kernels_dense.hip): sizes that allow it, the launch with tiles of
+// `tile` x `tile` (256 or 128), and its workgroups (tiles times batch).
+bool dense_sizes(const GemmArgs &g, const GemmForm &f);
+bool dense_aligned(const GemmArgs &g, const GemmForm &f);
+long long dense_tiles(const GemmArgs &g, const GemmForm &f, int tile);
+hipError_t launch_dense(const GemmArgs &g, const GemmForm &f, int tile, int splits, hipStream_t s);
 
 // q = scale * dy * act'(p) (p NULL: scale * dy), rounded to out's type, and its column sums. dy, p, out: [rows][n].
 // gated (u not NULL): out2 = dy * act(p), out = dy * u * act'(p).
