@@ -21,7 +21,8 @@ PROBE_SRC = os.path.join(PKG, "probes", "mfma_clock.hip")
 PROBE = os.path.join(PKG, "probes", "mfma_clock")
 SOURCES = ["ttt_api.hip", "kernels_bf16.hip", "kernels_f32.hip", "kernels_clip.hip", "kernels_target.hip", "kernels_misc.hip",
            "block_api.hip", "kernels_norm.hip", "kernels_embed.hip", "kernels_grads.hip",
-           "dense_api.hip", "kernels_linear.hip", "kernels_dense.hip", "kernels_adamw.hip"]
+           "dense_api.hip", "kernels_linear.hip", "kernels_dense.hip", "kernels_few.hip",
+           "kernels_adamw.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -413,6 +413,7 @@ hipError_t launch_join(const GemmArgs &g, const GemmForm &f, long long ti, long 
 }
 
 size_t gemm_ws_bytes(const GemmArgs &g, const GemmForm &f) {
+  if (few_sizes(g, f)) return 0;
   const size_t general = parts_bytes(general_tiles(g, f), choose_general(g, f));
   if (!dense_sizes(g, f)) return general;
   const Choice c = choose_dense(g, f);
@@ -420,6 +421,7 @@ size_t gemm_ws_bytes(const GemmArgs &g, const GemmForm &f) {
 }
 
 hipError_t launch_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
+  if (few_sizes(g, f)) return launch_few(g, f, s);
   if (dense_sizes(g, f) && dense_aligned(g, f)) {
     const Choice c = choose_dense(g, f);
     return launch_dense(g, f, c.tile, c.splits, s);

@@ -49,6 +49,10 @@ struct Parts {
 // The second launch of a split product (kernels_linear.hip); tiles: ti by tj of them per batch.
 hipError_t launch_join(const GemmArgs &g, const GemmForm &f, long long ti, long long tj, const Parts &p, hipStream_t s);
 
+// Forward products of few rows (kernels_few.hip).
+bool few_sizes(const GemmArgs &g, const GemmForm &f);
+hipError_t launch_few(const GemmArgs &g, const GemmForm &f, hipStream_t s);
+
 // bf16 operands whose rows start on 16 bytes (kernels_dense.hip): sizes that allow it, the launch with tiles of
 // `tile` x `tile` (256 or 128), and its workgroups (tiles times batch).
 bool dense_sizes(const GemmArgs &g, const GemmForm &f);
