@@ -8,6 +8,8 @@
 // the first is multiplied, so that a wave has 8 KB of weights in flight. The
 // waves' sums are added in LDS, in their order. Rows and tokens past the end
 // are read as the last one's, and their sums are not stored.
+#include <algorithm>
+
 #include "linear_dev.h"
 
 namespace {
@@ -155,9 +157,11 @@ hipError_t run(const GemmArgs &g, int waves, hipStream_t s) {
 bool few_sizes(const GemmArgs &g, const GemmForm &f) { return !f.a_trans && g.nj <= 64; }
 
 hipError_t launch_few(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
-  const long long groups = (g.ni + 15) / 16, steps = (g.nk + (f.f32 ? 15 : 31)) / (f.f32 ? 16 : 32);
-  int waves = 4;
-  while (waves < 8 && groups * waves < 2048 && steps >= 16 * waves) waves *= 2;
+  // waves: as many as give each the same number of turns, up to 16 and 64 KB of sums
+  const int unroll = g.nj <= 16 ? 8 : 4, fragments = (f.pair ? 2 : 1) * (g.nj <= 16 ? 1 : g.nj <= 32 ? 2 : 4);
+  const int step = f.f32 ? 16 : 32, most = std::min(16, 64 / fragments);
+  const int turns = std::max(1, (int)((g.nk + step * unroll - 1) / (step * unroll))), rounds = (turns + most - 1) / most;
+  const int waves = (turns + rounds - 1) / rounds;
   if (f.pair) return f.f32 ? run<float, float, true>(g, waves, s) : run<bf16_t, bf16_t, true>(g, waves, s);
   if (f.f32) return run<float, float, false>(g, waves, s);
   return f.out_f32 ? run<bf16_t, float, false>(g, waves, s) : run<bf16_t, bf16_t, false>(g, waves, s);

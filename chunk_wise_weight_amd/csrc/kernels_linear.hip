@@ -309,89 +309,180 @@ size_t parts_bytes(long long tiles, const Choice &c) {
 
 // ---------------------------------------------------------------------------
 // The gradient at the pre-activations, elementwise, and its sums over the rows
-// for the biases. A thread takes eight columns and a run of rows; the runs'
-// sums are added in a fixed order by k_column_sums.
+// for the biases. Without sums the arrays are taken as they lie, end to end.
+// With sums a wave takes 512 columns (eight per lane) of every fourth row of a
+// run; the waves' sums are added in LDS, the runs' by k_column_sums, each in a
+// fixed order. Either way a thread loads all of a step before it stores any.
 
-constexpr int kSumThreads = 256;
-// runs of rows: enough workgroups to fill the device, and at least 32 rows each where that many are there
-long long row_runs(long long rows, long long n) {
-  const long long groups = (n + kSumThreads * 8 - 1) / (kSumThreads * 8);
-  const long long most = (rows + 31) / 32, want = (2048 + groups - 1) / groups;
-  return most < want ? (most > 0 ? most : 1) : want;
-}
-
-template <typename D, typename T, bool GATED>
-__global__ __launch_bounds__(kSumThreads) void k_act_grad(ActGradArgs a, long long runs) {
-  const long long c = ((long long)blockIdx.x * kSumThreads + threadIdx.x) * 8;
-  const int left = clamp8(a.n - c);
-  if (left == 0) return;
-  const long long run = blockIdx.y, r0 = a.rows * run / runs, r1 = a.rows * (run + 1) / runs;
-  float s1[8] = {}, s2[8] = {};
-  for (long long r = r0; r < r1; ++r) {
-    const long long at = r * a.n + c;
-    float dy[8], q[8];
-    get(reinterpret_cast<const D *>(a.dy) + at, left, dy);
+// Eight elements of the step from `at` on, `left` of them there.
+template <typename D, typename T, bool GATED, bool NT>
+struct ActStep {
+  Raw8<D> dy;
+  Raw8<T> p, u;
+  template <typename V>
+  static __device__ __forceinline__ Raw8<V> fetch(const void *base, long long at, int left) {
+    const V *q = reinterpret_cast<const V *>(base) + at;
+    if (!NT || left < 8) return load_some(q, left);
+    Raw8<V> r;
+    u32x4_any *to = reinterpret_cast<u32x4_any *>(&r);
+    const u32x4_any *from = reinterpret_cast<const u32x4_any *>(q);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof r / 16; ++i) to[i] = __builtin_nontemporal_load(from + i);
+    return r;
+  }
+  static __device__ __forceinline__ void keep(void *base, long long at, int left, const float (&v)[8]) {
+    T *q = reinterpret_cast<T *>(base) + at;
+    if constexpr (NT && sizeof(T) == 2) {
+      if (left >= 8) {
+        stream_w(q, true, v);
+        end_of_stores();
+        return;
+      }
+    }
+    put(q, left, v);
+  }
+  __device__ __forceinline__ void load(const ActGradArgs &a, long long at, int left) {
+    dy = fetch<D>(a.dy, at, left);
+    if (GATED || a.p) p = fetch<T>(a.p, at, left);
+    if constexpr (GATED) u = fetch<T>(a.u, at, left);
+  }
+  // q, and with a pair also q2, rounded and kept
+  __device__ __forceinline__ void apply(const ActGradArgs &a, long long at, int left, float (&q)[8], float (&q2)[8]) const {
+    float d[8], x[8], y[8];
+    expand(dy, d);
     if constexpr (GATED) {
-      float p[8], u[8], q2[8];
-      get(reinterpret_cast<const T *>(a.p) + at, left, p);
-      get(reinterpret_cast<const T *>(a.u) + at, left, u);
+      expand(p, x);
+      expand(u, y);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float f, df;
-        act_grad_of(p[e], a.act, f, df);
-        q[e] = dy[e] * u[e] * df;
-        q2[e] = dy[e] * f;
-        s2[e] += q2[e];
+        act_grad_of(x[e], a.act, f, df);
+        q[e] = d[e] * y[e] * df;
+        q2[e] = d[e] * f;
       }
-      put(reinterpret_cast<T *>(a.out2) + at, left, q2);
+      keep(a.out2, at, left, q2);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = a.scale * dy[e];
+      for (int e = 0; e < 8; ++e) q[e] = a.scale * d[e];
       if (a.p) {
-        float p[8];
-        get(reinterpret_cast<const T *>(a.p) + at, left, p);
+        expand(p, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float f, df;
-          act_grad_of(p[e], a.act, f, df);
+          act_grad_of(x[e], a.act, f, df);
           q[e] *= df;
         }
       }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s1[e] += q[e];
-    if (a.out) put(reinterpret_cast<T *>(a.out) + at, left, q);
+    if (a.out) keep(a.out, at, left, q);
   }
-  if (a.sum) {
-    put(a.part + run * a.n + c, left, s1);
-    if constexpr (GATED) put(a.part + (runs + run) * a.n + c, left, s2);
+};
+
+constexpr int kFlat = 2;  // steps of a thread
+template <typename D, typename T, bool GATED, bool NT>
+__global__ __launch_bounds__(kThreads) void k_act_grad(ActGradArgs a) {
+  const long long n = a.rows * a.n, at = (group_index() * kFlat * kThreads + threadIdx.x) * 8;
+  ActStep<D, T, GATED, NT> st[kFlat];
+#pragma unroll
+  for (int k = 0; k < kFlat; ++k) st[k].load(a, at + k * kThreads * 8, clamp8(n - at - k * kThreads * 8));
+#pragma unroll
+  for (int k = 0; k < kFlat; ++k) {
+    float q[8], q2[8];
+    st[k].apply(a, at + k * kThreads * 8, clamp8(n - at - k * kThreads * 8), q, q2);
   }
   end_of_stores();
 }
 
-__global__ __launch_bounds__(kSumThreads) void k_column_sums(const float *part, long long runs, long long n, float *sum,
-                                                             float *sum2, int accumulate) {
-  const long long c = (long long)blockIdx.x * kSumThreads + threadIdx.x;
-  if (c >= n) return;
-  float *out = blockIdx.y ? sum2 : sum;
+constexpr int kWaveCols = 512, kSumWaves = kThreads / 64;
+// runs of rows: enough workgroups to fill the device, of at least four rows per wave
+long long row_runs(long long rows, long long n) {
+  const long long groups = (n + kWaveCols - 1) / kWaveCols;
+  return std::max(1LL, std::min((rows + 4 * kSumWaves - 1) / (4 * kSumWaves), (2048 + groups - 1) / groups));
+}
+
+template <typename D, typename T, bool GATED, bool NT>
+__global__ __launch_bounds__(kThreads) void k_act_grad_sums(ActGradArgs a, long long runs) {
+  __shared__ __attribute__((aligned(16))) float red[kSumWaves][GATED ? 2 : 1][kWaveCols];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const long long c = (long long)blockIdx.x * kWaveCols + lane * 8;
+  const int left = clamp8(a.n - c);
+  const long long run = blockIdx.y, r1 = a.rows * (run + 1) / runs;
+  float s1[8] = {}, s2[8] = {};
+  for (long long r = a.rows * run / runs + w; r < r1; r += 2 * kSumWaves) {
+    ActStep<D, T, GATED, NT> st[2];
+    const bool two = r + kSumWaves < r1;
+    st[0].load(a, r * a.n + c, left);
+    st[1].load(a, (two ? r + kSumWaves : r) * a.n + c, two ? left : 0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k == 1 && !two) break;
+      float q[8], q2[8];
+      st[k].apply(a, (r + k * kSumWaves) * a.n + c, left, q, q2);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s1[e] += q[e];
+        if constexpr (GATED) s2[e] += q2[e];
+      }
+    }
+  }
+  __builtin_memcpy(&red[w][0][lane * 8], s1, 32);
+  if constexpr (GATED) __builtin_memcpy(&red[w][1][lane * 8], s2, 32);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kWaveCols * (GATED ? 2 : 1); i += kThreads) {
+    const int half = i / kWaveCols, k = i % kWaveCols;
+    const long long col = (long long)blockIdx.x * kWaveCols + k;
+    if (col >= a.n) continue;
+    float s = red[0][half][k];
+#pragma unroll
+    for (int v = 1; v < kSumWaves; ++v) s += red[v][half][k];
+    a.part[(half * runs + run) * a.n + col] = s;
+  }
+}
+
+// A workgroup adds the runs of 64 columns, a wave every sixteenth.
+__global__ __launch_bounds__(1024) void k_column_sums(const float *part, long long runs, long long n, float *sum,
+                                                      float *sum2, int accumulate) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const long long c = (long long)blockIdx.x * 64 + lane;
   const float *p = part + blockIdx.y * runs * n + c;
   float s = 0.f;
-  for (long long r = 0; r < runs; ++r) s += p[r * n];
+  if (c < n) {
+#pragma unroll 4
+    for (long long r = w; r < runs; r += 16) s += p[r * n];
+  }
+  red[w][lane] = s;
+  __syncthreads();
+  if (w != 0 || c >= n) return;
+#pragma unroll
+  for (int v = 1; v < 16; ++v) s += red[v][lane];
+  float *out = blockIdx.y ? sum2 : sum;
   out[c] = accumulate ? out[c] + s : s;
+}
+
+// arrays of more bytes than this are read and written past the caches, of which the last level holds 256 MiB
+constexpr long long kStreamBytes = 512LL << 20;
+
+template <typename D, typename T, bool GATED, bool NT>
+hipError_t run_act_grad(const ActGradArgs &a, hipStream_t s) {
+  if (!a.sum) {
+    const long long groups = (a.rows * a.n + kFlat * kThreads * 8 - 1) / (kFlat * kThreads * 8);
+    if (groups > 0) hipLaunchKernelGGL((k_act_grad<D, T, GATED, NT>), group_grid(groups), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  const long long runs = row_runs(a.rows, a.n);
+  hipLaunchKernelGGL((k_act_grad_sums<D, T, GATED, NT>),
+                     dim3((unsigned)((a.n + kWaveCols - 1) / kWaveCols), (unsigned)runs), dim3(kThreads), 0, s, a, runs);
+  hipLaunchKernelGGL(k_column_sums, dim3((unsigned)((a.n + 63) / 64), GATED ? 2 : 1), dim3(1024), 0, s, a.part, runs,
+                     a.n, a.sum, a.sum2, a.accumulate);
+  return hipGetLastError();
 }
 
 template <typename D, typename T>
 hipError_t run_act_grad(const ActGradArgs &a, hipStream_t s) {
-  const long long runs = row_runs(a.rows, a.n);
-  const dim3 grid((unsigned)((a.n + kSumThreads * 8 - 1) / (kSumThreads * 8)), (unsigned)runs);
-  if (a.u)
-    hipLaunchKernelGGL((k_act_grad<D, T, true>), grid, dim3(kSumThreads), 0, s, a, runs);
-  else
-    hipLaunchKernelGGL((k_act_grad<D, T, false>), grid, dim3(kSumThreads), 0, s, a, runs);
-  if (a.sum)
-    hipLaunchKernelGGL(k_column_sums, dim3((unsigned)((a.n + kSumThreads - 1) / kSumThreads), a.u ? 2 : 1),
-                       dim3(kSumThreads), 0, s, a.part, runs, a.n, a.sum, a.sum2, a.accumulate);
-  return hipGetLastError();
+  const bool nt = a.rows * a.n * (long long)(sizeof(D) + (a.u ? 4 : a.p ? 2 : 1) * sizeof(T)) > kStreamBytes;
+  if (a.u) return nt ? run_act_grad<D, T, true, true>(a, s) : run_act_grad<D, T, true, false>(a, s);
+  return nt ? run_act_grad<D, T, false, true>(a, s) : run_act_grad<D, T, false, false>(a, s);
 }
 
 template <typename T, typename O>
