@@ -19,16 +19,37 @@ struct AdamTable {
   int tensor0;  // number in the call's list of tensor 0
 };
 
+// What all elements of a step share.
+struct AdamStep {
+  float lr1, root2;  // lr / (1 - b1^t), (1 - b2^t)^-1/2
+  float shrink;      // lr decay
+  uint32_t key;      // of the random bits, from seed and step
+};
 struct AdamArgs {
-  double beta1, beta2, eps, lr, decay, tau;
+  double beta1, beta2, lr, decay, tau;
   double log1, log2;  // of the betas
-  long long step;
+  float eps;
+  AdamStep fixed;  // where neither of the next two is given
   const long long *step_dev;
   const float *lr_dev;
+  long long step;
   const float *norm;  // nullable
   uint32_t seed;
 };
 
-hipError_t launch_adamw(const AdamTable &t, const AdamArgs &a, bool bits8, hipStream_t s);
+// The random bits' mixing: two rounds of a shift and a multiplication by an odd
+// constant, which reach every bit of the result.
+__host__ __device__ inline uint32_t adam_mix(uint32_t h) {
+  h = (h ^ (h >> 16)) * 0x6C8E9CF5u;
+  h = (h ^ (h >> 13)) * 0x51ED2701u;
+  return h ^ (h >> 16);
+}
+constexpr uint32_t kGolden = 0x9E3779B1u;  // 2^32 by the golden ratio, odd
+__host__ __device__ inline uint32_t adam_key(uint32_t seed, long long step) {
+  return adam_mix(seed + kGolden * adam_mix((uint32_t)step));
+}
+
+// stream: the arrays are more than the caches hold
+hipError_t launch_adamw(const AdamTable &t, const AdamArgs &a, bool bits8, bool stream, hipStream_t s);
 // values of codes: out[i] (in w) from codes m[i] or v[i] (in m) by tops row `second`
-hipError_t launch_adamw_values(const AdamTable &t, bool second, hipStream_t s);
+hipError_t launch_adamw_values(const AdamTable &t, bool second, bool stream, hipStream_t s);

@@ -130,6 +130,7 @@ int run_dw(const char *where, const void *const *q, const void *x, int count, tt
 
 constexpr int kMaxTensors = 1 << 20;
 constexpr long long kMaxNumel = 1LL << 40;
+constexpr long long kStreamAdam = 512LL << 20;  // arrays of more bytes pass by the caches
 
 // Tables of the tensors that have elements. With `join`, tensors that follow
 // one another in every array (views of flat buffers) are taken as one.
@@ -484,7 +485,7 @@ int ttt_adamw(void *const *w, const int32_t *w_dt, const void *const *g, const i
     AdamArgs a{};
     a.beta1 = beta1;
     a.beta2 = beta2;
-    a.eps = eps;
+    a.eps = (float)eps;
     a.lr = lr;
     a.decay = weight_decay;
     a.tau = tau;
@@ -495,9 +496,16 @@ int ttt_adamw(void *const *w, const int32_t *w_dt, const void *const *g, const i
     a.lr_dev = lr_dev;
     a.norm = norm;
     a.seed = seed;
+    a.fixed.lr1 = (float)(lr / -std::expm1((double)step * a.log1));
+    a.fixed.root2 = (float)(1.0 / std::sqrt(-std::expm1((double)step * a.log2)));
+    a.fixed.shrink = (float)(lr * weight_decay);
+    a.fixed.key = adam_key(seed, step);
+    long long bytes = 0;
+    for (const Extent &x : ex) bytes += (long long)(x.hi - x.lo);
+    const bool stream = bytes > kStreamAdam;
     const Many all{w, m, v, copies, g, bits8 ? tops : nullptr, numel, w_dt, g_dt, n, (int)state};
     return run_many(all, !bits8, [&](const AdamTable &t) {
-      return ttt_launched(launch_adamw(t, a, bits8, (hipStream_t)hip_stream), kWhere);
+      return ttt_launched(launch_adamw(t, a, bits8, stream, (hipStream_t)hip_stream), kWhere);
     });
   } catch (...) {
     return ttt_fail(TTT_E_NOMEM, "%s: out of host memory", kWhere);
@@ -522,10 +530,12 @@ int ttt_adamw_values(const void *const *codes, const int16_t *const *tops, int m
     if (!rc) rc = check_extents(kWhere, ex);
     if (!rc) rc = ttt_check_device();
     if (rc) return rc;
+    long long bytes = 0;
+    for (const Extent &x : ex) bytes += (long long)(x.hi - x.lo);
     const Many all{(void *const *)out, (void *const *)codes, nullptr, nullptr, nullptr, (int16_t *const *)tops,
                    numel, nullptr, nullptr, n, 1};
     return run_many(all, false, [&](const AdamTable &t) {
-      return ttt_launched(launch_adamw_values(t, moment == 2, (hipStream_t)hip_stream), kWhere);
+      return ttt_launched(launch_adamw_values(t, moment == 2, bytes > kStreamAdam, (hipStream_t)hip_stream), kWhere);
     });
   } catch (...) {
     return ttt_fail(TTT_E_NOMEM, "%s: out of host memory", kWhere);

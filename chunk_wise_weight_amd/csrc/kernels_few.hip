@@ -88,14 +88,17 @@ __device__ __forceinline__ void scatter_sums(float (&v)[N]) {
   }
 }
 
-constexpr int few_waves(int tq) { return tq == 4 ? 8 : 16; }
+// Waves of a workgroup, at most, and steps loaded ahead: what gave the least of 1, 2 and 4 steps (8 tokens into the
+// pair: 29.1, 25.6, 22.8 us; 16 tokens 9728 -> 2560: 20.1, 20.5, 24.3).
+constexpr int kFewWaves = 8;
+constexpr int few_steps(bool pair, int tq) { return tq == 4 ? 1 : pair && tq == 2 ? 4 : 2; }
 
 template <typename T, typename O, bool PAIR, int TQ>
-__global__ __launch_bounds__(64 * few_waves(TQ)) void k_few(GemmArgs g) {
+__global__ __launch_bounds__(64 * kFewWaves) void k_few(GemmArgs g) {
   constexpr int E = 16 / sizeof(T), STEP = 16 * E;  // k of a lane's piece, of a step
-  constexpr int RQ = PAIR ? 8 : 4, U = RQ * TQ <= 8 ? 2 : 1;
+  constexpr int RQ = PAIR ? 8 : 4, U = few_steps(PAIR, TQ);
   constexpr int N = RQ * TQ * 4;
-  __shared__ float sums[few_waves(TQ)][N * 4];
+  __shared__ float sums[kFewWaves][N * 4];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
   const long long i0 = (long long)blockIdx.x * 16;
   const int nk = (int)g.nk, kl = (lane >> 2) * E;
@@ -180,10 +183,10 @@ __global__ __launch_bounds__(64 * few_waves(TQ)) void k_few(GemmArgs g) {
 
 template <typename T, typename O, bool PAIR, int TQ>
 hipError_t run(const GemmArgs &g, hipStream_t s) {
-  // 16 waves per CU where the workgroups allow it, each with the same number of turns
-  constexpr int U = (PAIR ? 8 : 4) * TQ <= 8 ? 2 : 1;
+  // about 4096 waves (a pair's load twice as much), each with the same number of turns
+  constexpr int U = few_steps(PAIR, TQ);
   const long long groups = (g.ni + 15) / 16;
-  const int most = (int)std::max(4LL, std::min((long long)few_waves(TQ), 4096 / groups));
+  const int most = (int)std::max(2LL, std::min((long long)kFewWaves, (PAIR ? 2048 : 4096) / groups));
   const int step = 256 / (int)sizeof(T) * U, turns = std::max(1, (int)((g.nk + step - 1) / step));
   const int rounds = (turns + most - 1) / most, waves = (turns + rounds - 1) / rounds;
   hipLaunchKernelGGL((k_few<T, O, PAIR, TQ>), dim3((unsigned)groups), dim3(64 * waves), 0, s, g);
