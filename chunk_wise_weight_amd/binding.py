@@ -11,7 +11,6 @@ import ctypes
 import os
 from array import array
 from functools import lru_cache
-from operator import attrgetter
 from typing import Dict, List, NamedTuple, Optional, Tuple
 
 import torch  # loads the HIP runtime the library binds to (same libamdhip64 soname)
@@ -708,47 +707,59 @@ def ttt_embed_grad(dx: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float
     return dE
 
 
-class _Many:
-    """Lists of tensors as the library takes them: host arrays of addresses, element counts and types. The attributes
-    are read by map() over the methods themselves: at hundreds of tensors this loop is what a call costs. A list entry
-    that is no tensor ends in their TypeError."""
+_read = None
 
-    _dtype = staticmethod(attrgetter("dtype"))
 
-    def __init__(self, c: _Call, grads):
-        self.n = len(grads)
-        self.sizes = array("q", map(torch.Tensor.numel, grads))
-        self.dtypes = list(map(self._dtype, grads))
-        found = set(self.dtypes)
-        if not _DT.keys() >= found:
-            raise ValueError("grads must be float32 or bfloat16")
-        if len(found) == 1:
-            kinds = array("i", [_DT[found.pop()]]) * self.n
-        else:
-            kinds = array("i", map(_DT.__getitem__, self.dtypes))
-        self._keep = (self._addresses(c, grads, "grads"), self.sizes, kinds)
-        self.args = tuple(a.buffer_info()[0] for a in self._keep) + (self.n,)
+def _reader():
+    """The native reader of tensor lists (once)."""
+    global _read
+    if _read is None:
+        try:
+            from ._tensor_lists import read
+        except ImportError as e:
+            raise RuntimeError("_tensor_lists.so is not built; run `python -m chunk_wise_weight_amd.build`") from e
+        _read = read
+    return _read
 
-    @staticmethod
-    def _addresses(c: _Call, ts, name: str) -> array:
-        if not all(map(torch.Tensor.is_contiguous, ts)):
-            raise ValueError(f"{name} must be contiguous")
-        where = set(map(torch.Tensor.get_device, ts))  # -1 for host tensors
-        if -1 in where:
-            raise ValueError(f"{name} must be device tensors")
-        if not where <= {c.device}:
-            raise ValueError(f"{name} must be on the current device")
+
+class _Read:
+    """Addresses, element counts and types of a list of tensors, each as the bytes of an array that the library reads
+    during the call."""
+
+    __slots__ = ("at", "numel", "kinds", "seen", "n")
+
+    def __init__(self, c: _Call, ts: list, name: str, types: int, what: str):
+        """types: a mask of those allowed, 1 << type (TTT_F32, TTT_BF16, 2 for uint8, 3 for int16); what: their names."""
+        self.at, self.numel, self.kinds, self.seen, faults = _reader()(ts, name, c.device)
+        self.n = len(ts)
+        if self.seen & ~types:
+            raise ValueError(f"{name} must be {what}")
+        if faults:
+            raise ValueError(f"{name} must be " + ("contiguous" if faults & 1 else "device tensors" if faults & 2 else
+                                                   "on the current device"))
         if c.stream is not None:
             for t in ts:
                 t.record_stream(c.stream)
-        return array("Q", map(torch.Tensor.data_ptr, ts))
 
-    def outputs(self, c: _Call, out) -> array:
-        if len(out) != self.n:
-            raise ValueError(f"out must have one tensor per gradient, got {len(out)} for {self.n}")
-        if array("q", map(torch.Tensor.numel, out)) != self.sizes or list(map(self._dtype, out)) != self.dtypes:
+
+_FLOATS = (1 << TTT_F32 | 1 << TTT_BF16, "float32 or bfloat16")
+
+
+class _Many:
+    """Lists of tensors as the library takes them: host arrays of addresses, element counts and types."""
+
+    def __init__(self, c: _Call, grads):
+        self.read = r = _Read(c, grads, "grads", *_FLOATS)
+        self.args = (r.at, r.numel, r.kinds, r.n)
+
+    def outputs(self, c: _Call, out) -> bytes:
+        out = list(out)
+        if len(out) != self.read.n:
+            raise ValueError(f"out must have one tensor per gradient, got {len(out)} for {self.read.n}")
+        r = _Read(c, out, "out", *_FLOATS)
+        if r.numel != self.read.numel or r.kinds != self.read.kinds:
             raise ValueError("out must have the gradients' dtypes and sizes")
-        return self._addresses(c, out, "out")
+        return r.at
 
 
 def _grads_call(grads, norm, stream):
@@ -761,7 +772,7 @@ def _grads_call(grads, norm, stream):
         pn = norm.data_ptr()
     else:
         pn = c.arg(norm, "norm", torch.float32, (1,))
-    nws = _grad_ws(m.n)
+    nws = _grad_ws(m.read.n)
     return c, m, norm, pn, c.scratch(nws), nws
 
 
@@ -779,7 +790,7 @@ def ttt_clip_grads(grads, tau: float, out=None, norm: Optional[torch.Tensor] = N
     stay as they are."""
     c, m, norm, pn, ws, nws = _grads_call(grads, norm, stream)
     po = None if out is None else m.outputs(c, out)
-    _check(lib().ttt_clip_grads(*m.args, float(tau), None if po is None else po.buffer_info()[0], pn, ws.data_ptr(),
+    _check(lib().ttt_clip_grads(*m.args, float(tau), po, pn, ws.data_ptr(),
                                 nws, c.on()), "ttt_clip_grads")
     return norm
 
@@ -958,44 +969,26 @@ def ttt_gated_grad(dz: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up
     return GatedGrads(dx, dw_gate, dw_up, db_gate, db_up)
 
 
-class _List:
-    """Lists of tensors of one call, as arrays of addresses that live as long as it does (the library copies them)."""
+_F32_ONLY, _BF16_ONLY = (1 << TTT_F32, "torch.float32"), (1 << TTT_BF16, "torch.bfloat16")
+_CODES, _TOPS = (1 << 2, "torch.uint8"), (1 << 3, "torch.int16")
 
-    def __init__(self, c: _Call, first):
-        self.c, self.n, self.keep = c, len(first), []
-        self.sizes = array("q", map(torch.Tensor.numel, first))
-        self.numel = self._put(self.sizes)
 
-    def _put(self, a: array) -> int:
-        self.keep.append(a)
-        return a.buffer_info()[0]
+def _sized(c: _Call, ts, name: str, types, like: _Read) -> _Read:
+    """A list with a tensor of each parameter's size."""
+    ts = list(ts)
+    if len(ts) != like.n:
+        raise ValueError(f"{name} must have one tensor per parameter, got {len(ts)} for {like.n}")
+    r = _Read(c, ts, name, *types)
+    if r.numel != like.numel:
+        raise ValueError(f"{name} must have the parameters' sizes")
+    return r
 
-    def kinds(self, ts, name: str) -> int:
-        found = set(map(_Many._dtype, ts))
-        if not _DT.keys() >= found:
-            raise ValueError(f"{name} must be float32 or bfloat16")
-        if len(found) == 1:
-            return self._put(array("i", [_DT[found.pop()]]) * self.n)
-        return self._put(array("i", [_DT[t.dtype] for t in ts]))
 
-    def like(self, ts, name: str, dtype=None) -> int:
-        """The addresses of tensors of the first list's sizes."""
-        if len(ts) != self.n:
-            raise ValueError(f"{name} must have one tensor per parameter, got {len(ts)} for {self.n}")
-        if array("q", map(torch.Tensor.numel, ts)) != self.sizes:
-            raise ValueError(f"{name} must have the parameters' sizes")
-        return self.of(ts, name, dtype)
-
-    def of(self, ts, name: str, dtype=None) -> int:
-        if dtype is not None and not set(map(_Many._dtype, ts)) <= {dtype}:
-            raise ValueError(f"{name} must be {dtype}")
-        return self._put(_Many._addresses(self.c, ts, name))
-
-    def tops(self, ts) -> int:
-        want = [(2, -(-n // 256)) for n in self.sizes]
-        if [tuple(t.shape) for t in ts] != want:
-            raise ValueError("tops must have one tensor [2][ceil(numel / 256)] per parameter")
-        return self.of(ts, "tops", torch.int16)
+def _tops(c: _Call, ts, like: _Read) -> _Read:
+    ts = list(ts)
+    if [tuple(t.shape) for t in ts] != [(2, -(-n // 256)) for n in array("q", like.numel)]:
+        raise ValueError("tops must have one tensor [2][ceil(numel / 256)] per parameter")
+    return _Read(c, ts, "tops", *_TOPS)
 
 
 def _list_call(ts, stream) -> _Call:
@@ -1008,7 +1001,11 @@ def _number(c: _Call, v, name: str, dtype) -> Tuple[object, Optional[int]]:
         return v, None
     if v.dtype != dtype or v.numel() != 1:
         raise ValueError(f"{name} must be a number or a {dtype} tensor of one element")
-    return 0, _Many._addresses(c, [v], name)[0]
+    if v.get_device() != c.device or c.device < 0:
+        raise ValueError(f"{name} must be {'on the current device' if v.is_cuda else 'a number or a device tensor'}")
+    if c.stream is not None:
+        v.record_stream(c.stream)
+    return 0, v.data_ptr()
 
 
 def ttt_adamw(params, grads, m, v, step, lr, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
@@ -1025,23 +1022,25 @@ def ttt_adamw(params, grads, m, v, step, lr, betas: Tuple[float, float] = (0.9, 
     place. copies: bfloat16 tensors that receive the rounded parameters. norm: what ttt_grad_norm gave for the
     gradients; one that is not finite clips nothing. step (1, 2, ...) and lr are numbers, or device tensors of one
     element (int64, float32) that a captured call reads anew at each replay."""
-    params, grads, m, v = list(params), list(grads), list(m), list(v)
-    c = _list_call(params, stream)
-    a = _List(c, params)
+    params, m = list(params), list(m)
     bits8 = bool(m) and _tensor(m[0], "m").dtype == torch.uint8
-    state = torch.uint8 if bits8 else torch.float32
     if bits8 and tops is None:
         raise ValueError("tops must be given with codes")
     if not 0 <= seed < 2 ** 32:
         raise ValueError(f"seed must be in [0, 2^32), got {seed}")
+    c = _list_call(params, stream)
+    p = _Read(c, params, "params", *_FLOATS)
+    g = _sized(c, grads, "grads", _FLOATS, p)
+    state = _CODES if bits8 else _F32_ONLY
+    m, v = _sized(c, m, "m", state, p), _sized(c, v, "v", state, p)
+    top = _tops(c, tops, p).at if bits8 else None
+    cs = None if copies is None else _sized(c, copies, "copies", _BF16_ONLY, p).at
     step, step_dev = _number(c, step, "step", torch.int64)
     lr, lr_dev = _number(c, lr, "lr", torch.float32)
     if not -2 ** 63 <= step < 2 ** 63:
         raise ValueError(f"step must be below 2^63, got {step}")
-    args = (a.of(params, "params"), a.kinds(params, "params"), a.like(grads, "grads"), a.kinds(grads, "grads"),
-            a.like(m, "m", state), a.like(v, "v", state), 8 if bits8 else 32, a.tops(list(tops)) if bits8 else None,
-            None if copies is None else a.like(list(copies), "copies", torch.bfloat16), a.numel, a.n)
-    _check(lib().ttt_adamw(*args, int(step), step_dev, float(lr), lr_dev, float(betas[0]), float(betas[1]), float(eps),
+    _check(lib().ttt_adamw(p.at, p.kinds, g.at, g.kinds, m.at, v.at, 8 if bits8 else 32, top, cs, p.numel, p.n,
+                           int(step), step_dev, float(lr), lr_dev, float(betas[0]), float(betas[1]), float(eps),
                            float(weight_decay), c.arg(norm, "norm", torch.float32, (1,)), float(tau), int(seed),
                            c.on()), "ttt_adamw")
 
@@ -1051,10 +1050,9 @@ def ttt_adamw_values(codes, tops, moment: int, out=None, stream=None) -> List[to
     (or into `out`)."""
     codes = list(codes)
     c = _list_call(codes, stream)
-    a = _List(c, codes)
-    pc = a.of(codes, "codes", torch.uint8)
-    pt = a.tops(list(tops))
+    r = _Read(c, codes, "codes", *_CODES)
+    top = _tops(c, tops, r)
     out = [c.like(t, torch.float32) for t in codes] if out is None else list(out)
-    po = a.like(out, "out", torch.float32)
-    _check(lib().ttt_adamw_values(pc, pt, int(moment), po, a.numel, a.n, c.on()), "ttt_adamw_values")
+    o = _sized(c, out, "out", _F32_ONLY, r)
+    _check(lib().ttt_adamw_values(r.at, top.at, int(moment), o.at, r.numel, r.n, c.on()), "ttt_adamw_values")
     return out

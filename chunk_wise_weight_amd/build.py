@@ -1,7 +1,8 @@
-"""Build libttt.so (the HIP library behind the C ABI) for gfx950 with hipcc.
+"""Build libttt.so (the HIP library behind the C ABI) for gfx950 with hipcc, and the binding's reader of tensor lists
+(host code, with g++).
 
 Usage: python -m chunk_wise_weight_amd.build [--verbose]
-The library is written next to this file, in-tree.
+Both are written next to this file, in-tree.
 """
 from __future__ import annotations
 
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +18,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libttt.so")
+# the binding's own extension module: reads what it needs of a list of tensors in one pass
+LISTS_SRC = os.path.join(CSRC, "tensor_lists.cpp")
+LISTS = os.path.join(PKG, "_tensor_lists.so")
 # a standalone program: MFMA throughput and shader clock under the power limit (not part of the library)
 PROBE_SRC = os.path.join(PKG, "probes", "mfma_clock.hip")
 PROBE = os.path.join(PKG, "probes", "mfma_clock")
@@ -42,6 +47,23 @@ def _hipcc() -> str:
     raise RuntimeError("hipcc not found; the ROCm toolchain is required to build libttt.so")
 
 
+def _build_lists(verbose: bool) -> None:
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{i}" for i in inc],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", LISTS_SRC, "-o", LISTS + ".tmp",
+           f"-L{os.path.join(at, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {LISTS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(LISTS + ".tmp", LISTS)
+
+
 def build(verbose: bool = False) -> str:
     hipcc = _hipcc()
     os.makedirs(OBJDIR, exist_ok=True)
@@ -60,7 +82,9 @@ def build(verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+        lists = ex.submit(_build_lists, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        lists.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:

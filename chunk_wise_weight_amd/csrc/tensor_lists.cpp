@@ -1,0 +1,82 @@
+// What the binding's calls on many tensors need of each, read in one pass over
+// the list: a Python attribute costs about a tenth of a microsecond, and a
+// step over the 144 small tensors of 36 layers reads five of each of its five
+// lists, 250 us, for a kernel of 8.
+//
+// read(list, name, device) -> (addresses, element counts, types, types seen, faults)
+//   three bytes objects of int64, int64 and int32, one entry per tensor, a mask
+//   of 1 << type and one of faults. Types are TTT_F32 0, TTT_BF16 1, uint8 2,
+//   int16 3, any other 4. Faults: 1 a tensor is not contiguous, 2 not on a
+//   device, 4 on another device than `device`; its address is then 0. Raises
+//   TypeError for what is no tensor, naming the list.
+#include <Python.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+namespace {
+
+int type_of(at::ScalarType t) {
+  switch (t) {
+    case at::kFloat: return 0;
+    case at::kBFloat16: return 1;
+    case at::kByte: return 2;
+    case at::kShort: return 3;
+    default: return 4;
+  }
+}
+
+PyObject *read_list(PyObject *list, const char *name, int device) {
+  const Py_ssize_t n = PyList_GET_SIZE(list);
+  PyObject *bytes[3];
+  const Py_ssize_t size[3] = {8, 8, 4};
+  for (int i = 0; i < 3; ++i) {
+    bytes[i] = PyBytes_FromStringAndSize(nullptr, n * size[i]);
+    if (!bytes[i]) {
+      while (i-- > 0) Py_DECREF(bytes[i]);
+      return nullptr;
+    }
+  }
+  auto *at = reinterpret_cast<int64_t *>(PyBytes_AS_STRING(bytes[0]));
+  auto *numel = reinterpret_cast<int64_t *>(PyBytes_AS_STRING(bytes[1]));
+  auto *kind = reinterpret_cast<int32_t *>(PyBytes_AS_STRING(bytes[2]));
+  long seen = 0, faults = 0;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject *o = PyList_GET_ITEM(list, i);
+    if (!THPVariable_Check(o)) {
+      PyErr_Format(PyExc_TypeError, "%s must be tensors, got %s", name, Py_TYPE(o)->tp_name);
+      for (PyObject *b : bytes) Py_DECREF(b);
+      return nullptr;
+    }
+    const at::Tensor &t = THPVariable_Unpack(o);
+    const long fault = t.layout() != at::kStrided || !t.is_contiguous() ? 1
+                       : !t.is_cuda()                                   ? 2
+                       : t.get_device() != device                       ? 4
+                                                                        : 0;
+    at[i] = fault ? 0 : reinterpret_cast<int64_t>(t.data_ptr());
+    numel[i] = t.numel();
+    kind[i] = type_of(t.scalar_type());
+    seen |= 1L << kind[i];
+    faults |= fault;
+  }
+  return Py_BuildValue("(NNNll)", bytes[0], bytes[1], bytes[2], seen, faults);
+}
+
+PyObject *read(PyObject *, PyObject *args) {
+  PyObject *list;
+  const char *name;
+  int device;
+  if (!PyArg_ParseTuple(args, "O!si", &PyList_Type, &list, &name, &device)) return nullptr;
+  try {
+    return read_list(list, name, device);
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+
+PyMethodDef methods[] = {{"read", read, METH_VARARGS, "addresses, element counts and types of a list of tensors"},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tensor_lists() { return PyModule_Create(&module); }
