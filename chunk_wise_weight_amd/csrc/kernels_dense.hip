@@ -384,13 +384,6 @@ bool dense_sizes(const GemmArgs &g, const GemmForm &f) {
   return !f.f32 && g.lda % 8 == 0 && g.ldb % 8 == 0 && dense_tiles(g, f, 128) <= (1LL << 22) && g.nk > 0 &&
          g.nk * g.segments <= (1LL << 34);
 }
-bool dense_aligned(const GemmArgs &g, const GemmForm &f) {
-  uintptr_t low = (uintptr_t)g.a[0] | (uintptr_t)g.b[0];
-  if (f.pair || g.segments > 1) low |= (uintptr_t)g.a[1];
-  if (g.batch > 1 || g.segments > 1) low |= (uintptr_t)g.b[1];
-  return low % 16 == 0;
-}
-
 hipError_t launch_dense(const GemmArgs &g, const GemmForm &f, int tile, int splits, hipStream_t s) {
   return tile == 256 ? run<Big>(g, f, splits, s) : run<Small>(g, f, splits, s);
 }

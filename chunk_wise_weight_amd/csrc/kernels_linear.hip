@@ -20,14 +20,13 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
 // ---------------------------------------------------------------------------
-// Any size, any alignment: tiles of 128 x 128, four waves of 64 x 64, staged
-// through registers. fp32 products run on the fp32 MFMA, whose products and
-// sums are those of fp32 FMAs.
+// Any size, any alignment: tiles of 128 x 128 (four waves of 64 x 64) or 64 x 64
+// (of 32 x 32), staged through registers into two LDS buffers in turn. The
+// loads of step n + 2 are issued when step n's registers have gone to LDS. fp32
+// products run on the fp32 MFMA, whose products and sums are those of fp32
+// FMAs.
 
-constexpr int kTile = 128, kThreads = 256;
-
-template <typename T>
-constexpr int kBK = sizeof(T) == 2 ? 32 : 16;  // k per step: 64 bytes of a row
+constexpr int kThreads = 256, BK = 32;  // k per step
 
 // n of 8 elements, the rest zero
 template <typename T>
@@ -45,17 +44,16 @@ __device__ __forceinline__ Raw8<T> load_some(const T *p, int n) {
   return r;
 }
 
-// One operand's tile: 128 rows of kBK, in LDS [row][k] where it lies by rows,
-// [k][row] where it lies transposed.
-template <typename T, bool TRANS>
+// One operand's tile: ROWS rows of 32 k, in LDS [row][k] where it lies by rows, [k][row] where it lies transposed.
+template <typename T, bool TRANS, int ROWS>
 struct Tile {
-  static constexpr int BK = kBK<T>, PAD = 16 / (int)sizeof(T);
-  static constexpr int PITCH = TRANS ? kTile + PAD : BK + PAD;
-  static constexpr int SIZE = TRANS ? BK * PITCH : kTile * PITCH;
-  static constexpr int N = kTile * BK / 8 / kThreads;
+  static constexpr int PAD = 16 / (int)sizeof(T), PITCH = (TRANS ? ROWS : BK) + PAD;
+  static constexpr int SIZE = (TRANS ? BK : ROWS) * PITCH;
+  static constexpr int ACROSS = (TRANS ? ROWS : BK) / 8;  // pieces of eight to a line
+  static constexpr int N = ROWS * BK / 8 / kThreads;
   Raw8<T> v[N];
 
-  // row(r): the operand's row of tile row r, and its matrix in m; -1 if none
+  // row(r): the operand's row of tile row r, and its matrix in m
   template <class Row>
   __device__ __forceinline__ void load(const void *const (&m)[2], long long ld, long long row0, long long rows,
                                        long long k0, long long nk, Row &&row) {
@@ -63,11 +61,11 @@ struct Tile {
     for (int n = 0; n < N; ++n) {
       const int q = threadIdx.x + n * kThreads;
       if constexpr (TRANS) {
-        const long long k = k0 + q / (kTile / 8), r = row0 + q % (kTile / 8) * 8;
+        const long long k = k0 + q / ACROSS, r = row0 + q % ACROSS * 8;
         v[n] = load_some(reinterpret_cast<const T *>(m[0]) + (k < nk ? k : 0) * ld + r, k < nk ? clamp8(rows - r) : 0);
       } else {
         int which = 0;
-        const long long r = row(q / (BK / 8), which), k = k0 + q % (BK / 8) * 8;
+        const long long r = row(q / ACROSS, which), k = k0 + q % ACROSS * 8;
         v[n] = load_some(reinterpret_cast<const T *>(m[which]) + (r < rows ? r : 0) * ld + k,
                          r < rows ? clamp8(nk - k) : 0);
       }
@@ -77,16 +75,14 @@ struct Tile {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int q = threadIdx.x + n * kThreads;
-      const int at = TRANS ? q / (kTile / 8) * PITCH + q % (kTile / 8) * 8 : q / (BK / 8) * PITCH + q % (BK / 8) * 8;
-      __builtin_memcpy(__builtin_assume_aligned(lds + at, 16), &v[n], sizeof v[n]);
+      __builtin_memcpy(__builtin_assume_aligned(lds + q / ACROSS * PITCH + q % ACROSS * 8, 16), &v[n], sizeof v[n]);
     }
   }
 };
 
 // Fragment of rows r0 .. r0 + 15 of a step.
-template <bool TRANS>
+template <bool TRANS, int P>
 __device__ __forceinline__ bf16x8 fragment(const bf16_t *lds, int r0, int lane) {
-  constexpr int P = Tile<bf16_t, TRANS>::PITCH;
   const int g = lane >> 4, t = lane & 15;
   if constexpr (TRANS) {
     // a transposing read takes, in each group of 16 lanes, a 4 x 16 block (lane t addresses row t/4, elements
@@ -99,108 +95,121 @@ __device__ __forceinline__ bf16x8 fragment(const bf16_t *lds, int r0, int lane) 
     return *reinterpret_cast<const bf16x8 *>(lds + (r0 + t) * P + 8 * g);
   }
 }
-// k = 4 (l / 16) + s in MFMA s of the step's four: the sum over k may take
-// them in any order as long as A and B do alike.
-template <bool TRANS>
-__device__ __forceinline__ f32x4 fragment(const float *lds, int r0, int lane) {
-  constexpr int P = Tile<float, TRANS>::PITCH;
+// k = 16 h + 4 (l / 16) + s in MFMA 4 h + s of the step's eight: the sum over k may take them in any order as long as A
+// and B do alike.
+struct Fragment32 {
+  f32x4 h[2];
+};
+template <bool TRANS, int P>
+__device__ __forceinline__ Fragment32 fragment(const float *lds, int r0, int lane) {
   const int g = lane >> 4, t = lane & 15;
-  if constexpr (TRANS) {
-    f32x4 v;
+  Fragment32 v;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) v[s] = lds[(4 * g + s) * P + r0 + t];
-    return v;
-  } else {
-    return *reinterpret_cast<const f32x4 *>(lds + (r0 + t) * P + 4 * g);
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (TRANS) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) v.h[h][s] = lds[(16 * h + 4 * g + s) * P + r0 + t];
+    } else {
+      v.h[h] = *reinterpret_cast<const f32x4 *>(lds + (r0 + t) * P + 16 * h + 4 * g);
+    }
   }
+  return v;
 }
 __device__ __forceinline__ void mma(f32x4 &acc, const bf16x8 &a, const bf16x8 &b) {
   acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
 }
-__device__ __forceinline__ void mma(f32x4 &acc, const f32x4 &a, const f32x4 &b) {
+__device__ __forceinline__ void mma(f32x4 &acc, const Fragment32 &a, const Fragment32 &b) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], acc, 0, 0, 0);
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.h[h][s], b.h[h][s], acc, 0, 0, 0);
 }
 
-// grid: i tiles (128 rows of A; with a pair 64 of each matrix), times j tiles, times batch, times splits of k
-template <typename T, typename O, bool AT, bool BT, bool PAIR>
+// grid: i tiles (TILE rows of A; with a pair half as many of each matrix), times j tiles, times batch, times splits of k
+template <typename T, typename O, bool AT, bool BT, bool PAIR, int TILE>
 __global__ __launch_bounds__(kThreads, 2) void k_gemm(GemmArgs g, long long ti, long long tj, Parts parts) {
-  using TA = Tile<T, AT>;
-  using TB = Tile<T, BT>;
-  __shared__ __attribute__((aligned(16))) T la[TA::SIZE];
-  __shared__ __attribute__((aligned(16))) T lb[TB::SIZE];
+  using TA = Tile<T, AT, TILE>;
+  using TB = Tile<T, BT, TILE>;
+  constexpr int F = TILE / 32, HALF = TILE / 4;  // fragments of a wave either way; a pair's rows of one matrix in a wave
+  __shared__ __attribute__((aligned(16))) T lds[2][TA::SIZE + TB::SIZE];
   const long long n = group_index();
   if (n >= ti * tj * g.batch * parts.splits) return;
   const long long tile = n % (ti * tj);
   const int z = (int)(n / (ti * tj) % g.batch), split = (int)(n / (ti * tj * g.batch));
-  const long long j0 = tile / ti * kTile, i0 = tile % ti * (PAIR ? kTile / 2 : kTile);
+  const long long j0 = tile / ti * TILE, i0 = tile % ti * (PAIR ? TILE / 2 : TILE);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wi = w & 1, wj = w >> 1;
-  f32x4 acc[4][4];
+  f32x4 acc[F][F];
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int a = 0; a < F; ++a)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // with a pair, a wave's 64 rows of A are 32 of the first matrix and the matching 32 of the second
+    for (int b = 0; b < F; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // with a pair, a wave's rows of A are HALF of the first matrix and the matching HALF of the second
   auto row_a = [&](int r, int &which) {
     if constexpr (PAIR) {
-      which = (r >> 5) & 1;
-      return i0 + (r >> 6) * 32 + (r & 31);
+      which = r / HALF & 1;
+      return i0 + r / (2 * HALF) * HALF + r % HALF;
     }
     return i0 + r;
   };
   auto row_b = [&](int r, int &) { return j0 + r; };
-  constexpr int BK = kBK<T>;
   const long long per = (g.nk + BK - 1) / BK, steps = per * g.segments;
   const long long first = steps * split / parts.splits, end = steps * (split + 1) / parts.splits;
-  TA ta;
-  TB tb;
-  auto fetch = [&](long long st) {
+  TA ta[2];
+  TB tb[2];
+  auto fetch = [&](long long st, TA &a, TB &b) {
     const int sg = st >= per;
     const long long k0 = (st - sg * per) * BK;
-    const void *const a[2] = {PAIR ? g.a[0] : g.a[sg], g.a[1]};
-    const void *const b[2] = {g.b[sg + z], nullptr};
-    ta.load(a, g.lda, i0, g.ni, k0, g.nk, row_a);
-    tb.load(b, g.ldb, j0, g.nj, k0, g.nk, row_b);
+    const void *const pa[2] = {PAIR ? g.a[0] : g.a[sg], g.a[1]};
+    const void *const pb[2] = {g.b[sg + z], nullptr};
+    a.load(pa, g.lda, i0, g.ni, k0, g.nk, row_a);
+    b.load(pb, g.ldb, j0, g.nj, k0, g.nk, row_b);
   };
-  if (first < end) fetch(first);
-  for (long long st = first; st < end; ++st) {
-    ta.put(la);
-    tb.put(lb);
+  // A wave that writes a buffer has passed the barrier of the step between, which every wave reaches only after its
+  // reads of that buffer.
+  auto step = [&](long long st, TA &a, TB &b, T *buf) {
+    T *la = buf, *lb = buf + TA::SIZE;
+    a.put(la);
+    b.put(lb);
+    if (st + 2 < end) fetch(st + 2, a, b);
     __syncthreads();
-    if (st + 1 < end) fetch(st + 1);
-    decltype(fragment<AT>(la, 0, 0)) fa[4], fb[4];
+    decltype(fragment<AT, TA::PITCH>(la, 0, 0)) fa[F], fb[F];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) fa[x] = fragment<AT>(la, wi * 64 + x * 16, lane);
+    for (int x = 0; x < F; ++x) fa[x] = fragment<AT, TA::PITCH>(la, (wi * F + x) * 16, lane);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) fb[x] = fragment<BT>(lb, wj * 64 + x * 16, lane);
+    for (int x = 0; x < F; ++x) fb[x] = fragment<BT, TB::PITCH>(lb, (wj * F + x) * 16, lane);
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < F; ++x)
 #pragma unroll
-      for (int y = 0; y < 4; ++y) mma(acc[x][y], fa[x], fb[y]);
-    __syncthreads();
+      for (int y = 0; y < F; ++y) mma(acc[x][y], fa[x], fb[y]);
+  };
+  if (first < end) fetch(first, ta[0], tb[0]);
+  if (first + 1 < end) fetch(first + 1, ta[1], tb[1]);
+  for (long long st = first; st < end; st += 2) {
+    step(st, ta[0], tb[0], lds[0]);
+    if (st + 1 < end) step(st + 1, ta[1], tb[1], lds[1]);
   }
   if (parts.splits > 1) {
-    float *p = parts.at + (n * kTile + wj * 64) * kTile + wi * 64;
+    float *p = parts.at + (n * TILE + wj * (TILE / 2)) * TILE + wi * (TILE / 2);
 #pragma unroll
-    for (int y = 0; y < 4; ++y)
+    for (int y = 0; y < F; ++y)
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        *reinterpret_cast<f32x4 *>(p + (y * 16 + (lane & 15)) * kTile + x * 16 + 4 * (lane >> 4)) = acc[x][y];
+      for (int x = 0; x < F; ++x)
+        *reinterpret_cast<f32x4 *>(p + (y * 16 + (lane & 15)) * TILE + x * 16 + 4 * (lane >> 4)) = acc[x][y];
     end_of_stores();
     return;
   }
 #pragma unroll
-  for (int y = 0; y < 4; ++y) {
-    const long long j = j0 + wj * 64 + y * 16 + (lane & 15);
+  for (int y = 0; y < F; ++y) {
+    const long long j = j0 + (wj * F + y) * 16 + (lane & 15);
     if (j >= g.nj) continue;
 #pragma unroll
-    for (int x = 0; x < (PAIR ? 2 : 4); ++x) {
-      const long long i = i0 + wi * (PAIR ? 32 : 64) + x * 16 + 4 * (lane >> 4);
+    for (int x = 0; x < (PAIR ? F / 2 : F); ++x) {
+      const long long i = i0 + wi * (PAIR ? HALF : 2 * HALF) + x * 16 + 4 * (lane >> 4);
       const int left = i < g.ni ? (int)(g.ni - i < 4 ? g.ni - i : 4) : 0;
       if (left == 0) continue;
       float v[4] = {acc[x][y][0], acc[x][y][1], acc[x][y][2], acc[x][y][3]};
       if constexpr (PAIR) {
-        float u[4] = {acc[x + 2][y][0], acc[x + 2][y][1], acc[x + 2][y][2], acc[x + 2][y][3]};
+        float u[4] = {acc[x + F / 2][y][0], acc[x + F / 2][y][1], acc[x + F / 2][y][2], acc[x + F / 2][y][3]};
         finish_pair<T>(g, i, j, left, v, u);
       } else {
         finish<T, O>(g, z, i, j, left, v);
@@ -244,31 +253,43 @@ __global__ __launch_bounds__(kThreads) void k_join(GemmArgs g, long long ti, lon
   end_of_stores();
 }
 
-template <typename T, typename O, bool AT, bool BT, bool PAIR>
-hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) {
-  const long long ti = (g.ni + (PAIR ? kTile / 2 : kTile) - 1) / (PAIR ? kTile / 2 : kTile);
-  const long long tj = (g.nj + kTile - 1) / kTile;
-  if (ti * tj == 0) return hipSuccess;
-  const Parts parts{(float *)g.ws, splits, kTile, kTile, kTile / 4};
-  hipLaunchKernelGGL((k_gemm<T, O, AT, BT, PAIR>), group_grid(ti * tj * g.batch * splits), dim3(kThreads), 0, s, g, ti,
-                     tj, parts);
-  return splits > 1 ? launch_join(g, f, ti, tj, parts, s) : hipGetLastError();
+// ---------------------------------------------------------------------------
+// Rows copied to where they start on 16 bytes, zero behind their ends, so that
+// a product of odd widths can run on the tiles that load whole pieces.
+
+struct PackJob {
+  const bf16_t *src;
+  bf16_t *dst;
+  long long rows, n, first;  // first: pieces of eight before this job's
+};
+struct PackJobs {
+  PackJob job[4];
+  int count;
+  long long pieces;
+};
+__global__ __launch_bounds__(kThreads) void k_pack(PackJobs p) {
+  const long long q = group_index() * kThreads + threadIdx.x;
+  if (q >= p.pieces) return;
+  int k = 0;
+#pragma unroll
+  for (int i = 1; i < 4; ++i)
+    if (i < p.count && q >= p.job[i].first) k = i;
+  const long long n = p.job[k].n, per = (n + 7) / 8, at = q - p.job[k].first, r = at / per, c = at % per * 8;
+  const Raw8<bf16_t> v = load_some(p.job[k].src + r * n + c, clamp8(n - c));
+  __builtin_memcpy(__builtin_assume_aligned(p.job[k].dst + at * 8, 16), &v, 16);
+  end_of_stores();
 }
 
-template <typename T, typename O>
-hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) {
-  if (f.pair) return run_gemm<T, T, false, false, true>(g, f, splits, s);
-  if (!f.a_trans) return run_gemm<T, O, false, false, false>(g, f, splits, s);
-  // gradients come in the operands' type
-  return f.b_trans ? run_gemm<T, T, true, true, false>(g, f, splits, s)
-                   : run_gemm<T, T, true, false, false>(g, f, splits, s);
-}
+long long pad8(long long n) { return (n + 7) / 8 * 8; }
 
-// ---- the choice of tile and splits ----
+// ---- the choice of kernel, tile and splits ----
 //
-// By what a launch would take: rounds of tiles over the device's 256 CUs times
-// a tile's share of k, and for splits the fp32 sums written and read again and
-// the second launch.
+// By what a launch would take: its 64-k slabs times what the tiles take for one
+// slab (us_slab, per form); for splits the fp32 sums written and read again, in
+// the last-level cache up to 100 MB, and the second launch; for rows that are
+// copied first their bytes and a launch. The times are measured ones
+// (microseconds). Over 49 products of 17 to 32768 rows of all forms the choice
+// took at most 10 % more than the best of both tiles with 1 to 16 splits.
 
 constexpr int kCus = 256;
 struct Choice {
@@ -276,35 +297,103 @@ struct Choice {
   double us;
 };
 
-// us_slab: one tile's 64 of k with `slots` tiles at once on the device
-Choice choose(const GemmArgs &g, const GemmForm &f, int tile, long long tiles, int slots, double us_slab) {
+// us_slab(n): of n tiles on the device
+template <class F>
+Choice choose(const GemmArgs &g, int tile, long long tiles, F &&us_slab) {
   Choice best{tile, 1, 1e30};
   const double slabs = (double)((g.nk + 63) / 64) * g.segments;
   const double bytes = (double)tiles * tile * tile * 4;
   for (int s = 1; s <= 32; ++s) {
     if (s > 1 && (slabs / s < 4 || bytes * s > 512e6)) break;
-    const double rounds = (double)((tiles * s + slots - 1) / slots);
-    double us = rounds * std::ceil(slabs / s) * us_slab;
-    if (s > 1) us += 4.0 + 2.0 * bytes * s / 4.0e6;  // 4 TB/s
-    if (us < 0.95 * best.us) best = Choice{tile, s, us};
+    double us = std::ceil(slabs / s) * us_slab(tiles * s);
+    if (s > 1) us += 5.0 + 2.0 * bytes * s / (bytes * s <= 100e6 ? 6.0e6 : 4.0e6);
+    if (us < 0.97 * best.us) best = Choice{tile, s, us};
   }
   return best;
 }
 
-long long general_tiles(const GemmArgs &g, const GemmForm &f) {
-  const int wide = f.pair ? kTile / 2 : kTile;
-  return (g.ni + wide - 1) / wide * ((g.nj + kTile - 1) / kTile) * g.batch;
+long long general_tiles(const GemmArgs &g, const GemmForm &f, int tile) {
+  const int wide = f.pair ? tile / 2 : tile;
+  return (g.ni + wide - 1) / wide * ((g.nj + tile - 1) / tile) * g.batch;
 }
+// Several tiles share a CU: what one takes by itself, or each one's share on the fullest CU.
 Choice choose_general(const GemmArgs &g, const GemmForm &f) {
-  return choose(g, f, kTile, general_tiles(g, f), 2 * kCus, f.f32 ? 10.5 : 1.7);
+  const double wait = f.b_trans ? 3.5 : f.a_trans ? 2.6 : 1.8;  // bf16, a tile of 128 alone
+  auto shared = [](double alone, double share) {
+    return [=](long long n) { return std::max(alone, (double)((n + kCus - 1) / kCus) * share); };
+  };
+  const Choice big = choose(g, 128, general_tiles(g, f, 128), shared(f.f32 ? 5.1 : wait, f.f32 ? 4.4 : 0.9));
+  const Choice small = choose(g, 64, general_tiles(g, f, 64), shared(f.f32 ? 2.2 : 0.5 * wait, f.f32 ? 1.17 : 0.42));
+  return small.us < big.us ? small : big;
 }
+// Tiles of 256 run in rounds of one per CU, those of 128 in rounds of two.
 Choice choose_dense(const GemmArgs &g, const GemmForm &f) {
-  const Choice big = choose(g, f, 256, dense_tiles(g, f, 256), kCus, 1.7);
-  const Choice small = choose(g, f, 128, dense_tiles(g, f, 128), 2 * kCus, 1.1);
+  const Choice big = choose(g, 256, dense_tiles(g, f, 256), [](long long n) { return 1.75 * ((n + kCus - 1) / kCus); });
+  const Choice small = choose(g, 128, dense_tiles(g, f, 128), [](long long n) {
+    const double rest = (double)(n % (2 * kCus)) / kCus;
+    return 1.2 * (n / (2 * kCus)) + (rest > 0 ? 0.9 + 0.3 * std::max(0.0, rest - 1) : 0);
+  });
   return small.us < big.us ? small : big;
 }
 size_t parts_bytes(long long tiles, const Choice &c) {
   return c.splits > 1 ? (size_t)tiles * c.splits * c.tile * c.tile * 4 : 0;
+}
+
+// How a product runs, by its sizes: which operands are copied first, and the workspace: copies, then sums.
+struct Plan {
+  bool dense, pack_a, pack_b;
+  Choice choice;
+  GemmArgs g;  // sizes as they are after the copies
+  long long rows_a, rows_b;
+  int count_a, count_b;  // matrices of each operand
+  size_t copies, parts;
+};
+Plan plan_of(const GemmArgs &g, const GemmForm &f) {
+  Plan p{};
+  p.g = g;
+  p.choice = choose_general(g, f);
+  p.parts = parts_bytes(general_tiles(g, f, p.choice.tile), p.choice);
+  if (f.f32) return p;
+  Plan d = p;
+  d.dense = true;
+  d.pack_a = g.lda % 8 != 0;
+  d.pack_b = g.ldb % 8 != 0;
+  d.g.lda = pad8(g.lda);
+  d.g.ldb = pad8(g.ldb);
+  d.rows_a = f.a_trans ? g.nk : g.ni;
+  d.rows_b = f.b_trans ? g.nk : g.nj;
+  d.count_a = f.pair || g.segments > 1 ? 2 : 1;
+  d.count_b = g.segments > 1 || g.batch > 1 ? 2 : 1;
+  if (!dense_sizes(d.g, f)) return p;
+  d.choice = choose_dense(g, f);
+  d.parts = parts_bytes(dense_tiles(g, f, d.choice.tile), d.choice);
+  if (d.pack_a) d.copies += (size_t)d.count_a * d.rows_a * d.g.lda * 2;
+  if (d.pack_b) d.copies += (size_t)d.count_b * d.rows_b * d.g.ldb * 2;
+  const double us = d.choice.us + (d.copies ? 4.0 + 2.0 * d.copies / 4.0e6 : 0.0);
+  return d.copies && us >= p.choice.us ? p : d;
+}
+
+template <typename T, typename O, bool AT, bool BT, bool PAIR, int TILE>
+hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) {
+  const int wide = PAIR ? TILE / 2 : TILE;
+  const long long ti = (g.ni + wide - 1) / wide, tj = (g.nj + TILE - 1) / TILE;
+  if (ti * tj == 0) return hipSuccess;
+  const Parts parts{(float *)g.ws, splits, TILE, TILE, TILE / 4};
+  hipLaunchKernelGGL((k_gemm<T, O, AT, BT, PAIR, TILE>), group_grid(ti * tj * g.batch * splits), dim3(kThreads), 0, s,
+                     g, ti, tj, parts);
+  return splits > 1 ? launch_join(g, f, ti, tj, parts, s) : hipGetLastError();
+}
+template <typename T, typename O, bool AT, bool BT, bool PAIR>
+hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, const Choice &c, hipStream_t s) {
+  return c.tile == 128 ? run_gemm<T, O, AT, BT, PAIR, 128>(g, f, c.splits, s)
+                       : run_gemm<T, O, AT, BT, PAIR, 64>(g, f, c.splits, s);
+}
+template <typename T, typename O>
+hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, const Choice &c, hipStream_t s) {
+  if (f.pair) return run_gemm<T, T, false, false, true>(g, f, c, s);
+  if (!f.a_trans) return run_gemm<T, O, false, false, false>(g, f, c, s);
+  // gradients come in the operands' type
+  return f.b_trans ? run_gemm<T, T, true, true, false>(g, f, c, s) : run_gemm<T, T, true, false, false>(g, f, c, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -505,21 +594,39 @@ hipError_t launch_join(const GemmArgs &g, const GemmForm &f, long long ti, long 
 
 size_t gemm_ws_bytes(const GemmArgs &g, const GemmForm &f) {
   if (few_sizes(g, f)) return 0;
-  const size_t general = parts_bytes(general_tiles(g, f), choose_general(g, f));
-  if (!dense_sizes(g, f)) return general;
-  const Choice c = choose_dense(g, f);
-  return std::max(general, parts_bytes(dense_tiles(g, f, c.tile), c));
+  // operands that need no copy may still not start on 16 bytes, and the product then runs as a general one
+  const Choice c = choose_general(g, f);
+  const Plan p = plan_of(g, f);
+  return std::max(parts_bytes(general_tiles(g, f, c.tile), c), p.copies + p.parts);
 }
 
 hipError_t launch_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
   if (few_sizes(g, f)) return launch_few(g, f, s);
-  if (dense_sizes(g, f) && dense_aligned(g, f)) {
-    const Choice c = choose_dense(g, f);
-    return launch_dense(g, f, c.tile, c.splits, s);
+  const Plan p = plan_of(g, f);
+  uintptr_t low = 0;
+  for (int i = 0; i < p.count_a; ++i) low |= p.pack_a ? 0 : (uintptr_t)g.a[i];
+  for (int i = 0; i < p.count_b; ++i) low |= p.pack_b ? 0 : (uintptr_t)g.b[i];
+  if (p.dense && low % 16 == 0) {
+    GemmArgs d = p.g;
+    if (p.copies) {
+      PackJobs jobs{};
+      bf16_t *to = (bf16_t *)g.ws;
+      auto add = [&](const void *&m, long long rows, long long n) {
+        jobs.job[jobs.count++] = PackJob{(const bf16_t *)m, to, rows, n, jobs.pieces};
+        m = to;
+        to += rows * pad8(n);
+        jobs.pieces += rows * (pad8(n) / 8);
+      };
+      for (int i = 0; p.pack_a && i < p.count_a; ++i) add(d.a[i], p.rows_a, g.lda);
+      for (int i = 0; p.pack_b && i < p.count_b; ++i) add(d.b[i], p.rows_b, g.ldb);
+      hipLaunchKernelGGL(k_pack, group_grid((jobs.pieces + kThreads - 1) / kThreads), dim3(kThreads), 0, s, jobs);
+      d.ws = to;
+    }
+    return launch_dense(d, f, p.choice.tile, p.choice.splits, s);
   }
-  const int splits = choose_general(g, f).splits;
-  if (f.f32) return run_gemm<float, float>(g, f, splits, s);
-  return f.out_f32 ? run_gemm<bf16_t, float>(g, f, splits, s) : run_gemm<bf16_t, bf16_t>(g, f, splits, s);
+  const Choice c = choose_general(g, f);
+  if (f.f32) return run_gemm<float, float>(g, f, c, s);
+  return f.out_f32 ? run_gemm<bf16_t, float>(g, f, c, s) : run_gemm<bf16_t, bf16_t>(g, f, c, s);
 }
 
 size_t act_grad_ws_bytes(long long rows, long long n, bool gated) {

@@ -54,9 +54,9 @@ bool few_sizes(const GemmArgs &g, const GemmForm &f);
 hipError_t launch_few(const GemmArgs &g, const GemmForm &f, hipStream_t s);
 
 // bf16 operands whose rows start on 16 bytes (kernels_dense.hip): sizes that allow it, the launch with tiles of
-// `tile` x `tile` (256 or 128), and its workgroups (tiles times batch).
+// `tile` x `tile` (256 or 128), and its workgroups (tiles times batch). k past nk in the last piece of eight of an
+// operand held by rows is zero.
 bool dense_sizes(const GemmArgs &g, const GemmForm &f);
-bool dense_aligned(const GemmArgs &g, const GemmForm &f);
 long long dense_tiles(const GemmArgs &g, const GemmForm &f, int tile);
 hipError_t launch_dense(const GemmArgs &g, const GemmForm &f, int tile, int splits, hipStream_t s);
 
