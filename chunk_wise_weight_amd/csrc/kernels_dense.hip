@@ -46,13 +46,13 @@ __device__ __forceinline__ int zsw(int k) { return ((k & 3) ^ ((k >> 3) & 1)) <<
 // barriers order them. No register outputs: the data goes to LDS at M0 + 16
 // bytes per lane. M0 is the compiler's register, saved and put back; one wait
 // state must pass between its write and the load.
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, bf16_t *lds, uint32_t voff, uint32_t soff) {
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, bf16_t *lds, uint32_t voff) {
   const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
   uint32_t keep;
   asm volatile(
-      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
       : "=&s"(keep)
-      : "s"(base), "v"(voff), "s"(rs), "s"(soff)
+      : "s"(base), "v"(voff), "s"(rs)
       : "memory");
 }
 
@@ -61,72 +61,69 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, long long 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, clamp_bytes(bytes), kBufferFlags);
 }
 
-// The loads of one operand's tile by one wave: 32 of its rows (or, transposed, 32 of a block's 64 k), four at 1 KB.
-template <bool TRANS, int NW>
+// The loads of one operand's tile by one wave: 8 N of its rows (or, transposed, 8 N of a block's 64 k), 1 KB each. The
+// chunks' permutations depend on the load only through its parity.
+template <bool TRANS, int N>
 struct Loads {
   const bf16_t *seg[2];  // first row of this wave's matrix, per segment; transposed: first column of its block
-  long long ld, rows;    // rows of the matrix left from there; transposed: elements of a row left from there
+  long long ld, rows;    // rows of the matrix left from there; transposed: columns before its block
   long long nk;
-  uint32_t vo[4];
-  int chunk[4];  // k of the lane's piece in a slab (by rows), row of k (transposed)
-  int lds0;      // element offset of the wave's share
+  uint32_t vo[N];
+  int k[2];  // of the lane's piece in a slab (by rows), for even and odd loads
+  int lds0;  // element offset of the wave's share
 
-  // by rows: row0 is the operand's row that the wave's first tile row w*32 holds
+  // by rows: row0 is the operand's row that the wave's first tile row holds; transposed: the tile's first column
   __device__ __forceinline__ void init(const void *s0, const void *s1, long long ld_, long long row0, long long nrows,
                                        long long nk_, int w, int lane) {
     ld = ld_;
     nk = nk_;
+    lds0 = w * 8 * N * SK;
     if constexpr (TRANS) {
-      const int blk = w >> 1, k0 = (w & 1) * 32;
-      const long long col = row0 + blk * 64;
+      const int k0 = w * 8 * N % 64;
+      const long long col = row0 + w * 8 * N / 64 * 64;
       seg[0] = (const bf16_t *)s0 + col;
       seg[1] = (const bf16_t *)s1 + col;
       rows = col;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int k = k0 + 8 * n + (lane >> 3);
-        chunk[n] = k;
-        vo[n] = (uint32_t)(k * ld * 2 + (((lane & 7) ^ zsw(k)) << 4));
+      for (int n = 0; n < N; ++n) {
+        const int kr = k0 + 8 * n + (lane >> 3);
+        vo[n] = (uint32_t)(kr * ld * 2 + (((lane & 7) ^ zsw(kr)) << 4));
       }
-      lds0 = (blk * 64 + k0) * 64;
     } else {
       seg[0] = (const bf16_t *)s0 + row0 * ld;
       seg[1] = (const bf16_t *)s1 + row0 * ld;
       rows = nrows - row0;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int r = 8 * n + (lane >> 3), c = (lane & 7) ^ swz(w * 32 + r);
-        chunk[n] = c * 8;
+      for (int n = 0; n < N; ++n) {
+        const int r = 8 * n + (lane >> 3), c = (lane & 7) ^ swz(r);
+        if (n < 2) k[n] = c * 8;
         vo[n] = (uint32_t)(r * ld * 2 + c * 16);
       }
-      lds0 = w * 32 * SK;
     }
   }
   struct Pre {
     __amdgpu_buffer_rsrc_t rs;
-    uint32_t soff;
-    int left;  // k left from the slab on
+    bool past[2];  // the lane's piece lies past the last k
   };
   __device__ __forceinline__ Pre prep(int sg, long long k0) const {
     Pre p;
     const bf16_t *s = sg ? seg[1] : seg[0];
     const long long left = nk - k0;
-    p.left = left > SK ? SK : (int)left;
     if constexpr (TRANS) {
-      // from the slab's first row to the end of the array
+      // from the slab's first row to the end of the array: rows past the last k lie behind it
       p.rs = rsrc(s + k0 * ld, (left * ld - rows) * 2);
-      p.soff = 0;
     } else {
+      // behind the last k of a row lies the next one
       p.rs = rsrc(s + k0, (rows * ld - k0) * 2);
-      p.soff = 0;
+      p.past[0] = k[0] >= left;
+      p.past[1] = k[1] >= left;
     }
     return p;
   }
   __device__ __forceinline__ void issue(const Pre &p, bf16_t *tile, int n) const {
-    // by rows the last slab's k past the end would read the next row
     uint32_t v = vo[n];
-    if (chunk[n] >= p.left) v = kOutOfRange;
-    dma16(p.rs, tile + lds0 + n * 8 * SK, v, p.soff);
+    if (!TRANS && p.past[n & 1]) v = kOutOfRange;
+    dma16(p.rs, tile + lds0 + n * 8 * SK, v);
   }
 };
 
@@ -134,8 +131,9 @@ template <int FI_, int FJ_, int WI_, int WJ_>
 struct Shape {
   static constexpr int FI = FI_, FJ = FJ_, WI = WI_, WJ = WJ_, NW = WI * WJ;
   static constexpr int TI = 16 * FI * WI, TJ = 16 * FJ * WJ;
-  static_assert(TI == 32 * NW && TJ == 32 * NW, "each wave loads 32 rows of each operand");
-  static constexpr int THREADS = 64 * NW, PER_CU = NW == 8 ? 1 : 2;
+  static constexpr int N = TI / (8 * NW);  // loads of a wave per operand and slab
+  static_assert(TI == TJ && N % 4 == 0, "square tiles; a wave's rows are whole 32s");
+  static constexpr int THREADS = 64 * NW, PER_CU = TI == 256 ? 1 : 2;
   static constexpr int SLAB = (TI + TJ) * SK;      // elements
   static constexpr int PITCH = 16 * FI + 4;        // of the epilogue's rows, fp32
   static constexpr int RING = 2 * SLAB * 2, OUT = NW * 32 * PITCH * 4;
@@ -146,7 +144,7 @@ using Small = Shape<4, 4, 2, 2>;
 
 // s_waitcnt immediate (gfx9): vmcnt(n), expcnt unchanged, lgkmcnt(0)
 constexpr unsigned wait_imm(int n) { return (unsigned)((n & 15) | 0x70 | (((n >> 4) & 3) << 14)); }
-// Every wave's loads but the last `later` (8 or none) have landed, and its reads of LDS are done.
+// Every wave's loads but the last LATER have landed, and its reads of LDS are done.
 template <int LATER>
 __device__ __forceinline__ void meet() {
   __builtin_amdgcn_s_waitcnt(wait_imm(LATER));
@@ -207,17 +205,18 @@ __global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int
   const long long i0 = (long long)tx * WIDE, j0 = (long long)ty * S::TJ;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wi = w % S::WI, wj = w / S::WI;
 
-  Loads<AT, S::NW> la;
-  Loads<BT, S::NW> lb;
+  constexpr int N = S::N, RW = 8 * N;  // rows of the tile that a wave loads
+  Loads<AT, N> la;
+  Loads<BT, N> lb;
   if constexpr (PAIR) {
-    // rows 32 w .. of the tile: group w*32 / (2 HALF), matrix and row within it
-    const int q = w * 32 % (2 * HALF);
-    const long long row = i0 + w * 32 / (2 * HALF) * HALF + q % HALF;
+    // rows RW w .. of the tile: their group of 2 HALF, the matrix and the row within it
+    const int q = w * RW % (2 * HALF);
+    const long long row = i0 + w * RW / (2 * HALF) * HALF + q % HALF;
     la.init(g.a[q / HALF], g.a[q / HALF], g.lda, row, g.ni, g.nk, w, lane);
   } else {
-    la.init(g.a[0], g.a[1], g.lda, AT ? i0 : i0 + w * 32, g.ni, g.nk, w, lane);
+    la.init(g.a[0], g.a[1], g.lda, AT ? i0 : i0 + w * RW, g.ni, g.nk, w, lane);
   }
-  lb.init(g.b[z], g.b[1], g.ldb, BT ? j0 : j0 + w * 32, g.nj, g.nk, w, lane);
+  lb.init(g.b[z], g.b[1], g.ldb, BT ? j0 : j0 + w * RW, g.nj, g.nk, w, lane);
 
   const int per = (int)((g.nk + SK - 1) / SK), slabs = per * g.segments;
   const int first = (int)((long long)slabs * split / parts.splits);
@@ -232,19 +231,19 @@ __global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int
   auto tile_a = [&](int sl) { return ring + (sl & 1) * S::SLAB; };
   auto tile_b = [&](int sl) { return ring + (sl & 1) * S::SLAB + S::TI * SK; };
   struct Pre {
-    typename Loads<AT, S::NW>::Pre a;
-    typename Loads<BT, S::NW>::Pre b;
+    typename Loads<AT, N>::Pre a;
+    typename Loads<BT, N>::Pre b;
   };
   auto prep = [&](int sl) {
     const int sg = sl >= per;
     const long long k0 = (long long)(sl - sg * per) * SK;
     return Pre{la.prep(sg, k0), lb.prep(sg, k0)};
   };
-  auto issue = [&](const Pre &p, int sl, int n) {  // load n of 8
-    if (n < 4)
+  auto issue = [&](const Pre &p, int sl, int n) {  // load n of 2 N
+    if (n < N)
       la.issue(p.a, tile_a(sl), n);
     else
-      lb.issue(p.b, tile_b(sl), n - 4);
+      lb.issue(p.b, tile_b(sl), n - N);
   };
   bf16x8 lo[HF], hi[HF], fb[2][FJ];
   const int ra = wi * 16 * FI, rb = wj * 16 * FJ;
@@ -278,7 +277,7 @@ __global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int
       }
       if (REFILL) {
 #pragma unroll
-        for (int n = (x - 1) * 8 / (FI - 1); n < x * 8 / (FI - 1); ++n) issue(p, sl + 2, n);
+        for (int n = (x - 1) * 2 * N / (FI - 1); n < x * 2 * N / (FI - 1); ++n) issue(p, sl + 2, n);
       }
       pin();
     }
@@ -288,12 +287,12 @@ __global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int
   if (first < end) {
     Pre p = prep(first);
 #pragma unroll
-    for (int n = 0; n < 8; ++n) issue(p, first, n);
+    for (int n = 0; n < 2 * N; ++n) issue(p, first, n);
     if (first + 1 < end) {
       p = prep(first + 1);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) issue(p, first + 1, n);
-      meet<8>();
+      for (int n = 0; n < 2 * N; ++n) issue(p, first + 1, n);
+      meet<2 * N>();
     } else {
       meet<0>();
     }
