@@ -41,12 +41,19 @@ __device__ __forceinline__ int lds_off(int r, int c) { return r * SK + ((c ^ swz
 // gives the rows that are served at a time disjoint banks.
 __device__ __forceinline__ int zsw(int k) { return ((k & 3) ^ ((k >> 3) & 1)) << 1; }
 
-// A load the compiler does not track: tracked, it would wait for every load in
-// flight before each transposing read. The kernel's own counted waits and
-// barriers order them. No register outputs: the data goes to LDS at M0 + 16
-// bytes per lane. M0 is the compiler's register, saved and put back; one wait
-// state must pass between its write and the load.
+// 16 bytes per lane from memory to LDS. TRACKED: as the compiler's own. With
+// transposing reads it would then wait for every load in flight before each of
+// them (1.29 -> 1.64 ms for 32768 x 9728 x 2560), so there the load is one that
+// it does not track, ordered by the kernel's counted waits and barriers alone.
+// It has no register outputs: the data goes to LDS at M0 + 16 bytes per lane.
+// M0 is the compiler's register, saved and put back; one wait state must pass
+// between its write and the load.
+template <bool TRACKED>
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, bf16_t *lds, uint32_t voff) {
+  if constexpr (TRACKED) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)lds, 16, voff, 0, 0, 0);
+    return;
+  }
   const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
   uint32_t keep;
   asm volatile(
@@ -56,9 +63,8 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, bf16_t *lds, ui
       : "memory");
 }
 
-__device__ __forceinline__ int clamp_bytes(long long n) { return n < 0 ? 0 : n > 0x7fffffffLL ? 0x7fffffff : (int)n; }
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, long long bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, clamp_bytes(bytes), kBufferFlags);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, bytes > 0 ? bytes : 0, kBufferFlags);
 }
 
 // The loads of one operand's tile by one wave: 8 N of its rows (or, transposed, 8 N of a block's 64 k), 1 KB each. The
@@ -66,7 +72,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, long long 
 template <bool TRANS, int N>
 struct Loads {
   const bf16_t *seg[2];  // first row of this wave's matrix, per segment; transposed: first column of its block
-  long long ld, rows;    // rows of the matrix left from there; transposed: columns before its block
+  int ld;
+  int span;  // bytes from there to the end of the wave's rows; transposed: of the columns before its block
   long long nk;
   uint32_t vo[N];
   int k[2];  // of the lane's piece in a slab (by rows), for even and odd loads
@@ -75,7 +82,7 @@ struct Loads {
   // by rows: row0 is the operand's row that the wave's first tile row holds; transposed: the tile's first column
   __device__ __forceinline__ void init(const void *s0, const void *s1, long long ld_, long long row0, long long nrows,
                                        long long nk_, int w, int lane) {
-    ld = ld_;
+    ld = (int)ld_;
     nk = nk_;
     lds0 = w * 8 * N * SK;
     if constexpr (TRANS) {
@@ -83,7 +90,7 @@ struct Loads {
       const long long col = row0 + w * 8 * N / 64 * 64;
       seg[0] = (const bf16_t *)s0 + col;
       seg[1] = (const bf16_t *)s1 + col;
-      rows = col;
+      span = (int)col * 2;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         const int kr = k0 + 8 * n + (lane >> 3);
@@ -92,7 +99,8 @@ struct Loads {
     } else {
       seg[0] = (const bf16_t *)s0 + row0 * ld;
       seg[1] = (const bf16_t *)s1 + row0 * ld;
-      rows = nrows - row0;
+      const long long rows = nrows - row0;
+      span = (int)(rows < 0 ? 0 : rows > 8 * N ? 8 * N : rows) * ld * 2;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         const int r = 8 * n + (lane >> 3), c = (lane & 7) ^ swz(r);
@@ -110,20 +118,21 @@ struct Loads {
     const bf16_t *s = sg ? seg[1] : seg[0];
     const long long left = nk - k0;
     if constexpr (TRANS) {
-      // from the slab's first row to the end of the array: rows past the last k lie behind it
-      p.rs = rsrc(s + k0 * ld, (left * ld - rows) * 2);
+      // from the slab's first row to the end of its last: rows past the last k lie behind it
+      p.rs = rsrc(s + k0 * ld, (int)(left < SK ? left : SK) * ld * 2 - span);
     } else {
       // behind the last k of a row lies the next one
-      p.rs = rsrc(s + k0, (rows * ld - k0) * 2);
+      p.rs = rsrc(s + k0, span - (int)k0 * 2);
       p.past[0] = k[0] >= left;
       p.past[1] = k[1] >= left;
     }
     return p;
   }
+  template <bool TRACKED>
   __device__ __forceinline__ void issue(const Pre &p, bf16_t *tile, int n) const {
     uint32_t v = vo[n];
     if (!TRANS && p.past[n & 1]) v = kOutOfRange;
-    dma16(p.rs, tile + lds0 + n * 8 * SK, v);
+    dma16<TRACKED>(p.rs, tile + lds0 + n * 8 * SK, v);
   }
 };
 
@@ -184,6 +193,9 @@ __device__ __forceinline__ int xcd_tile(int n, int N) {
   const int xcd = n % kXcds, m = n / kXcds, q = N / kXcds, r = N % kXcds;
   return xcd * q + (xcd < r ? xcd : r) + m;
 }
+// Bands of four: the 32 tiles of an XCD at a time are 4 x 8. (32768 x 9728 x 2560: 1263 us; 1295 in bands of 8, 1355 of
+// 16, and 2 and 3 cost products of wide outputs 1 to 2 %.)
+constexpr int kBand = 4;
 // Tile t of nx by ny in bands of H along y, y fastest inside a band: neighbours share operands.
 __device__ __forceinline__ void band_tile(int t, int nx, int ny, int H, int &x, int &y) {
   const int full = ny / H, per = H * nx, band = t / per, h = band < full ? H : ny - full * H, r = t - band * per;
@@ -201,7 +213,7 @@ __global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int
   const int logical = xcd_tile(blockIdx.x, gridDim.x);
   const int split = logical / per_split, rest = logical % per_split, z = rest / (nti * ntj);
   int tx, ty;
-  band_tile(rest % (nti * ntj), nti, ntj, 8, tx, ty);
+  band_tile(rest % (nti * ntj), nti, ntj, kBand, tx, ty);
   const long long i0 = (long long)tx * WIDE, j0 = (long long)ty * S::TJ;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wi = w % S::WI, wj = w / S::WI;
 
@@ -241,9 +253,9 @@ __global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int
   };
   auto issue = [&](const Pre &p, int sl, int n) {  // load n of 2 N
     if (n < N)
-      la.issue(p.a, tile_a(sl), n);
+      la.template issue<!AT && !BT>(p.a, tile_a(sl), n);
     else
-      lb.issue(p.b, tile_b(sl), n - N);
+      lb.template issue<!AT && !BT>(p.b, tile_b(sl), n - N);
   };
   bf16x8 lo[HF], hi[HF], fb[2][FJ];
   const int ra = wi * 16 * FI, rb = wj * 16 * FJ;
@@ -317,8 +329,21 @@ __global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int
   const int ii = lane % LANES * 8;
   const long long i = i0 + wi * (PAIR ? HALF : 2 * HALF) + ii;
   const int left = clamp8(g.ni - i);
+  constexpr int ROUNDS = 32 / STEP;
+  const O *res = PAIR ? nullptr : reinterpret_cast<const O *>(g.res[z]);
 #pragma unroll
   for (int q = 0; q < FJ / 2; ++q) {
+    const long long jq = j0 + rb + 32 * q;
+    Raw8<O> old[PAIR ? 1 : ROUNDS];  // the residual, on its way while the sums go through LDS
+    if constexpr (!PAIR) {
+      if (res && parts.splits == 1) {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+          const long long j = jq + r * STEP + lane / LANES;
+          old[r] = load_some(res + j * g.ldo + i, j < g.nj ? left : 0);
+        }
+      }
+    }
 #pragma unroll
     for (int x = 0; x < FI; ++x)
 #pragma unroll
@@ -326,23 +351,23 @@ __global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int
         *reinterpret_cast<f32x4 *>(stg + (16 * y + (lane & 15)) * S::PITCH + 16 * x + 4 * (lane >> 4)) = acc[x][2 * q + y];
     // the wave's own LDS writes and reads run in order
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-#pragma unroll 2
-    for (int r = 0; r < 32; r += STEP) {
-      const int row = r + lane / LANES;
-      const long long j = j0 + rb + 32 * q + row;
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+      const int row = r * STEP + lane / LANES;
+      const long long j = jq + row;
       float v[8], u[8];
       __builtin_memcpy(v, __builtin_assume_aligned(stg + row * S::PITCH + ii, 16), 32);
       if constexpr (PAIR) __builtin_memcpy(u, __builtin_assume_aligned(stg + row * S::PITCH + HALF + ii, 16), 32);
       if (parts.splits > 1) {
-        float *p = parts.at + (((long long)split * per_split + (long long)z * nti * ntj + (long long)ty * nti + tx) * S::TJ + rb + 32 * q + row) * S::TI +
-                   wi * 2 * HALF + ii;
+        float *p = parts.at + (((long long)split * per_split + (long long)z * nti * ntj + (long long)ty * nti + tx) * S::TJ +
+                               rb + 32 * q + row) * S::TI + wi * 2 * HALF + ii;
         __builtin_memcpy(__builtin_assume_aligned(p, 16), v, 32);
         if constexpr (PAIR) __builtin_memcpy(__builtin_assume_aligned(p + HALF, 16), u, 32);
       } else if (j < g.nj && left > 0) {
         if constexpr (PAIR)
           finish_pair<bf16_t>(g, i, j, left, v, u);
         else
-          finish<bf16_t, O>(g, z, i, j, left, v);
+          finish<bf16_t, O>(g, z, i, j, left, v, &old[r]);
       }
       end_of_stores();
     }

@@ -28,22 +28,6 @@ typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
 constexpr int kThreads = 256, BK = 32;  // k per step
 
-// n of 8 elements, the rest zero
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_some(const T *p, int n) {
-  Raw8<T> r = {};
-  if (n >= 8) {
-    __builtin_memcpy(&r, p, sizeof r);
-  } else if (n > 0) {
-    T v[8] = {};
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) v[i] = p[i];
-    __builtin_memcpy(&r, v, sizeof r);
-  }
-  return r;
-}
-
 // One operand's tile: ROWS rows of 32 k, in LDS [row][k] where it lies by rows, [k][row] where it lies transposed.
 template <typename T, bool TRANS, int ROWS>
 struct Tile {

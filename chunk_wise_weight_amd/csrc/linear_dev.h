@@ -57,9 +57,26 @@ __device__ __forceinline__ void put(bf16_t *p, int n, const float (&v)[W]) {
     if (i < n) p[i] = f32_to_bf16(v[i]);
 }
 
-// n of the W elements from (i, j) on are there.
+// n of 8 elements, the rest zero
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_some(const T *p, int n) {
+  Raw8<T> r = {};
+  if (n >= 8) {
+    __builtin_memcpy(&r, p, sizeof r);
+  } else if (n > 0) {
+    T v[8] = {};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) v[i] = p[i];
+    __builtin_memcpy(&r, v, sizeof r);
+  }
+  return r;
+}
+
+// n of the W elements from (i, j) on are there. old: the residual's eight, loaded before.
 template <typename T, typename O, int W>
-__device__ __forceinline__ void finish(const GemmArgs &g, int z, long long i, long long j, int n, float (&v)[W]) {
+__device__ __forceinline__ void finish(const GemmArgs &g, int z, long long i, long long j, int n, float (&v)[W],
+                                       const Raw8<O> *old = nullptr) {
   const long long at = j * g.ldo + i;
   float w[W];
   if (g.bias[0]) {
@@ -71,7 +88,14 @@ __device__ __forceinline__ void finish(const GemmArgs &g, int z, long long i, lo
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] = g.scale * act_of(v[e], g.act);
   if (g.res[z]) {
-    get(reinterpret_cast<const O *>(g.res[z]) + at, n, w);
+    if constexpr (W == 8) {
+      if (old)
+        expand(*old, w);
+      else
+        get(reinterpret_cast<const O *>(g.res[z]) + at, n, w);
+    } else {
+      get(reinterpret_cast<const O *>(g.res[z]) + at, n, w);
+    }
 #pragma unroll
     for (int e = 0; e < W; ++e) v[e] += w[e];
   }
