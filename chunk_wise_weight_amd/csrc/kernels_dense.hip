@@ -365,9 +365,9 @@ __global__ __launch_bounds__(S::THREADS, S::PER_CU) void k_dense(GemmArgs g, int
         if constexpr (PAIR) __builtin_memcpy(__builtin_assume_aligned(p + HALF, 16), u, 32);
       } else if (j < g.nj && left > 0) {
         if constexpr (PAIR)
-          finish_pair<bf16_t>(g, i, j, left, v, u);
+          finish_pair<bf16_t, true>(g, i, j, left, v, u);
         else
-          finish<bf16_t, O>(g, z, i, j, left, v, &old[r]);
+          finish<bf16_t, O, true>(g, z, i, j, left, v, &old[r]);
       }
       end_of_stores();
     }

@@ -57,6 +57,34 @@ __device__ __forceinline__ void put(bf16_t *p, int n, const float (&v)[W]) {
     if (i < n) p[i] = f32_to_bf16(v[i]);
 }
 
+// The same, past the caches' keeping where eight are there: the tiles of a large
+// product are written while others still read their operands (the pair of 32768
+// x 2560 x 9728 with g and u kept: 2859 -> 2627 us).
+template <typename T, int W>
+__device__ __forceinline__ void put_past(T *p, int n, const float (&v)[W]) {
+  if constexpr (W == 8) {
+    if (n >= 8) {
+      if constexpr (sizeof(T) == 2) {
+        stream_w(p, true, v);
+      } else {
+        typedef f32x4 any __attribute__((aligned(4)));
+        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<any *>(p));
+        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<any *>(p + 4));
+      }
+      end_of_stores();
+      return;
+    }
+  }
+  put(p, n, v);
+}
+template <bool NT, typename T, int W>
+__device__ __forceinline__ void put_out(T *p, int n, const float (&v)[W]) {
+  if constexpr (NT)
+    put_past(p, n, v);
+  else
+    put(p, n, v);
+}
+
 // n of 8 elements, the rest zero
 template <typename T>
 __device__ __forceinline__ Raw8<T> load_some(const T *p, int n) {
@@ -74,7 +102,7 @@ __device__ __forceinline__ Raw8<T> load_some(const T *p, int n) {
 }
 
 // n of the W elements from (i, j) on are there. old: the residual's eight, loaded before.
-template <typename T, typename O, int W>
+template <typename T, typename O, bool NT = false, int W>
 __device__ __forceinline__ void finish(const GemmArgs &g, int z, long long i, long long j, int n, float (&v)[W],
                                        const Raw8<O> *old = nullptr) {
   const long long at = j * g.ldo + i;
@@ -84,7 +112,7 @@ __device__ __forceinline__ void finish(const GemmArgs &g, int z, long long i, lo
 #pragma unroll
     for (int e = 0; e < W; ++e) v[e] += w[e];
   }
-  if (g.pre[0]) put(reinterpret_cast<T *>(g.pre[0]) + at, n, v);
+  if (g.pre[0]) put_out<NT>(reinterpret_cast<T *>(g.pre[0]) + at, n, v);
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] = g.scale * act_of(v[e], g.act);
   if (g.res[z]) {
@@ -99,10 +127,10 @@ __device__ __forceinline__ void finish(const GemmArgs &g, int z, long long i, lo
 #pragma unroll
     for (int e = 0; e < W; ++e) v[e] += w[e];
   }
-  put(reinterpret_cast<O *>(g.out[z]) + at, n, v);
+  put_out<NT>(reinterpret_cast<O *>(g.out[z]) + at, n, v);
 }
 // the gated pair: a the gate's products, u the other's
-template <typename T, int W>
+template <typename T, bool NT = false, int W>
 __device__ __forceinline__ void finish_pair(const GemmArgs &g, long long i, long long j, int n, float (&a)[W],
                                             float (&u)[W]) {
   const long long at = j * g.ldo + i;
@@ -116,10 +144,10 @@ __device__ __forceinline__ void finish_pair(const GemmArgs &g, long long i, long
     for (int e = 0; e < W; ++e) u[e] += w[e];
   }
   if (g.pre[0]) {
-    put(reinterpret_cast<T *>(g.pre[0]) + at, n, a);
-    put(reinterpret_cast<T *>(g.pre[1]) + at, n, u);
+    put_out<NT>(reinterpret_cast<T *>(g.pre[0]) + at, n, a);
+    put_out<NT>(reinterpret_cast<T *>(g.pre[1]) + at, n, u);
   }
 #pragma unroll
   for (int e = 0; e < W; ++e) w[e] = act_of(a[e], g.act) * u[e];
-  put(reinterpret_cast<T *>(g.out[0]) + at, n, w);
+  put_out<NT>(reinterpret_cast<T *>(g.out[0]) + at, n, w);
 }
