@@ -199,7 +199,11 @@ int check_array(const char *where, const char *name, int i, const void *p, size_
   if (!bytes) return TTT_OK;
   if (!p) return ttt_fail(TTT_E_NULL, "%s: %s of tensor %d is NULL", where, name, i);
   if ((uintptr_t)p % elem) return ttt_fail(TTT_E_ARG, "%s: %s of tensor %d is not aligned to its elements", where, name, i);
-  e.push_back({(uintptr_t)p, (uintptr_t)p + bytes, out});
+  // views of one buffer in their order are one extent
+  if (!e.empty() && e.back().hi == (uintptr_t)p && e.back().out == out)
+    e.back().hi += bytes;
+  else
+    e.push_back({(uintptr_t)p, (uintptr_t)p + bytes, out});
   return TTT_OK;
 }
 
@@ -465,17 +469,23 @@ int ttt_adamw(void *const *w, const int32_t *w_dt, const void *const *g, const i
     if (norm && !(tau > 0)) return ttt_fail(TTT_E_ARG, "%s: tau must be greater than 0", kWhere);
     std::vector<Extent> ex;
     const size_t state = bits8 ? 1 : 4;
-    for (int i = 0; i < n && !rc; ++i) {
+    for (int i = 0; i < n; ++i)
       if (!known((ttt_dtype)w_dt[i]) || !known((ttt_dtype)g_dt[i]))
         return ttt_fail(TTT_E_DTYPE, "%s: tensor %d has an unknown dtype", kWhere, i);
-      const size_t ws = size_of((ttt_dtype)w_dt[i]), gs = size_of((ttt_dtype)g_dt[i]), k = (size_t)numel[i];
-      rc = check_array(kWhere, "w", i, w[i], k * ws, ws, true, ex);
-      if (!rc) rc = check_array(kWhere, "g", i, g[i], k * gs, gs, false, ex);
-      if (!rc) rc = check_array(kWhere, "m", i, m[i], k * state, state, true, ex);
-      if (!rc) rc = check_array(kWhere, "v", i, v[i], k * state, state, true, ex);
-      if (!rc && bits8) rc = check_array(kWhere, "tops", i, tops[i], block_count(numel[i]) * 4, 2, true, ex);
-      if (!rc && copies && copies[i]) rc = check_array(kWhere, "the copy", i, copies[i], k * 2, 2, true, ex);
-    }
+    auto list = [&](const char *name, const void *const *p, const int32_t *dt, size_t elem, bool out) {
+      for (int i = 0; i < n && !rc; ++i) {
+        const size_t size = dt ? size_of((ttt_dtype)dt[i]) : elem;
+        rc = check_array(kWhere, name, i, p[i], (size_t)numel[i] * size, size, out, ex);
+      }
+    };
+    list("w", w, w_dt, 0, true);
+    list("g", g, g_dt, 0, false);
+    list("m", m, nullptr, state, true);
+    list("v", v, nullptr, state, true);
+    for (int i = 0; i < n && !rc && bits8; ++i)
+      rc = check_array(kWhere, "tops", i, tops[i], block_count(numel[i]) * 4, 2, true, ex);
+    for (int i = 0; i < n && !rc && copies; ++i)
+      if (copies[i]) rc = check_array(kWhere, "the copy", i, copies[i], (size_t)numel[i] * 2, 2, true, ex);
     if (!rc) rc = check_scalar(kWhere, "step_dev", step_dev, 8, ex);
     if (!rc) rc = check_scalar(kWhere, "lr_dev", lr_dev, 4, ex);
     if (!rc) rc = check_scalar(kWhere, "norm", norm, 4, ex);
