@@ -22,6 +22,8 @@
 // would decide a code, and the same step computed elsewhere (a replica, a
 // resumed run on other software) would drift apart. The pass is bound by
 // memory either way.
+#include <type_traits>
+
 #include "adamw.h"
 #include "vec8.h"
 
@@ -128,56 +130,138 @@ __device__ __forceinline__ uint32_t get_codes(const uint8_t *p, int n) {
     if (i < n) u |= (uint32_t)p[i] << (8 * i);
   return u;
 }
+// Eight elements likewise.
+struct Eight {
+  uint32_t u[8];
+};
 template <bool NT>
-__device__ __forceinline__ void put_codes(uint8_t *p, int n, uint32_t u) {
-  if (n >= 4) {
-    keep<NT, u32_el>(p, u);
+__device__ __forceinline__ Eight get8(const void *p, int f32, long long at, int n) {
+  Eight r = {};
+  if (n >= 8) {
+    if (f32) {
+      const float *q = reinterpret_cast<const float *>(p) + at;
+      const u32x4_el a = fetch<NT, u32x4_el>(q), b = fetch<NT, u32x4_el>(q + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r.u[i] = a[i];
+        r.u[4 + i] = b[i];
+      }
+    } else {
+      const u32x4_any v = fetch<NT, u32x4_any>(reinterpret_cast<const bf16_t *>(p) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.u[i] = v[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      if (i >= n) continue;
+      if (f32)
+        r.u[i] = reinterpret_cast<const uint32_t *>(p)[at + i];
+      else
+        r.u[i / 2] |= (uint32_t)reinterpret_cast<const bf16_t *>(p)[at + i] << (16 * (i & 1));
+    }
+  }
+  return r;
+}
+__device__ __forceinline__ void expand(const Eight &r, int f32, float (&v)[8]) {
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.u[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(r.u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.u[i] & 0xffff0000u);
+    }
+  }
+}
+template <bool NT>
+__device__ __forceinline__ void put8(void *p, int f32, long long at, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    if (f32) {
+      float *q = reinterpret_cast<float *>(p) + at;
+      keep<NT>(q, u32x4_el{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+      keep<NT>(q + 4, u32x4_el{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
+    } else {
+      keep<NT>(reinterpret_cast<bf16_t *>(p) + at, u32x4_any{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])});
+    }
+    end_of_stores();
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      if (i >= n) continue;
+      if (f32)
+        reinterpret_cast<float *>(p)[at + i] = v[i];
+      else
+        reinterpret_cast<bf16_t *>(p)[at + i] = f32_to_bf16(v[i]);
+    }
+  }
+}
+typedef uint32_t u32x2_code __attribute__((ext_vector_type(2), aligned(1)));
+struct Codes8 {
+  uint32_t u[2];
+};
+template <bool NT>
+__device__ __forceinline__ Codes8 get_codes8(const uint8_t *p, int n) {
+  if (n >= 8) {
+    const u32x2_code v = fetch<NT, u32x2_code>(p);
+    return {{v[0], v[1]}};
+  }
+  Codes8 r = {};
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < n) r.u[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
+  return r;
+}
+template <bool NT>
+__device__ __forceinline__ void put_codes8(uint8_t *p, int n, const Codes8 &c) {
+  if (n >= 8) {
+    keep<NT>(p, u32x2_code{c.u[0], c.u[1]});
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (i < n) p[i] = (uint8_t)(u >> (8 * i));
+  for (int i = 0; i < 7; ++i)
+    if (i < n) p[i] = (uint8_t)(c.u[i / 4] >> (8 * (i & 3)));
 }
 
-// The value of the low byte of c under a block's top, lowest = top - most.
-template <int MOST>
-__device__ __forceinline__ float decode(uint32_t c, int lowest) {
-  const int code = (int)(c & MOST), k = max(lowest + code, 0);
-  const uint32_t u = code ? (uint32_t)k << 20 : 0u;
-  return __uint_as_float(MOST == 127 ? u | (c & 128u) << 24 : u);
+// The value of byte e of c under a block's top, lowest = top - most. HIGH: every code but 0 stands for a pattern above 0.
+template <int MOST, bool HIGH>
+__device__ __forceinline__ float decode(uint32_t c, int e, int lowest) {
+  const uint32_t code = c >> (8 * e) & MOST;
+  const int k = lowest + (int)code;
+  const uint32_t u = code ? (uint32_t)(HIGH ? k : max(k, 0)) << 20 : 0u;
+  return __uint_as_float(MOST == 127 ? u | (c << (24 - 8 * e) & 0x80000000u) : u);
 }
 
 constexpr uint32_t kQuietNan = 0x7FC00000u;  // every NaN's pattern here, so that tops stay below 2^11
 
-__device__ __forceinline__ uint32_t magnitude(float x) { return min(__float_as_uint(x) & 0x7fffffffu, kQuietNan); }
-
-// The code of x of magnitude mag under a block's lowest = top - most, with 16 random bits r.
-template <int MOST>
+// The code of x, of magnitude mag, under a block's lowest = top - most, with 16 random bits r. HIGH: as above, and no
+// NaN among the block's.
+template <int MOST, bool HIGH>
 __device__ __forceinline__ uint32_t encode(float x, uint32_t mag, int lowest, uint32_t r) {
+  if (!HIGH) mag = min(mag, kQuietNan);
   int c = (int)((mag + (r << 4)) >> 20) - lowest;
-  if (MOST == 127) {
-    if (__any(c < 1)) {  // below the block's smallest value, which few are
-      const float least = __uint_as_float(lowest > -1 ? (uint32_t)(lowest + 1) << 20 : 0u);
-      const int low = __uint_as_float(mag) >= ((float)r + 0.5f) * 0x1p-16f * least;
-      c = c < 1 ? low : c;
-    }
-  } else {
-    c = max(c, 1);
+  if (MOST == 255) return (uint32_t)(HIGH ? max(c, (int)min(mag, 1u)) : mag ? max(c, 1) : 0);
+  uint32_t sign = __float_as_uint(x) >> 24 & 128u;
+  if (!HIGH || __any(c < 1)) {  // below the block's smallest value, which few are
+    const float least = __uint_as_float(lowest > -1 ? (uint32_t)(lowest + 1) << 20 : 0u);
+    const int low = __uint_as_float(mag) >= ((float)r + 0.5f) * 0x1p-16f * least;
+    c = mag == 0 ? 0 : c < 1 ? low : c;
+    sign = c ? sign : 0;
   }
-  c = mag ? c : 0;
-  return MOST == 127 && c ? (uint32_t)c | (__float_as_uint(x) >> 24 & 128u) : (uint32_t)c;
+  return (uint32_t)c | sign;
 }
 
-// The largest of a wave's values, in every lane: by rotations within the rows of 16 lanes, then between rows.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+// The largest of the values of a wave's lower or upper 32 lanes, in each of them: by rotations within the rows of 16
+// lanes, then between two rows.
+__device__ __forceinline__ uint32_t half_max(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, true));  // row_ror:8
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, true));
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, true));
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, true));
   const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = max((uint32_t)a[0], (uint32_t)a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return max((uint32_t)b[0], (uint32_t)b[1]);
+  return max((uint32_t)a[0], (uint32_t)a[1]);
 }
 
 __device__ __forceinline__ AdamStep step_of(const AdamArgs &a) {
@@ -224,107 +308,167 @@ __device__ __forceinline__ bool place_of(const AdamTable &t, Place &p) {
   return true;
 }
 
-// FULL: every element of the chunk is there.
-template <bool BITS8, bool NT, bool FULL>
+// The betas and the gradients' factor.
+struct Rates {
+  double b1, b2, factor;
+  bool clipped;
+};
+__device__ __forceinline__ Rates rates_of(const AdamArgs &a) {
+  Rates r{a.beta1, a.beta2, 1.0, false};
+  if (a.norm) {
+    const double n = (double)*a.norm;
+    r.clipped = n > a.tau && n <= 3.4028234663852886e38;  // a norm that is not finite clips nothing
+    if (r.clipped) r.factor = a.tau / n;
+  }
+  return r;
+}
+__device__ __forceinline__ float moved(float w, float m, float v, const AdamStep &s, float eps, bool small) {
+  const float q = s.lr1 * m * __builtin_amdgcn_rcpf(fmaf(root(v, small), s.root2, eps));
+  return fmaf(-s.shrink, w, w) - q;
+}
+
+// fp32 moments: a wave takes four blocks of a chunk, a lane four elements of each. Everything is loaded before anything
+// is stored. FULL: every element of the chunk is there.
+template <bool NT, bool FULL>
 __device__ __forceinline__ void step_chunk(const AdamTable &t, const AdamArgs &a, const Place &p) {
   const int i = p.i, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int w_f32 = t.w_f32[i], g_f32 = t.g_f32[i];
   const long long at0 = p.at + wave * kAdamBlock + lane * 4;
-  const int left0 = FULL ? kAdamChunk : p.n - wave * kAdamBlock - lane * 4;
+  const int left0 = p.n - wave * kAdamBlock - lane * 4;
   constexpr int SKIP = kThreads / 64 * kAdamBlock;  // from a wave's block to its next
-  // everything is loaded before anything is stored
   Four w[kWaveSteps], g[kWaveSteps], m[kWaveSteps], v[kWaveSteps];
-  int top[kWaveSteps][2];
-  long long blocks = 0;
-  if (BITS8) blocks = (long long)(t.first[i + 1] - t.first[i] - 1) * (kAdamChunk / kAdamBlock) +
-                      (t.tail[i] + kAdamBlock - 1) / kAdamBlock;
 #pragma unroll
   for (int k = 0; k < kWaveSteps; ++k) {
     const long long at = at0 + k * SKIP;
     const int left = FULL ? 4 : left0 - k * SKIP;
     w[k] = get<NT>(t.w[i], w_f32, at, left);
     g[k] = get<NT>(t.g[i], g_f32, at, left);
-    if constexpr (BITS8) {
-      m[k].u[0] = get_codes<NT>((const uint8_t *)t.m[i] + at, left);
-      v[k].u[0] = get_codes<NT>((const uint8_t *)t.v[i] + at, left);
-      const long long block = (p.at + wave * kAdamBlock + k * SKIP) / kAdamBlock;
-      const bool there = FULL || wave * kAdamBlock + k * SKIP < p.n;
-      top[k][0] = there ? t.top[i][block] : 0;
-      top[k][1] = there ? t.top[i][blocks + block] : 0;
-    } else {
-      m[k] = get<NT>(t.m[i], 1, at, left);
-      v[k] = get<NT>(t.v[i], 1, at, left);
-    }
+    m[k] = get<NT>(t.m[i], 1, at, left);
+    v[k] = get<NT>(t.v[i], 1, at, left);
   }
   const AdamStep s = step_of(a);
-  const double b1 = a.beta1, b2 = a.beta2;
-  double factor = 1.0;  // of the gradients
-  bool clipped = false;
-  if (a.norm) {
-    const double n = (double)*a.norm;
-    clipped = n > a.tau && n <= 3.4028234663852886e38;  // a norm that is not finite clips nothing
-    if (clipped) factor = a.tau / n;
-  }
-  // fp64 holds the factor's square with the betas; fp32 takes it to the gradient first
-  const double o1 = (1.0 - b1) * factor, o2 = (1.0 - b2) * factor * factor;
-  const float b1f = (float)b1, b2f = (float)b2, o1f = (float)(1.0 - b1), o2f = (float)(1.0 - b2);
+  const Rates r = rates_of(a);
+  const float b1 = (float)r.b1, b2 = (float)r.b2, o1 = (float)(1.0 - r.b1), o2 = (float)(1.0 - r.b2);
   const bool small = a.eps < 1e-10f;
-  const uint32_t key = BITS8 ? adam_mix(s.key + kGolden * (uint32_t)(t.tensor0 + i + 1)) : 0u;
 #pragma unroll
   for (int k = 0; k < kWaveSteps; ++k) {
-    if (!FULL && wave * kAdamBlock + k * SKIP >= p.n) break;  // the wave's block is there, or none of it
     const long long at = at0 + k * SKIP;
     const int left = FULL ? 4 : left0 - k * SKIP;
     float x[4], mk[4], vk[4], wk[4];
     expand(g[k], g_f32, x);
     expand(w[k], w_f32, wk);
-    if constexpr (BITS8) {
-      uint32_t mm = 0, mv = 0, am[4], av[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const double d = (double)x[e];
-        mk[e] = (float)(b1 * (double)decode<127>(m[k].u[0] >> (8 * e), top[k][0] - 127) + o1 * d);
-        vk[e] = (float)(b2 * (double)decode<255>(v[k].u[0] >> (8 * e), top[k][1] - 255) + o2 * d * d);
-        am[e] = magnitude(mk[e]);
-        av[e] = magnitude(vk[e]);
-        mm = max(mm, am[e]);
-        mv = max(mv, av[e]);
-      }
-      const int um = (int)((wave_max(mm) + 0xFFFFFu) >> 20), uv = (int)((wave_max(mv) + 0xFFFFFu) >> 20);
-      const long long block = (p.at + wave * kAdamBlock + k * SKIP) / kAdamBlock;
-      if (lane == 0) {
-        t.top[i][block] = (int16_t)um;
-        t.top[i][blocks + block] = (int16_t)uv;
-      }
-      uint32_t nm = 0, nv = 0;
-      const uint32_t place = key + (uint32_t)at * kGolden;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t r = adam_mix(place + e * kGolden);
-        nm |= encode<127>(mk[e], am[e], um - 127, r & 0xFFFFu) << (8 * e);
-        nv |= encode<255>(vk[e], av[e], uv - 255, r >> 16) << (8 * e);
-      }
-      put_codes<NT>((uint8_t *)t.m[i] + at, left, nm);
-      put_codes<NT>((uint8_t *)t.v[i] + at, left, nv);
-    } else {
-      expand(m[k], 1, mk);
-      expand(v[k], 1, vk);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float d = clipped ? (float)((double)x[e] * factor) : x[e];
-        mk[e] = fmaf(b1f, mk[e], o1f * d);
-        vk[e] = fmaf(b2f, vk[e], o2f * d * d);
-      }
-      put<NT>(t.m[i], 1, at, left, mk);
-      put<NT>(t.v[i], 1, at, left, vk);
-    }
+    expand(m[k], 1, mk);
+    expand(v[k], 1, vk);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float q = s.lr1 * mk[e] * __builtin_amdgcn_rcpf(fmaf(root(vk[e], small), s.root2, a.eps));
-      wk[e] = fmaf(-s.shrink, wk[e], wk[e]) - q;
+      // the factor to the gradient first: its square may leave fp32
+      const float d = r.clipped ? (float)((double)x[e] * r.factor) : x[e];
+      mk[e] = fmaf(b1, mk[e], o1 * d);
+      vk[e] = fmaf(b2, vk[e], o2 * d * d);
+      wk[e] = moved(wk[e], mk[e], vk[e], s, a.eps, small);
     }
+    put<NT>(t.m[i], 1, at, left, mk);
+    put<NT>(t.v[i], 1, at, left, vk);
     put<NT>(t.w[i], w_f32, at, left, wk);
     if (t.copy[i]) put<NT>(t.copy[i], 0, at, left, wk);
+  }
+  end_of_stores();
+}
+
+// 8-bit moments: half a wave takes a block, a lane eight elements of it, two blocks one after the other.
+constexpr int kHalfSteps = kAdamChunk / kAdamBlock / (kThreads / 32);
+
+template <bool NT, bool FULL>
+__device__ __forceinline__ void step_chunk8(const AdamTable &t, const AdamArgs &a, const Place &p) {
+  const int i = p.i, lane = threadIdx.x & 31, half = threadIdx.x >> 5;
+  const int w_f32 = t.w_f32[i], g_f32 = t.g_f32[i];
+  constexpr int SKIP = kThreads / 32 * kAdamBlock;  // from a half's block to its next
+  const long long at0 = p.at + half * kAdamBlock + lane * 8;
+  const int left0 = p.n - half * kAdamBlock - lane * 8;
+  const long long block0 = p.at / kAdamBlock + half;
+  const long long blocks = (long long)(t.first[i + 1] - t.first[i] - 1) * (kAdamChunk / kAdamBlock) +
+                           (t.tail[i] + kAdamBlock - 1) / kAdamBlock;
+  Eight w[kHalfSteps], g[kHalfSteps];
+  Codes8 m[kHalfSteps], v[kHalfSteps];
+  int tm[kHalfSteps], tv[kHalfSteps];
+#pragma unroll
+  for (int k = 0; k < kHalfSteps; ++k) {
+    const long long at = at0 + k * SKIP;
+    const int left = FULL ? 8 : left0 - k * SKIP;
+    w[k] = get8<NT>(t.w[i], w_f32, at, left);
+    g[k] = get8<NT>(t.g[i], g_f32, at, left);
+    m[k] = get_codes8<NT>((const uint8_t *)t.m[i] + at, left);
+    v[k] = get_codes8<NT>((const uint8_t *)t.v[i] + at, left);
+    const bool there = FULL || left + lane * 8 > 0;  // the block is there
+    const long long block = block0 + k * (kThreads / 32);
+    tm[k] = there ? t.top[i][block] : 0;
+    tv[k] = there ? t.top[i][blocks + block] : 0;
+  }
+  const AdamStep s = step_of(a);
+  const Rates r = rates_of(a);
+  // fp64 holds the factor's square with the betas
+  const double b1 = r.b1, b2 = r.b2, o1 = (1.0 - b1) * r.factor, o2 = (1.0 - b2) * r.factor * r.factor;
+  const bool small = a.eps < 1e-10f;
+  const uint32_t key = adam_mix(s.key + kGolden * (uint32_t)(t.tensor0 + i + 1));
+#pragma unroll
+  for (int k = 0; k < kHalfSteps; ++k) {
+    const long long at = at0 + k * SKIP;
+    const int left = FULL ? 8 : left0 - k * SKIP;
+    const bool there = FULL || left + lane * 8 > 0;
+    float x[8], mk[8], vk[8], wk[8];
+    expand(g[k], g_f32, x);
+    // both blocks' tops far above the smallest fp32 number, as they are but for moments below 10^-28 or of 0
+    const bool high = !__any(tm[k] < 128 || tv[k] < 256);
+    auto recur = [&](auto hi) {
+      constexpr bool HIGH = decltype(hi)::value;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const double d = (double)x[e];
+        mk[e] = (float)(b1 * (double)decode<127, HIGH>(m[k].u[e / 4], e % 4, tm[k] - 127) + o1 * d);
+        vk[e] = (float)(b2 * (double)decode<255, HIGH>(v[k].u[e / 4], e % 4, tv[k] - 255) + o2 * d * d);
+      }
+    };
+    if (high)
+      recur(std::true_type{});
+    else
+      recur(std::false_type{});
+    uint32_t mm = 0, mv = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      mm = max(mm, __float_as_uint(mk[e]) & 0x7fffffffu);
+      mv = max(mv, __float_as_uint(vk[e]) & 0x7fffffffu);
+    }
+    mm = half_max(mm);
+    mv = half_max(mv);
+    const int um = (int)((min(mm, kQuietNan) + 0xFFFFFu) >> 20), uv = (int)((min(mv, kQuietNan) + 0xFFFFFu) >> 20);
+    if (lane == 0 && there) {
+      const long long block = block0 + k * (kThreads / 32);
+      t.top[i][block] = (int16_t)um;
+      t.top[i][blocks + block] = (int16_t)uv;
+    }
+    Codes8 nm, nv;
+    const uint32_t place = key + (uint32_t)at * kGolden;
+    auto codes = [&](auto hi) {
+      constexpr bool HIGH = decltype(hi)::value;
+      nm = nv = Codes8{};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t rnd = adam_mix(place + e * kGolden);
+        nm.u[e / 4] |= encode<127, HIGH>(mk[e], __float_as_uint(mk[e]) & 0x7fffffffu, um - 127, rnd & 0xFFFFu) << (8 * (e % 4));
+        nv.u[e / 4] |= encode<255, HIGH>(vk[e], __float_as_uint(vk[e]) & 0x7fffffffu, uv - 255, rnd >> 16) << (8 * (e % 4));
+      }
+    };
+    if (!__any(um < 128 || uv < 256 || mm > 0x7f800000u || mv > 0x7f800000u))
+      codes(std::true_type{});
+    else
+      codes(std::false_type{});
+    put_codes8<NT>((uint8_t *)t.m[i] + at, left, nm);
+    put_codes8<NT>((uint8_t *)t.v[i] + at, left, nv);
+    expand(w[k], w_f32, wk);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wk[e] = moved(wk[e], mk[e], vk[e], s, a.eps, small);
+    put8<NT>(t.w[i], w_f32, at, left, wk);
+    if (t.copy[i]) put8<NT>(t.copy[i], 0, at, left, wk);
   }
   end_of_stores();
 }
@@ -333,10 +477,17 @@ template <bool BITS8, bool NT>
 __global__ __launch_bounds__(kThreads) void k_adamw(AdamTable t, AdamArgs a) {
   Place p;
   if (!place_of(t, p)) return;
-  if (p.n == kAdamChunk)
-    step_chunk<BITS8, NT, true>(t, a, p);
-  else
-    step_chunk<BITS8, NT, false>(t, a, p);
+  if (p.n == kAdamChunk) {
+    if constexpr (BITS8)
+      step_chunk8<NT, true>(t, a, p);
+    else
+      step_chunk<NT, true>(t, a, p);
+  } else {
+    if constexpr (BITS8)
+      step_chunk8<NT, false>(t, a, p);
+    else
+      step_chunk<NT, false>(t, a, p);
+  }
 }
 
 template <bool SECOND, bool NT>
@@ -359,8 +510,7 @@ __global__ __launch_bounds__(kThreads) void k_values(AdamTable t) {
     const int off = (k * (kThreads / 64) + wave) * kAdamBlock;
     float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = SECOND ? decode<255>(c[k] >> (8 * e), top[k] - 255)
-                                              : decode<127>(c[k] >> (8 * e), top[k] - 127);
+    for (int e = 0; e < 4; ++e) v[e] = SECOND ? decode<255, false>(c[k], e, top[k] - 255) : decode<127, false>(c[k], e, top[k] - 127);
     put<NT>(t.w[i], 1, p.at + off + lane * 4, p.n - off - lane * 4, v);
   }
   end_of_stores();

@@ -99,14 +99,25 @@ __device__ __forceinline__ Fragment32 fragment(const float *lds, int r0, int lan
   }
   return v;
 }
-__device__ __forceinline__ void mma(f32x4 &acc, const bf16x8 &a, const bf16x8 &b) {
-  acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+// A step's products. The fp32 ones that add to one sum are F apart: one directly behind the other would wait for it.
+template <int F>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[F][F], const bf16x8 (&a)[F], const bf16x8 (&b)[F]) {
+#pragma unroll
+  for (int x = 0; x < F; ++x)
+#pragma unroll
+    for (int y = 0; y < F; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[x], b[y], acc[x][y], 0, 0, 0);
 }
-__device__ __forceinline__ void mma(f32x4 &acc, const Fragment32 &a, const Fragment32 &b) {
+template <int F>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[F][F], const Fragment32 (&a)[F], const Fragment32 (&b)[F]) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int x = 0; x < F; ++x)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.h[h][s], b.h[h][s], acc, 0, 0, 0);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int y = 0; y < F; ++y)
+          acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[x].h[h][s], b[y].h[h][s], acc[x][y], 0, 0, 0);
 }
 
 // grid: i tiles (TILE rows of A; with a pair half as many of each matrix), times j tiles, times batch, times splits of k
@@ -161,10 +172,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm(GemmArgs g, long long ti, 
     for (int x = 0; x < F; ++x) fa[x] = fragment<AT, TA::PITCH>(la, (wi * F + x) * 16, lane);
 #pragma unroll
     for (int x = 0; x < F; ++x) fb[x] = fragment<BT, TB::PITCH>(lb, (wj * F + x) * 16, lane);
-#pragma unroll
-    for (int x = 0; x < F; ++x)
-#pragma unroll
-      for (int y = 0; y < F; ++y) mma(acc[x][y], fa[x], fb[y]);
+    multiply(acc, fa, fb);
   };
   if (first < end) fetch(first, ta[0], tb[0]);
   if (first + 1 < end) fetch(first + 1, ta[1], tb[1]);
