@@ -375,7 +375,9 @@ __device__ __forceinline__ void step_chunk(const AdamTable &t, const AdamArgs &a
   end_of_stores();
 }
 
-// 8-bit moments: half a wave takes a block, a lane eight elements of it, two blocks one after the other.
+// 8-bit moments: half a wave takes a block, a lane eight elements of it, two blocks one after the other. (277M bf16
+// weights: 680 us; 729 with four elements per lane, 750 with a block each for 512 threads. 66 vector instructions per
+// element are 480 us of it, the bytes at the rate of the fp32 form 490.)
 constexpr int kHalfSteps = kAdamChunk / kAdamBlock / (kThreads / 32);
 
 template <bool NT, bool FULL>
