@@ -37,6 +37,8 @@ struct AdamArgs {
   uint32_t seed;
 };
 
+static_assert(sizeof(AdamTable) + sizeof(AdamArgs) <= 4096, "every launch may pass 4 KiB of arguments");
+
 // The random bits' mixing: two rounds of a shift and a multiplication by an odd
 // constant, which reach every bit of the result.
 __host__ __device__ inline uint32_t adam_mix(uint32_t h) {

@@ -321,6 +321,39 @@ def test_many_tensors_and_none():
     assert ttt.ttt_adamw_values([], [], 1) == []
 
 
+def test_elements_past_32_bits():
+    """A tensor of 2^31 + 5000 elements: its last chunk and those around the border are what their formula gives."""
+    n = (1 << 31) + 5000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w, grad = torch.empty(n, dtype=BF16, device="cuda"), torch.empty(n, dtype=BF16, device="cuda")
+    for t in (w, grad):
+        t[:5000] = torch.randn(5000, generator=g, device="cuda")
+        t[5000:(1 << 31) - 5000] = 0.5
+        t[(1 << 31) - 5000:] = torch.randn(10000, generator=g, device="cuda")
+    m, v = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
+    tops = torch.zeros((2, -(-n // 256)), dtype=torch.int16, device="cuda")
+    at = [slice(0, 4096), slice((1 << 31) - 4096, 1 << 31), slice(1 << 31, n)]
+    old = [w[a].clone() for a in at]
+    ttt.ttt_adamw([w], [grad], [m], [v], 2, 1e-2, tops=[tops], seed=5, **HYPER)
+    for a, ow in zip(at, old):
+        gd = grad[a].double().cpu().numpy()
+        m1, v1 = ((1 - 0.9) * gd).astype(np.float32), ((1 - 0.999) * gd * gd).astype(np.float32)
+        key = mix((5 + GOLDEN * mix(2)) & 0xFFFFFFFF)
+        key = mix((key + GOLDEN) & 0xFFFFFFFF)
+        e = np.arange(a.start, a.stop, dtype=np.uint64) & np.uint64(0xFFFFFFFF)
+        r = mix((np.uint64(key) + e * np.uint64(GOLDEN)) & np.uint64(0xFFFFFFFF)).astype(np.int64)
+        cm, tm = encode(m1, r & 0xFFFF, 127)
+        cv, tv = encode(v1, r >> 16, 255)
+        blocks = slice(a.start // 256, -(-a.stop // 256))
+        assert np.array_equal(tops[0, blocks].cpu().numpy(), tm) and np.array_equal(tops[1, blocks].cpu().numpy(), tv)
+        assert np.array_equal(m[a].cpu().numpy(), cm) and np.array_equal(v[a].cpu().numpy(), cv)
+        want = step64(ow, grad[a], torch.zeros_like(ow), torch.zeros_like(ow), 2, 1e-2, **HYPER)
+        err = 2 * U32 * want[0].abs() + U32 * ow.double().abs() + want[3].abs() * 18 * U32
+        assert_close(w[a], want[0].cpu(), (err + half_step(BF16) * (want[0].abs() + err)).cpu(), "w")
+    vals = ttt.ttt_adamw_values([m], [tops], 1)[0]
+    assert np.array_equal(vals[at[2]].cpu().numpy(), values(m[at[2]].cpu().numpy(), tops[0, (1 << 31) // 256:].cpu().numpy(), 127))
+
+
 def test_refusals_on_the_device():
     x, m = torch.zeros(10, device="cuda"), torch.zeros(10, device="cuda")
     v, g = torch.zeros(10, device="cuda"), torch.zeros(10, device="cuda")

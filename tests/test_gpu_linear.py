@@ -14,6 +14,7 @@ import pytest
 import torch
 
 import chunk_wise_weight_amd as ttt
+from chunk_wise_weight_amd import binding
 from tests.block_util import U32, assert_close, half_step
 
 pytestmark = pytest.mark.gpu
@@ -243,6 +244,76 @@ def gated_grad_case(M, K, f, dt, act, off, accumulate=False):
 def test_gated_grad(M, K, f, dt, off):
     gated_grad_case(M, K, f, dt, "silu", off)
     gated_grad_case(M, K, f, dt, "gelu", off, accumulate=True)
+
+
+@pytest.mark.parametrize("off", OFFS)
+@pytest.mark.parametrize("M,K,N", [(1500, 1021, 1031), (700, 2049, 1027)])
+def test_odd_widths_that_are_copied(M, K, N, off):
+    """Rows that do not start on 16 bytes are copied to a workspace first where that pays."""
+    pad = (K + 7) // 8 * 8
+    # q, then at least the copies of q and x for the weight's gradient
+    assert binding._dense_ws("ttt_linear_grad_ws_bytes", M, K, N, 1) > 2 * M * N + 2 * M * pad
+    linear_case(M, K, N, BF16, F32, "silu", True, True, 0.5, off)
+    gated_case(M, K, N, BF16, "gelu", True, off)
+    linear_grad_case(M, K, N, BF16, BF16, "gelu", 1.0, off, accumulate=True)
+    gated_grad_case(M, K, N, BF16, "silu", off)
+
+
+@pytest.mark.parametrize("M,K,N", [(2048, 4096, 256), (40, 8192, 128), (1300, 72, 2056), (5000, 264, 64)])
+def test_splits_of_k_and_long_sums(M, K, N):
+    """Few tiles and a long k (its parts are summed apart and joined), and a weight's gradient over many rows."""
+    linear_case(M, K, N, BF16, F32, None, True, True, 1.0, 0)
+    linear_grad_case(M, K, N, BF16, BF16, "silu", 1.0, 0, accumulate=True)
+    gated_case(M, K, N, BF16, "silu", False, 0)
+
+
+def test_rows_past_32_bits():
+    """300000 rows of 8192: 2.4e9 results, the last ones 4.9 GB on. Rows are independent, so each must be what a call on
+    it and its neighbours alone gives (the same kernel and tile: bit for bit), and the weight's gradient what its two
+    halves give together."""
+    M, K, N = 300000, 64, 8192
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((M, K), generator=g, device="cuda").to(BF16)
+    w = (torch.randn((N, K), generator=g, device="cuda") / 8).to(BF16)
+    y = ttt.ttt_linear(x, w, act="silu")
+    for r in (0, 262143, 262144, M - 600):
+        want = x[r:r + 600].double() @ w.double().T
+        want = want * torch.sigmoid(want)
+        err = 64 * U32 + half_step(BF16)
+        assert bool(((y[r:r + 600].double() - want).abs() <= err * want.abs() + 1e-4).all()), r
+    z, a, b = ttt.ttt_gated(x, w, w, act="relu", keep=True)
+    assert torch.equal(a, b) and torch.equal(a[-1000:], ttt.ttt_linear(x[-1000:].contiguous(), w))
+    assert not bool(torch.isnan(z[::4099]).any())
+    del z, a, b
+    got = ttt.ttt_linear_grad(y, x, w, bias=True)
+    top = ttt.ttt_linear_grad(y[:150000], x[:150000], w)
+    low = ttt.ttt_linear_grad(y[150000:], x[150000:], w)
+    assert torch.equal(got.dx[:150000], top.dx) and torch.equal(got.dx[150000:], low.dx)
+    both = top.dw.double() + low.dw.double()
+    scale = both.abs().max()
+    assert float((got.dw.double() - both).abs().max()) <= 3 * half_step(BF16) * float(scale)
+    want = sum(part.double().sum(0) for part in y.split(50000))
+    assert float((got.dbias.double() - want).abs().max()) <= 1e-5 * float(want.abs().max())
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own."""
+    g = torch.Generator().manual_seed(6)
+    x, w = make((1500, 512), BF16, g).cuda(), make((520, 512), BF16, g, 0.05).cuda()
+    dy = [make((1500, 520), F32, g).cuda() for _ in range(2)]
+    want = [ttt.ttt_linear_grad(d, x, w, bias=True) for d in dy]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[] for _ in range(2)]
+    for _ in range(10):
+        for k, s in enumerate(streams):
+            got[k].append(ttt.ttt_linear_grad(dy[k], x, w, bias=True, stream=s))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for r in got[k]:
+            for a, b in zip(r, want[k]):
+                assert torch.equal(a, b)
 
 
 def test_gradients_against_differences():
