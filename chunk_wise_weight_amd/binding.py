@@ -95,9 +95,11 @@ def lib() -> ctypes.CDLL:
     L.ttt_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, sz, vp]
     L.ttt_clip_grads.argtypes = [vp, vp, vp, i32, f32, vp, vp, vp, sz, vp]
     psz, f64 = ctypes.POINTER(sz), ctypes.c_double
-    for fn in (L.ttt_linear_ws_bytes, L.ttt_gated_ws_bytes, L.ttt_linear_grad_ws_bytes, L.ttt_gated_grad_ws_bytes):
+    for fn in (L.ttt_linear_ws_bytes, L.ttt_gated_ws_bytes, L.ttt_gated_grad_ws_bytes):
         fn.argtypes = [i64, i32, i32, i32, psz]
         fn.restype = i32
+    L.ttt_linear_grad_ws_bytes.argtypes = [i64, i32, i32, i32, i32, i32, psz]
+    L.ttt_linear_grad_ws_bytes.restype = i32
     L.ttt_linear.argtypes = [vp, vp, i32, vp, i32, f32, vp, i64, i32, i32, vp, vp, i32, vp, sz, vp]
     L.ttt_gated.argtypes = [vp, vp, vp, i32, vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, sz, vp]
     L.ttt_linear_grad.argtypes = [vp, i32, vp, vp, i32, vp, i32, f32, i64, i32, i32, vp, vp, vp, i32, vp, sz, vp]
@@ -808,9 +810,9 @@ def _act(act: Optional[str], gated: bool = False) -> int:
 
 
 @lru_cache(maxsize=1024)
-def _dense_ws(name: str, rows: int, n_in: int, n_out: int, dt: int) -> int:
+def _dense_ws(name: str, rows: int, n_in: int, n_out: int, dt: int, *more: int) -> int:
     n = ctypes.c_size_t()
-    _check(getattr(lib(), name)(rows, n_in, n_out, dt, ctypes.byref(n)), name)
+    _check(getattr(lib(), name)(rows, n_in, n_out, dt, *more, ctypes.byref(n)), name)
     return n.value
 
 
@@ -932,7 +934,7 @@ def ttt_linear_grad(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: Opt
     dx, pdx = _grad_out(c, dx, "dx", need_dx, False, x.shape, dt)
     dw, pdw = _grad_out(c, dw, "dw", need_dw, accumulate, (out, n), dt)
     dbias, pdb = _grad_out(c, dbias, "dbias", bias, accumulate, (out,), torch.float32)
-    nws = _dense_ws("ttt_linear_grad_ws_bytes", rows, n, out, _DT[dt])
+    nws = _dense_ws("ttt_linear_grad_ws_bytes", rows, n, out, _DT[dt], _DT[dy.dtype], kind)
     ws = c.scratch(nws)
     _check(lib().ttt_linear_grad(pdy, _DT[dy.dtype], px, pw, _DT[dt], pp, kind, float(scale), rows, n, out, pdx, pdw,
                                  pdb, 1 if accumulate else 0, ws.data_ptr(), nws, c.on()), "ttt_linear_grad")

@@ -90,9 +90,10 @@ struct GradScratch {
   size_t q, part, gemm;
   size_t bytes() const { return q + part + gemm; }
 };
-GradScratch grad_scratch(int64_t rows, int in, int out, ttt_dtype dt, int count) {
+// q: q (or dg and du) is made, not dy itself
+GradScratch grad_scratch(int64_t rows, int in, int out, ttt_dtype dt, int count, bool q) {
   GradScratch s;
-  s.q = padded((size_t)rows * out * size_of(dt)) * count;
+  s.q = q ? padded((size_t)rows * out * size_of(dt)) * count : 0;
   s.part = padded(act_grad_ws_bytes(rows, out, count == 2));
   s.gemm = padded(std::max(gemm_ws_bytes(sizes_dx(rows, in, out, count), form_dx(dt)),
                            gemm_ws_bytes(sizes_dw(rows, in, out, count), form_dw(dt))));
@@ -322,11 +323,14 @@ int ttt_gated(const void *x, const void *W_gate, const void *W_up, ttt_dtype dt,
   return ttt_launched(launch_gemm(a, form_y(dt, true, dt), (hipStream_t)hip_stream), kWhere);
 }
 
-int ttt_linear_grad_ws_bytes(int64_t rows, int in, int out, ttt_dtype dt, size_t *bytes) {
-  if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_linear_grad_ws_bytes: bytes is NULL");
-  const int rc = check_dense("ttt_linear_grad_ws_bytes", dt, rows, in, out);
+int ttt_linear_grad_ws_bytes(int64_t rows, int in, int out, ttt_dtype dt, ttt_dtype y_dt, int act, size_t *bytes) {
+  static const char *kWhere = "ttt_linear_grad_ws_bytes";
+  if (!bytes) return ttt_fail(TTT_E_NULL, "%s: bytes is NULL", kWhere);
+  int rc = check_dense(kWhere, dt, rows, in, out);
+  if (!rc) rc = check_y(kWhere, dt, y_dt);
+  if (!rc) rc = check_act(kWhere, act, false);
   if (rc) return rc;
-  *bytes = grad_scratch(rows, in, out, dt, 1).bytes();
+  *bytes = grad_scratch(rows, in, out, dt, 1, act != TTT_ACT_NONE || y_dt != dt).bytes();
   return TTT_OK;
 }
 
@@ -342,7 +346,9 @@ int ttt_linear_grad(const void *dy, ttt_dtype y_dt, const void *x, const void *W
   if (act == TTT_ACT_NONE) pre = nullptr;
   if (rows > 0 && (!dy || (dW && !x) || (dx && !W) || (act != TTT_ACT_NONE && !pre)))
     return ttt_fail(TTT_E_NULL, "%s: dy, x, W or pre is NULL", kWhere);
-  const GradScratch sc = grad_scratch(rows, in, out, dt, 1);
+  // dy itself serves as q where it has the products' type; the scale is then theirs
+  const bool made = act != TTT_ACT_NONE || y_dt != dt;
+  const GradScratch sc = grad_scratch(rows, in, out, dt, 1, made);
   rc = check_ws(kWhere, ws, ws_bytes, sc.bytes());
   if (rc) return rc;
   const size_t e = size_of(dt), ye = size_of(y_dt), no = (size_t)rows * out, ni = (size_t)rows * in;
@@ -357,8 +363,7 @@ int ttt_linear_grad(const void *dy, ttt_dtype y_dt, const void *x, const void *W
   if (!rc) rc = ttt_check_device();
   if (rc) return rc;
   const hipStream_t s = (hipStream_t)hip_stream;
-  // dy itself serves as q where it has the products' type; the scale is then theirs
-  const bool pass = rows > 0 && (pre || y_dt != dt);
+  const bool pass = rows > 0 && made;
   const void *q = pass ? ws : dy;
   if (pass || dbias) {
     ActGradArgs a{};
@@ -388,7 +393,7 @@ int ttt_gated_grad_ws_bytes(int64_t rows, int in, int f, ttt_dtype dt, size_t *b
   if (!bytes) return ttt_fail(TTT_E_NULL, "ttt_gated_grad_ws_bytes: bytes is NULL");
   const int rc = check_dense("ttt_gated_grad_ws_bytes", dt, rows, in, f);
   if (rc) return rc;
-  *bytes = grad_scratch(rows, in, f, dt, 2).bytes();
+  *bytes = grad_scratch(rows, in, f, dt, 2, true).bytes();
   return TTT_OK;
 }
 
@@ -403,7 +408,7 @@ int ttt_gated_grad(const void *dz, const void *x, const void *W_gate, const void
     return ttt_fail(TTT_E_NULL, "%s: one of dW_gate, dW_up or of db_gate, db_up is NULL", kWhere);
   if (rows > 0 && (!dz || !g || !u || (dW_gate && !x) || (dx && (!W_gate || !W_up))))
     return ttt_fail(TTT_E_NULL, "%s: dz, x, W_gate, W_up, g or u is NULL", kWhere);
-  const GradScratch sc = grad_scratch(rows, in, f, dt, 2);
+  const GradScratch sc = grad_scratch(rows, in, f, dt, 2, true);
   rc = check_ws(kWhere, ws, ws_bytes, sc.bytes());
   if (rc) return rc;
   const size_t e = size_of(dt), no = (size_t)rows * f * e, ni = (size_t)rows * in * e, nw = (size_t)f * in * e;

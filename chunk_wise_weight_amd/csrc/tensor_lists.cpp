@@ -12,6 +12,8 @@
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <memory>
+
 namespace {
 
 int type_of(at::ScalarType t) {
@@ -24,26 +26,24 @@ int type_of(at::ScalarType t) {
   }
 }
 
+struct Release {
+  void operator()(PyObject *o) const { Py_DECREF(o); }
+};
+using Bytes = std::unique_ptr<PyObject, Release>;
+Bytes bytes_of(Py_ssize_t n) { return Bytes(PyBytes_FromStringAndSize(nullptr, n)); }
+
 PyObject *read_list(PyObject *list, const char *name, int device) {
   const Py_ssize_t n = PyList_GET_SIZE(list);
-  PyObject *bytes[3];
-  const Py_ssize_t size[3] = {8, 8, 4};
-  for (int i = 0; i < 3; ++i) {
-    bytes[i] = PyBytes_FromStringAndSize(nullptr, n * size[i]);
-    if (!bytes[i]) {
-      while (i-- > 0) Py_DECREF(bytes[i]);
-      return nullptr;
-    }
-  }
-  auto *at = reinterpret_cast<int64_t *>(PyBytes_AS_STRING(bytes[0]));
-  auto *numel = reinterpret_cast<int64_t *>(PyBytes_AS_STRING(bytes[1]));
-  auto *kind = reinterpret_cast<int32_t *>(PyBytes_AS_STRING(bytes[2]));
+  const Bytes ats = bytes_of(n * 8), numels = bytes_of(n * 8), kinds = bytes_of(n * 4);
+  if (!ats || !numels || !kinds) return nullptr;
+  auto *at = reinterpret_cast<int64_t *>(PyBytes_AS_STRING(ats.get()));
+  auto *numel = reinterpret_cast<int64_t *>(PyBytes_AS_STRING(numels.get()));
+  auto *kind = reinterpret_cast<int32_t *>(PyBytes_AS_STRING(kinds.get()));
   long seen = 0, faults = 0;
   for (Py_ssize_t i = 0; i < n; ++i) {
     PyObject *o = PyList_GET_ITEM(list, i);
     if (!THPVariable_Check(o)) {
       PyErr_Format(PyExc_TypeError, "%s must be tensors, got %s", name, Py_TYPE(o)->tp_name);
-      for (PyObject *b : bytes) Py_DECREF(b);
       return nullptr;
     }
     const at::Tensor &t = THPVariable_Unpack(o);
@@ -57,7 +57,7 @@ PyObject *read_list(PyObject *list, const char *name, int device) {
     seen |= 1L << kind[i];
     faults |= fault;
   }
-  return Py_BuildValue("(NNNll)", bytes[0], bytes[1], bytes[2], seen, faults);
+  return Py_BuildValue("(OOOll)", ats.get(), numels.get(), kinds.get(), seen, faults);
 }
 
 PyObject *read(PyObject *, PyObject *args) {

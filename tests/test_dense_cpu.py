@@ -111,7 +111,15 @@ def test_valid_calls_without_a_device():
 def test_workspace_queries():
     n = ctypes.c_size_t()
     L = ttt.lib()
-    for q in (L.ttt_linear_ws_bytes, L.ttt_gated_ws_bytes, L.ttt_linear_grad_ws_bytes, L.ttt_gated_grad_ws_bytes):
+    q = L.ttt_linear_grad_ws_bytes
+    assert q(1000, 64, 64, 1, 1, 0, ctypes.byref(n)) == 0
+    small = n.value
+    # q is made with an activation, or from an fp32 dy
+    for y_dt, act in ((0, 0), (1, 2), (0, 2)):
+        assert q(1000, 64, 64, 1, y_dt, act, ctypes.byref(n)) == 0 and n.value >= small + 1000 * 64 * 2
+    assert q(100, 64, 64, 0, 1, 0, ctypes.byref(n)) == DTYPE
+    assert q(100, 64, 64, 1, 1, 9, ctypes.byref(n)) == ARG
+    for q in (L.ttt_linear_ws_bytes, L.ttt_gated_ws_bytes, L.ttt_gated_grad_ws_bytes):
         assert q(100, 64, 64, 1, ctypes.byref(n)) == 0
         assert q(100, 64, 64, 1, None) == NULL
         assert q(100, 0, 64, 1, ctypes.byref(n)) == SHAPE

@@ -251,8 +251,8 @@ def test_gated_grad(M, K, f, dt, off):
 def test_odd_widths_that_are_copied(M, K, N, off):
     """Rows that do not start on 16 bytes are copied to a workspace first where that pays."""
     pad = (K + 7) // 8 * 8
-    # q, then at least the copies of q and x for the weight's gradient
-    assert binding._dense_ws("ttt_linear_grad_ws_bytes", M, K, N, 1) > 2 * M * N + 2 * M * pad
+    # at least the copies of q and x for the weight's gradient
+    assert binding._dense_ws("ttt_linear_grad_ws_bytes", M, K, N, 1, 1, 0) > 2 * M * N + 2 * M * pad
     linear_case(M, K, N, BF16, F32, "silu", True, True, 0.5, off)
     gated_case(M, K, N, BF16, "gelu", True, off)
     linear_grad_case(M, K, N, BF16, BF16, "gelu", 1.0, off, accumulate=True)
