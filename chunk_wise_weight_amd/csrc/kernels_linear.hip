@@ -250,8 +250,8 @@ __global__ __launch_bounds__(kThreads) void k_join(GemmArgs g, long long ti, lon
 // a product of odd widths can run on the tiles that load whole pieces.
 
 struct PackJob {
-  const bf16_t *src;
-  bf16_t *dst;
+  const void *src;
+  void *dst;
   long long rows, n, first;  // first: pieces of eight before this job's
 };
 struct PackJobs {
@@ -259,6 +259,7 @@ struct PackJobs {
   int count;
   long long pieces;
 };
+template <typename T>
 __global__ __launch_bounds__(kThreads) void k_pack(PackJobs p) {
   const long long q = group_index() * kThreads + threadIdx.x;
   if (q >= p.pieces) return;
@@ -267,8 +268,8 @@ __global__ __launch_bounds__(kThreads) void k_pack(PackJobs p) {
   for (int i = 1; i < 4; ++i)
     if (i < p.count && q >= p.job[i].first) k = i;
   const long long n = p.job[k].n, per = (n + 7) / 8, at = q - p.job[k].first, r = at / per, c = at % per * 8;
-  const Raw8<bf16_t> v = load_some(p.job[k].src + r * n + c, clamp8(n - c));
-  __builtin_memcpy(__builtin_assume_aligned(p.job[k].dst + at * 8, 16), &v, 16);
+  const Raw8<T> v = load_some((const T *)p.job[k].src + r * n + c, clamp8(n - c));
+  __builtin_memcpy(__builtin_assume_aligned((T *)p.job[k].dst + at * 8, 16), &v, sizeof v);
   end_of_stores();
 }
 
@@ -280,8 +281,9 @@ long long pad8(long long n) { return (n + 7) / 8 * 8; }
 // slab (us_slab, per form); for splits the fp32 sums written and read again, in
 // the last-level cache up to 100 MB, and the second launch; for rows that are
 // copied first their bytes and a launch. The times are measured ones
-// (microseconds). Over 49 products of 17 to 32768 rows of all forms the choice
-// took at most 10 % more than the best of both tiles with 1 to 16 splits.
+// (microseconds). Over 38 products of 17 to 20000 rows of all forms and both
+// types the choice took at most 10 % more than the best of both kernels' tiles
+// with 1 to 12 splits.
 
 constexpr int kCus = 256;
 struct Choice {
@@ -309,23 +311,28 @@ long long general_tiles(const GemmArgs &g, const GemmForm &f, int tile) {
   return (g.ni + wide - 1) / wide * ((g.nj + tile - 1) / tile) * g.batch;
 }
 // Several tiles share a CU: what one takes by itself, or each one's share on the fullest CU.
+auto shared(double alone, double share) {
+  return [=](long long n) { return std::max(alone, (double)((n + kCus - 1) / kCus) * share); };
+}
 Choice choose_general(const GemmArgs &g, const GemmForm &f) {
   const double wait = f.b_trans ? 3.5 : f.a_trans ? 2.6 : 1.8;  // bf16, a tile of 128 alone
-  auto shared = [](double alone, double share) {
-    return [=](long long n) { return std::max(alone, (double)((n + kCus - 1) / kCus) * share); };
-  };
   const Choice big = choose(g, 128, general_tiles(g, f, 128), shared(f.f32 ? 5.1 : wait, f.f32 ? 4.4 : 0.9));
   const Choice small = choose(g, 64, general_tiles(g, f, 64), shared(f.f32 ? 2.2 : 0.5 * wait, f.f32 ? 1.17 : 0.42));
   return small.us < big.us ? small : big;
 }
-// Tiles of 256 run in rounds of one per CU, those of 128 in rounds of two.
+// Here bf16 tiles of 256 run in rounds of one per CU and those of 128 in rounds of two; the others share as above.
 Choice choose_dense(const GemmArgs &g, const GemmForm &f) {
-  const Choice big = choose(g, 256, dense_tiles(g, f, 256), [](long long n) { return 1.75 * ((n + kCus - 1) / kCus); });
-  const Choice small = choose(g, 128, dense_tiles(g, f, 128), [](long long n) {
+  auto pairs = [](long long n) {
     const double rest = (double)(n % (2 * kCus)) / kCus;
     return 1.2 * (n / (2 * kCus)) + (rest > 0 ? 0.9 + 0.3 * std::max(0.0, rest - 1) : 0);
-  });
-  return small.us < big.us ? small : big;
+  };
+  const long long mid = dense_tiles(g, f, 128), small = dense_tiles(g, f, 64);
+  Choice best = f.f32 ? choose(g, 128, mid, shared(4.4, 3.97)) : choose(g, 128, mid, pairs);
+  const Choice s = choose(g, 64, small, f.f32 ? shared(1.45, 1.08) : shared(0.34, 0.25));
+  if (s.us < best.us) best = s;
+  if (f.f32) return best;  // four fp32 tiles of 128 take what one of 256 does
+  const Choice b = choose(g, 256, dense_tiles(g, f, 256), shared(1.75, 1.75));
+  return best.us < b.us ? best : b;
 }
 size_t parts_bytes(long long tiles, const Choice &c) {
   return c.splits > 1 ? (size_t)tiles * c.splits * c.tile * c.tile * 4 : 0;
@@ -345,13 +352,12 @@ Plan plan_of(const GemmArgs &g, const GemmForm &f) {
   p.g = g;
   p.choice = choose_general(g, f);
   p.parts = parts_bytes(general_tiles(g, f, p.choice.tile), p.choice);
-  if (f.f32) return p;
   Plan d = p;
   d.dense = true;
-  d.pack_a = g.lda % 8 != 0;
-  d.pack_b = g.ldb % 8 != 0;
-  d.g.lda = pad8(g.lda);
-  d.g.ldb = pad8(g.ldb);
+  d.pack_a = g.lda % (f.f32 ? 4 : 8) != 0;
+  d.pack_b = g.ldb % (f.f32 ? 4 : 8) != 0;
+  if (d.pack_a) d.g.lda = pad8(g.lda);
+  if (d.pack_b) d.g.ldb = pad8(g.ldb);
   d.rows_a = f.a_trans ? g.nk : g.ni;
   d.rows_b = f.b_trans ? g.nk : g.nj;
   d.count_a = f.pair || g.segments > 1 ? 2 : 1;
@@ -359,8 +365,8 @@ Plan plan_of(const GemmArgs &g, const GemmForm &f) {
   if (!dense_sizes(d.g, f)) return p;
   d.choice = choose_dense(g, f);
   d.parts = parts_bytes(dense_tiles(g, f, d.choice.tile), d.choice);
-  if (d.pack_a) d.copies += (size_t)d.count_a * d.rows_a * d.g.lda * 2;
-  if (d.pack_b) d.copies += (size_t)d.count_b * d.rows_b * d.g.ldb * 2;
+  if (d.pack_a) d.copies += (size_t)d.count_a * d.rows_a * d.g.lda * (f.f32 ? 4 : 2);
+  if (d.pack_b) d.copies += (size_t)d.count_b * d.rows_b * d.g.ldb * (f.f32 ? 4 : 2);
   const double us = d.choice.us + (d.copies ? 4.0 + 2.0 * d.copies / 4.0e6 : 0.0);
   return d.copies && us >= p.choice.us ? p : d;
 }
@@ -602,16 +608,17 @@ hipError_t launch_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
     GemmArgs d = p.g;
     if (p.copies) {
       PackJobs jobs{};
-      bf16_t *to = (bf16_t *)g.ws;
+      char *to = (char *)g.ws;
       auto add = [&](const void *&m, long long rows, long long n) {
-        jobs.job[jobs.count++] = PackJob{(const bf16_t *)m, to, rows, n, jobs.pieces};
+        jobs.job[jobs.count++] = PackJob{m, to, rows, n, jobs.pieces};
         m = to;
-        to += rows * pad8(n);
+        to += rows * pad8(n) * (f.f32 ? 4 : 2);
         jobs.pieces += rows * (pad8(n) / 8);
       };
       for (int i = 0; p.pack_a && i < p.count_a; ++i) add(d.a[i], p.rows_a, g.lda);
       for (int i = 0; p.pack_b && i < p.count_b; ++i) add(d.b[i], p.rows_b, g.ldb);
-      hipLaunchKernelGGL(k_pack, group_grid((jobs.pieces + kThreads - 1) / kThreads), dim3(kThreads), 0, s, jobs);
+      hipLaunchKernelGGL(f.f32 ? k_pack<float> : k_pack<bf16_t>, group_grid((jobs.pieces + kThreads - 1) / kThreads),
+                         dim3(kThreads), 0, s, jobs);
       d.ws = to;
     }
     return launch_dense(d, f, p.choice.tile, p.choice.splits, s);

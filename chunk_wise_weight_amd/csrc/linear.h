@@ -53,9 +53,9 @@ hipError_t launch_join(const GemmArgs &g, const GemmForm &f, long long ti, long 
 bool few_sizes(const GemmArgs &g, const GemmForm &f);
 hipError_t launch_few(const GemmArgs &g, const GemmForm &f, hipStream_t s);
 
-// bf16 operands whose rows start on 16 bytes (kernels_dense.hip): sizes that allow it, the launch with tiles of
-// `tile` x `tile` (256 or 128), and its workgroups (tiles times batch). k past nk in the last piece of eight of an
-// operand held by rows is zero.
+// Operands whose rows start on 16 bytes (kernels_dense.hip): sizes that allow it, the launch with tiles of `tile` x
+// `tile` (64, 128 or, in bf16, 256), and its workgroups (tiles times batch). k past nk in the last 16 bytes of a row of
+// an operand held by rows is zero.
 bool dense_sizes(const GemmArgs &g, const GemmForm &f);
 long long dense_tiles(const GemmArgs &g, const GemmForm &f, int tile);
 hipError_t launch_dense(const GemmArgs &g, const GemmForm &f, int tile, int splits, hipStream_t s);

@@ -267,6 +267,17 @@ def test_splits_of_k_and_long_sums(M, K, N):
     gated_case(M, K, N, BF16, "silu", False, 0)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("M,K,N", [(40, 2048, 320), (300, 520, 392), (1233, 1024, 512), (2100, 264, 2052), (1500, 1021, 1031),
+                                   (19, 40, 2056)])
+def test_tiles_of_each_side(M, K, N, dt):
+    """Sizes between which the tile's side and the number of parts change, in both types and every form."""
+    linear_case(M, K, N, dt, F32, "gelu", True, True, 0.5, 0)
+    gated_case(M, K, N, dt, "silu", True, 0)
+    linear_grad_case(M, K, N, dt, dt, "silu", 1.0, 0, accumulate=True)
+    gated_grad_case(M, K, N, dt, "gelu", 0)
+
+
 def test_rows_past_32_bits():
     """300000 rows of 8192: 2.4e9 results, the last ones 4.9 GB on. Rows are independent, so each must be what a call on
     it and its neighbours alone gives (the same kernel and tile: bit for bit), and the weight's gradient what its two
