@@ -61,20 +61,23 @@ GemmArgs sizes_y(int64_t rows, int in, int out) {
   g.scale = 1.f;
   return g;
 }
-GemmArgs sizes_dx(int64_t rows, int in, int out, int pairs) {
+// ldq: from one row of q to the next
+GemmArgs sizes_dx(int64_t rows, int in, int out, int pairs, int ldq) {
   GemmArgs g{};
   g.lda = g.ldo = g.ni = in;
-  g.ldb = g.nk = out;
+  g.ldb = ldq;
+  g.nk = out;
   g.nj = rows;
   g.segments = pairs;
   g.batch = 1;
   g.scale = 1.f;
   return g;
 }
-GemmArgs sizes_dw(int64_t rows, int in, int out, int count) {
+GemmArgs sizes_dw(int64_t rows, int in, int out, int count, int ldq) {
   GemmArgs g{};
   g.lda = g.ldo = g.ni = in;
-  g.ldb = g.nj = out;
+  g.ldb = ldq;
+  g.nj = out;
   g.nk = rows;
   g.segments = 1;
   g.batch = count;
@@ -85,24 +88,28 @@ GemmForm form_y(ttt_dtype dt, bool pair, ttt_dtype y) { return form(dt, false, f
 GemmForm form_dx(ttt_dtype dt) { return form(dt, true, false, false, dt == TTT_F32); }
 GemmForm form_dw(ttt_dtype dt) { return form(dt, true, true, false, dt == TTT_F32); }
 
-// Workspace of the gradients: q (or dg and du), the biases' sums, the products' splits.
+// Workspace of the gradients: q (or dg and du), the biases' sums, the products' splits. Rows of q that is made start on
+// whole pieces of eight, zero behind their ends, as the products would otherwise copy them (gated gradients of 8192 x
+// 2560 x 9721 in bf16: 2013 -> 1589 us; of 2000 x 512 x 1365 in fp32, which were not copied: 185 -> 157).
 struct GradScratch {
   size_t q, part, gemm;
+  int ldq;
   size_t bytes() const { return q + part + gemm; }
 };
 // q: q (or dg and du) is made, not dy itself
 GradScratch grad_scratch(int64_t rows, int in, int out, ttt_dtype dt, int count, bool q) {
   GradScratch s;
-  s.q = q ? padded((size_t)rows * out * size_of(dt)) * count : 0;
+  s.ldq = q ? (out + 7) / 8 * 8 : out;
+  s.q = q ? padded((size_t)rows * s.ldq * size_of(dt)) * count : 0;
   s.part = padded(act_grad_ws_bytes(rows, out, count == 2));
-  s.gemm = padded(std::max(gemm_ws_bytes(sizes_dx(rows, in, out, count), form_dx(dt)),
-                           gemm_ws_bytes(sizes_dw(rows, in, out, count), form_dw(dt))));
+  s.gemm = padded(std::max(gemm_ws_bytes(sizes_dx(rows, in, out, count, s.ldq), form_dx(dt)),
+                           gemm_ws_bytes(sizes_dw(rows, in, out, count, s.ldq), form_dw(dt))));
   return s;
 }
 
-int run_dx(const char *where, const void *const *q, const void *const *W, int pairs, ttt_dtype dt, float scale,
+int run_dx(const char *where, const void *const *q, int ldq, const void *const *W, int pairs, ttt_dtype dt, float scale,
            int64_t rows, int in, int out, void *dx, void *ws, hipStream_t s) {
-  GemmArgs g = sizes_dx(rows, in, out, pairs);
+  GemmArgs g = sizes_dx(rows, in, out, pairs, ldq);
   for (int i = 0; i < pairs; ++i) {
     g.a[i] = W[i];
     g.b[i] = q[i];
@@ -113,9 +120,9 @@ int run_dx(const char *where, const void *const *q, const void *const *W, int pa
   return ttt_launched(launch_gemm(g, form_dx(dt), s), where);
 }
 
-int run_dw(const char *where, const void *const *q, const void *x, int count, ttt_dtype dt, float scale, int64_t rows,
-           int in, int out, void *const *dW, int accumulate, void *ws, hipStream_t s) {
-  GemmArgs g = sizes_dw(rows, in, out, count);
+int run_dw(const char *where, const void *const *q, int ldq, const void *x, int count, ttt_dtype dt, float scale,
+           int64_t rows, int in, int out, void *const *dW, int accumulate, void *ws, hipStream_t s) {
+  GemmArgs g = sizes_dw(rows, in, out, count, ldq);
   g.a[0] = x;
   for (int i = 0; i < count; ++i) {
     g.b[i] = q[i];
@@ -374,6 +381,7 @@ int ttt_linear_grad(const void *dy, ttt_dtype y_dt, const void *x, const void *W
     a.part = (float *)((char *)ws + sc.q);
     a.rows = rows;
     a.n = out;
+    a.ldo = sc.ldq;
     a.scale = scale;
     a.act = act;
     a.accumulate = accumulate != 0;
@@ -384,8 +392,8 @@ int ttt_linear_grad(const void *dy, ttt_dtype y_dt, const void *x, const void *W
   }
   const float left = pass ? 1.f : scale;
   void *split_ws = (char *)ws + sc.q + sc.part;
-  if (dx && rows > 0) rc = run_dx(kWhere, &q, &W, 1, dt, left, rows, in, out, dx, split_ws, s);
-  if (dW && !rc) rc = run_dw(kWhere, &q, x, 1, dt, left, rows, in, out, &dW, accumulate, split_ws, s);
+  if (dx && rows > 0) rc = run_dx(kWhere, &q, sc.ldq, &W, 1, dt, left, rows, in, out, dx, split_ws, s);
+  if (dW && !rc) rc = run_dw(kWhere, &q, sc.ldq, x, 1, dt, left, rows, in, out, &dW, accumulate, split_ws, s);
   return rc;
 }
 
@@ -439,6 +447,7 @@ int ttt_gated_grad(const void *dz, const void *x, const void *W_gate, const void
     a.part = (float *)((char *)ws + sc.q);
     a.rows = rows;
     a.n = f;
+    a.ldo = sc.ldq;
     a.scale = 1.f;
     a.act = act;
     a.accumulate = accumulate != 0;
@@ -447,8 +456,8 @@ int ttt_gated_grad(const void *dz, const void *x, const void *W_gate, const void
     if (rc) return rc;
   }
   void *split_ws = (char *)ws + sc.q + sc.part;
-  if (dx && rows > 0) rc = run_dx(kWhere, q, W, 2, dt, 1.f, rows, in, f, dx, split_ws, s);
-  if (dW_gate && !rc) rc = run_dw(kWhere, q, x, 2, dt, 1.f, rows, in, f, dW, accumulate, split_ws, s);
+  if (dx && rows > 0) rc = run_dx(kWhere, q, sc.ldq, W, 2, dt, 1.f, rows, in, f, dx, split_ws, s);
+  if (dW_gate && !rc) rc = run_dw(kWhere, q, sc.ldq, x, 2, dt, 1.f, rows, in, f, dW, accumulate, split_ws, s);
   return rc;
 }
 

@@ -397,9 +397,10 @@ hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, const Choice &c, hipSt
 // ---------------------------------------------------------------------------
 // The gradient at the pre-activations, elementwise, and its sums over the rows
 // for the biases. Without sums the arrays are taken as they lie, end to end.
-// With sums a wave takes 512 columns (eight per lane) of every fourth row of a
-// run; the waves' sums are added in LDS, the runs' by k_column_sums, each in a
-// fixed order. Either way a thread loads all of a step before it stores any.
+// With sums, or where rows are set apart, a wave takes 512 columns (eight per
+// lane) of every fourth row of a run; the waves' sums are added in LDS, the
+// runs' by k_column_sums, each in a fixed order. Either way a thread loads all
+// of a step before it stores any.
 
 // Eight elements of the step from `at` on, `left` of them there.
 template <typename D, typename T, bool GATED, bool NT>
@@ -417,7 +418,13 @@ struct ActStep {
     for (int i = 0; i < (int)sizeof r / 16; ++i) to[i] = __builtin_nontemporal_load(from + i);
     return r;
   }
-  static __device__ __forceinline__ void keep(void *base, long long at, int left, const float (&v)[8]) {
+  // pad: a short run becomes a whole one
+  static __device__ __forceinline__ void keep(void *base, long long at, int left, bool pad, float (&v)[8]) {
+    if (pad && left < 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < left ? v[e] : 0.f;
+      if (left > 0) left = 8;
+    }
     T *q = reinterpret_cast<T *>(base) + at;
     if constexpr (NT && sizeof(T) == 2) {
       if (left >= 8) {
@@ -433,8 +440,9 @@ struct ActStep {
     if (GATED || a.p) p = fetch<T>(a.p, at, left);
     if constexpr (GATED) u = fetch<T>(a.u, at, left);
   }
-  // q, and with a pair also q2, rounded and kept
-  __device__ __forceinline__ void apply(const ActGradArgs &a, long long at, int left, float (&q)[8], float (&q2)[8]) const {
+  // q, and with a pair also q2, rounded and kept at `to`
+  __device__ __forceinline__ void apply(const ActGradArgs &a, long long to, int left, float (&q)[8], float (&q2)[8]) const {
+    const bool pad = a.ldo > a.n;
     float d[8], x[8], y[8];
     expand(dy, d);
     if constexpr (GATED) {
@@ -447,7 +455,7 @@ struct ActStep {
         q[e] = d[e] * y[e] * df;
         q2[e] = d[e] * f;
       }
-      keep(a.out2, at, left, q2);
+      keep(a.out2, to, left, pad, q2);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) q[e] = a.scale * d[e];
@@ -461,7 +469,7 @@ struct ActStep {
         }
       }
     }
-    if (a.out) keep(a.out, at, left, q);
+    if (a.out) keep(a.out, to, left, pad, q);
   }
 };
 
@@ -504,13 +512,17 @@ __global__ __launch_bounds__(kThreads) void k_act_grad_sums(ActGradArgs a, long 
     for (int k = 0; k < 2; ++k) {
       if (k == 1 && !two) break;
       float q[8], q2[8];
-      st[k].apply(a, (r + k * kSumWaves) * a.n + c, left, q, q2);
+      st[k].apply(a, (r + k * kSumWaves) * a.ldo + c, left, q, q2);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         s1[e] += q[e];
         if constexpr (GATED) s2[e] += q2[e];
       }
     }
+  }
+  if (!a.sum) {
+    end_of_stores();
+    return;
   }
   __builtin_memcpy(&red[w][0][lane * 8], s1, 32);
   if constexpr (GATED) __builtin_memcpy(&red[w][1][lane * 8], s2, 32);
@@ -552,7 +564,7 @@ constexpr long long kStreamBytes = 512LL << 20;
 
 template <typename D, typename T, bool GATED, bool NT>
 hipError_t run_act_grad(const ActGradArgs &a, hipStream_t s) {
-  if (!a.sum) {
+  if (!a.sum && a.ldo == a.n) {
     const long long groups = (a.rows * a.n + kFlat * kThreads * 8 - 1) / (kFlat * kThreads * 8);
     if (groups > 0) hipLaunchKernelGGL((k_act_grad<D, T, GATED, NT>), group_grid(groups), dim3(kThreads), 0, s, a);
     return hipGetLastError();
@@ -560,6 +572,7 @@ hipError_t run_act_grad(const ActGradArgs &a, hipStream_t s) {
   const long long runs = row_runs(a.rows, a.n);
   hipLaunchKernelGGL((k_act_grad_sums<D, T, GATED, NT>),
                      dim3((unsigned)((a.n + kWaveCols - 1) / kWaveCols), (unsigned)runs), dim3(kThreads), 0, s, a, runs);
+  if (!a.sum) return hipGetLastError();
   hipLaunchKernelGGL(k_column_sums, dim3((unsigned)((a.n + 63) / 64), GATED ? 2 : 1), dim3(1024), 0, s, a.part, runs,
                      a.n, a.sum, a.sum2, a.accumulate);
   return hipGetLastError();

@@ -60,14 +60,15 @@ bool dense_sizes(const GemmArgs &g, const GemmForm &f);
 long long dense_tiles(const GemmArgs &g, const GemmForm &f, int tile);
 hipError_t launch_dense(const GemmArgs &g, const GemmForm &f, int tile, int splits, hipStream_t s);
 
-// q = scale * dy * act'(p) (p NULL: scale * dy), rounded to out's type, and its column sums. dy, p, out: [rows][n].
+// q = scale * dy * act'(p) (p NULL: scale * dy), rounded to out's type, and its column sums. dy, p, u: [rows][n]; out,
+// out2: rows of n at ldo, which is n or n rounded up to eight, and then zeros behind.
 // gated (u not NULL): out2 = dy * act(p), out = dy * u * act'(p).
 struct ActGradArgs {
   const void *dy, *p, *u;
   void *out, *out2;  // nullable: only the sums are wanted
   float *sum, *sum2;  // [n] fp32, nullable
   float *part;        // act_grad_ws_bytes(rows, n, gated), with sum
-  long long rows, n;
+  long long rows, n, ldo;
   float scale;
   int act, accumulate;  // accumulate: the sums are added to sum, sum2
   bool dy_f32, f32;     // types of dy; of p, u, out, out2
