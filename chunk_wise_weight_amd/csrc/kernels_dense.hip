@@ -5,7 +5,7 @@
 // it with v_mfma_f32_16x16x32_bf16, or in fp32 with four v_mfma_f32_16x16x4_f32
 // for every one of those. Tiles of 256 x 256 take eight waves of 128 x 64, one
 // workgroup per CU; tiles of 128 x 128 four of 64 x 64, two workgroups per CU;
-// tiles of 64 x 64 four of 32 x 32, three per CU. k runs in slabs of one
+// tiles of 64 x 64 four of 32 x 32, three or four per CU. k runs in slabs of one
 // 128-byte line (64 k in bf16, 32 in fp32): a load instruction moves eight
 // lines into LDS (16 bytes per lane), SLABS of them are held, and the loads of
 // slab n + SLABS are issued behind the MFMAs of slab n's second half, into the
@@ -167,8 +167,12 @@ struct Shape {
   static constexpr int SMEM = RING > OUT ? RING : OUT;
 };
 using Big = Shape<8, 4, 2, 4, 2, 1>;
+template <typename T>
 using Small = Shape<4, 4, 2, 2, 2, 2>;
-using Tiny = Shape<2, 2, 2, 2, 3, 3>;
+// Tiles of 64: bf16 waits for memory and gains by a third slab (256 x 2560 x 2560 15 us, 22 with two); fp32 waits for its
+// MFMAs and gains by more workgroups (4096 x 1024 x 1024 70 us, 75 with three slabs).
+template <typename T>
+using Tiny = Shape<2, 2, 2, 2, sizeof(T) == 2 ? 3 : 2, sizeof(T) == 2 ? 3 : 4>;
 
 // s_waitcnt immediate (gfx9): vmcnt(n), expcnt unchanged, lgkmcnt(0)
 constexpr unsigned wait_imm(int n) { return (unsigned)((n & 15) | 0x70 | (((n >> 4) & 3) << 14)); }
@@ -445,12 +449,10 @@ hipError_t run(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) 
   if (!f.a_trans) return run<S, T, O, false, false, false>(g, f, splits, s);
   return f.b_trans ? run<S, T, T, true, true, false>(g, f, splits, s) : run<S, T, T, true, false, false>(g, f, splits, s);
 }
-template <class S>
+template <template <typename> class S>
 hipError_t run(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) {
-  if constexpr (S::TI < 256) {
-    if (f.f32) return run<S, float, float>(g, f, splits, s);
-  }
-  return f.out_f32 ? run<S, bf16_t, float>(g, f, splits, s) : run<S, bf16_t, bf16_t>(g, f, splits, s);
+  if (f.f32) return run<S<float>, float, float>(g, f, splits, s);
+  return f.out_f32 ? run<S<bf16_t>, bf16_t, float>(g, f, splits, s) : run<S<bf16_t>, bf16_t, bf16_t>(g, f, splits, s);
 }
 
 }  // namespace
@@ -467,6 +469,7 @@ bool dense_sizes(const GemmArgs &g, const GemmForm &f) {
          g.nk * g.segments <= (1LL << 34);
 }
 hipError_t launch_dense(const GemmArgs &g, const GemmForm &f, int tile, int splits, hipStream_t s) {
-  if (tile == 256 && !f.f32) return run<Big>(g, f, splits, s);
+  if (tile == 256 && !f.f32)
+    return f.out_f32 ? run<Big, bf16_t, float>(g, f, splits, s) : run<Big, bf16_t, bf16_t>(g, f, splits, s);
   return tile == 128 ? run<Small>(g, f, splits, s) : run<Tiny>(g, f, splits, s);
 }

@@ -291,16 +291,16 @@ struct Choice {
   double us;
 };
 
-// us_slab(n): of n tiles on the device
+// us_slab(n): of n tiles on the device; us_once: what else they take when they are not split
 template <class F>
-Choice choose(const GemmArgs &g, int tile, long long tiles, F &&us_slab) {
+Choice choose(const GemmArgs &g, int tile, long long tiles, F &&us_slab, double us_once = 0) {
   Choice best{tile, 1, 1e30};
   const double slabs = (double)((g.nk + 63) / 64) * g.segments;
   const double bytes = (double)tiles * tile * tile * 4;
   for (int s = 1; s <= 32; ++s) {
     if (s > 1 && (slabs / s < 4 || bytes * s > 512e6)) break;
     double us = std::ceil(slabs / s) * us_slab(tiles * s);
-    if (s > 1) us += 5.0 + 2.0 * bytes * s / (bytes * s <= 100e6 ? 6.0e6 : 4.0e6);
+    us += s == 1 ? us_once : 5.0 + 2.0 * bytes * s / (bytes * s <= 100e6 ? 6.0e6 : 4.0e6);
     if (us < 0.97 * best.us) best = Choice{tile, s, us};
   }
   return best;
@@ -328,10 +328,12 @@ Choice choose_dense(const GemmArgs &g, const GemmForm &f) {
   };
   const long long mid = dense_tiles(g, f, 128), small = dense_tiles(g, f, 64);
   Choice best = f.f32 ? choose(g, 128, mid, shared(4.4, 3.97)) : choose(g, 128, mid, pairs);
-  const Choice s = choose(g, 64, small, f.f32 ? shared(1.45, 1.08) : shared(0.34, 0.25));
+  const Choice s = choose(g, 64, small, f.f32 ? shared(1.45, 1.03) : shared(0.34, 0.25));
   if (s.us < best.us) best = s;
   if (f.f32) return best;  // four fp32 tiles of 128 take what one of 256 does
-  const Choice b = choose(g, 256, dense_tiles(g, f, 256), shared(1.75, 1.75));
+  // a tile of 256 stores by itself on its CU, and odd rows take it 7 us longer (4099 x 1021 x 2047: 53, with tiles of 128 48)
+  const long long n = dense_tiles(g, f, 256);
+  const Choice b = choose(g, 256, n, shared(1.75, 1.75), g.ldo % 8 ? 7.0 * ((n + kCus - 1) / kCus) : 0);
   return best.us < b.us ? best : b;
 }
 size_t parts_bytes(long long tiles, const Choice &c) {
