@@ -24,7 +24,9 @@ typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 // (of 32 x 32), staged through registers into two LDS buffers in turn. The
 // loads of step n + 2 are issued when step n's registers have gone to LDS. fp32
 // products run on the fp32 MFMA, whose products and sums are those of fp32
-// FMAs.
+// FMAs. Measured: 4099 x 1021 x 2047 in bf16 53 us, 320 TFLOP/s, bound by the
+// waits for its loads (8192 x 1021 x 4095 157 us, 104 with rows copied and tiles
+// that go straight to LDS); in fp32 181 us, 95 TFLOP/s.
 
 constexpr int kThreads = 256, BK = 32;  // k per step
 
@@ -247,7 +249,8 @@ __global__ __launch_bounds__(kThreads) void k_join(GemmArgs g, long long ti, lon
 
 // ---------------------------------------------------------------------------
 // Rows copied to where they start on 16 bytes, zero behind their ends, so that
-// a product of odd widths can run on the tiles that load whole pieces.
+// a product of odd widths can run on the tiles that load whole pieces (12.6 MB:
+// 10.6 us, half of it a launch and its ramp).
 
 struct PackJob {
   const void *src;
@@ -402,7 +405,8 @@ hipError_t run_gemm(const GemmArgs &g, const GemmForm &f, const Choice &c, hipSt
 // With sums, or where rows are set apart, a wave takes 512 columns (eight per
 // lane) of every fourth row of a run; the waves' sums are added in LDS, the
 // runs' by k_column_sums, each in a fixed order. Either way a thread loads all
-// of a step before it stores any.
+// of a step before it stores any. Bound by memory: 32768 x 9728 of a pair 556 us,
+// 5.7 TB/s; 8192 x 4096 with sums 41 us, 4.9 TB/s, and 4.7 us to add them.
 
 // Eight elements of the step from `at` on, `left` of them there.
 template <typename D, typename T, bool GATED, bool NT>
