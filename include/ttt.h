@@ -497,13 +497,13 @@ int ttt_gated(const void *x, const void *W_gate, const void *W_up, ttt_dtype dt,
  * The products of bf16 calls take q, dg and du as bf16 (one more rounding, half
  * a step of each term; where q is dy, in bf16 and without an activation, there
  * is none); the biases' gradients sum the unrounded ones. Every sum's order is
- * fixed by the sizes and types and by whether the bf16 operands start on 16
- * bytes (the kernels for those that do are the faster ones): the same call
- * gives the same bits.
+ * fixed by the sizes and types and by whether the operands start on 16 bytes
+ * (the kernels for those that do are the faster ones): the same call gives the
+ * same bits.
  *
  * ws holds q (or dg and du) where they are made, and fp32 sums of the biases'
- * gradients and of products whose k is split; odd widths of bf16 operands are
- * copied to it too where that pays. Its size: the _ws_bytes queries.
+ * gradients and of products whose k is split; operands of odd widths are copied
+ * to it too where that pays. Its size: the _ws_bytes queries.
  */
 int ttt_linear_grad_ws_bytes(int64_t rows, int in, int out, ttt_dtype dt, ttt_dtype y_dt, int act, size_t *bytes);
 int ttt_linear_grad(const void *dy, ttt_dtype y_dt, const void *x, const void *W, ttt_dtype dt, const void *pre,

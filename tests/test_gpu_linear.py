@@ -278,6 +278,24 @@ def test_tiles_of_each_side(M, K, N, dt):
     gated_grad_case(M, K, N, dt, "gelu", 0)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("M,K,N", [(3, 5, 7), (130, 72, 1365), (700, 513, 1027)])
+def test_odd_widths_with_and_without_sums(M, K, N, dt):
+    """The bias' sums come with the elementwise pass or not at all; the other gradients are the same bits."""
+    g = torch.Generator().manual_seed(M + K + N)
+    dy, pre, u = (make((M, N), dt, g).cuda() for _ in range(3))
+    x, w, v = make((M, K), dt, g).cuda(), make((N, K), dt, g).cuda(), make((N, K), dt, g).cuda()
+    a, b = (ttt.ttt_linear_grad(dy, x, w, act="silu", pre=pre, bias=k) for k in (True, False))
+    assert b.dbias is None and torch.equal(a.dx, b.dx) and torch.equal(a.dw, b.dw)
+    a, b = (ttt.ttt_gated_grad(dy, x, w, v, pre, u, bias=k) for k in (True, False))
+    assert b.db_up is None and all(torch.equal(s, t) for s, t in zip(a[:3], b[:3]))
+    # the last column's sums, next to which q has its zeros
+    s = torch.sigmoid(pre.double())
+    want = dy.double() * u.double() * s * (1 + pre.double() * (1 - s))
+    err = (64 + 2 * (M + 3)) * U32 * want.abs().sum(0) + 64 * U32 * (dy.double() * u.double()).abs().sum(0)
+    assert_close(a.db_gate, want.sum(0).cpu(), err.cpu(), "db_gate")
+
+
 def test_rows_past_32_bits():
     """300000 rows of 8192: 2.4e9 results, the last ones 4.9 GB on. Rows are independent, so each must be what a call on
     it and its neighbours alone gives (the same kernel and tile: bit for bit), and the weight's gradient what its two
