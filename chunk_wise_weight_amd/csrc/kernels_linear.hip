@@ -286,7 +286,10 @@ long long pad8(long long n) { return (n + 7) / 8 * 8; }
 // copied first their bytes and a launch. The times are measured ones
 // (microseconds). Over 38 products of 17 to 20000 rows of all forms and both
 // types the choice took at most 10 % more than the best of both kernels' tiles
-// with 1 to 12 splits.
+// with 1 to 12 splits. The general kernel's bf16 shares are those of odd rows,
+// which it exists for (0.9 and 0.42 with rows of whole pieces): with the lower
+// ones gradients of odd widths were not copied that gain by it (20000 x 513 x
+// 1365 257 us, 163 with the copy).
 
 constexpr int kCus = 256;
 struct Choice {
@@ -319,8 +322,8 @@ auto shared(double alone, double share) {
 }
 Choice choose_general(const GemmArgs &g, const GemmForm &f) {
   const double wait = f.b_trans ? 3.5 : f.a_trans ? 2.6 : 1.8;  // bf16, a tile of 128 alone
-  const Choice big = choose(g, 128, general_tiles(g, f, 128), shared(f.f32 ? 5.1 : wait, f.f32 ? 4.4 : 0.9));
-  const Choice small = choose(g, 64, general_tiles(g, f, 64), shared(f.f32 ? 2.2 : 0.5 * wait, f.f32 ? 1.17 : 0.42));
+  const Choice big = choose(g, 128, general_tiles(g, f, 128), shared(f.f32 ? 5.1 : wait, f.f32 ? 4.4 : 1.5));
+  const Choice small = choose(g, 64, general_tiles(g, f, 64), shared(f.f32 ? 2.2 : 0.5 * wait, f.f32 ? 1.17 : 0.6));
   return small.us < big.us ? small : big;
 }
 // Here bf16 tiles of 256 run in rounds of one per CU and those of 128 in rounds of two; the others share as above.
