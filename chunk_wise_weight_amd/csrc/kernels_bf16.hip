@@ -46,6 +46,7 @@
 #include <type_traits>
 
 #include "launch.h"
+#include "lds_dma.h"
 
 namespace {
 
@@ -66,8 +67,6 @@ struct Slab {
   bf16_t a[BM * SK];
   bf16_t b[32 * WN * NBJ * SK];
 };
-
-typedef __attribute__((address_space(3))) void lds_void;
 
 // The eight 16-byte chunks of each 128-byte LDS row are XOR-swizzled; with
 // this pattern the fragment reads (32 consecutive rows, one chunk) are free of
@@ -114,33 +113,11 @@ constexpr int loads_per_slab() { return loads_a<WN, NBJ>() + 32 * WN * NBJ / (2 
 // chunk (l%8) ^ swz(row). Load n of wave w (of NW) moves rows
 // w*ROWS/NW + 8n .. +8.
 
-// LDS DMA issued as an instruction the compiler does not track (the state
-// update's loads). The compiler treats a tracked LDS DMA as a pending write to
-// LDS, and before a transposing read (ds_read_b64_tr_b16) it cannot tell that
-// the read's buffer is not the one in flight, so it waits for every DMA: the
-// ring's lookahead would be lost once per slab. Untracked, the loads are
-// ordered by the kernel's own counted waits and barriers alone (slab_wait),
-// which is how the ring is built anyway. No register outputs: the data goes
-// to LDS at M0 + 16 (4) bytes per lane. M0 is the compiler's register: the
-// block saves it in a scalar register of its own and puts it back.
-__device__ __forceinline__ void dma16_untracked(__amdgpu_buffer_rsrc_t rs, void *lds, uint32_t voff, uint32_t soff) {
-  const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
-  uint32_t keep;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
-      : "=&s"(keep)
-      : "s"(base), "v"(voff), "s"(rs), "s"(soff)
-      : "memory");
-}
-__device__ __forceinline__ void dma4_untracked(__amdgpu_buffer_rsrc_t rs, void *lds, uint32_t voff, uint32_t soff) {
-  const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
-  uint32_t keep;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dword %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
-      : "=&s"(keep)
-      : "s"(base), "v"(voff), "s"(rs), "s"(soff)
-      : "memory");
-}
+// The state update's loads are untracked (lds_dma.h): before each of its
+// transposing reads the compiler would wait for every tracked one in flight,
+// and the ring's lookahead would be lost once per slab. They are ordered by the
+// kernel's own counted waits and barriers (slab_wait), which is how the ring is
+// built anyway.
 
 // Row-major operand: element (r, k) at base[r*ld + k], base at the tile's
 // first row. Rows r >= nrows read zero: the lane offset holds the whole row

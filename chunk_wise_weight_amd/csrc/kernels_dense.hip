@@ -35,6 +35,7 @@
 // 4096 x 1024 x 2048 33 (22).
 #include <type_traits>
 
+#include "lds_dma.h"
 #include "linear_dev.h"
 
 namespace {
@@ -46,7 +47,6 @@ constexpr int EL = 16 / (int)sizeof(T);  // elements of a 16-byte chunk
 constexpr uint32_t kBufferFlags = 0x00020000u;  // raw buffer descriptor word 3 on the gfx9 family
 constexpr uint32_t kOutOfRange = 0x80000000u;   // past every descriptor's end
 
-typedef __attribute__((address_space(3))) void lds_void;
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
@@ -61,22 +61,12 @@ __device__ __forceinline__ int zsw(int k) { return ((k & 3) ^ ((k >> 3) & 1)) <<
 // transposing reads it would then wait for every load in flight before each of
 // them (1.29 -> 1.64 ms for 32768 x 9728 x 2560), so there the load is one that
 // it does not track, ordered by the kernel's counted waits and barriers alone.
-// It has no register outputs: the data goes to LDS at M0 + 16 bytes per lane.
-// M0 is the compiler's register, saved and put back; one wait state must pass
-// between its write and the load.
 template <bool TRACKED>
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, void *lds, uint32_t voff) {
-  if constexpr (TRACKED) {
+  if constexpr (TRACKED)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)lds, 16, voff, 0, 0, 0);
-    return;
-  }
-  const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
-  uint32_t keep;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
-      : "=&s"(keep)
-      : "s"(base), "v"(voff), "s"(rs)
-      : "memory");
+  else
+    dma16_untracked(rs, lds, voff);
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, int bytes) {
