@@ -47,14 +47,13 @@
 
 #include "launch.h"
 #include "lds_dma.h"
+#include "tiles.h"
 
 namespace {
 
 constexpr int BM = 256;  // tile rows along i
 constexpr int BK = 32;   // k per MFMA stage
 constexpr int SK = 64;   // k per load slab: one 128-byte line of every row
-constexpr uint32_t kBufferFlags = 0x00020000u;  // raw buffer descriptor word 3 on the gfx9 family
-constexpr uint32_t kOutOfRange = 0x80000000u;   // offset past num_records: the load returns zero
 
 template <int NBJ>
 struct Acc {
@@ -68,22 +67,8 @@ struct Slab {
   bf16_t b[32 * WN * NBJ * SK];
 };
 
-// The eight 16-byte chunks of each 128-byte LDS row are XOR-swizzled; with
-// this pattern the fragment reads (32 consecutive rows, one chunk) are free of
-// bank conflicts, also while LDS-DMA writes land (measured with rocprofv3).
-__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 // element offset of (row r, logical 16-byte chunk c) inside an N x 64 bf16 LDS tile
 __device__ __forceinline__ int lds_off(int r, int c) { return r * SK + ((c ^ swz(r)) << 3); }
-
-// Chunk swizzle of the kAZ tile (below): k row r holds logical chunk c at
-// c ^ zsw(r). A transposing read of one 16-lane group g covers 4 consecutive
-// k rows r0 + 8g .. +3 and one pair of adjacent chunks in each; the LDS
-// serves 32 lanes (two groups, 8 rows apart) at a time. zsw(r) =
-// 2*((r%4) ^ (r/8 % 2)) gives the 4 rows of one parity (rows of a 128-byte
-// stride alternate between the two halves of the 64 banks) of the two groups
-// the four disjoint chunk pairs of that half, so the read is free of bank
-// conflicts.
-__device__ __forceinline__ int zsw(int r) { return ((r & 3) ^ ((r >> 3) & 1)) << 1; }
 
 template <int NBJ>
 __device__ __forceinline__ void acc_zero(Acc<NBJ> &acc) {
@@ -340,9 +325,6 @@ struct SlabLoads {
   }
 };
 
-// s_waitcnt immediate (gfx9): vmcnt(n), expcnt unchanged, lgkmcnt(0).
-constexpr unsigned wait_imm(int n) { return (unsigned)((n & 15) | 0x70 | (((n >> 4) & 3) << 14)); }
-
 // Wait until at most `later` slabs of this wave's loads (LPS loads per slab)
 // are still in flight and its own LDS reads are done, then meet every wave at
 // the barrier: their loads of the awaited slab have landed too, and every
@@ -382,31 +364,13 @@ struct Frag {
 //             reads.
 constexpr int kARows = 0, kAPlanes = 1, kAZ = 2;
 
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-
-// A fragment of a kAZ tile: rows 16gi + l%16 of a 64-row block (lane l), k
-// 8(l/16) .. +7 of the stage, from two transposing reads (ds_read_b64_tr_b16)
-// of 4 k rows each. In each 16-lane group g, lane t addresses k row
-// 8g + t/4 (+4 for the second read), columns 4(t%4) .. +3 of the fragment's
-// 16 (one 8-byte piece), and receives column t of the 4 rows. This is lane
-// l's element offset for gi = 0; the chunk pair of fragment gi is gi
-// further on, which in the swizzled row is `^ (gi << 4)` (zsw is even, so
-// the XOR leaves the 8-byte half within the chunk alone).
-__device__ __forceinline__ int az_lane_off(int lane) {
-  const int t = lane & 15, g = lane >> 4;
-  const int krow = 8 * g + (t >> 2);
-  const int chunk = ((t & 3) >> 1) ^ zsw(krow);
-  return krow * 64 + chunk * 8 + 4 * (t & 1);
-}
-
 // The A fragments of rows 64hf .. 64hf+63 of the wave's 128 (hf = 0, 1) for
 // stage half h (0 or 1) of an LDS slab.
 template <int WN, int NBJ, int AMODE = kARows>
 __device__ __forceinline__ void read_a(bf16x8 (&a)[4], const Slab<WN, NBJ> &st, int h, int hf, int wm, int lane) {
   const int c = 4 * h + (lane >> 4);
   if constexpr (AMODE == kAZ) {
-    const int lo = az_lane_off(lane);
+    const int lo = z_lane_off(lane);
 #pragma unroll
     for (int gi = 0; gi < 4; ++gi) {
       const bf16_t *pa = st.a + (wm * 2 + hf) * 4096 + h * 2048 + (lo ^ (gi << 4));
@@ -439,9 +403,6 @@ __device__ __forceinline__ void frag_mma(Acc<NBJ> &acc, const bf16x8 &a, const b
   for (int gj = 0; gj < 2 * NBJ; ++gj)
     acc.v[GI][gj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[gj], acc.v[GI][gj], 0, 0, 0);
 }
-
-// Keep the compiler from moving instructions across this point.
-__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
 
 // Issue point P (0..6) of a stage that refills a slab: loads [P*LPS/7, (P+1)*LPS/7).
 template <int LPS, int P, class SL, class S>
@@ -568,18 +529,6 @@ constexpr int kSmemOut = cmax(kRingBytes, 256 * LY_P * 2);
 // wave coordinates: wm selects the 128-row half along i, wn the column slice along j
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// Workgroups of a launch are handed to the 8 XCDs round-robin (workgroup n to
-// XCD n % 8), and each XCD has its own L2. Renumber them so that XCD k works
-// through one contiguous range of the logical tile order: the workgroups
-// resident on an XCD at one time are then neighbours in that order and share
-// operand tiles in its L2. A bijection on [0, N).
-constexpr int kXcds = 8;
-__device__ __forceinline__ int xcd_tile(int n, int N) {
-  const int xcd = n % kXcds, m = n / kXcds;
-  const int q = N / kXcds, r = N % kXcds;
-  return xcd * q + (xcd < r ? xcd : r) + m;
-}
-
 // The same within each round of R workgroups (R: the workgroups resident at
 // once, one per CU, in launch order): round r's workgroups take logical tiles
 // r*R .. r*R + R - 1, XCD k a contiguous range of them. Where the logical order
@@ -598,18 +547,6 @@ __device__ __forceinline__ int xcd_tile_rounds(int n, int N, int R) {
 // R for the kernels of one workgroup per CU: the compute units, rounded down
 // to a multiple of the XCD count (at least one per XCD).
 static int launch_round(int cus) { return cus >= kXcds ? cus / kXcds * kXcds : kXcds; }
-
-// Logical tile t of an nx x ny grid, in bands of H rows along y; inside a band
-// y runs fastest, so H consecutive tiles share one x and nx*H consecutive tiles
-// cover the band. The last band may be shorter.
-__device__ __forceinline__ void band_tile(int t, int nx, int ny, int H, int &x, int &y) {
-  const int full = ny / H, per = H * nx;
-  const int band = t / per;
-  const int h = band < full ? H : ny - full * H;
-  const int r = t - band * per;
-  x = r / h;
-  y = band * H + r % h;
-}
 
 // Stages kt .. kt_end-1 of an nk-stage K loop without hooks (kt even), with
 // each stage's parity and refill fixed at compile time: the stages of slabs

@@ -37,6 +37,7 @@
 
 #include "lds_dma.h"
 #include "linear_dev.h"
+#include "tiles.h"
 
 namespace {
 
@@ -44,19 +45,9 @@ template <typename T>
 constexpr int SK = 128 / (int)sizeof(T);  // k per slab: one line
 template <typename T>
 constexpr int EL = 16 / (int)sizeof(T);  // elements of a 16-byte chunk
-constexpr uint32_t kBufferFlags = 0x00020000u;  // raw buffer descriptor word 3 on the gfx9 family
-constexpr uint32_t kOutOfRange = 0x80000000u;   // past every descriptor's end
 
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-
-__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 template <typename T>
 __device__ __forceinline__ int lds_off(int r, int c) { return r * SK<T> + (c ^ swz(r)) * EL<T>; }
-// A transposing read covers rows r0 + 8g .. +3 of k (g: the group of 16 lanes) and a pair of adjacent chunks; this
-// gives the rows that are served at a time disjoint banks.
-__device__ __forceinline__ int zsw(int k) { return ((k & 3) ^ ((k >> 3) & 1)) << 1; }
-
 // 16 bytes per lane from memory to LDS. TRACKED: as the compiler's own. With
 // transposing reads it would then wait for every load in flight before each of
 // them (1.29 -> 1.64 ms for 32768 x 9728 x 2560), so there the load is one that
@@ -164,19 +155,11 @@ using Small = Shape<4, 4, 2, 2, 2, 2>;
 template <typename T>
 using Tiny = Shape<2, 2, 2, 2, sizeof(T) == 2 ? 3 : 2, sizeof(T) == 2 ? 3 : 4>;
 
-// s_waitcnt immediate (gfx9): vmcnt(n), expcnt unchanged, lgkmcnt(0)
-constexpr unsigned wait_imm(int n) { return (unsigned)((n & 15) | 0x70 | (((n >> 4) & 3) << 14)); }
 // Every wave's loads but the last LATER have landed, and its reads of LDS are done.
 template <int LATER>
 __device__ __forceinline__ void meet() {
   __builtin_amdgcn_s_waitcnt(wait_imm(LATER));
   asm volatile("s_barrier" ::: "memory");
-}
-__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
-
-__device__ __forceinline__ int z_lane_off(int lane) {
-  const int t = lane & 15, k = 8 * (lane >> 4) + (t >> 2);
-  return k * 64 + (((t & 3) >> 1) ^ zsw(k)) * 8 + 4 * (t & 1);
 }
 // 16 bytes per lane of 16 rows: eight bf16 k, or four fp32 ones of the sixteen that half a slab has.
 template <typename T>
@@ -231,22 +214,9 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[N], const f32x4 &a, const 
     for (int y = 0; y < N; ++y) acc[y] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[y][s], acc[y], 0, 0, 0);
 }
 
-// Workgroups go to the 8 XCDs in turn, and each has an L2 of its own: XCD k
-// takes one contiguous range of the tiles' order (a bijection on [0, N)).
-constexpr int kXcds = 8;
-__device__ __forceinline__ int xcd_tile(int n, int N) {
-  const int xcd = n % kXcds, m = n / kXcds, q = N / kXcds, r = N % kXcds;
-  return xcd * q + (xcd < r ? xcd : r) + m;
-}
 // Bands of four: the 32 tiles of an XCD at a time are 4 x 8. (32768 x 9728 x 2560: 1263 us; 1295 in bands of 8, 1355 of
 // 16, and 2 and 3 cost products of wide outputs 1 to 2 %.)
 constexpr int kBand = 4;
-// Tile t of nx by ny in bands of H along y, y fastest inside a band: neighbours share operands.
-__device__ __forceinline__ void band_tile(int t, int nx, int ny, int H, int &x, int &y) {
-  const int full = ny / H, per = H * nx, band = t / per, h = band < full ? H : ny - full * H, r = t - band * per;
-  x = r / h;
-  y = band * H + r % h;
-}
 
 template <class S, typename T, typename O, bool AT, bool BT, bool PAIR>
 __global__ __launch_bounds__(S::THREADS, S::PER_CU * S::NW / 4) void k_dense(GemmArgs g, int nti, int ntj, Parts parts) {

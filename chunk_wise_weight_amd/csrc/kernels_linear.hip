@@ -13,11 +13,9 @@
 
 #include "grid.h"
 #include "linear_dev.h"
+#include "tiles.h"
 
 namespace {
-
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
 // ---------------------------------------------------------------------------
 // Any size, any alignment: tiles of 128 x 128 (four waves of 64 x 64) or 64 x 64
