@@ -509,7 +509,7 @@ int ttt_adamw(void *const *w, const int32_t *w_dt, const void *const *g, const i
     AdamArgs a{};
     a.beta1 = beta1;
     a.beta2 = beta2;
-    a.eps = (float)eps;
+    a.eps = eps > 0 ? std::max((float)eps, 0x1p-149f) : 0.f;  // an eps above 0 stays so: 0 / eps is 0
     a.lr = lr;
     a.decay = weight_decay;
     a.tau = tau;

@@ -278,13 +278,14 @@ __device__ __forceinline__ AdamStep step_of(const AdamArgs &a) {
   return s;
 }
 
-// sqrt(v) by the hardware's root (1 ulp), with `small` also of the denormals, which it may take as 0: their roots are
-// below 2^-63, which is nothing beside an eps of 10^-10.
+// sqrt(v) by the hardware's root (1 ulp), with `small` also of the denormals, which it may take as 0: their roots times
+// root2 are below 2^-63 root2, half a step of an eps from 2 10^-12 root2 on.
 __device__ __forceinline__ float root(float v, bool small) {
   if (!small) return __builtin_amdgcn_sqrtf(v);
   const bool tiny = v < 0x1p-96f;
   return __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p-32f : 1.f);
 }
+__device__ __forceinline__ bool small_eps(float eps, float root2) { return eps < 2e-12f * root2; }
 
 // A chunk's tensor, its first element and its elements. One chunk per workgroup.
 struct Place {
@@ -322,8 +323,15 @@ __device__ __forceinline__ Rates rates_of(const AdamArgs &a) {
   }
   return r;
 }
+// With `small` the denominator may be a denormal, which the hardware's reciprocal may take as 0 (and 0 / eps would be 0
+// times infinity); below 2^-96 it is scaled, and the moment alike before lr1 makes it smaller.
 __device__ __forceinline__ float moved(float w, float m, float v, const AdamStep &s, float eps, bool small) {
-  const float q = s.lr1 * m * __builtin_amdgcn_rcpf(fmaf(root(v, small), s.root2, eps));
+  const float d = fmaf(root(v, small), s.root2, eps);
+  float q;
+  if (small && d < 0x1p-96f)
+    q = s.lr1 * (m * 0x1p96f * __builtin_amdgcn_rcpf(d * 0x1p96f));
+  else
+    q = s.lr1 * m * __builtin_amdgcn_rcpf(d);
   return fmaf(-s.shrink, w, w) - q;
 }
 
@@ -349,7 +357,7 @@ __device__ __forceinline__ void step_chunk(const AdamTable &t, const AdamArgs &a
   const AdamStep s = step_of(a);
   const Rates r = rates_of(a);
   const float b1 = (float)r.b1, b2 = (float)r.b2, o1 = (float)(1.0 - r.b1), o2 = (float)(1.0 - r.b2);
-  const bool small = a.eps < 1e-10f;
+  const bool small = small_eps(a.eps, s.root2);
 #pragma unroll
   for (int k = 0; k < kWaveSteps; ++k) {
     const long long at = at0 + k * SKIP;
@@ -410,7 +418,7 @@ __device__ __forceinline__ void step_chunk8(const AdamTable &t, const AdamArgs &
   const Rates r = rates_of(a);
   // fp64 holds the factor's square with the betas
   const double b1 = r.b1, b2 = r.b2, o1 = (1.0 - b1) * r.factor, o2 = (1.0 - b2) * r.factor * r.factor;
-  const bool small = a.eps < 1e-10f;
+  const bool small = small_eps(a.eps, s.root2);
   const uint32_t key = adam_mix(s.key + kGolden * (uint32_t)(t.tensor0 + i + 1));
 #pragma unroll
   for (int k = 0; k < kHalfSteps; ++k) {
