@@ -335,6 +335,18 @@ __device__ __forceinline__ float moved(float w, float m, float v, const AdamStep
   return fmaf(-s.shrink, w, w) - q;
 }
 
+// A beta in two fp32 parts, so that it and `rest` = 1 - beta add up to one: rounded to one part, a beta2 of 0.9999 is off
+// by U / 4 of every moment it meets and by 10^-4 of what it leaves to the gradient (U = 2^-24).
+struct Decay {
+  float hi, lo, rest;
+  __device__ __forceinline__ explicit Decay(double b) : hi((float)b), lo((float)(b - (double)hi)), rest((float)(1.0 - b)) {}
+  // beta x, rounded once; an infinity's small part must not meet its large one as another infinity, or as 0 times it
+  __device__ __forceinline__ float of(float x) const {
+    constexpr float kMost = 3.4028234663852886e38f;
+    return fmaf(hi, x, lo * __builtin_amdgcn_fmed3f(x, -kMost, kMost));
+  }
+};
+
 // fp32 moments: a wave takes four blocks of a chunk, a lane four elements of each. Everything is loaded before anything
 // is stored. FULL: every element of the chunk is there.
 template <bool NT, bool FULL>
@@ -356,7 +368,7 @@ __device__ __forceinline__ void step_chunk(const AdamTable &t, const AdamArgs &a
   }
   const AdamStep s = step_of(a);
   const Rates r = rates_of(a);
-  const float b1 = (float)r.b1, b2 = (float)r.b2, o1 = (float)(1.0 - r.b1), o2 = (float)(1.0 - r.b2);
+  const Decay b1(r.b1), b2(r.b2);
   const bool small = small_eps(a.eps, s.root2);
 #pragma unroll
   for (int k = 0; k < kWaveSteps; ++k) {
@@ -371,8 +383,8 @@ __device__ __forceinline__ void step_chunk(const AdamTable &t, const AdamArgs &a
     for (int e = 0; e < 4; ++e) {
       // the factor to the gradient first: its square may leave fp32
       const float d = r.clipped ? (float)((double)x[e] * r.factor) : x[e];
-      mk[e] = fmaf(b1, mk[e], o1 * d);
-      vk[e] = fmaf(b2, vk[e], o2 * d * d);
+      mk[e] = fmaf(b1.rest, d, b1.of(mk[e]));
+      vk[e] = fmaf(b2.rest * d, d, b2.of(vk[e]));
       wk[e] = moved(wk[e], mk[e], vk[e], s, a.eps, small);
     }
     put<NT>(t.m[i], 1, at, left, mk);
