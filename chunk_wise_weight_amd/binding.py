@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
+import warnings
 from array import array
 from functools import lru_cache
 from typing import Dict, List, NamedTuple, Optional, Tuple
@@ -709,18 +711,50 @@ def ttt_embed_grad(dx: torch.Tensor, ids: torch.Tensor, vocab: int, scale: float
     return dE
 
 
+_KINDS = {torch.float32: TTT_F32, torch.bfloat16: TTT_BF16, torch.uint8: 2, torch.int16: 3}
+
+
+def _read_python(ts: list, name: str, device: int):
+    """What the native reader (csrc/tensor_lists.cpp) gives, for where it is not there: about a microsecond a tensor, an
+    eighth of that in native code."""
+    at, numel, kinds, seen, faults = array("Q"), array("q"), array("i"), 0, 0
+    for t in ts:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be tensors, got {type(t).__name__}")
+        fault = (1 if t.layout != torch.strided or not t.is_contiguous() else 2 if not t.is_cuda else
+                 4 if t.get_device() != device else 0)
+        kind = _KINDS.get(t.dtype, 4)
+        at.append(0 if fault else t.data_ptr())
+        numel.append(t.numel())
+        kinds.append(kind)
+        seen |= 1 << kind
+        faults |= fault
+    return at.tobytes(), numel.tobytes(), kinds.tobytes(), seen, faults
+
+
+def built_for() -> str:
+    """The torch and Python that a native reader must have been built for."""
+    return f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
 _read = None
 
 
 def _reader():
-    """The native reader of tensor lists (once)."""
+    """The reader of tensor lists (chosen once): native, or in Python where no native one was built for this torch and
+    Python."""
     global _read
     if _read is None:
         try:
-            from ._tensor_lists import read
+            from . import _tensor_lists
+            other = getattr(_tensor_lists, "built_for", "another torch")
+            if other != built_for():
+                raise ImportError(f"it was built for {other}, this is {built_for()}")
+            _read = _tensor_lists.read
         except ImportError as e:
-            raise RuntimeError("_tensor_lists.so is not built; run `python -m chunk_wise_weight_amd.build`") from e
-        _read = read
+            warnings.warn(f"lists of tensors are read in Python, about a microsecond a tensor: no _tensor_lists.so ({e}); "
+                          "run `python -m chunk_wise_weight_amd.build`", RuntimeWarning, stacklevel=2)
+            _read = _read_python
     return _read
 
 

@@ -1,5 +1,5 @@
 """Build libttt.so (the HIP library behind the C ABI) for gfx950 with hipcc, and the binding's reader of tensor lists
-(host code, with g++).
+(host code, with g++; where there is none, the binding reads them in Python).
 
 Usage: python -m chunk_wise_weight_amd.build [--verbose]
 Both are written next to this file, in-tree.
@@ -11,6 +11,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -47,21 +48,33 @@ def _hipcc() -> str:
     raise RuntimeError("hipcc not found; the ROCm toolchain is required to build libttt.so")
 
 
-def _build_lists(verbose: bool) -> None:
+def _build_lists(verbose: bool) -> bool:
+    """The native list reader. Where it cannot be built (no host compiler, no Python headers) the binding reads lists in
+    Python; what an earlier build left is then removed."""
     import torch
+
+    from .binding import built_for
 
     at = os.path.dirname(torch.__file__)
     inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{i}" for i in inc],
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", LISTS_SRC, "-o", LISTS + ".tmp",
-           f"-L{os.path.join(at, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DBUILT_FOR="{built_for()}"', LISTS_SRC,
+           "-o", LISTS + ".tmp", f"-L{os.path.join(at, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on {LISTS_SRC}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.returncode != 0 and f"{r.stdout}\n{r.stderr}"
+    except OSError as e:
+        failed = str(e)
+    if failed:
+        if os.path.exists(LISTS):
+            os.remove(LISTS)
+        warnings.warn(f"{cmd[0]} failed on {LISTS_SRC}; lists of tensors will be read in Python:\n{failed}", RuntimeWarning)
+        return False
     os.replace(LISTS + ".tmp", LISTS)
+    return True
 
 
 def build(verbose: bool = False) -> str:

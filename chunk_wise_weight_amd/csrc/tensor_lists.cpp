@@ -79,4 +79,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_lists", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensor_lists() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__tensor_lists() {
+  PyObject *m = PyModule_Create(&module);
+  // the torch and Python whose layout of a tensor this was built for: the binding compares them with its own
+  if (m && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
