@@ -20,6 +20,7 @@ from .binding import (  # noqa: F401
     ttt_adamw,
     ttt_adamw_values,
     ttt_clip_grads,
+    ttt_dense_plan,
     ttt_destroy,
     ttt_embed,
     ttt_embed_grad,

@@ -29,7 +29,7 @@ EXPORTS = ("ttt_init", "ttt_forward_chunked", "ttt_forward_docs", "ttt_reset", "
            "ttt_norm_pre", "ttt_norm_post", "ttt_norm_ws_bytes", "ttt_norm_pre_grad", "ttt_norm_post_grad",
            "ttt_embed", "ttt_embed_grad_ws_bytes", "ttt_embed_grad", "ttt_grad_ws_bytes", "ttt_grad_norm",
            "ttt_clip_grads", "ttt_linear_ws_bytes", "ttt_linear", "ttt_gated_ws_bytes", "ttt_gated",
-           "ttt_linear_grad_ws_bytes", "ttt_linear_grad", "ttt_gated_grad_ws_bytes", "ttt_gated_grad", "ttt_adamw",
+           "ttt_linear_grad_ws_bytes", "ttt_linear_grad", "ttt_gated_grad_ws_bytes", "ttt_gated_grad", "ttt_dense_plan", "ttt_adamw",
            "ttt_adamw_values")
 
 _lib = None
@@ -106,6 +106,8 @@ def lib() -> ctypes.CDLL:
     L.ttt_gated.argtypes = [vp, vp, vp, i32, vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, sz, vp]
     L.ttt_linear_grad.argtypes = [vp, i32, vp, vp, i32, vp, i32, f32, i64, i32, i32, vp, vp, vp, i32, vp, sz, vp]
     L.ttt_gated_grad.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+    L.ttt_dense_plan.argtypes = [i32, i64, i32, i32, i32, i32, ip, ip, ip, ip]
+    L.ttt_dense_plan.restype = i32
     L.ttt_adamw.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i64, vp, f64, vp, f64, f64, f64, f64, vp,
                             f64, ctypes.c_uint32, vp]
     L.ttt_adamw_values.argtypes = [vp, vp, i32, vp, vp, i32, vp]
@@ -1003,6 +1005,29 @@ def ttt_gated_grad(dz: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up
     _check(lib().ttt_gated_grad(pdz, px, pg, pu, _DT[dt], pkg, pku, kind, rows, n, f, pdx, pdg, pdu, pbg, pbu,
                                 1 if accumulate else 0, ws.data_ptr(), nws, c.on()), "ttt_gated_grad")
     return GatedGrads(dx, dw_gate, dw_up, db_gate, db_up)
+
+
+_PRODUCTS = ("linear", "gated", "linear_dx", "linear_dw", "gated_dx", "gated_dw")  # TTT_PRODUCT_* in include/ttt.h
+_KERNELS = ("few", "direct", "general")  # TTT_KERNEL_*
+
+
+def ttt_dense_plan(product: str, rows: int, n_in: int, n_out: int, dtype: torch.dtype, q_made: bool = False) -> Dict:
+    """How a product of ttt_linear, ttt_gated or their gradients runs on arrays that start on 16 bytes, as a dict of
+    kernel ("few", "direct" or "general"), tile, splits and copies; host-only, works without a GPU. product: "linear",
+    "gated", "linear_dx", "linear_dw", "gated_dx" or "gated_dw". q_made: ttt_linear_grad has an activation, or dy another
+    dtype than x."""
+    if product not in _PRODUCTS:
+        raise ValueError(f"product must be one of {list(_PRODUCTS)}, got {product!r}")
+    if dtype not in _DT:
+        raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+    for n, name in ((n_in, "n_in"), (n_out, "n_out")):
+        if n >= _INT:
+            raise _too_large(n, name)
+    got = [ctypes.c_int() for _ in range(4)]
+    _check(lib().ttt_dense_plan(_PRODUCTS.index(product), rows, n_in, n_out, _DT[dtype],
+                                1 if q_made else 0, *map(ctypes.byref, got)), "ttt_dense_plan")
+    kernel, tile, splits, copies = (v.value for v in got)
+    return {"kernel": _KERNELS[kernel], "tile": tile, "splits": splits, "copies": copies}
 
 
 _F32_ONLY, _BF16_ONLY = (1 << TTT_F32, "torch.float32"), (1 << TTT_BF16, "torch.bfloat16")

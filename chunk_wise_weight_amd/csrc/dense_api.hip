@@ -96,10 +96,11 @@ struct GradScratch {
   int ldq;
   size_t bytes() const { return q + part + gemm; }
 };
+int made_ld(int out) { return (out + 7) / 8 * 8; }
 // q: q (or dg and du) is made, not dy itself
 GradScratch grad_scratch(int64_t rows, int in, int out, ttt_dtype dt, int count, bool q) {
   GradScratch s;
-  s.ldq = q ? (out + 7) / 8 * 8 : out;
+  s.ldq = q ? made_ld(out) : out;
   s.q = q ? padded((size_t)rows * s.ldq * size_of(dt)) * count : 0;
   s.part = padded(act_grad_ws_bytes(rows, out, count == 2));
   s.gemm = padded(std::max(gemm_ws_bytes(sizes_dx(rows, in, out, count, s.ldq), form_dx(dt)),
@@ -459,6 +460,30 @@ int ttt_gated_grad(const void *dz, const void *x, const void *W_gate, const void
   if (dx && rows > 0) rc = run_dx(kWhere, q, sc.ldq, W, 2, dt, 1.f, rows, in, f, dx, split_ws, s);
   if (dW_gate && !rc) rc = run_dw(kWhere, q, sc.ldq, x, 2, dt, 1.f, rows, in, f, dW, accumulate, split_ws, s);
   return rc;
+}
+
+int ttt_dense_plan(int product, int64_t rows, int in, int out, ttt_dtype dt, int q_made, int *kernel, int *tile,
+                   int *splits, int *copies) {
+  static const char *kWhere = "ttt_dense_plan";
+  const int rc = check_dense(kWhere, dt, rows, in, out);
+  if (rc) return rc;
+  const bool gated = product == TTT_PRODUCT_GATED_DX || product == TTT_PRODUCT_GATED_DW;
+  const int ldq = gated || q_made ? made_ld(out) : out;
+  GemmPlan p{};
+  switch (product) {
+    case TTT_PRODUCT_LINEAR: p = gemm_plan(sizes_y(rows, in, out), form_y(dt, false, dt)); break;
+    case TTT_PRODUCT_GATED: p = gemm_plan(sizes_y(rows, in, out), form_y(dt, true, dt)); break;
+    case TTT_PRODUCT_LINEAR_DX:
+    case TTT_PRODUCT_GATED_DX: p = gemm_plan(sizes_dx(rows, in, out, gated ? 2 : 1, ldq), form_dx(dt)); break;
+    case TTT_PRODUCT_LINEAR_DW:
+    case TTT_PRODUCT_GATED_DW: p = gemm_plan(sizes_dw(rows, in, out, gated ? 2 : 1, ldq), form_dw(dt)); break;
+    default: return ttt_fail(TTT_E_ARG, "%s: unknown product %d", kWhere, product);
+  }
+  if (kernel) *kernel = p.kernel;
+  if (tile) *tile = p.tile;
+  if (splits) *splits = p.splits;
+  if (copies) *copies = p.copies;
+  return TTT_OK;
 }
 
 int ttt_adamw(void *const *w, const int32_t *w_dt, const void *const *g, const int32_t *g_dt, void *const *m,

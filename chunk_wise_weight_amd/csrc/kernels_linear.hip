@@ -618,6 +618,13 @@ size_t gemm_ws_bytes(const GemmArgs &g, const GemmForm &f) {
   return std::max(parts_bytes(general_tiles(g, f, c.tile), c), p.copies + p.parts);
 }
 
+GemmPlan gemm_plan(const GemmArgs &g, const GemmForm &f) {
+  if (few_sizes(g, f)) return GemmPlan{TTT_KERNEL_FEW, 0, 1, 0};
+  const Plan p = plan_of(g, f);
+  const int copies = p.dense ? (p.pack_a ? p.count_a : 0) + (p.pack_b ? p.count_b : 0) : 0;
+  return GemmPlan{p.dense ? TTT_KERNEL_DIRECT : TTT_KERNEL_GENERAL, p.choice.tile, p.choice.splits, copies};
+}
+
 hipError_t launch_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
   if (few_sizes(g, f)) return launch_few(g, f, s);
   const Plan p = plan_of(g, f);

@@ -36,6 +36,12 @@ struct GemmForm {
 
 // Workspace of a product by its sizes (ni, nj, nk, segments, batch) and form alone, wherever its arrays lie.
 size_t gemm_ws_bytes(const GemmArgs &g, const GemmForm &f);
+// How it runs where its arrays start on 16 bytes: on a kernel of TTT_KERNEL_*, tiles of `tile` (0: none), k in `splits`
+// parts, with `copies` operands copied first.
+struct GemmPlan {
+  int kernel, tile, splits, copies;
+};
+GemmPlan gemm_plan(const GemmArgs &g, const GemmForm &f);
 hipError_t launch_gemm(const GemmArgs &g, const GemmForm &f, hipStream_t s);
 
 // Sums of a part of k, fp32, for k_join: [splits][batch][tiles][tj][ti], tiles in the order j, i, of ti rows of A (with

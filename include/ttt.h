@@ -515,6 +515,31 @@ int ttt_gated_grad(const void *dz, const void *x, const void *W_gate, const void
                    float *db_gate, float *db_up, int accumulate, void *ws, size_t ws_bytes, void *hip_stream);
 
 /*
+ * ttt_dense_plan — host-only query of how one product of the calls above runs
+ * (no device work; usable without a GPU), for arrays that start on 16 bytes:
+ *   q_made : for the two products of ttt_linear_grad: q is made, i.e. there is
+ *            an activation or dy is not of type dt (0: dy itself serves).
+ *   *kernel: TTT_KERNEL_FEW for up to 16 rows forward, TTT_KERNEL_DIRECT with
+ *            tiles from memory straight to LDS, TTT_KERNEL_GENERAL through
+ *            registers;  *tile: the tiles' side (0 with TTT_KERNEL_FEW);
+ *   *splits: parts of k that are summed apart and joined by a second launch;
+ *   *copies: matrices copied to rows of whole 16-byte pieces first.
+ * Any output pointer may be NULL. Which sizes run how may change from one
+ * version of the library to the next.
+ */
+enum {
+  TTT_PRODUCT_LINEAR = 0,     /* ttt_linear: x W^T */
+  TTT_PRODUCT_GATED = 1,      /* ttt_gated: x W_gate^T and x W_up^T */
+  TTT_PRODUCT_LINEAR_DX = 2,  /* ttt_linear_grad: q W */
+  TTT_PRODUCT_LINEAR_DW = 3,  /* q^T x */
+  TTT_PRODUCT_GATED_DX = 4,   /* ttt_gated_grad: dg W_gate + du W_up */
+  TTT_PRODUCT_GATED_DW = 5    /* dg^T x and du^T x */
+};
+enum { TTT_KERNEL_FEW = 0, TTT_KERNEL_DIRECT = 1, TTT_KERNEL_GENERAL = 2 };
+int ttt_dense_plan(int product, int64_t rows, int in, int out, ttt_dtype dt, int q_made, int *kernel, int *tile,
+                   int *splits, int *copies);
+
+/*
  * ttt_adamw — one AdamW step over many tensors:
  *
  *   g' = g * min(1, tau / N)                    (norm not NULL: N = *norm)
