@@ -956,7 +956,8 @@ def ttt_linear_grad(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: Opt
     """Gradients of ttt_linear: with q = scale * dy * act'(pre), dx = q w, dw = q^T x and, with bias, dbias = sum q.
 
     dy [...][out] in the dtype y had; pre as ttt_linear kept it (needed with an activation). dx and dw have x's dtype,
-    dbias is float32. With accumulate, dw and dbias are added to the tensors given for them."""
+    dbias is float32. With a bfloat16 x the products take q rounded to bfloat16, also from a float32 dy; with float32 x
+    and w nothing is rounded to fewer bits. With accumulate, dw and dbias are added to the tensors given for them."""
     rows, n = _rows(x, "x")
     out = _weight_shape(w, "w", n)
     c = _Call(x.device, stream)
@@ -985,7 +986,8 @@ def ttt_gated_grad(dz: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up
     """Gradients of ttt_gated: with dg = dz * u * act'(g) and du = dz * act(g), dx = dg w_gate + du w_up,
     dw_gate = dg^T x, dw_up = du^T x and, with bias, db_gate = sum dg, db_up = sum du.
 
-    g, u as ttt_gated kept them. dx and the weights' gradients have x's dtype, the biases' are float32. With accumulate
+    g, u as ttt_gated kept them. dx and the weights' gradients have x's dtype, the biases' are float32; the products take
+    dg and du rounded to x's dtype. With accumulate
     the weights' and biases' gradients are added to the tensors given for them."""
     rows, n = _rows(x, "x")
     f = _weight_shape(w_gate, "w_gate", n)
