@@ -283,11 +283,13 @@ long long pad8(long long n) { return (n + 7) / 8 * 8; }
 // the last-level cache up to 100 MB, and the second launch; for rows that are
 // copied first their bytes and a launch. The times are measured ones
 // (microseconds). Over 38 products of 17 to 20000 rows of all forms and both
-// types the choice took at most 10 % more than the best of both kernels' tiles
-// with 1 to 12 splits. The general kernel's bf16 shares are those of odd rows,
-// which it exists for (0.9 and 0.42 with rows of whole pieces): with the lower
-// ones gradients of odd widths were not copied that gain by it (20000 x 513 x
-// 1365 257 us, 163 with the copy).
+// types the choice took at most 7 % more than the best of both kernels' tiles
+// with 1 to 12 splits. The general kernel's bf16 shares are those of odd rows:
+// with lower ones (0.9 and 0.42) gradients of odd widths were not copied that
+// gain by it (20000 x 513 x 1365 257 us, 163 with the copy). They serve rows of
+// whole pieces alike, which come here where an array does not start on 16
+// bytes: over 16 of those it took at most 9 % more than the best (with the lower
+// ones up to 30: dx of 8192 x 1024 x 4096 181 us, 139).
 
 constexpr int kCus = 256;
 struct Choice {
@@ -335,9 +337,11 @@ Choice choose_dense(const GemmArgs &g, const GemmForm &f) {
   const Choice s = choose(g, 64, small, f.f32 ? shared(1.45, 1.03) : shared(0.34, 0.25));
   if (s.us < best.us) best = s;
   if (f.f32) return best;  // four fp32 tiles of 128 take what one of 256 does
-  // a tile of 256 stores by itself on its CU, and odd rows take it 7 us longer (4099 x 1021 x 2047: 53, with tiles of 128 48)
+  // a tile of 256 stores by itself on its CU, and odd rows of results take it some 4 us longer. Of nine products, with and
+  // without GELU, bf16 results then take at most 3 % more than in the best tile (4099 x 1021 x 2047: tiles of 256 44 us, of
+  // 128 46), fp32 ones, whose stores fit no such number, up to 17 % (45 and 55, but 8192 x 1024 x 4095: 115 and 101)
   const long long n = dense_tiles(g, f, 256);
-  const Choice b = choose(g, 256, n, shared(1.75, 1.75), g.ldo % 8 ? 7.0 * ((n + kCus - 1) / kCus) : 0);
+  const Choice b = choose(g, 256, n, shared(1.75, 1.75), g.ldo % 8 ? 4.0 * ((n + kCus - 1) / kCus) : 0);
   return best.us < b.us ? best : b;
 }
 size_t parts_bytes(long long tiles, const Choice &c) {
