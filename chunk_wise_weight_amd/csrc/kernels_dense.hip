@@ -397,6 +397,7 @@ hipError_t run(const GemmArgs &g, const GemmForm &f, int splits, hipStream_t s) 
   const int wide = PAIR ? S::TI / 2 : S::TI;
   const long long ti = (g.ni + wide - 1) / wide, tj = (g.nj + S::TJ - 1) / S::TJ;
   if (ti * tj == 0) return hipSuccess;
+  if (ti * tj * g.batch * splits * S::THREADS >= 1LL << 32) return hipErrorInvalidConfiguration;
   const Parts parts{(float *)g.ws, splits, S::TI, S::TJ, 8 * S::FI};
   hipLaunchKernelGGL((k_dense<S, T, O, AT, BT, PAIR>), dim3((unsigned)(ti * tj * g.batch * splits)), dim3(S::THREADS), 0,
                      s, g, (int)ti, (int)tj, parts);
@@ -422,7 +423,8 @@ long long dense_tiles(const GemmArgs &g, const GemmForm &f, int tile) {
   return (g.ni + wide - 1) / wide * ((g.nj + tile - 1) / tile) * g.batch;
 }
 
-// Rows are whole 16-byte pieces; the tiles fit a launch (its threads count in 32 bits) with up to 32 splits, and k an int.
+// Rows are whole 16-byte pieces, k fits an int, and the tiles a launch, whose threads count in 32 bits: 2^23 tiles of 64
+// and as many larger ones as hold them. Split tiles are fewer by far: their sums may take 512 MB (choose()).
 bool dense_sizes(const GemmArgs &g, const GemmForm &f) {
   const int el = f.f32 ? 4 : 8;
   return g.lda % el == 0 && g.ldb % el == 0 && dense_tiles(g, f, 64) <= (1LL << 23) && g.nk > 0 &&

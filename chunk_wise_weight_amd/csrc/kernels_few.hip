@@ -202,6 +202,10 @@ hipError_t run(const GemmArgs &g, hipStream_t s) {
 
 }  // namespace
 
+// Up to 16 rows of tokens. Against the tiles that 17 rows take (with the call, some 11 us of host time at least): one to
+// four tokens 9728 -> 2560 13.0 us and 17.2, eight 15.8, the pair 22.8 and 24.7; fp32 9728 -> 2560 32 to 37 and 40; odd
+// widths 11.4 and 14 to 28. From 9 rows on large bf16 weights would gain by the tiles: 12 and 16 rows 18.0 and 19.5, the
+// pair 29.2 and 30.0 (17.1 and 25.0). They stay here, where no call needs a workspace.
 bool few_sizes(const GemmArgs &g, const GemmForm &f) { return !f.a_trans && g.nj <= 16; }
 
 hipError_t launch_few(const GemmArgs &g, const GemmForm &f, hipStream_t s) {
