@@ -1049,9 +1049,10 @@ def _sized(c: _Call, ts, name: str, types, like: _Read) -> _Read:
 
 def _tops(c: _Call, ts, like: _Read) -> _Read:
     ts = list(ts)
+    r = _Read(c, ts, "tops", *_TOPS)
     if [tuple(t.shape) for t in ts] != [(2, -(-n // 256)) for n in array("q", like.numel)]:
         raise ValueError("tops must have one tensor [2][ceil(numel / 256)] per parameter")
-    return _Read(c, ts, "tops", *_TOPS)
+    return r
 
 
 def _list_call(ts, stream) -> _Call:
@@ -1083,7 +1084,7 @@ def ttt_adamw(params, grads, m, v, step, lr, betas: Tuple[float, float] = (0.9, 
     `tops`, int16 [2][ceil(numel / 256)] per parameter (all zeros at the start, as the codes): see include/ttt.h for
     what a code stands for, ttt_adamw_values for its values. They are rounded at random, by `seed`, the step and the
     place. copies: bfloat16 tensors that receive the rounded parameters. norm: what ttt_grad_norm gave for the
-    gradients; one that is not finite clips nothing. step (1, 2, ...) and lr are numbers, or device tensors of one
+    gradients; one that is not finite clips nothing, and without one tau does not count. step (1, 2, ...) and lr are numbers, or device tensors of one
     element (int64, float32) that a captured call reads anew at each replay."""
     params, m = list(params), list(m)
     bits8 = bool(m) and _tensor(m[0], "m").dtype == torch.uint8

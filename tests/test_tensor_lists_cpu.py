@@ -87,3 +87,11 @@ def test_the_build_goes_on_without_a_host_compiler(monkeypatch, tmp_path, cxx):
     with pytest.warns(RuntimeWarning, match="read in Python"):
         assert build._build_lists(False) is False
     assert not left.exists()
+
+
+def test_every_list_names_what_is_no_tensor_in_it(monkeypatch):
+    """Also tops, whose shapes are looked at."""
+    call = binding._Call(torch.device("cpu"), None)
+    like = types.SimpleNamespace(numel=b"", n=0)
+    with pytest.raises(TypeError, match="tops must be tensors, got NoneType"):
+        binding._tops(call, [None], like)
