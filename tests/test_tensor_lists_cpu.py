@@ -89,7 +89,7 @@ def test_the_build_goes_on_without_a_host_compiler(monkeypatch, tmp_path, cxx):
     assert not left.exists()
 
 
-def test_every_list_names_what_is_no_tensor_in_it(monkeypatch):
+def test_every_list_names_what_is_no_tensor_in_it():
     """Also tops, whose shapes are looked at."""
     call = binding._Call(torch.device("cpu"), None)
     like = types.SimpleNamespace(numel=b"", n=0)
