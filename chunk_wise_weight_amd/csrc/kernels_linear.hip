@@ -337,11 +337,11 @@ Choice choose_dense(const GemmArgs &g, const GemmForm &f) {
   const Choice s = choose(g, 64, small, f.f32 ? shared(1.45, 1.03) : shared(0.34, 0.25));
   if (s.us < best.us) best = s;
   if (f.f32) return best;  // four fp32 tiles of 128 take what one of 256 does
-  // a tile of 256 stores by itself on its CU, and odd rows of results take it some 4 us longer. Of nine products, with and
-  // without GELU, bf16 results then take at most 3 % more than in the best tile (4099 x 1021 x 2047: tiles of 256 44 us, of
-  // 128 46), fp32 ones, whose stores fit no such number, up to 17 % (45 and 55, but 8192 x 1024 x 4095: 115 and 101)
+  // A tile of 256 stores by itself on its CU, and odd rows of results take it 7 us longer where there is a bias (4099 x 1021
+  // x 2047 with bias and GELU: 56 us, with tiles of 128 51, of 64 47; 8192 x 1024 x 4095: 87, 98, 123). Without one it takes
+  // less: 44 us against 45 and 45 (fp32 results 44, 55, 50), and the rule, which knows sizes alone, then takes those.
   const long long n = dense_tiles(g, f, 256);
-  const Choice b = choose(g, 256, n, shared(1.75, 1.75), g.ldo % 8 ? 4.0 * ((n + kCus - 1) / kCus) : 0);
+  const Choice b = choose(g, 256, n, shared(1.75, 1.75), g.ldo % 8 ? 7.0 * ((n + kCus - 1) / kCus) : 0);
   return best.us < b.us ? best : b;
 }
 size_t parts_bytes(long long tiles, const Choice &c) {
