@@ -25,7 +25,17 @@ struct AdamStep {
   float shrink;      // lr decay
   uint32_t key;      // of the random bits, from seed and step
 };
+// A beta in two fp32 parts, so that it and `rest` = 1 - beta add up to one: rounded to one part, a beta2 of 0.9999 is off
+// by U / 4 of every moment it meets and by 10^-4 of what it leaves to the gradient (U = 2^-24).
+struct AdamDecay {
+  float hi, lo, rest;
+};
+inline AdamDecay adam_decay(double b) {
+  const float hi = (float)b;
+  return {hi, (float)(b - (double)hi), (float)(1.0 - b)};
+}
 struct AdamArgs {
+  AdamDecay decay1, decay2;  // fp32 moments
   double beta1, beta2, lr, decay, tau;
   double log1, log2;  // of the betas
   float eps;

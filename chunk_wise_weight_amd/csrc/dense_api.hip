@@ -532,6 +532,8 @@ int ttt_adamw(void *const *w, const int32_t *w_dt, const void *const *g, const i
     if (!rc) rc = ttt_check_device();
     if (rc) return rc;
     AdamArgs a{};
+    a.decay1 = adam_decay(beta1);
+    a.decay2 = adam_decay(beta2);
     a.beta1 = beta1;
     a.beta2 = beta2;
     a.eps = eps > 0 ? std::max((float)eps, 0x1p-149f) : 0.f;  // an eps above 0 stays so: 0 / eps is 0

@@ -17,11 +17,13 @@
 // step divides by its root.
 //
 // The moments of the 8-bit form are computed in fp64 and rounded to fp32 once
-// before they become codes. fp32 sums would do for the moments, but not for a
-// value next to the border between two codes: there the order of the roundings
-// would decide a code, and the same step computed elsewhere (a replica, a
-// resumed run on other software) would drift apart. The pass is bound by
-// memory either way.
+// before they become codes. fp32 sums would do for the moments, but where they
+// are computed elsewhere (a replica, a resumed run on other software) another
+// order of their roundings would change the last bit of every second value and,
+// where that lies next to the border between two codes, some 10^-5 of the codes.
+// In fp64 another order of the products and sums, which the definition leaves
+// open, reaches the fp32 value in some 10^-8 of all cases and a code in some
+// 10^-13. On this library the codes are the same on every run.
 #include <type_traits>
 
 #include "adamw.h"
@@ -278,10 +280,11 @@ __device__ __forceinline__ AdamStep step_of(const AdamArgs &a) {
   return s;
 }
 
-// sqrt(v) by the hardware's root (1 ulp), with `small` also of the denormals, which it may take as 0: their roots times
+// sqrt(v) by the hardware's root (1 ulp), with SMALL also of the denormals, which it may take as 0: their roots times
 // root2 are below 2^-63 root2, half a step of an eps from 2 10^-12 root2 on.
-__device__ __forceinline__ float root(float v, bool small) {
-  if (!small) return __builtin_amdgcn_sqrtf(v);
+template <bool SMALL>
+__device__ __forceinline__ float root(float v) {
+  if (!SMALL) return __builtin_amdgcn_sqrtf(v);
   const bool tiny = v < 0x1p-96f;
   return __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p-32f : 1.f);
 }
@@ -323,29 +326,30 @@ __device__ __forceinline__ Rates rates_of(const AdamArgs &a) {
   }
   return r;
 }
-// With `small` the denominator may be a denormal, which the hardware's reciprocal may take as 0 (and 0 / eps would be 0
+// With SMALL the denominator may be a denormal, which the hardware's reciprocal may take as 0 (and 0 / eps would be 0
 // times infinity); below 2^-96 it is scaled, and the moment alike before lr1 makes it smaller.
-__device__ __forceinline__ float moved(float w, float m, float v, const AdamStep &s, float eps, bool small) {
-  const float d = fmaf(root(v, small), s.root2, eps);
-  float q;
-  if (small && d < 0x1p-96f)
-    q = s.lr1 * (m * 0x1p96f * __builtin_amdgcn_rcpf(d * 0x1p96f));
-  else
-    q = s.lr1 * m * __builtin_amdgcn_rcpf(d);
+template <bool SMALL>
+__device__ __forceinline__ float moved(float w, float m, float v, const AdamStep &s, float eps) {
+  const float d = fmaf(root<SMALL>(v), s.root2, eps);
+  float q = s.lr1 * m * __builtin_amdgcn_rcpf(d);
+  if (SMALL && d < 0x1p-96f) q = s.lr1 * (m * 0x1p96f * __builtin_amdgcn_rcpf(d * 0x1p96f));
   return fmaf(-s.shrink, w, w) - q;
 }
+// f(std::true_type) where eps is small, else f(std::false_type): all threads take one branch, and it is the elements' loop
+// that is in it (a branch for each of them costs the 8-bit form 3 %).
+template <class F>
+__device__ __forceinline__ void by_eps(float eps, float root2, F &&f) {
+  if (small_eps(eps, root2))
+    f(std::true_type{});
+  else
+    f(std::false_type{});
+}
 
-// A beta in two fp32 parts, so that it and `rest` = 1 - beta add up to one: rounded to one part, a beta2 of 0.9999 is off
-// by U / 4 of every moment it meets and by 10^-4 of what it leaves to the gradient (U = 2^-24).
-struct Decay {
-  float hi, lo, rest;
-  __device__ __forceinline__ explicit Decay(double b) : hi((float)b), lo((float)(b - (double)hi)), rest((float)(1.0 - b)) {}
-  // beta x, rounded once; an infinity's small part must not meet its large one as another infinity, or as 0 times it
-  __device__ __forceinline__ float of(float x) const {
-    constexpr float kMost = 3.4028234663852886e38f;
-    return fmaf(hi, x, lo * __builtin_amdgcn_fmed3f(x, -kMost, kMost));
-  }
-};
+// beta x, rounded once; an infinity's small part must not meet its large one as another infinity, or as 0 times it
+__device__ __forceinline__ float decayed(const AdamDecay &b, float x) {
+  constexpr float kMost = 3.4028234663852886e38f;
+  return fmaf(b.hi, x, b.lo * __builtin_amdgcn_fmed3f(x, -kMost, kMost));
+}
 
 // fp32 moments: a wave takes four blocks of a chunk, a lane four elements of each. Everything is loaded before anything
 // is stored. FULL: every element of the chunk is there.
@@ -368,8 +372,7 @@ __device__ __forceinline__ void step_chunk(const AdamTable &t, const AdamArgs &a
   }
   const AdamStep s = step_of(a);
   const Rates r = rates_of(a);
-  const Decay b1(r.b1), b2(r.b2);
-  const bool small = small_eps(a.eps, s.root2);
+  const AdamDecay b1 = a.decay1, b2 = a.decay2;
 #pragma unroll
   for (int k = 0; k < kWaveSteps; ++k) {
     const long long at = at0 + k * SKIP;
@@ -383,10 +386,13 @@ __device__ __forceinline__ void step_chunk(const AdamTable &t, const AdamArgs &a
     for (int e = 0; e < 4; ++e) {
       // the factor to the gradient first: its square may leave fp32
       const float d = r.clipped ? (float)((double)x[e] * r.factor) : x[e];
-      mk[e] = fmaf(b1.rest, d, b1.of(mk[e]));
-      vk[e] = fmaf(b2.rest * d, d, b2.of(vk[e]));
-      wk[e] = moved(wk[e], mk[e], vk[e], s, a.eps, small);
+      mk[e] = fmaf(b1.rest, d, decayed(b1, mk[e]));
+      vk[e] = fmaf(b2.rest * d, d, decayed(b2, vk[e]));
     }
+    by_eps(a.eps, s.root2, [&](auto small) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) wk[e] = moved<decltype(small)::value>(wk[e], mk[e], vk[e], s, a.eps);
+    });
     put<NT>(t.m[i], 1, at, left, mk);
     put<NT>(t.v[i], 1, at, left, vk);
     put<NT>(t.w[i], w_f32, at, left, wk);
@@ -396,8 +402,8 @@ __device__ __forceinline__ void step_chunk(const AdamTable &t, const AdamArgs &a
 }
 
 // 8-bit moments: half a wave takes a block, a lane eight elements of it, two blocks one after the other. (277M bf16
-// weights: 680 us; 729 with four elements per lane, 750 with a block each for 512 threads. 66 vector instructions per
-// element are 480 us of it, the bytes at the rate of the fp32 form 490.)
+// weights: 660 us. When this form took 680, four elements per lane took 729 and a block each for 512 threads 750. 66 vector
+// instructions per element are 480 us of it, the bytes at the rate of the fp32 form 490.)
 constexpr int kHalfSteps = kAdamChunk / kAdamBlock / (kThreads / 32);
 
 template <bool NT, bool FULL>
@@ -430,7 +436,6 @@ __device__ __forceinline__ void step_chunk8(const AdamTable &t, const AdamArgs &
   const Rates r = rates_of(a);
   // fp64 holds the factor's square with the betas
   const double b1 = r.b1, b2 = r.b2, o1 = (1.0 - b1) * r.factor, o2 = (1.0 - b2) * r.factor * r.factor;
-  const bool small = small_eps(a.eps, s.root2);
   const uint32_t key = adam_mix(s.key + kGolden * (uint32_t)(t.tensor0 + i + 1));
 #pragma unroll
   for (int k = 0; k < kHalfSteps; ++k) {
@@ -487,8 +492,10 @@ __device__ __forceinline__ void step_chunk8(const AdamTable &t, const AdamArgs &
     put_codes8<NT>((uint8_t *)t.m[i] + at, left, nm);
     put_codes8<NT>((uint8_t *)t.v[i] + at, left, nv);
     expand(w[k], w_f32, wk);
+    by_eps(a.eps, s.root2, [&](auto small) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) wk[e] = moved(wk[e], mk[e], vk[e], s, a.eps, small);
+      for (int e = 0; e < 8; ++e) wk[e] = moved<decltype(small)::value>(wk[e], mk[e], vk[e], s, a.eps);
+    });
     put8<NT>(t.w[i], w_f32, at, left, wk);
     if (t.copy[i]) put8<NT>(t.copy[i], 0, at, left, wk);
   }
