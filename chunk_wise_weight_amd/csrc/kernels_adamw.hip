@@ -19,11 +19,11 @@
 // The moments of the 8-bit form are computed in fp64 and rounded to fp32 once
 // before they become codes. fp32 sums would do for the moments, but where they
 // are computed elsewhere (a replica, a resumed run on other software) another
-// order of their roundings would change the last bit of every second value and,
-// where that lies next to the border between two codes, some 10^-5 of the codes.
-// In fp64 another order of the products and sums, which the definition leaves
-// open, reaches the fp32 value in some 10^-8 of all cases and a code in some
-// 10^-13. On this library the codes are the same on every run.
+// order of their roundings would change the last bit of every second value, and
+// one bit in 2^20 is a border between two codes: some 10^-6 of the codes would
+// differ at every step. In fp64 another order of the products and sums, which the
+// definition leaves open, reaches the fp32 value in some 10^-8 of all cases and a
+// code in some 10^-14. On this library the codes are the same on every run.
 #include <type_traits>
 
 #include "adamw.h"

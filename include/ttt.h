@@ -499,8 +499,8 @@ int ttt_gated(const void *x, const void *W_gate, const void *W_up, ttt_dtype dt,
  * dy. Beside the rounding of the results it makes the error of dx and dW 1.41
  * times what products of exact q would leave (in the mean square 0.0023 and
  * 0.0017 of the result); a caller who needs those takes the fp32 form, with x
- * and W in fp32. Where q is dy, in bf16 and without an activation, there
- * is none); the biases' gradients sum the unrounded ones. Every sum's order is
+ * and W in fp32. Where q is dy, in bf16 and without an activation, there is no
+ * such rounding. The biases' gradients sum the unrounded ones. Every sum's order is
  * fixed by the sizes and types and by whether the operands start on 16 bytes
  * (the kernels for those that do are the faster ones): the same call gives the
  * same bits.
