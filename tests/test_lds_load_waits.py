@@ -52,7 +52,7 @@ def loads_and_exposed(asm_text):
     return count, bad
 
 
-def test_checker_flags_what_is_too_close():
+def test_what_is_too_close_is_found():
     load = "buffer_load_dwordx4 v1, s[8:11], s0 offen lds\n"
     assert loads_and_exposed("s_mov_b32 m0, s4\n" + load) == (1, [("s_mov_b32 m0, s4", load.strip())])
     assert loads_and_exposed("s_mov_b32 m0, s4\ns_nop 0\n" + load) == (1, [])
